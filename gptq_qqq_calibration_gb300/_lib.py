@@ -12,7 +12,7 @@ import threading
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgptq_hess.so")
 
-HESS_BF16, HESS_F32 = 0, 1
+HESS_BF16, HESS_F32, HESS_F16 = 0, 1, 2
 (HESS_OK, HESS_ERR_INVALID, HESS_ERR_UNSUPPORTED, HESS_ERR_OOM, HESS_ERR_CUDA, HESS_ERR_TIMEOUT,
  HESS_ERR_NOT_PD, HESS_ERR_INTERNAL) = range(8)
 STATUS_NAMES = {0: "HESS_OK", 1: "HESS_ERR_INVALID", 2: "HESS_ERR_UNSUPPORTED", 3: "HESS_ERR_OOM",
@@ -24,7 +24,7 @@ OPTIONS = {"flush_tokens": 1, "max_pending": 2, "chunk_tokens": 3, "wait_timeout
 _vp, _i32, _i64, _f64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_double
 _fp = ctypes.POINTER(ctypes.c_float)
 
-# name -> (restype, argtypes); mirrors include/hess.h and include/gptq.h
+# name -> (restype, argtypes); mirrors the headers in include/
 PROTOTYPES = {
     "hess_create": (_i32, [_i64, ctypes.POINTER(_vp)]),
     "hess_add_batch": (_i32, [_vp, _vp, _i64, _i32, _vp]),
@@ -63,6 +63,12 @@ PROTOTYPES = {
     "gptq_read_factor": (_i32, [_vp, _vp, _vp]),
     "gptq_quantize": (_i32, [_vp, _vp, _i32, _i64, _i32, _vp, _vp, _vp, _vp, ctypes.POINTER(_f64)]),
     "gptq_destroy": (_i32, [_vp]),
+    "distill_forward": (_i32, [_vp, _i64, _i64, _i64, _i32, _vp, _i32, _vp, _i32, _i64, _vp, _vp, _f64, _vp, _vp,
+                               _vp]),
+    "distill_backward": (_i32, [_vp, _i64, _i64, _i64, _i32, _vp, _i32, _vp, _i32, _i64, _vp, _vp, _f64, _vp, _vp,
+                                _vp, _i64, _vp]),
+    "distill_step": (_i32, [_vp, _i64, _i64, _i64, _i32, _vp, _i32, _vp, _i32, _i64, _vp, _vp, _f64, _vp, _vp, _i64,
+                            _vp]),
     "hess_last_error": (ctypes.c_char_p, []),
     "hess_abi_version": (_i32, []),
 }

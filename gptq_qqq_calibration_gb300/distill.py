@@ -1,0 +1,139 @@
+"""Python binding of the distillation loss in ``include/distill.h``.
+
+Argument marshalling only: tensors become device pointers, sizes and row
+strides; the loss and its gradient run in the library's CUDA kernels.  The
+functions carry the C names and allocate their outputs; ``distill_loss`` is
+the same loss as a node of an autograd graph.
+"""
+
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+
+from . import _lib
+from ._lib import HESS_BF16, HESS_F16, HESS_F32, check
+
+__all__ = ["distill_forward", "distill_backward", "distill_step", "distill_loss"]
+
+_DTYPES = {torch.bfloat16: HESS_BF16, torch.float16: HESS_F16, torch.float32: HESS_F32}
+_STATS = 8  # floats of one row of the statistics (DISTILL_STATS)
+
+
+def _stream(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+def _rows2d(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
+    """(rows, vocab, row stride in elements) of a [..., vocab] tensor whose
+    rows are evenly spaced and contiguous inside."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    if t.dim() == 0 or t.shape[-1] == 0:
+        raise ValueError(f"{name} must have at least one column")
+    vocab = t.shape[-1]
+    if t.is_contiguous():
+        return t.numel() // vocab, vocab, vocab
+    if t.dim() != 2 or (vocab > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < vocab):
+        raise ValueError(f"{name} must be contiguous, or a 2-D view whose rows are contiguous")
+    return t.shape[0], vocab, t.stride(0) if t.shape[0] > 1 else vocab
+
+
+def _vector(t: Optional[torch.Tensor], rows: int, name: str):
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != rows:
+        raise ValueError(f"{name} must be a contiguous float32 CUDA tensor with one value a row")
+    return t.data_ptr()
+
+
+def _common(logits, top_logits, top_index, temperature, teacher_lse, weights):
+    rows, vocab, ld = _rows2d(logits, "logits")
+    for t, name in ((top_logits, "top_logits"), (top_index, "top_index")):
+        if not t.is_cuda or not t.is_contiguous() or t.dim() < 1:
+            raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if top_logits.dtype not in _DTYPES:
+        raise ValueError(f"top_logits must be bfloat16, float16 or float32, got {top_logits.dtype}")
+    if top_index.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"top_index must be int32 or int64, got {top_index.dtype}")
+    top = top_logits.shape[-1]
+    if top_index.shape != top_logits.shape or top_logits.numel() != rows * top:
+        raise ValueError("top_logits and top_index must both be [rows, top]")
+    return rows, (logits.data_ptr(), ld, rows, vocab, _DTYPES[logits.dtype], top_logits.data_ptr(),
+                  _DTYPES[top_logits.dtype], top_index.data_ptr(), top_index.element_size(), top,
+                  _vector(teacher_lse, rows, "teacher_lse"), _vector(weights, rows, "weights"), float(temperature))
+
+
+def _output(out: Optional[torch.Tensor], logits: torch.Tensor) -> Tuple[torch.Tensor, int]:
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    elif out.shape != logits.shape or out.dtype != logits.dtype:
+        raise ValueError("the gradient must have the logits' shape and type")
+    return out, _rows2d(out, "the gradient")[2]
+
+
+def distill_forward(logits: torch.Tensor, top_logits: torch.Tensor, top_index: torch.Tensor,
+                    temperature: float = 1.0, teacher_lse: Optional[torch.Tensor] = None,
+                    weights: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Loss of every row [rows] and the statistics ``distill_backward`` takes."""
+    rows, args = _common(logits, top_logits, top_index, temperature, teacher_lse, weights)
+    loss = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    stats = torch.empty((rows, _STATS), dtype=torch.float32, device=logits.device)
+    check(_lib.load().distill_forward(*args, loss.data_ptr(), stats.data_ptr(), _stream(stream)))
+    return loss, stats
+
+
+def distill_backward(logits: torch.Tensor, stats: torch.Tensor, top_logits: torch.Tensor, top_index: torch.Tensor,
+                     temperature: float = 1.0, teacher_lse: Optional[torch.Tensor] = None,
+                     weights: Optional[torch.Tensor] = None, grad: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of ``(grad * loss).sum()`` (``loss.sum()`` without grad) with
+    respect to the logits; ``out`` may be ``logits``."""
+    rows, args = _common(logits, top_logits, top_index, temperature, teacher_lse, weights)
+    if not stats.is_cuda or stats.dtype != torch.float32 or not stats.is_contiguous() or \
+            stats.numel() != rows * _STATS:
+        raise ValueError("stats must be the tensor distill_forward returned for these logits")
+    out, ldd = _output(out, logits)
+    check(_lib.load().distill_backward(*args, stats.data_ptr(), _vector(grad, rows, "grad"), out.data_ptr(), ldd,
+                                       _stream(stream)))
+    return out
+
+
+def distill_step(logits: torch.Tensor, top_logits: torch.Tensor, top_index: torch.Tensor, temperature: float = 1.0,
+                 teacher_lse: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Loss of every row and the gradient of their sum, in one pass over the
+    logits; ``out`` may be ``logits``."""
+    rows, args = _common(logits, top_logits, top_index, temperature, teacher_lse, weights)
+    loss = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    out, ldd = _output(out, logits)
+    check(_lib.load().distill_step(*args, loss.data_ptr(), out.data_ptr(), ldd, _stream(stream)))
+    return loss, out
+
+
+class _DistillLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, top_logits, top_index, temperature, teacher_lse, weights):
+        loss, stats = distill_forward(logits, top_logits, top_index, temperature, teacher_lse, weights)
+        ctx.save_for_backward(logits, stats, top_logits, top_index, teacher_lse, weights)
+        ctx.temperature = temperature
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        logits, stats, top_logits, top_index, teacher_lse, weights = ctx.saved_tensors
+        return (distill_backward(logits, stats, top_logits, top_index, ctx.temperature, teacher_lse, weights,
+                                 grad=grad.contiguous()), None, None, None, None, None)
+
+
+def distill_loss(logits: torch.Tensor, top_logits: torch.Tensor, top_index: torch.Tensor, temperature: float = 1.0,
+                 teacher_lse: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Loss of every row [rows] as a node of an autograd graph; only the
+    logits get a gradient."""
+    return _DistillLoss.apply(logits, top_logits, top_index, float(temperature), teacher_lse, weights)
