@@ -63,6 +63,12 @@ PROTOTYPES = {
     "gptq_read_factor": (_i32, [_vp, _vp, _vp]),
     "gptq_quantize": (_i32, [_vp, _vp, _i32, _i64, _i32, _vp, _vp, _vp, _vp, ctypes.POINTER(_f64)]),
     "gptq_destroy": (_i32, [_vp]),
+    "gated_ff_create": (_i32, [_i64, _i64, _i64, _i32, _i32, ctypes.POINTER(_vp)]),
+    "gated_ff_forward": (_i32, [_vp, _vp, _i64, _vp, _vp, _vp, _vp]),
+    "gated_ff_backward": (_i32, [_vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "gated_ff_sync": (_i32, [_vp, _vp]),
+    "gated_ff_set_timeout": (_i32, [_vp, _i64]),
+    "gated_ff_destroy": (_i32, [_vp]),
     "distill_forward": (_i32, [_vp, _i64, _i64, _i64, _i32, _vp, _i32, _vp, _i32, _i64, _vp, _vp, _f64, _vp, _vp,
                                _vp]),
     "distill_backward": (_i32, [_vp, _i64, _i64, _i64, _i32, _vp, _i32, _vp, _i32, _i64, _vp, _vp, _f64, _vp, _vp,

@@ -1,0 +1,810 @@
+// Gated feed-forward projections h = act(X Wg^T) * (X Wu^T) and their gradient
+// (formulas and conventions: include/gated_ff.h).
+//
+// Four contractions share one tensor-core loop; what differs is which operand
+// is contiguous along the contraction (K-major) and which along its own rows
+// (MN-major), and what happens to the finished tile:
+//
+//   forward   A = X [n, d]   K-major    B = Wg | Wu [f, d] K-major   sum over d
+//   dg, du    the same products, then dh joins in the epilogue
+//   dX        A = dg, du     K-major    B = Wg, Wu         MN-major  sum over f, twice
+//   dWg, dWu  A = dg | du    MN-major   B = X              MN-major  sum over n
+//
+// Tile: 256 x 256 on a pair of SMs (tcgen05 cta_group::2), the largest one
+// instruction covers, so each SM receives 32 KB per 64 steps of the
+// contraction for its share of 256 x 256 x 64 products.  In the forward
+// product the pair's B halves are 128 rows of Wg (even CTA) and the same 128
+// rows of Wu (odd CTA): g and u of a token land in the same tensor-memory
+// lane, 128 columns apart, and meet in the epilogue's registers.  Tensor
+// memory holds two tiles, so one tile's epilogue runs under the next one's
+// products.
+//
+// Every operand box is 64 x 64 elements with the 128-byte swizzle, whichever
+// way it is contiguous: boxes stacked in shared memory serve both the K-major
+// and the MN-major descriptors, and one tensor map per matrix is enough.
+// Edges cost nothing: the copies fill zeros past the end of a matrix.
+#include <cstdarg>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <mutex>
+#include <new>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "device_ptr.h"
+#include "gated_ff.h"
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace hk {
+namespace {
+
+constexpr int kKB = 64;                            // contraction steps of one stage
+constexpr int kStages = 6;
+constexpr uint32_t kBoxBytes = 64 * 64 * 2;
+constexpr uint32_t kOperandBytes = 2 * kBoxBytes;  // 128 rows of A, or of B, per CTA
+constexpr uint32_t kStageBytes = 2 * kOperandBytes;
+constexpr int kEpiWarps = 8;
+constexpr int kFirstEpiWarp = 4;
+constexpr int kThreads = (kFirstEpiWarp + kEpiWarps) * 32;
+constexpr uint32_t kTmemCols = 512;  // two 256-column tiles
+constexpr int kNumBarriers = 2 * kStages + 5;
+constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + 8 * kNumBarriers + 16;
+constexpr unsigned long long kDrainLimitNs = 1000000000ull;
+constexpr unsigned long long kAbortSettleNs = 2000000ull;
+constexpr int kGroupM = 8;  // row tiles that run side by side (their B boxes meet in L2)
+
+enum { kMapX, kMapWg, kMapWu, kMapDg, kMapDu, kMaps };
+enum { kForward, kActGrad, kGradients };  // what a launch computes
+
+struct FfParams {
+    CUtensorMap maps[kMaps];
+    int32_t n, d, f;
+    int32_t act;
+    int32_t tiles_x;  // kGradients: tiles of dX (first), then 2 * tiles_w tiles of dWg and dWu
+    int32_t tiles_w;
+    int32_t n_units;
+    uint32_t fmt;     // operand format of the instruction descriptor: 0 = f16, 1 = bf16
+    void* out0;       // h | dg | dX
+    void* out1;       // - | du | dWg
+    void* out2;       // - | -  | dWu
+    const void* dh;
+    uint32_t* status;
+    unsigned long long timeout_ns;
+};
+
+// Tile u of tm x tn, in groups of kGroupM row tiles walked column by column.
+__host__ __device__ inline void tile_at(int u, int tm, int tn, int& m, int& n) {
+    const int per = kGroupM * tn;
+    const int g = u / per, r = u - g * per;
+    const int rows = tm - g * kGroupM < kGroupM ? tm - g * kGroupM : kGroupM;
+    n = r / rows;
+    m = g * kGroupM + (r - n * rows);
+}
+
+struct Unit {
+    int kind;   // 0: X times weights, 1: dX, 2: dW
+    int m0, n0;  // first row of A and of B (kind 0: of each weight)
+    int which;  // kind 2: 0 = gate, 1 = up
+    int n_kb;
+    int split;  // kind 1: k-blocks of the gate half
+};
+
+template <int kWhat>
+__device__ __forceinline__ Unit unit_at(const FfParams& p, int u) {
+    Unit r{};
+    int m, n;
+    if constexpr (kWhat != kGradients) {
+        tile_at(u, (p.n + 255) / 256, (p.f + 127) / 128, m, n);
+        r.m0 = m * 256;
+        r.n0 = n * 128;
+        r.n_kb = (p.d + kKB - 1) / kKB;
+    } else if (u < p.tiles_x) {
+        tile_at(u, (p.n + 255) / 256, (p.d + 255) / 256, m, n);
+        r.kind = 1;
+        r.m0 = m * 256;
+        r.n0 = n * 256;
+        r.split = (p.f + kKB - 1) / kKB;
+        r.n_kb = 2 * r.split;
+    } else {
+        u -= p.tiles_x;
+        r.which = u >= p.tiles_w ? 1 : 0;
+        tile_at(u - r.which * p.tiles_w, (p.f + 255) / 256, (p.d + 255) / 256, m, n);
+        r.kind = 2;
+        r.m0 = m * 256;
+        r.n0 = n * 256;
+        r.n_kb = (p.n + kKB - 1) / kKB;
+    }
+    return r;
+}
+
+__device__ __forceinline__ uint32_t instr_desc(uint32_t fmt, bool a_mn, bool b_mn) {
+    return (1u << 4) | (fmt << 7) | (fmt << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+           ((256u >> 3) << 17) | ((256u >> 4) << 24);
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t (&a)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
+          "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15])
+        : "r"(t)
+        : "memory");
+}
+// Waits for the loads above; `a` and `b` pass through so that no use of them moves before the wait.
+__device__ __forceinline__ void tmem_wait16(uint32_t (&a)[16], uint32_t (&b)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                   "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]),
+                   "+r"(a[15])::"memory");
+    asm volatile(""
+                 : "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7]),
+                   "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]), "+r"(b[12]), "+r"(b[13]), "+r"(b[14]),
+                   "+r"(b[15])::"memory");
+}
+
+template <class T>
+struct Half2;
+template <>
+struct Half2<__nv_bfloat16> {
+    static __device__ uint32_t pack(float a, float b) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        uint32_t w;
+        memcpy(&w, &h, 4);
+        return w;
+    }
+    static __device__ float2 unpack(uint32_t w) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+};
+template <>
+struct Half2<__half> {
+    static __device__ uint32_t pack(float a, float b) {
+        const __half2 h = __floats2half2_rn(a, b);
+        uint32_t w;
+        memcpy(&w, &h, 4);
+        return w;
+    }
+    static __device__ float2 unpack(uint32_t w) {
+        __half2 h;
+        memcpy(&h, &w, 4);
+        return __half22float2(h);
+    }
+};
+
+// act(g) = g s and act'(g) = s + g s (1 - s) z', with s = 1 / (1 + e^-z):
+// z = g for silu; z = 2 sqrt(2/pi) (g + 0.044715 g^3) for gelu, whose
+// (1 + tanh(z / 2)) / 2 is the same s.
+__device__ __forceinline__ float gate_sigmoid(float g, int act, float& dz) {
+    float z = g;
+    dz = 1.0f;
+    if (act == GATED_FF_GELU_TANH) {
+        const float c = 1.5957691216057308f, g2 = g * g;
+        z = c * g * fmaf(0.044715f, g2, 1.0f);
+        dz = c * fmaf(3.0f * 0.044715f, g2, 1.0f);
+    }
+    return __fdividef(1.0f, 1.0f + __expf(-z));
+}
+
+// Eight consecutive values of one row.
+template <class T>
+__device__ __forceinline__ void store8(T* p, const float* x) {
+    uint4 v;
+    v.x = Half2<T>::pack(x[0], x[1]);
+    v.y = Half2<T>::pack(x[2], x[3]);
+    v.z = Half2<T>::pack(x[4], x[5]);
+    v.w = Half2<T>::pack(x[6], x[7]);
+    *reinterpret_cast<uint4*>(p) = v;
+}
+
+// Epilogue of one tile by one warp: its 32 lanes are 32 rows of this CTA's 128
+// (lane quarter warp % 4), and it takes half of the columns, 16 at a time.
+template <class T, int kWhat>
+__device__ __forceinline__ void finish_tile(const FfParams& p, const Unit& un, uint32_t acc, int half, int64_t row) {
+    if constexpr (kWhat != kGradients) {
+        const bool in = row < p.n;
+#pragma unroll 1
+        for (int c = half * 64; c < half * 64 + 64; c += 16) {
+            const int col = un.n0 + c;
+            uint32_t g[16], u[16];
+            tmem_ld16(acc + c, g);
+            tmem_ld16(acc + 128 + c, u);
+            uint4 dv[2] = {};
+            if constexpr (kWhat == kActGrad) {
+                const T* const dh = static_cast<const T*>(p.dh) + row * p.f + col;
+                if (in && col < p.f) dv[0] = *reinterpret_cast<const uint4*>(dh);
+                if (in && col + 8 < p.f) dv[1] = *reinterpret_cast<const uint4*>(dh + 8);
+            }
+            tmem_wait16(g, u);
+            if constexpr (kWhat == kForward) {
+                float h[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float dz;
+                    const float gi = __uint_as_float(g[i]);
+                    h[i] = gi * gate_sigmoid(gi, p.act, dz) * __uint_as_float(u[i]);
+                }
+                T* const out = static_cast<T*>(p.out0) + row * p.f + col;
+                if (in && col < p.f) store8(out, h);
+                if (in && col + 8 < p.f) store8(out + 8, h + 8);
+            } else {
+                const uint32_t w[8] = {dv[0].x, dv[0].y, dv[0].z, dv[0].w, dv[1].x, dv[1].y, dv[1].z, dv[1].w};
+                float dg[16], du[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 d2 = Half2<T>::unpack(w[i / 2]);
+                    const float dh = (i & 1) ? d2.y : d2.x;
+                    float dz;
+                    const float gi = __uint_as_float(g[i]);
+                    const float s = gate_sigmoid(gi, p.act, dz);
+                    du[i] = dh * (gi * s);
+                    dg[i] = dh * __uint_as_float(u[i]) * fmaf(gi * s * (1.0f - s), dz, s);
+                }
+                T* const og = static_cast<T*>(p.out0) + row * p.f + col;
+                T* const ou = static_cast<T*>(p.out1) + row * p.f + col;
+                if (in && col < p.f) {
+                    store8(og, dg);
+                    store8(ou, du);
+                }
+                if (in && col + 8 < p.f) {
+                    store8(og + 8, dg + 8);
+                    store8(ou + 8, du + 8);
+                }
+            }
+        }
+    } else {
+        const bool in = row < (un.kind == 1 ? p.n : p.f);
+        T* const out = static_cast<T*>(un.kind == 1 ? p.out0 : un.which ? p.out2 : p.out1) + row * p.d;
+#pragma unroll 1
+        for (int c = half * 128; c < half * 128 + 128; c += 32) {
+            uint32_t a[16], b[16];
+            tmem_ld16(acc + c, a);
+            tmem_ld16(acc + c + 16, b);
+            tmem_wait16(a, b);
+            float x[32];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                x[i] = __uint_as_float(a[i]);
+                x[16 + i] = __uint_as_float(b[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+                if (in && un.n0 + c + i < p.d) store8(out + un.n0 + c + i, x + i);
+        }
+    }
+}
+
+// Warp roles of both CTAs: warp 0 copies this CTA's operand boxes (its bytes
+// count on the even CTA's barrier), warp 1 of the even CTA issues the pair's
+// MMAs, warps 4-11 finish tiles.  Every wait is bounded.
+template <class T, int kWhat>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    gated_ff_kernel(const __grid_constant__ FfParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* const gbase = smem_raw + (base - raw);
+    const uint32_t bar0 = base + kStages * kStageBytes;
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + kStages * kStageBytes + 8 * kNumBarriers);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
+    auto accf_bar = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
+    auto acce_bar = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4);
+    __shared__ int aborted;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1;
+    const int n_pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(accf_bar(b), 1);
+            mbar_init(acce_bar(b), 2 * kEpiWarps);
+        }
+        mbar_init(drain_bar, 1);
+        aborted = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    const unsigned long long limit = p.timeout_ns;
+
+    if (warp == 0 && lane == 0) {
+        bool ok = true;
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int u = pair; ok && u < p.n_units; u += n_pairs) {
+            const Unit un = unit_at<kWhat>(p, u);
+            const int m = un.m0 + static_cast<int>(rank) * 128;
+            const int n = un.kind == 0 ? un.n0 : un.n0 + static_cast<int>(rank) * 128;
+            for (int kb = 0; kb < un.n_kb; ++kb) {
+                if (!mbar_wait_cluster(empty_bar(stage), phase ^ 1u, limit)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sA = base + stage * kStageBytes, sB = sA + kOperandBytes;
+                const uint32_t fb = mapa_shared(full_bar(stage), 0);
+                if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * kStageBytes);
+                int k = kb * kKB;
+                if (un.kind == 0) {
+                    const CUtensorMap* const w = &p.maps[rank == 0 ? kMapWg : kMapWu];
+                    tma_load_2d_pair(sA, &p.maps[kMapX], fb, k, m);
+                    tma_load_2d_pair(sA + kBoxBytes, &p.maps[kMapX], fb, k, m + 64);
+                    tma_load_2d_pair(sB, w, fb, k, n);
+                    tma_load_2d_pair(sB + kBoxBytes, w, fb, k, n + 64);
+                } else if (un.kind == 1) {
+                    const bool up = kb >= un.split;
+                    const CUtensorMap* const a = &p.maps[up ? kMapDu : kMapDg];
+                    const CUtensorMap* const w = &p.maps[up ? kMapWu : kMapWg];
+                    if (up) k -= un.split * kKB;
+                    tma_load_2d_pair(sA, a, fb, k, m);
+                    tma_load_2d_pair(sA + kBoxBytes, a, fb, k, m + 64);
+                    tma_load_2d_pair(sB, w, fb, n, k);
+                    tma_load_2d_pair(sB + kBoxBytes, w, fb, n + 64, k);
+                } else {
+                    const CUtensorMap* const a = &p.maps[un.which ? kMapDu : kMapDg];
+                    tma_load_2d_pair(sA, a, fb, m, k);
+                    tma_load_2d_pair(sA + kBoxBytes, a, fb, m + 64, k);
+                    tma_load_2d_pair(sB, &p.maps[kMapX], fb, n, k);
+                    tma_load_2d_pair(sB + kBoxBytes, &p.maps[kMapX], fb, n + 64, k);
+                }
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (!ok) {
+            atomicOr(p.status, kStatusTimeoutLoad);
+            aborted = 1;
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        bool ok = true;
+        int stage = 0;
+        uint32_t phase = 0;
+        int ab = 0;
+        uint32_t aphase = 0;
+        for (int u = pair; ok && u < p.n_units; u += n_pairs) {
+            const Unit un = unit_at<kWhat>(p, u);
+            // K-major: 16 steps are 32 bytes of a row, 8-row groups are 1,024
+            // bytes apart.  MN-major: 16 steps are 16 rows of 128 bytes, the
+            // second 64 columns are a box further.
+            const bool a_mn = un.kind == 2, b_mn = un.kind != 0;
+            const uint32_t a_step = a_mn ? 2048u : 32u, b_step = b_mn ? 2048u : 32u;
+            const uint32_t a_lbo = a_mn ? kBoxBytes : 16u, b_lbo = b_mn ? kBoxBytes : 16u;
+            const uint32_t idesc = instr_desc(p.fmt, a_mn, b_mn);
+            if (!mbar_wait_cluster(acce_bar(ab), aphase ^ 1u, limit)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t acc = tmem + static_cast<uint32_t>(ab) * 256u;
+            for (int kb = 0; kb < un.n_kb; ++kb) {
+                if (!mbar_wait_cluster(full_bar(stage), phase, limit)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sA = base + stage * kStageBytes, sB = sA + kOperandBytes;
+#pragma unroll
+                for (int j = 0; j < kKB / 16; ++j)
+                    umma_f16_pair(acc, smem_desc_sw128(sA + j * a_step, a_lbo, 1024u),
+                                  smem_desc_sw128(sB + j * b_step, b_lbo, 1024u), idesc, (kb | j) != 0 ? 1u : 0u);
+                tc_commit_pair_mc(empty_bar(stage), 0x3);
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) break;
+            tc_commit_pair_mc(accf_bar(ab), 0x3);
+            if (++ab == 2) {
+                ab = 0;
+                aphase ^= 1u;
+            }
+        }
+        if (!ok) {
+            atomicOr(p.status, kStatusTimeoutMma);
+            aborted = 1;
+        }
+        // every MMA issued has completed before the pair's memories are released
+        tc_commit_pair_mc(drain_bar, 0x1);
+        if (!mbar_wait(drain_bar, 0, kDrainLimitNs)) atomicOr(p.status, kStatusTimeoutDrain);
+    } else if (warp >= kFirstEpiWarp) {
+        bool ok = true;
+        int ab = 0;
+        uint32_t aphase = 0;
+        const int q = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
+        const uint32_t acce0 = mapa_shared(acce_bar(0), 0);
+        for (int u = pair; u < p.n_units; u += n_pairs) {
+            const Unit un = unit_at<kWhat>(p, u);
+            if (!mbar_wait_cluster(accf_bar(ab), aphase, limit)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(ab) * 256u;
+            const int64_t row = static_cast<int64_t>(un.m0) + static_cast<int>(rank) * 128 + q * 32 + lane;
+            finish_tile<T, kWhat>(p, un, acc, half, row);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(acce0 + 8u * ab);
+            if (++ab == 2) {
+                ab = 0;
+                aphase ^= 1u;
+            }
+        }
+        if (!ok && lane == 0) {
+            atomicOr(p.status, kStatusTimeoutEpilogue);
+            aborted = 1;
+        }
+    }
+
+    // After a timeout a CTA cannot watch its own copies land (they count on the
+    // even CTA's barrier): it gives them time before its memory goes.
+    __syncthreads();
+    if (*reinterpret_cast<volatile int*>(&aborted) != 0) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < kAbortSettleNs) __nanosleep(1000);
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------- host side
+
+hess_status ff_fail(hess_status s, const char* fmt, ...) {
+    char buf[384];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    set_last_error(buf);
+    return s;
+}
+
+#define FF_TRY(call)                                                                           \
+    do {                                                                                       \
+        cudaError_t e_ = (call);                                                               \
+        if (e_ != cudaSuccess)                                                                 \
+            return ff_fail(HESS_ERR_CUDA, "%s failed: %s", #call, cudaGetErrorString(e_));     \
+    } while (0)
+
+bool ff_injected(const char* what) {
+    const char* f = std::getenv("HESS_FAULT");
+    return f && std::strcmp(f, what) == 0;
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn ff_encode_fn() {
+    static EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<EncodeTiledFn>(p);
+        return static_cast<EncodeTiledFn>(nullptr);
+    }();
+    return fn;
+}
+
+// Row-major [rows, cols] of 16-bit elements, 64 x 64 boxes, zeros past the edges.
+hess_status ff_encode(CUtensorMap* m, const void* ptr, int32_t dtype, int64_t rows, int64_t cols) {
+    EncodeTiledFn fn = ff_encode_fn();
+    if (!fn) return ff_fail(HESS_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    if (ff_injected("encode"))
+        return ff_fail(HESS_ERR_UNSUPPORTED, "injected tensor-map failure (HESS_FAULT=encode)");
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2u};
+    const cuuint32_t box[2] = {64u, 64u}, es[2] = {1u, 1u};
+    const CUresult r = fn(m, dtype == HESS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                          2, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return ff_fail(HESS_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled failed (%d) for [%lld, %lld]",
+                       static_cast<int>(r), static_cast<long long>(rows), static_cast<long long>(cols));
+    return HESS_OK;
+}
+
+// Per-device set-up: shared-memory limits, and how many pairs stay resident.
+hess_status ff_prepare(int dev, int* pairs) {
+    static std::mutex mu;
+    static int count[128] = {};
+    std::lock_guard<std::mutex> lk(mu);
+    if (dev < 0 || dev >= 128) return ff_fail(HESS_ERR_UNSUPPORTED, "device index %d", dev);
+    if (!count[dev]) {
+        for (auto fn : {gated_ff_kernel<__nv_bfloat16, kForward>, gated_ff_kernel<__nv_bfloat16, kActGrad>,
+                        gated_ff_kernel<__nv_bfloat16, kGradients>, gated_ff_kernel<__half, kForward>,
+                        gated_ff_kernel<__half, kActGrad>, gated_ff_kernel<__half, kGradients>})
+            FF_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(kSmemBytes)));
+        int sms = 0;
+        FF_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(sms & ~1), 1, 1);
+        cfg.blockDim = dim3(kThreads, 1, 1);
+        cfg.dynamicSmemBytes = kSmemBytes;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, gated_ff_kernel<__nv_bfloat16, kForward>, &cfg) != cudaSuccess ||
+            clusters <= 0) {
+            cudaGetLastError();
+            clusters = sms / 2;
+        }
+        count[dev] = clusters;
+    }
+    *pairs = count[dev];
+    return HESS_OK;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+}  // namespace hk
+
+struct gated_ff_ctx {
+    std::mutex mu;
+    int device = 0;
+    int pairs = 0;
+    int64_t d = 0, f = 0, train_tokens = 0;
+    int32_t dtype = 0, act = 0;
+    void* dg = nullptr;  // [train_tokens, f] each
+    void* du = nullptr;
+    uint32_t* status = nullptr;
+    cudaEvent_t ev = nullptr;  // the workspace's last user
+    cudaStream_t last = nullptr;
+    bool used = false;
+    unsigned long long timeout_ns = 2000000000ull;
+};
+
+namespace hk {
+namespace {
+
+hess_status ff_check_device(const gated_ff_ctx* g) {
+    int cur = -1;
+    FF_TRY(cudaGetDevice(&cur));
+    if (cur != g->device)
+        return ff_fail(HESS_ERR_INVALID, "handle belongs to device %d but device %d is current", g->device, cur);
+    return HESS_OK;
+}
+
+hess_status ff_check(const gated_ff_ctx* g, const void* p, const char* name) {
+    if (!p) return ff_fail(HESS_ERR_INVALID, "%s is NULL", name);
+    if (reinterpret_cast<uintptr_t>(p) % 16) return ff_fail(HESS_ERR_INVALID, "%s is not 16-byte aligned", name);
+    char why[128];
+    if (const char* w = device_ptr_problem(p, g->device, why)) return ff_fail(HESS_ERR_INVALID, "%s %s", name, w);
+    return HESS_OK;
+}
+
+#define FF_CHECK(expr)                       \
+    do {                                     \
+        const hess_status st_ = (expr);      \
+        if (st_ != HESS_OK) return st_;      \
+    } while (0)
+
+void ff_params(FfParams& p, const gated_ff_ctx* g, int64_t n) {
+    p.n = static_cast<int32_t>(n);
+    p.d = static_cast<int32_t>(g->d);
+    p.f = static_cast<int32_t>(g->f);
+    p.act = g->act;
+    p.fmt = g->dtype == HESS_BF16 ? 1u : 0u;
+    p.status = g->status;
+    p.timeout_ns = g->timeout_ns;
+}
+
+template <int kWhat>
+hess_status ff_launch(const gated_ff_ctx* g, const FfParams& p, cudaStream_t s) {
+    const int pairs = p.n_units < g->pairs ? p.n_units : g->pairs;
+    if (g->dtype == HESS_BF16)
+        gated_ff_kernel<__nv_bfloat16, kWhat><<<2 * pairs, kThreads, kSmemBytes, s>>>(p);
+    else
+        gated_ff_kernel<__half, kWhat><<<2 * pairs, kThreads, kSmemBytes, s>>>(p);
+    FF_TRY(cudaGetLastError());
+    return HESS_OK;
+}
+
+hess_status ff_tokens(int64_t n) {
+    if (n < 0) return ff_fail(HESS_ERR_INVALID, "n_tokens < 0");
+    if (n > (int64_t(1) << 26)) return ff_fail(HESS_ERR_UNSUPPORTED, "n_tokens > 2^26");
+    return HESS_OK;
+}
+
+void ff_free(gated_ff_ctx* g) {
+    cudaFree(g->dg);
+    cudaFree(g->du);
+    cudaFree(g->status);
+    if (g->ev) cudaEventDestroy(g->ev);
+}
+
+}  // namespace
+}  // namespace hk
+
+using hk::ff_fail;
+
+#define FF_EXPORT extern "C" __attribute__((visibility("default")))
+
+FF_EXPORT hess_status gated_ff_create(int64_t d, int64_t f, int64_t train_tokens, int32_t dtype, int32_t act,
+                                      gated_ff_t* out) {
+    if (!out) return ff_fail(HESS_ERR_INVALID, "out is NULL");
+    *out = nullptr;
+    if (d <= 0 || f <= 0) return ff_fail(HESS_ERR_INVALID, "d and f must be positive");
+    if (train_tokens < 0) return ff_fail(HESS_ERR_INVALID, "train_tokens < 0");
+    if (d % 8 || f % 8) return ff_fail(HESS_ERR_UNSUPPORTED, "d and f must be multiples of 8");
+    if (d > 65536 || f > 65536) return ff_fail(HESS_ERR_UNSUPPORTED, "d or f exceeds 65536");
+    if (train_tokens > (int64_t(1) << 26)) return ff_fail(HESS_ERR_UNSUPPORTED, "train_tokens > 2^26");
+    if (dtype == HESS_F32) return ff_fail(HESS_ERR_UNSUPPORTED, "gated_ff takes bf16 or f16");
+    if (dtype != HESS_BF16 && dtype != HESS_F16) return ff_fail(HESS_ERR_INVALID, "unknown dtype %d", dtype);
+    if (act != GATED_FF_SILU && act != GATED_FF_GELU_TANH)
+        return ff_fail(HESS_ERR_INVALID, "unknown activation %d", act);
+    if (hk::ff_injected("alloc")) return ff_fail(HESS_ERR_OOM, "injected allocation failure (HESS_FAULT=alloc)");
+    int dev = 0, pairs = 0;
+    FF_TRY(cudaGetDevice(&dev));
+    FF_TRY(hk::ensure_context());
+    FF_CHECK(hk::ff_prepare(dev, &pairs));
+    gated_ff_ctx* g = new (std::nothrow) gated_ff_ctx();
+    if (!g) return ff_fail(HESS_ERR_OOM, "host allocation failed");
+    g->device = dev;
+    g->pairs = pairs;
+    g->d = d;
+    g->f = f;
+    g->train_tokens = train_tokens;
+    g->dtype = dtype;
+    g->act = act;
+    const size_t bytes = static_cast<size_t>(train_tokens) * static_cast<size_t>(f) * 2;
+    cudaError_t e = cudaMalloc(&g->status, sizeof(uint32_t));
+    if (e == cudaSuccess) e = cudaMemset(g->status, 0, sizeof(uint32_t));
+    if (e == cudaSuccess && bytes) e = cudaMalloc(&g->dg, bytes);
+    if (e == cudaSuccess && bytes) e = cudaMalloc(&g->du, bytes);
+    if (e == cudaSuccess) e = cudaEventCreateWithFlags(&g->ev, cudaEventDisableTiming);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+    if (e != cudaSuccess) {
+        const hess_status s = e == cudaErrorMemoryAllocation ? HESS_ERR_OOM : HESS_ERR_CUDA;
+        if (s == HESS_ERR_OOM) cudaGetLastError();
+        hk::ff_free(g);
+        delete g;
+        return ff_fail(s, "gated_ff_create: %s", cudaGetErrorString(e));
+    }
+    *out = g;
+    return HESS_OK;
+}
+
+FF_EXPORT hess_status gated_ff_forward(gated_ff_t g, const void* X, int64_t n_tokens, const void* W_gate,
+                                       const void* W_up, void* H_out, hess_stream_t stream) {
+    if (!g) return ff_fail(HESS_ERR_INVALID, "handle is NULL");
+    FF_CHECK(hk::ff_tokens(n_tokens));
+    if (n_tokens == 0) return HESS_OK;
+    std::lock_guard<std::mutex> lk(g->mu);
+    FF_CHECK(hk::ff_check_device(g));
+    FF_CHECK(hk::ff_check(g, X, "X"));
+    FF_CHECK(hk::ff_check(g, W_gate, "W_gate"));
+    FF_CHECK(hk::ff_check(g, W_up, "W_up"));
+    FF_CHECK(hk::ff_check(g, H_out, "H_out"));
+    FF_TRY(hk::ensure_context());
+    hk::FfParams p{};
+    hk::ff_params(p, g, n_tokens);
+    FF_CHECK(hk::ff_encode(&p.maps[hk::kMapX], X, g->dtype, n_tokens, g->d));
+    FF_CHECK(hk::ff_encode(&p.maps[hk::kMapWg], W_gate, g->dtype, g->f, g->d));
+    FF_CHECK(hk::ff_encode(&p.maps[hk::kMapWu], W_up, g->dtype, g->f, g->d));
+    p.out0 = H_out;
+    p.n_units = static_cast<int32_t>(hk::ceil_div(n_tokens, 256) * hk::ceil_div(g->f, 128));
+    return hk::ff_launch<hk::kForward>(g, p, static_cast<cudaStream_t>(stream));
+}
+
+FF_EXPORT hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_tokens, const void* W_gate,
+                                        const void* W_up, const void* dH, void* dX_out, void* dW_gate_out,
+                                        void* dW_up_out, hess_stream_t stream) {
+    using hk::ceil_div;
+    if (!g) return ff_fail(HESS_ERR_INVALID, "handle is NULL");
+    FF_CHECK(hk::ff_tokens(n_tokens));
+    if ((dW_gate_out == nullptr) != (dW_up_out == nullptr))
+        return ff_fail(HESS_ERR_INVALID, "dW_gate_out and dW_up_out must both be given or both be NULL");
+    std::lock_guard<std::mutex> lk(g->mu);
+    if (n_tokens > g->train_tokens)
+        return ff_fail(HESS_ERR_INVALID, "n_tokens %lld exceeds the handle's train_tokens %lld",
+                           static_cast<long long>(n_tokens), static_cast<long long>(g->train_tokens));
+    FF_CHECK(hk::ff_check_device(g));
+    const bool want_x = dX_out != nullptr && n_tokens > 0, want_w = dW_gate_out != nullptr;
+    if (n_tokens > 0) {
+        FF_CHECK(hk::ff_check(g, X, "X"));
+        FF_CHECK(hk::ff_check(g, W_gate, "W_gate"));
+        FF_CHECK(hk::ff_check(g, W_up, "W_up"));
+        FF_CHECK(hk::ff_check(g, dH, "dH"));
+    }
+    if (want_x) FF_CHECK(hk::ff_check(g, dX_out, "dX_out"));
+    if (want_w) {
+        FF_CHECK(hk::ff_check(g, dW_gate_out, "dW_gate_out"));
+        FF_CHECK(hk::ff_check(g, dW_up_out, "dW_up_out"));
+    }
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (n_tokens == 0) {
+        if (want_w) {
+            const size_t bytes = static_cast<size_t>(g->f) * static_cast<size_t>(g->d) * 2;
+            FF_TRY(cudaMemsetAsync(dW_gate_out, 0, bytes, s));
+            FF_TRY(cudaMemsetAsync(dW_up_out, 0, bytes, s));
+        }
+        return HESS_OK;
+    }
+    if (!want_x && !want_w) return HESS_OK;
+    FF_TRY(hk::ensure_context());
+    hk::FfParams p{};
+    hk::ff_params(p, g, n_tokens);
+    FF_CHECK(hk::ff_encode(&p.maps[hk::kMapX], X, g->dtype, n_tokens, g->d));
+    FF_CHECK(hk::ff_encode(&p.maps[hk::kMapWg], W_gate, g->dtype, g->f, g->d));
+    FF_CHECK(hk::ff_encode(&p.maps[hk::kMapWu], W_up, g->dtype, g->f, g->d));
+    FF_CHECK(hk::ff_encode(&p.maps[hk::kMapDg], g->dg, g->dtype, n_tokens, g->f));
+    FF_CHECK(hk::ff_encode(&p.maps[hk::kMapDu], g->du, g->dtype, n_tokens, g->f));
+    if (g->used && g->last != s) FF_TRY(cudaStreamWaitEvent(s, g->ev, 0));
+    p.dh = dH;
+    p.out0 = g->dg;
+    p.out1 = g->du;
+    p.n_units = static_cast<int32_t>(ceil_div(n_tokens, 256) * ceil_div(g->f, 128));
+    FF_CHECK(hk::ff_launch<hk::kActGrad>(g, p, s));
+    p.out0 = dX_out;
+    p.out1 = dW_gate_out;
+    p.out2 = dW_up_out;
+    p.tiles_x = want_x ? static_cast<int32_t>(ceil_div(n_tokens, 256) * ceil_div(g->d, 256)) : 0;
+    p.tiles_w = want_w ? static_cast<int32_t>(ceil_div(g->f, 256) * ceil_div(g->d, 256)) : 0;
+    p.n_units = p.tiles_x + 2 * p.tiles_w;
+    const hess_status st = hk::ff_launch<hk::kGradients>(g, p, s);
+    FF_TRY(cudaEventRecord(g->ev, s));
+    g->last = s;
+    g->used = true;
+    return st;
+}
+
+FF_EXPORT hess_status gated_ff_sync(gated_ff_t g, hess_stream_t stream) {
+    if (!g) return ff_fail(HESS_ERR_INVALID, "handle is NULL");
+    std::lock_guard<std::mutex> lk(g->mu);
+    FF_CHECK(hk::ff_check_device(g));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint32_t word = 0;
+    FF_TRY(cudaMemcpyAsync(&word, g->status, sizeof(word), cudaMemcpyDeviceToHost, s));
+    FF_TRY(cudaStreamSynchronize(s));
+    if (word == 0) return HESS_OK;
+    FF_TRY(cudaMemsetAsync(g->status, 0, sizeof(word), s));
+    return ff_fail(HESS_ERR_TIMEOUT, "a device-side wait ran out (status 0x%x); results are invalid", word);
+}
+
+FF_EXPORT hess_status gated_ff_set_timeout(gated_ff_t g, int64_t ns) {
+    if (!g) return ff_fail(HESS_ERR_INVALID, "handle is NULL");
+    if (ns < 0) return ff_fail(HESS_ERR_INVALID, "the limit must not be negative");
+    std::lock_guard<std::mutex> lk(g->mu);
+    g->timeout_ns = static_cast<unsigned long long>(ns);
+    return HESS_OK;
+}
+
+FF_EXPORT hess_status gated_ff_destroy(gated_ff_t g) {
+    if (!g) return HESS_OK;
+    int cur = 0;
+    FF_TRY(cudaGetDevice(&cur));
+    FF_TRY(cudaSetDevice(g->device));
+    const cudaError_t e = cudaDeviceSynchronize();
+    hk::ff_free(g);
+    cudaSetDevice(cur);
+    delete g;
+    if (e != cudaSuccess) return ff_fail(HESS_ERR_CUDA, "gated_ff_destroy: %s", cudaGetErrorString(e));
+    return HESS_OK;
+}

@@ -27,6 +27,23 @@ def _stream(stream) -> int:
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Allocated on the stream that will write it, so that the caching
+    allocator orders the memory's former users before the kernel."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _used_on(stream, *tensors) -> None:
+    """Tensors of another stream stay allocated until `stream` is done with them."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _rows2d(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
     """(rows, vocab, row stride in elements) of a [..., vocab] tensor whose
     rows are evenly spaced and contiguous inside."""
@@ -69,9 +86,9 @@ def _common(logits, top_logits, top_index, temperature, teacher_lse, weights):
                   _vector(teacher_lse, rows, "teacher_lse"), _vector(weights, rows, "weights"), float(temperature))
 
 
-def _output(out: Optional[torch.Tensor], logits: torch.Tensor) -> Tuple[torch.Tensor, int]:
+def _output(out: Optional[torch.Tensor], logits: torch.Tensor, stream) -> Tuple[torch.Tensor, int]:
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out = _empty(logits.shape, logits.dtype, logits.device, stream)
     elif out.shape != logits.shape or out.dtype != logits.dtype:
         raise ValueError("the gradient must have the logits' shape and type")
     return out, _rows2d(out, "the gradient")[2]
@@ -82,9 +99,10 @@ def distill_forward(logits: torch.Tensor, top_logits: torch.Tensor, top_index: t
                     weights: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Loss of every row [rows] and the statistics ``distill_backward`` takes."""
     rows, args = _common(logits, top_logits, top_index, temperature, teacher_lse, weights)
-    loss = torch.empty(rows, dtype=torch.float32, device=logits.device)
-    stats = torch.empty((rows, _STATS), dtype=torch.float32, device=logits.device)
+    loss = _empty(rows, torch.float32, logits.device, stream)
+    stats = _empty((rows, _STATS), torch.float32, logits.device, stream)
     check(_lib.load().distill_forward(*args, loss.data_ptr(), stats.data_ptr(), _stream(stream)))
+    _used_on(stream, logits, top_logits, top_index, teacher_lse, weights)
     return loss, stats
 
 
@@ -98,9 +116,10 @@ def distill_backward(logits: torch.Tensor, stats: torch.Tensor, top_logits: torc
     if not stats.is_cuda or stats.dtype != torch.float32 or not stats.is_contiguous() or \
             stats.numel() != rows * _STATS:
         raise ValueError("stats must be the tensor distill_forward returned for these logits")
-    out, ldd = _output(out, logits)
+    out, ldd = _output(out, logits, stream)
     check(_lib.load().distill_backward(*args, stats.data_ptr(), _vector(grad, rows, "grad"), out.data_ptr(), ldd,
                                        _stream(stream)))
+    _used_on(stream, logits, stats, top_logits, top_index, teacher_lse, weights, grad, out)
     return out
 
 
@@ -110,9 +129,10 @@ def distill_step(logits: torch.Tensor, top_logits: torch.Tensor, top_index: torc
     """Loss of every row and the gradient of their sum, in one pass over the
     logits; ``out`` may be ``logits``."""
     rows, args = _common(logits, top_logits, top_index, temperature, teacher_lse, weights)
-    loss = torch.empty(rows, dtype=torch.float32, device=logits.device)
-    out, ldd = _output(out, logits)
+    loss = _empty(rows, torch.float32, logits.device, stream)
+    out, ldd = _output(out, logits, stream)
     check(_lib.load().distill_step(*args, loss.data_ptr(), out.data_ptr(), ldd, _stream(stream)))
+    _used_on(stream, logits, top_logits, top_index, teacher_lse, weights, out)
     return loss, out
 
 

@@ -1,0 +1,172 @@
+"""Python binding of the gated feed-forward projections in ``include/gated_ff.h``.
+
+Argument marshalling only: the projections, the activation and the gradients
+run in the library's CUDA kernels.  Functions carry the C names; ``GatedFF``
+wraps a handle and can be called as a node of an autograd graph.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+from . import _lib
+from ._lib import HESS_BF16, HESS_F16, HESS_F32, check
+
+__all__ = ["gated_ff_create", "gated_ff_forward", "gated_ff_backward", "gated_ff_sync", "gated_ff_set_timeout",
+           "gated_ff_destroy", "GatedFF"]
+
+_DTYPES = {torch.bfloat16: HESS_BF16, torch.float16: HESS_F16, torch.float32: HESS_F32}
+ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
+
+
+def _stream(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+def _empty(shape, like: torch.Tensor, stream) -> torch.Tensor:
+    """Allocated on the stream that will write it, so that the caching
+    allocator orders the memory's former users before the kernel."""
+    if stream is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+
+
+def _used_on(stream, *tensors) -> None:
+    """Tensors of another stream stay allocated until `stream` is done with them."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def gated_ff_create(d: int, f: int, train_tokens: int, dtype: int, act: int) -> int:
+    g = ctypes.c_void_p()
+    check(_lib.load().gated_ff_create(int(d), int(f), int(train_tokens), int(dtype), int(act), ctypes.byref(g)))
+    return g.value
+
+
+def gated_ff_forward(g: int, X, n_tokens: int, W_gate, W_up, H_out, stream=None) -> None:
+    check(_lib.load().gated_ff_forward(g, X.data_ptr(), int(n_tokens), W_gate.data_ptr(), W_up.data_ptr(),
+                                       H_out.data_ptr(), _stream(stream)))
+
+
+def gated_ff_backward(g: int, X, n_tokens: int, W_gate, W_up, dH, dX_out, dW_gate_out, dW_up_out,
+                      stream=None) -> None:
+    check(_lib.load().gated_ff_backward(
+        g, X.data_ptr(), int(n_tokens), W_gate.data_ptr(), W_up.data_ptr(), dH.data_ptr(),
+        *(t.data_ptr() if t is not None else None for t in (dX_out, dW_gate_out, dW_up_out)), _stream(stream)))
+
+
+def gated_ff_sync(g: int, stream=None) -> None:
+    check(_lib.load().gated_ff_sync(g, _stream(stream)))
+
+
+def gated_ff_set_timeout(g: int, ns: int) -> None:
+    check(_lib.load().gated_ff_set_timeout(g, int(ns)))
+
+
+def gated_ff_destroy(g: int) -> None:
+    check(_lib.load().gated_ff_destroy(g))
+
+
+class GatedFF:
+    """``h = act(x W_gate^T) * (x W_up^T)`` for one pair of widths (d, f).
+
+    ``forward`` and ``backward`` take [..., d] and [..., f] tensors of the
+    object's type; weights are [f, d] and belong to the caller, so one object
+    serves every layer of these widths.  ``train_tokens`` is the most tokens a
+    backward call will have (its workspace is 4 f bytes a token).  Called as a
+    function, the object is a node of an autograd graph.
+    """
+
+    def __init__(self, d: int, f: int, train_tokens: int = 0, dtype: torch.dtype = torch.bfloat16,
+                 activation: str = "silu"):
+        self.handle = None
+        if dtype not in _DTYPES:
+            raise ValueError(f"dtype must be bfloat16 or float16, got {dtype}")
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+        self.d, self.f, self.dtype = int(d), int(f), dtype
+        self.handle = gated_ff_create(d, f, train_tokens, _DTYPES[dtype], ACTIVATIONS[activation])
+
+    def _check(self, t: torch.Tensor, name: str, width: int, rows: Optional[int] = None) -> int:
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor")
+        if t.dtype != self.dtype:
+            raise ValueError(f"{name} must be {self.dtype}, got {t.dtype}")
+        if t.dim() == 0 or t.shape[-1] != width:
+            raise ValueError(f"{name} must have a last dimension of {width}")
+        n = t.numel() // width
+        if rows is not None and n != rows:
+            raise ValueError(f"{name} must have {rows} rows, got {n}")
+        return n
+
+    def _inputs(self, X, W_gate, W_up) -> int:
+        n = self._check(X, "X", self.d)
+        self._check(W_gate, "W_gate", self.d, self.f)
+        self._check(W_up, "W_up", self.d, self.f)
+        return n
+
+    def forward(self, X: torch.Tensor, W_gate: torch.Tensor, W_up: torch.Tensor,
+                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        n = self._inputs(X, W_gate, W_up)
+        if out is None:
+            out = _empty((*X.shape[:-1], self.f), X, stream)
+        else:
+            self._check(out, "out", self.f, n)
+        gated_ff_forward(self.handle, X, n, W_gate, W_up, out, stream)
+        _used_on(stream, X, W_gate, W_up, out)
+        return out
+
+    def backward(self, X: torch.Tensor, W_gate: torch.Tensor, W_up: torch.Tensor, dH: torch.Tensor,
+                 want_dx: bool = True, want_dw: bool = True, stream=None
+                 ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], Optional[torch.Tensor]]:
+        """(dX, dW_gate, dW_up); None for what is not wanted."""
+        n = self._inputs(X, W_gate, W_up)
+        self._check(dH, "dH", self.f, n)
+        dx = _empty(X.shape, X, stream) if want_dx else None
+        dwg = _empty(W_gate.shape, X, stream) if want_dw else None
+        dwu = _empty(W_up.shape, X, stream) if want_dw else None
+        gated_ff_backward(self.handle, X, n, W_gate, W_up, dH, dx, dwg, dwu, stream)
+        _used_on(stream, X, W_gate, W_up, dH)
+        return dx, dwg, dwu
+
+    def __call__(self, X: torch.Tensor, W_gate: torch.Tensor, W_up: torch.Tensor) -> torch.Tensor:
+        return _GatedFF.apply(self, X, W_gate, W_up)
+
+    def sync(self, stream=None) -> None:
+        gated_ff_sync(self.handle, stream)
+
+    def close(self) -> None:
+        if self.handle:
+            gated_ff_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class _GatedFF(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, op, X, W_gate, W_up):
+        ctx.op = op
+        ctx.save_for_backward(X, W_gate, W_up)
+        return op.forward(X, W_gate, W_up)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dH):
+        X, W_gate, W_up = ctx.saved_tensors
+        want = ctx.needs_input_grad
+        dx, dwg, dwu = ctx.op.backward(X, W_gate, W_up, dH.contiguous(), want_dx=want[1],
+                                       want_dw=want[2] or want[3])
+        return None, dx, dwg if want[2] else None, dwu if want[3] else None

@@ -60,7 +60,7 @@ typedef void* hess_stream_t;                 /* a cudaStream_t */
 typedef enum {
     HESS_BF16 = 0, /* bfloat16: tensor-core products, exact in fp32 */
     HESS_F32 = 1,  /* float32: its own kernel, fp32-accurate products */
-    HESS_F16 = 2   /* float16: taken by distill.h only; the calls of this header
+    HESS_F16 = 2   /* float16: taken by gated_ff.h and distill.h; the calls of this header
                       and of gptq.h refuse it with HESS_ERR_INVALID */
 } hess_dtype;
 
