@@ -54,7 +54,9 @@ struct DistillArgs {
     const float* grad;  // backward only
     double inv_tau;
     float tau;
-    float k2;
+    float inv_hi, inv_lo;  // 1 / tau as the sum of two floats
+    float k2;              // log2(e) / tau, rounded
+    float k2_slip;         // 1 / tau - k2 ln 2: what that rounding leaves out
     float* loss;
     float* stats;
     void* dlogits;
@@ -165,13 +167,26 @@ __device__ __forceinline__ int64_t load_index(const DistillArgs& a, int64_t i) {
                               : static_cast<int64_t>(static_cast<const int32_t*>(a.top_index)[i]);
 }
 
-// exp of an fp64 argument to fp32 accuracy: the part of the argument that its
-// rounding to fp32 drops comes back as a factor 1 + lo.
-__device__ __forceinline__ float exp_wide(double x) {
-    const float hi = static_cast<float>(x);
-    if (!(hi > -1e30f)) return hi == hi ? 0.0f : hi;
-    const float lo = static_cast<float>(x - static_cast<double>(hi));
-    return expf(hi) * (1.0f + lo);
+// exp(t / tau - base) for a teacher logit; base is the teacher's log-sum
+// (`full`) or, times 1 / tau, the largest listed logit.  The argument is
+// rounded relative to itself, not to t / tau.
+__device__ __forceinline__ float teacher_exp(const DistillArgs& a, float t, float base, bool full) {
+    const float d = full ? t : t - base;
+    const float x = fmaf(d, a.inv_hi, full ? -base : 0.0f);
+    return expf(fmaf(d, a.inv_lo, x));
+}
+
+// Natural logarithm to about 2^-25 of the mantissa's own: the exponent's part
+// is added in fp64, so a large result carries no larger error.
+__device__ __forceinline__ double log_wide(float x) {
+    if (!(x > 0.0f) || x == INFINITY) return static_cast<double>(logf(x));
+    int e;
+    float m = frexpf(x, &e);
+    if (m < 0.70710678f) {
+        m *= 2.0f;
+        e -= 1;
+    }
+    return static_cast<double>(logf(m)) + static_cast<double>(e) * kLn2;
 }
 
 // 2^(a - b) with b >= a; 0 when a is -inf (whatever b is).
@@ -249,38 +264,165 @@ __device__ __forceinline__ V warp_reduce(V x, Op op) {
     return x;
 }
 
-// Every thread gets the result; `red` holds kWarps values and is free to be
-// reused after the next barrier.
-template <class V, class Op>
-__device__ __forceinline__ V block_reduce(V x, V* red, Op op) {
-    x = warp_reduce(x, op);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-    __syncthreads();
-    V r = red[0];
-#pragma unroll
-    for (int i = 1; i < kWarps; ++i) r = op(r, red[i]);
-    return r;
-}
-
 struct MaxOp {
     __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
-template <class V>
 struct AddOp {
-    __device__ V operator()(V a, V b) const { return a + b; }
+    __device__ float operator()(float a, float b) const { return a + b; }
 };
 
+// Sum of float pairs (hi, lo) over a warp: every addition keeps its error.
+__device__ __forceinline__ void warp_sum_pairs(float& hi, float& lo) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float h = __shfl_xor_sync(0xffffffffu, hi, o), l = __shfl_xor_sync(0xffffffffu, lo, o);
+        float e;
+        hi = two_sum_f32(hi, h, e);
+        lo += l + e;
+    }
+}
+
+// What the warp that reads the teacher's list leaves for the others.
 struct Shared {
-    float red_max[kWarps], red_max2[kWarps];
-    float red_sum[kWarps], red_top[kWarps];
-    float red_cmax[kWarps];
-    double red_d[2][kWarps];
-    float4 part[kMaxCluster];  // each CTA's (M2o, S_o, S_top, listed columns)
+    int live, bad;
+    float tm, m_top;     // largest listed logit, teacher's and student's
+    float p_hi, p_lo;    // sum of the list's exponentials
+    float p_inv;
+    float a;             // sum of p (t - s) / tau
+    float2 part[kMaxCluster * kWarps];  // (maximum, sum) of every warp of the cluster's slices
+    float2 top[kMaxCluster];            // (sum over the listed columns, their number) of every slice
 };
 
 __host__ __device__ constexpr size_t align16(size_t n) { return (n + 15) & ~size_t(15); }
 // Dynamic shared memory: the chunk, then four arrays of `top` words.
 size_t row_smem(int chunk, int top) { return size_t(chunk) * 16 + align16(size_t(top) * 4) * 4; }
+
+// The teacher's list of a row, by one warp: columns, exponentials and the
+// student's logits there (they are read here, before any gradient is stored).
+template <class T>
+__device__ __forceinline__ void read_list(const DistillArgs& a, int64_t row, const T* logits, int* s_idx,
+                                          float* s_p, float* s_s, Shared& sh) {
+    constexpr int kBatch = 4;  // loads in flight per lane
+    const int K = a.top, lane = threadIdx.x & 31;
+    bool any = false, bad = false;
+    float tm = kNegInf, mt = kNegInf;
+    for (int k0 = lane; k0 < K; k0 += 32 * kBatch) {
+        int64_t j[kBatch];
+        float t[kBatch], s[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int k = k0 + 32 * i;
+            j[i] = k < K ? load_index(a, row * K + k) : -1;
+            t[i] = k < K ? load_top(a, row * K + k) : kNegInf;
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (t[i] == kNegInf) j[i] = -1;
+            if (j[i] >= a.vocab) {
+                bad = true;
+                j[i] = -1;
+            }
+            s[i] = j[i] >= 0 ? Elem<T>::to_f(logits[j[i]]) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int k = k0 + 32 * i;
+            if (k >= K) break;
+            s_idx[k] = j[i] >= 0 ? static_cast<int>(j[i]) : -1;
+            s_p[k] = t[i];
+            s_s[k] = s[i];
+            if (j[i] >= 0) {
+                any = true;
+                tm = fmaxf(tm, t[i]);
+                mt = fmaxf(mt, s[i]);
+            }
+        }
+    }
+    tm = warp_reduce(tm, MaxOp());
+    mt = warp_reduce(mt, MaxOp());
+    const bool full = a.lse != nullptr;
+    const float base = full ? a.lse[row] : tm;
+    float hi = 0.0f, lo = 0.0f, sum = 0.0f;
+    for (int k = lane; k < K; k += 32) {
+        float e = 0.0f;
+        if (s_idx[k] >= 0) {
+            const float t = s_p[k], s = s_s[k];
+            e = teacher_exp(a, t, base, full);
+            if (e != 0.0f)
+                sum += s == kNegInf ? INFINITY : e * fmaf(s, a.k2_slip, fmaf(t - s, a.inv_hi, (t - s) * a.inv_lo));
+            float err;
+            hi = two_sum_f32(hi, e, err);
+            lo += err;
+        }
+        s_p[k] = e;
+    }
+    warp_sum_pairs(hi, lo);
+    sum = warp_reduce(sum, AddOp());
+    const float p_inv = full ? 1.0f : 1.0f / (hi + lo);
+    __syncwarp();
+    if (!full)
+        for (int k = lane; k < K; k += 32) s_p[k] *= p_inv;
+    any = __any_sync(0xffffffffu, any);
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) {
+        sh.live = any || bad;
+        sh.bad = bad;
+        sh.tm = tm;
+        sh.m_top = mt;
+        sh.p_hi = hi;
+        sh.p_lo = lo;
+        sh.p_inv = p_inv;
+        sh.a = sum;
+    }
+    __syncwarp();
+}
+
+// Takes the listed columns out of a chunk, by one warp: s_lead gets the mass
+// of a column at its first slot and -1 at others, and the student's
+// exponentials there are summed.  Each slot first writes its number into the
+// chunk: one that reads another's back shares its column.
+template <class T>
+__device__ __forceinline__ void take_out(const DistillArgs& a, T* e, int j0, int j1, int j_base, const int* s_idx,
+                                         const float* s_p, const float* s_s, float* s_lead, float m2_top,
+                                         float& sum_top, float& listed) {
+    const int K = a.top, lane = threadIdx.x & 31;
+    for (int k = lane; k < K; k += 32) {
+        const int j = s_idx[k];
+        if (j < j0 || j >= j1) continue;
+        const uint16_t tag = static_cast<uint16_t>(k);
+        memcpy(&e[j - j_base], &tag, 2);
+    }
+    __syncwarp();
+    bool twice = false;
+    for (int k = lane; k < K; k += 32) {
+        const int j = s_idx[k];
+        if (j < j0 || j >= j1) continue;
+        uint16_t tag;
+        memcpy(&tag, &e[j - j_base], 2);
+        twice |= tag != k;
+    }
+    twice = __any_sync(0xffffffffu, twice);
+    for (int k = lane; k < K; k += 32) {
+        const int j = s_idx[k];
+        if (j < j0 || j >= j1) continue;
+        e[j - j_base] = Elem<T>::from_f(kNegInf);
+        float p = s_p[k];
+        bool first = true;
+        if (twice) {  // rare: a column's first slot takes the sum over its slots
+            p = 0.0f;
+            for (int l = 0; l < K; ++l) {
+                if (s_idx[l] != j) continue;
+                first = first && l >= k;
+                p += s_p[l];
+            }
+        }
+        s_lead[k] = first ? p : -1.0f;
+        if (first) {
+            sum_top += m2_top == kNegInf ? 0.0f : ex2(fmaf(s_s[k], a.k2, -m2_top));
+            listed += 1.0f;
+        }
+    }
+}
 
 // One row per cluster.
 template <class T, bool kGrad>
@@ -291,7 +433,7 @@ __global__ void __launch_bounds__(kThreads) distill_row_kernel(const DistillArgs
     const int K = a.top;
     const size_t kstep = align16(size_t(K) * 4) / 4;
     int* const s_idx = reinterpret_cast<int*>(buf + a.chunk);   // column, -1 for an empty slot
-    float* const s_p = reinterpret_cast<float*>(s_idx) + kstep;  // teacher logit, then p
+    float* const s_p = reinterpret_cast<float*>(s_idx) + kstep;  // p
     float* const s_s = s_p + kstep;                              // student logit
     float* const s_lead = s_s + kstep;                           // p of the column at its first slot, else -1
 
@@ -304,40 +446,18 @@ __global__ void __launch_bounds__(kThreads) distill_row_kernel(const DistillArgs
     T* const out = kGrad ? static_cast<T*>(a.dlogits) + row * a.ldd : nullptr;
     const bool same = kGrad && ((reinterpret_cast<uintptr_t>(out) & 15u) / sizeof(T)) == static_cast<unsigned>(v.off);
     const float w = a.weights ? a.weights[row] : 1.0f;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n_chunks = max(1, (g_hi - g_lo + a.chunk - 1) / a.chunk);
 
     bool live = w != 0.0f;
-    const int n_chunks = max(1, (g_hi - g_lo + a.chunk - 1) / a.chunk);
-    if (live) load_chunk<T>(v, a.vocab, g_lo, min(g_hi, g_lo + a.chunk), buf);
-
-    // ---- the teacher's list, and the student's logits at its columns
-    bool bad = false;
-    float tm = kNegInf, m_top = kNegInf;
     if (live) {
-        bool any = false;
-        for (int k = tid; k < K; k += kThreads) {
-            int64_t j = load_index(a, row * K + k);
-            const float t = load_top(a, row * K + k);
-            if (t == kNegInf) j = -1;
-            if (j >= a.vocab) {
-                bad = true;
-                j = -1;
-            }
-            const float s = j >= 0 ? Elem<T>::to_f(v.row[j]) : 0.0f;
-            s_idx[k] = j >= 0 ? static_cast<int>(j) : -1;
-            s_p[k] = t;
-            s_s[k] = s;
-            if (j >= 0) {
-                any = true;
-                tm = fmaxf(tm, t);
-                m_top = fmaxf(m_top, s);
-            }
-        }
-        bad = __syncthreads_or(bad);
-        live = __syncthreads_or(any) || bad;
+        load_chunk<T>(v, a.vocab, g_lo, min(g_hi, g_lo + a.chunk), buf);
+        if (warp == 0) read_list<T>(a, row, v.row, s_idx, s_p, s_s, sh);
+        cp_async_wait();
+        __syncthreads();
+        live = sh.live != 0;
     }
     if (!live) {
-        cp_async_wait();
         if (kGrad) zero_slice<T>(v, out, a.vocab, same, g_lo, g_hi);
         if (rank == 0 && tid < DISTILL_STATS) {
             if (tid == 0) a.loss[row] = 0.0f;
@@ -345,87 +465,31 @@ __global__ void __launch_bounds__(kThreads) distill_row_kernel(const DistillArgs
         }
         return;  // the whole cluster leaves here, as all of it read the same row
     }
-    tm = block_reduce(tm, sh.red_max, MaxOp());
-    m_top = block_reduce(m_top, sh.red_max2, MaxOp());
-    const double z = a.lse ? static_cast<double>(a.lse[row]) : static_cast<double>(tm) * a.inv_tau;
-    // P = sum e_k; A = sum e_k (t_k / tau - ln of the student's numerator)
-    double P = 0.0, A = 0.0;
-    const double s_scale = static_cast<double>(a.k2) * kLn2;
-    for (int k = tid; k < K; k += kThreads) {
-        float e = 0.0f;
-        if (s_idx[k] >= 0) {
-            const double t = static_cast<double>(s_p[k]) * a.inv_tau;
-            e = exp_wide(t - z);
-            if (e != 0.0f) A += static_cast<double>(e) * (t - static_cast<double>(s_s[k]) * s_scale);
-            P += static_cast<double>(e);
-        }
-        s_p[k] = e;
-    }
-    P = block_reduce(P, sh.red_d[0], AddOp<double>());
-    A = block_reduce(A, sh.red_d[1], AddOp<double>());
-    const float p_inv = a.lse ? 1.0f : static_cast<float>(1.0 / P);
-    for (int k = tid; k < K; k += kThreads) s_p[k] *= p_inv;
+    const float m2_top = sh.m_top * a.k2;  // reference of the listed columns (all slices use this one)
 
-    // ---- maxima and sums of this CTA's slice
-    const float m2_top = m_top * a.k2;  // reference of the listed columns (all slices use this one)
-    float m2 = kNegInf, sum = 0.0f, sum_top = 0.0f, n_listed = 0.0f;
+    // ---- maximum and sum of this thread's part of the slice
+    float m2 = kNegInf, sum = 0.0f, sum_top = 0.0f, listed = 0.0f;
     for (int c = 0; c < n_chunks; ++c) {
-        const int g0 = g_lo + c * a.chunk, g1 = min(g_hi, g0 + a.chunk), n = max(0, g1 - g0);
+        const int g0 = g_lo + c * a.chunk, n = max(0, min(g_hi, g0 + a.chunk) - g0);
         if (c > 0) {
             __syncthreads();  // the chunk before is no longer read
-            load_chunk<T>(v, a.vocab, g0, g1, buf);
+            load_chunk<T>(v, a.vocab, g0, g0 + n, buf);
+            cp_async_wait();
+            __syncthreads();
         }
-        cp_async_wait();
-        __syncthreads();
-        // Listed columns leave the chunk.  Each slot first writes its number
-        // there: a slot that reads another's back shares its column.
-        T* const e = reinterpret_cast<T*>(buf);
-        const int j_base = g0 * kPer - v.off;
-        bool twice = false;
-        for (int k = tid; k < K; k += kThreads) {
-            const int j = s_idx[k];
-            if (j >= max(j_base, 0) && j < j_base + n * kPer) {
-                const uint16_t tag = static_cast<uint16_t>(k);
-                memcpy(&e[j - j_base], &tag, 2);
-            }
-        }
-        __syncthreads();
-        for (int k = tid; k < K; k += kThreads) {
-            const int j = s_idx[k];
-            if (j >= max(j_base, 0) && j < j_base + n * kPer) {
-                uint16_t tag;
-                memcpy(&tag, &e[j - j_base], 2);
-                twice |= tag != k;
-                s_lead[k] = s_p[k];
-            }
-        }
-        twice = __syncthreads_or(twice);
-        for (int k = tid; k < K; k += kThreads) {
-            const int j = s_idx[k];
-            if (j < max(j_base, 0) || j >= j_base + n * kPer) continue;
-            e[j - j_base] = Elem<T>::from_f(kNegInf);
-            bool first = true;
-            if (twice) {  // rare: the first slot of a column takes the sum of its slots
-                float p = 0.0f;
-                for (int l = 0; l < K; ++l) {
-                    if (s_idx[l] != j) continue;
-                    first = first && l >= k;
-                    p += s_p[l];
-                }
-                s_lead[k] = first ? p : -1.0f;
-            }
-            if (first) {
-                sum_top += ex2(fmaf(s_s[k], a.k2, -m2_top));
-                n_listed += 1.0f;
-            }
+        if (warp == 0) {
+            const int j_base = g0 * kPer - v.off;
+            take_out<T>(a, reinterpret_cast<T*>(buf), max(j_base, 0), j_base + n * kPer, j_base, s_idx, s_p, s_s,
+                        s_lead, m2_top, sum_top, listed);
         }
         __syncthreads();
         float m = kNegInf;
         for (int g = tid; g < n; g += kThreads) m = fmaxf(m, Elem<T>::max_of(buf[g]));
-        m = block_reduce(m, sh.red_cmax, MaxOp());
-        const float m2c = fmaxf(m2, m * a.k2);
-        sum *= rescale(m2, m2c);
-        m2 = m2c;
+        m *= a.k2;
+        if (m > m2) {
+            sum *= rescale(m2, m);
+            m2 = m;
+        }
         const float ref = m2 == kNegInf ? 0.0f : m2;
         for (int g = tid; g < n; g += kThreads) {
             float x[kPer];
@@ -434,56 +498,69 @@ __global__ void __launch_bounds__(kThreads) distill_row_kernel(const DistillArgs
             for (int i = 0; i < kPer; ++i) sum += ex2(fmaf(x[i], a.k2, -ref));
         }
     }
-    // m_top is +inf or NaN-free here unless a logit was; -inf when every listed logit is -inf
-    if (m2_top == kNegInf) sum_top = 0.0f;
-    sum = block_reduce(sum, sh.red_sum, AddOp<float>());
-    sum_top = block_reduce(sum_top, sh.red_top, AddOp<float>());
-    n_listed = static_cast<float>(block_reduce(static_cast<double>(n_listed), sh.red_d[0], AddOp<double>()));
 
-    // ---- the row's sums
-    if (tid < static_cast<int>(C)) {
-        const uint32_t dst = mapa_shared(smem_u32(&sh.part[rank]), tid);
-        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "f"(m2), "f"(sum),
-                     "f"(sum_top), "f"(n_listed)
-                     : "memory");
+    // ---- the row's sums: every warp's pair goes to every CTA of the cluster
+    {
+        const float mw = warp_reduce(m2, MaxOp());
+        sum = warp_reduce(sum * rescale(m2, mw), AddOp());
+        if (warp == 0) {
+            sum_top = warp_reduce(sum_top, AddOp());
+            listed = warp_reduce(listed, AddOp());
+        }
+        if (lane < static_cast<int>(C)) {
+            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(
+                             mapa_shared(smem_u32(&sh.part[rank * kWarps + warp]), lane)),
+                         "f"(mw), "f"(sum)
+                         : "memory");
+            if (warp == 0)
+                asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(
+                                 mapa_shared(smem_u32(&sh.top[rank]), lane)),
+                             "f"(sum_top), "f"(listed)
+                             : "memory");
+        }
     }
     cluster_sync_all();
-    float m2o = kNegInf, s_o = 0.0f, s_t = 0.0f, listed = 0.0f;
-    for (uint32_t r = 0; r < C; ++r) m2o = fmaxf(m2o, sh.part[r].x);
+    float m2o = kNegInf, s_o = 0.0f, s_t = 0.0f;
+    listed = 0.0f;
+    for (uint32_t i = lane; i < C * kWarps; i += 32) m2o = fmaxf(m2o, sh.part[i].x);
+    m2o = warp_reduce(m2o, MaxOp());
+    for (uint32_t i = lane; i < C * kWarps; i += 32) s_o += sh.part[i].y * rescale(sh.part[i].x, m2o);
+    s_o = warp_reduce(s_o, AddOp());
     for (uint32_t r = 0; r < C; ++r) {
-        const float4 q = sh.part[r];
-        s_o += q.y * rescale(q.x, m2o);
-        s_t += q.z;
-        listed += q.w;
+        s_t += sh.top[r].x;
+        listed += sh.top[r].y;
     }
     const float M2 = fmaxf(m2o, m2_top);
     const float f_o = rescale(m2o, M2);
     const float S = s_o * f_o + s_t * rescale(m2_top, M2);
-    const float inv_S = bad ? NAN : 1.0f / S;
-    double p_r = a.lse ? 1.0 - P : 0.0;
-    if (!(p_r > 0.0) || listed >= static_cast<float>(a.vocab)) p_r = p_r == p_r ? 0.0 : p_r;
+    const float inv_S = sh.bad ? NAN : 1.0f / S;
+    // the teacher's mass outside its list; none where the list names every column
+    float p_r = a.lse ? (1.0f - sh.p_hi) - sh.p_lo : 0.0f;
+    if (p_r < 0.0f || listed >= static_cast<float>(a.vocab)) p_r = 0.0f;
     float B = f_o * inv_S;
-    if (p_r > 0.0 && s_o > 0.0f) B -= static_cast<float>(p_r) / s_o;
+    if (p_r > 0.0f && s_o > 0.0f) B -= p_r / s_o;
     const float ref_o = m2o == kNegInf ? 0.0f : m2o;
 
-    // ---- the loss, by one thread of the last warp of CTA 0
+    // ---- the loss, by one thread (a few fp64 operations a row: that pipe is slow)
     if (rank == 0 && tid == kThreads - 32) {
-        const double l2s = log2(static_cast<double>(S)) + static_cast<double>(M2);
-        double L = A;
-        double mass = P;
-        if (!a.lse) {
-            L = A / P - log(P);
-            mass = 1.0;
+        const double ln_sum = static_cast<double>(M2) * kLn2 + log_wide(S);  // of the student
+        double L;
+        if (a.lse) {
+            const double P = static_cast<double>(sh.p_hi) + static_cast<double>(sh.p_lo);
+            L = static_cast<double>(sh.a) + P * (ln_sum - static_cast<double>(a.lse[row]));
+        } else {
+            L = static_cast<double>(sh.a * sh.p_inv) + ln_sum - static_cast<double>(sh.tm) * a.inv_tau -
+                log_wide(sh.p_hi + sh.p_lo);
         }
-        L += mass * (l2s * kLn2 - z);
-        if (p_r > 0.0)
-            L += p_r * (log(p_r) - kLn2 * (log2(static_cast<double>(s_o)) + static_cast<double>(m2o) - l2s));
-        if (p_r != p_r || bad) L = NAN;
-        a.loss[row] = static_cast<float>(static_cast<double>(w) * a.tau * a.tau * L);
+        if (p_r != 0.0f)
+            L += static_cast<double>(p_r) *
+                 (log_wide(p_r) - (static_cast<double>(m2o) * kLn2 + log_wide(s_o) - ln_sum));
+        if (sh.bad) L = NAN;
+        a.loss[row] = static_cast<float>(static_cast<double>(w * a.tau * a.tau) * L);
         if (!kGrad) {
             float4* const st = reinterpret_cast<float4*>(a.stats + row * DISTILL_STATS);
             st[0] = make_float4(M2, inv_S, ref_o, B);
-            st[1] = make_float4(tm, p_inv, 1.0f, 0.0f);
+            st[1] = make_float4(sh.tm, sh.p_inv, 1.0f, 0.0f);
         }
     }
     if constexpr (kGrad) {
@@ -547,7 +624,8 @@ __global__ void __launch_bounds__(kThreads) distill_backward_kernel(const Distil
     if (tid == 0) s_n = 0;
     __syncthreads();
     const int j0 = max(0, g_lo * kPer - v.off), j1 = min(a.vocab, g_hi * kPer - v.off);
-    const double z = a.lse ? static_cast<double>(a.lse[row]) : static_cast<double>(st1.x) * a.inv_tau;
+    const bool full = a.lse != nullptr;
+    const float base = full ? a.lse[row] : st1.x;
     for (int k = tid; k < a.top; k += kThreads) {
         const int64_t j = load_index(a, row * a.top + k);
         if (j < j0 || j >= j1) continue;
@@ -557,7 +635,7 @@ __global__ void __launch_bounds__(kThreads) distill_backward_kernel(const Distil
         s_j[n] = static_cast<int>(j);
         s_slot[n] = k;
         s_s[n] = Elem<T>::to_f(v.row[j]);
-        s_p[n] = exp_wide(static_cast<double>(t) * a.inv_tau - z) * st1.y;
+        s_p[n] = teacher_exp(a, t, base, full) * st1.y;
     }
     __syncthreads();
     for (int g = g_lo + tid; g < g_hi; g += kThreads * kInFlight) {
@@ -677,7 +755,10 @@ hess_status ds_args(DistillArgs& a, const void* logits, int64_t ld, int64_t rows
     a.weights = weights;
     a.inv_tau = 1.0 / temperature;
     a.tau = static_cast<float>(temperature);
+    a.inv_hi = static_cast<float>(a.inv_tau);
+    a.inv_lo = static_cast<float>(a.inv_tau - static_cast<double>(a.inv_hi));
     a.k2 = static_cast<float>(1.0 / (temperature * kLn2));
+    a.k2_slip = static_cast<float>(a.inv_tau - static_cast<double>(a.k2) * kLn2);
     return HESS_OK;
 }
 
