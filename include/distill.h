@@ -61,7 +61,7 @@ extern "C" {
  *   logits      : [rows, vocab], element type `dtype` (HESS_BF16, HESS_F16,
  *                 HESS_F32), aligned to its element; row r starts at element
  *                 r * ld (ld >= vocab).  Read only.
- *   rows        : >= 0 (0 is a no-op);  vocab : 1 .. 2^30.
+ *   rows        : >= 0 (0 is a no-op);  vocab : 1 .. 2^22, else UNSUPPORTED.
  *   top_logits  : [rows, top] contiguous, element type `top_dtype`.
  *   top_index   : [rows, top] contiguous, signed integers of index_bytes bytes
  *                 (4 or 8).
