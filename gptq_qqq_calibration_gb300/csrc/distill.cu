@@ -6,12 +6,15 @@
 // exponentials before the first gradient can be written, so the logits are
 // needed twice: a CTA (a cluster of CTAs, when there are few rows) takes one
 // row, sums it straight from memory, and reads it again, from L2, for the
-// gradient.  With two CTAs of 512 threads an SM the rows in flight are 304,
-// 78 MB at 128,000 bf16 columns, which the 129 MB L2 holds as long as the
-// gradient's stores leave it first (they are marked to).
+// gradient.  The L2 holds what is in flight (58 MB: launch_typed) as long as
+// the gradient's stores leave it first, which they are marked to do.  What bounds
+// it is memory: 8,192 rows of 128,000 bf16 logits (an eighth without weight) take
+// 689 us for the loss and the gradient, 84 % of the rate of a copy of the bytes
+// it cannot do without, and 300 us for the loss alone, 90 %.  What is left are
+// the dependent loads at a row's start, 4 to 5 us that only other CTAs hide.
 // Keeping the rows in shared memory instead (a cluster per row, bulk copies, a
-// warp for each list) was built too: its phases wait for one another in each
-// SM, and it took 821 us where this takes <<step>> (8,192 x 128,000 bf16).
+// warp for each list) was built too: its phases wait for one another inside
+// each SM, and the same step took it 821 us.
 //
 // Exponentials are 2^(s k2 - M2) with k2 = log2(e) / tau and M2 = max(s) k2,
 // one FMA and one ex2 per element.  The listed columns are left out of the
@@ -66,7 +69,8 @@ struct DistillArgs {
     float* stats;
     void* dlogits;
     int64_t ldd;
-    int32_t slice;  // 16-byte granules of a row per CTA
+    int32_t slice;     // 16-byte granules of a row per CTA, a multiple of kSegment
+    int32_t segments;  // of a row, at most
 };
 
 // ---------------------------------------------------------------- elements
@@ -230,6 +234,13 @@ struct Pair {
 // 2^(a - b) with b >= a; 0 when a is -inf (whatever b is).
 __device__ __forceinline__ float rescale(float a, float b) { return a == kNegInf ? 0.0f : ex2(a - b); }
 
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float x) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
 __device__ __forceinline__ void st_cluster_f32x2(uint32_t addr, float x, float y) {
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
@@ -358,83 +369,98 @@ __device__ __forceinline__ int edge_column(const RowView<T>& v, const Slice<T>& 
     return j >= 0 && j < vocab ? j : -1;
 }
 
-// Sum of 2^(x k2 - m2) over this thread's part of a slice; with kFull without
-// the listed columns.
-template <class T, bool kFull, bool kKeep>
-__device__ __forceinline__ float exp_sum(const RowView<T>& v, const Slice<T>& sl, int vocab, float k2, float m2) {
-    const uint64_t kk = both(k2), ref = both(-m2);
-    const int nt = blockDim.x;
-    uint64_t s0 = 0, s1 = 0;
-    int g = sl.a + threadIdx.x;
-    for (; g + 3 * nt < sl.b; g += 4 * nt) {
-        uint4 b[4];
+// A row is summed in segments of 256 granules, eight a lane, one warp each; the
+// segments' sums are added in a fixed order.  So a row's bits do not depend on
+// how many CTAs and threads it is given, and not on the rows beside it.
+constexpr int kSegment = 256;
+
+// Granule g for the sums: whole, or with -inf in the place of other rows' elements.
+template <class T, bool kKeep>
+__device__ __forceinline__ uint4 any_granule(const RowView<T>& v, const Slice<T>& sl, int vocab, int g) {
+    if (g >= sl.a && g < sl.b) return load_granule<kKeep>(v.granule(g));
+    float x[Elem<T>::kPer];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = load_granule<kKeep>(v.granule(g + i * nt));
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            add_exps<T, kFull>(b[i], kFull ? sl.bits(g + i * nt) : 0u, kk, ref, s0, s1);
+    for (int k = 0; k < Elem<T>::kPer; ++k) {
+        const int j = g * Elem<T>::kPer + k - v.off;
+        x[k] = g < sl.hi && j >= 0 && j < vocab ? Elem<T>::to_f(v.row[j]) : kNegInf;
     }
-    for (; g < sl.b; g += nt)
-        add_exps<T, kFull>(load_granule<kKeep>(v.granule(g)), kFull ? sl.bits(g) : 0u, kk, ref, s0, s1);
+    return Elem<T>::pack(x);
+}
+template <class T, bool kFull>
+__device__ __forceinline__ uint32_t any_bits(const Slice<T>& sl, int g) {
+    return kFull && g < sl.hi ? sl.bits(g) : 0u;
+}
+
+// Sum of the segment from granule g0 on with reference m2, in every lane.
+template <class T, bool kFull, bool kKeep>
+__device__ __forceinline__ float segment_sum(const RowView<T>& v, const Slice<T>& sl, int vocab, int g0, float k2,
+                                             float m2) {
+    const uint64_t kk = both(k2), ref = both(-m2);
+    const int lane = threadIdx.x & 31;
+    uint64_t s0 = 0, s1 = 0;
+    if (g0 >= sl.a && g0 + kSegment <= sl.b) {
+#pragma unroll 1
+        for (int g = g0 + lane; g < g0 + kSegment; g += 128) {
+            uint4 b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = load_granule<kKeep>(v.granule(g + 32 * i));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                add_exps<T, kFull>(b[i], kFull ? sl.bits(g + 32 * i) : 0u, kk, ref, s0, s1);
+        }
+    } else {  // the row's first or last; the same order
+#pragma unroll 1
+        for (int g = g0 + lane; g < g0 + kSegment; g += 32)
+            add_exps<T, kFull>(any_granule<T, kKeep>(v, sl, vocab, g), any_bits<T, kFull>(sl, g), kk, ref, s0, s1);
+    }
     float x, y;
     unpack2(add2(s0, s1), x, y);
-    x += y;
-    for (int e = 0; e < 2; ++e) {
-        const int j = edge_column(v, sl, vocab, e, threadIdx.x);
-        if (j >= 0 && !(kFull && (sl.bits(e == 0 ? sl.lo : sl.b) >> threadIdx.x & 1u)))
-            x += ex2(fmaf(Elem<T>::to_f(v.row[j]), k2, -m2));
-    }
-    return x;
+    return warp_reduce(x + y, AddOp());
 }
 
-// Largest logit of this thread's part of a slice (with kFull as above).
+// The segment's own maximum, times k2.
 template <class T, bool kFull>
-__device__ __forceinline__ float slice_max(const RowView<T>& v, const Slice<T>& sl, int vocab) {
+__device__ __noinline__ float segment_max(const RowView<T>& v, const Slice<T>& sl, int vocab, int g0, float k2) {
     float m = kNegInf;
-    for (int g = sl.a + threadIdx.x; g < sl.b; g += blockDim.x) {
+#pragma unroll 1
+    for (int g = g0 + static_cast<int>(threadIdx.x & 31); g < g0 + kSegment; g += 32) {
         float x[Elem<T>::kPer];
-        Elem<T>::unpack(__ldcg(reinterpret_cast<const uint4*>(v.granule(g))), x);
-        const uint32_t bits = kFull ? sl.bits(g) : 0u;
+        Elem<T>::unpack(any_granule<T, true>(v, sl, vocab, g), x);
+        const uint32_t bits = any_bits<T, kFull>(sl, g);
 #pragma unroll
-        for (int i = 0; i < Elem<T>::kPer; ++i) m = fmaxf(m, bits >> i & 1u ? kNegInf : x[i]);
+        for (int k = 0; k < Elem<T>::kPer; ++k) m = fmaxf(m, bits >> k & 1u ? kNegInf : x[k]);
     }
-    for (int e = 0; e < 2; ++e) {
-        const int j = edge_column(v, sl, vocab, e, threadIdx.x);
-        if (j >= 0 && !(kFull && (sl.bits(e == 0 ? sl.lo : sl.b) >> threadIdx.x & 1u)))
-            m = fmaxf(m, Elem<T>::to_f(v.row[j]));
-    }
-    return m;
+    return warp_reduce(m, MaxOp()) * k2;
 }
 
-// Reference and sum of a warp's share of a slice, the same in every lane.  One
-// pass suffices when the listed columns' maximum `guess` is a fair reference
-// for the others, as it nearly always is: a sum that neither overflows nor
+// Reference and sum of a segment.  The listed columns' maximum `guess` nearly
+// always is a fair reference for the others: a sum that neither overflows nor
 // comes near underflow is as exact with one reference as with another.
-// Otherwise the share's own maximum is taken first.
+// Otherwise the segment's own maximum is taken.
 template <class T, bool kFull, bool kKeep>
-__device__ __forceinline__ void slice_sums(const RowView<T>& v, const Slice<T>& sl, int vocab, float k2, float guess,
-                                           float& m2, float& sum) {
-    m2 = guess;
-    sum = 0.0f;
-    if (fabsf(guess) < 1e30f) sum = warp_reduce(exp_sum<T, kFull, kKeep>(v, sl, vocab, k2, guess), AddOp());
-    if (sum > 1e-12f && sum < 1e30f) return;
-    m2 = warp_reduce(slice_max<T, kFull>(v, sl, vocab), MaxOp()) * k2;
-    sum = warp_reduce(exp_sum<T, kFull, kKeep>(v, sl, vocab, k2, m2 == kNegInf ? 0.0f : m2), AddOp());
+__device__ __forceinline__ float2 segment(const RowView<T>& v, const Slice<T>& sl, int vocab, int g0, float k2,
+                                          float guess) {
+    float m2 = fabsf(guess) < 1e30f ? guess : 0.0f;
+    float sum = segment_sum<T, kFull, kKeep>(v, sl, vocab, g0, k2, m2);
+    if (!(sum > 1e-27f && sum < 1e30f)) {
+        m2 = segment_max<T, kFull>(v, sl, vocab, g0, k2);
+        sum = segment_sum<T, kFull, kKeep>(v, sl, vocab, g0, k2, m2 == kNegInf ? 0.0f : m2);
+    }
+    return make_float2(m2, sum);
 }
 
-// The sums of a whole row, from the warps' parts; every lane gets them.
+// The sums of a whole row; every lane gets them.
 struct RowSums {
     float M2, S, inv_S;   // reference and sum of the whole row
-    float m2o, s_o;       // of the columns outside the list
+    float m2o, s_o;       // of the columns outside the list (with kFull; else the same)
     float ref_o, B;       // gradient outside the list: w tau B 2^(s k2 - ref_o)
     float p_r;            // the teacher's mass outside its list
 };
-// part: (reference, sum) of every warp of the cluster, over the columns outside
-// the list (kFull) or over all of them; top, with kFull: (sum over the listed
-// columns, their number).
+// part: (reference, sum) of every segment; s_exp, with kFull: the student's
+// exponential of every listed column, -1 for a slot that stands for none.
 template <bool kFull>
-__device__ __forceinline__ RowSums row_sums(const DistillArgs& a, const ListInfo& info, const float2* part,
-                                            const float2* top, int n_part) {
+__device__ __forceinline__ RowSums row_sums(const DistillArgs& a, const ListInfo& info, const float2* part, int n_part,
+                                            const float* s_exp) {
     const int lane = threadIdx.x & 31;
     RowSums r;
     r.m2o = kNegInf;
@@ -448,20 +474,22 @@ __device__ __forceinline__ RowSums row_sums(const DistillArgs& a, const ListInfo
     r.p_r = 0.0f;
     float f_o = 1.0f;
     if (kFull) {
-        float s_t = 0.0f, listed = 0.0f;
-        for (int i = lane; i < n_part; i += 32) {
-            s_t += top[i].x;
-            listed += top[i].y;
-        }
+        float s_t = 0.0f;
+        int listed = 0;
+        for (int k = lane; k < a.top; k += 32)
+            if (!(s_exp[k] < 0.0f)) {
+                s_t += s_exp[k];
+                ++listed;
+            }
         s_t = warp_reduce(s_t, AddOp());
-        listed = warp_reduce(listed, AddOp());
+        listed = __reduce_add_sync(0xffffffffu, listed);
         const float m2_top = info.m_top * a.k2;
         r.M2 = fmaxf(r.m2o, m2_top);
         f_o = rescale(r.m2o, r.M2);
         r.S = r.s_o * f_o + s_t * rescale(m2_top, r.M2);
         r.p_r = (1.0f - info.p_hi) - info.p_lo;
         // none where the list names every column
-        if (r.p_r < 0.0f || listed >= static_cast<float>(a.vocab)) r.p_r = 0.0f;
+        if (r.p_r < 0.0f || listed >= a.vocab) r.p_r = 0.0f;
     }
     r.inv_S = info.bad ? NAN : 1.0f / r.S;
     r.B = f_o * r.inv_S;
@@ -572,35 +600,35 @@ __device__ __forceinline__ void write_slice(const DistillArgs& a, const RowView<
     }
 }
 
-// Dynamic shared memory: the bits of a slice's listed columns, then four arrays
-// of `top` words: column or -1 for an empty slot, p before its normalisation,
-// the student's logit, and the column's p or -1 where another slot has it.
+// Dynamic shared memory: the bits of a slice's listed columns, the sums of the
+// whole row's segments, and kListArrays arrays of `top` words.
+constexpr int kListArrays = 6;
 __host__ __device__ constexpr size_t align16(size_t n) { return (n + 15) & ~size_t(15); }
 __host__ __device__ constexpr size_t bit_bytes(int slice) { return align16(static_cast<size_t>(slice)); }
+__host__ __device__ constexpr size_t part_bytes(int segments) { return align16(static_cast<size_t>(segments) * 8); }
 __host__ __device__ constexpr size_t list_bytes(int top) { return align16(static_cast<size_t>(top) * 4); }
-size_t dynamic_bytes(int slice, int top) { return bit_bytes(slice) + 4 * list_bytes(top); }
-
-struct Scratch {
-    float tm[kMaxWarps], mt[kMaxWarps];
-    float hi[kMaxWarps], lo[kMaxWarps], a[kMaxWarps];
-    // every warp of the cluster: (reference, sum) over its share of the slice,
-    // and (sum over its share of the listed columns, their number)
-    float2 part[kMaxCluster * kMaxWarps];
-    float2 top[kMaxCluster * kMaxWarps];
-};
+size_t dynamic_bytes(int slice, int segments, int top) {
+    return bit_bytes(slice) + part_bytes(segments) + kListArrays * list_bytes(top);
+}
 
 // One row per cluster; kFull: the teacher's log-sum is given.
 template <class T, bool kGrad, bool kFull>
-__global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const DistillArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillArgs a) {
     constexpr int kPer = Elem<T>::kPer;
     extern __shared__ uint4 dyn[];
-    __shared__ Scratch sh;
+    __shared__ float w_tm[kMaxWarps], w_mt[kMaxWarps];
+    __shared__ int w_flags[kMaxWarps];
     const int K = a.top, tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31, n_warps = nt >> 5;
-    uint32_t* const bits = reinterpret_cast<uint32_t*>(dyn);
-    int* const s_idx = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(dyn) + bit_bytes(a.slice));
-    float* const s_p = reinterpret_cast<float*>(s_idx) + list_bytes(K) / 4;
-    float* const s_s = s_p + list_bytes(K) / 4;
-    float* const s_lead = s_s + list_bytes(K) / 4;
+    uint8_t* const base = reinterpret_cast<uint8_t*>(dyn);
+    uint32_t* const bits = reinterpret_cast<uint32_t*>(base);
+    float2* const part = reinterpret_cast<float2*>(base + bit_bytes(a.slice));
+    const size_t step = list_bytes(K) / 4;
+    int* const s_idx = reinterpret_cast<int*>(base + bit_bytes(a.slice) + part_bytes(a.segments));
+    float* const s_p = reinterpret_cast<float*>(s_idx) + step;  // p before its normalisation
+    float* const s_s = s_p + step;                              // the student's logit
+    float* const s_a = s_s + step;                              // the slot's term of the loss
+    float* const s_lead = s_a + step;                           // the column's p, or -1 where another slot has it
+    float* const s_exp = s_lead + step;                         // the student's exponential, or -1
 
     uint32_t C;
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(C));
@@ -610,102 +638,112 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const DistillAr
     const Slice<T> sl(v, a.vocab, static_cast<int>(rank), a.slice, reinterpret_cast<const uint8_t*>(bits));
     T* const out = kGrad ? static_cast<T*>(a.dlogits) + row * a.ldd : nullptr;
     const bool same = kGrad && ((reinterpret_cast<uintptr_t>(out) & 15u) / sizeof(T)) == static_cast<unsigned>(v.off);
+    // the row's scalars and the first entries of its list come together
     const float w = a.weights ? a.weights[row] : 1.0f;
     const float lse = kFull ? a.lse[row] : 0.0f;
+    const int64_t j_first = tid < K ? load_index(a, row * K + tid) : -1;
+    const float t_first = tid < K ? load_top(a, row * K + tid) : kNegInf;
+    for (int i = tid; i < static_cast<int>(bit_bytes(a.slice) / 16); i += nt) dyn[i] = make_uint4(0, 0, 0, 0);
 
     // ---- the teacher's list, and the student's logits at its columns
-    bool any = false, bad = false;
     float tm = kNegInf, mt = kNegInf;
-    if (w != 0.0f) {
-        for (int i = tid; i < static_cast<int>(bit_bytes(a.slice) / 16); i += nt) dyn[i] = make_uint4(0, 0, 0, 0);
-        for (int k = tid; k < K; k += nt) {
-            const int64_t j = load_index(a, row * K + k);
-            const float t = load_top(a, row * K + k);
-            const bool held = j >= 0 && t != kNegInf;
-            const bool in = held && j < a.vocab;
-            bad |= held && !in;
-            any |= held;
-            s_idx[k] = in ? static_cast<int>(j) : -1;
-            s_p[k] = t;
-            if (in) {
-                const float s = Elem<T>::to_f(v.row[j]);
-                s_s[k] = s;
-                tm = fmaxf(tm, t);
-                mt = fmaxf(mt, s);
+    {
+        bool any = false, bad = false;
+        if (w != 0.0f) {
+            // The slice sets out for L2 while the list is worked on (8,192 x
+            // 128,000 bf16: 744 -> 689 us; without the gradient it only gets in the
+            // way of the loads, 300 -> 367 us).
+            if (kGrad && lane == 0) {
+                const int per = (sl.b - sl.a + n_warps - 1) / n_warps;
+                const int g0 = sl.a + warp * per, g1 = min(sl.b, g0 + per);
+                if (g0 < g1) prefetch_l2_bulk(v.granule(g0), static_cast<uint32_t>(g1 - g0) * 16u);
+            }
+            for (int k = tid; k < K; k += nt) {
+                const int64_t j = k == tid ? j_first : load_index(a, row * K + k);
+                const float t = k == tid ? t_first : load_top(a, row * K + k);
+                const bool held = j >= 0 && t != kNegInf;
+                const bool in = held && j < a.vocab;
+                bad |= held && !in;
+                any |= held;
+                s_idx[k] = in ? static_cast<int>(j) : -1;
+                s_p[k] = t;
+                s_exp[k] = -1.0f;
+                if (in) {
+                    const float s = Elem<T>::to_f(v.row[j]);
+                    s_s[k] = s;
+                    tm = fmaxf(tm, t);
+                    mt = fmaxf(mt, s);
+                }
             }
         }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, o));
+            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+        }
+        any = __any_sync(0xffffffffu, any);
+        bad = __any_sync(0xffffffffu, bad);
+        if (lane == 0) {
+            w_tm[warp] = tm;
+            w_mt[warp] = mt;
+            w_flags[warp] = (any ? 1 : 0) | (bad ? 2 : 0);
+        }
     }
-    if (!__syncthreads_or(any)) {  // no weight or no list: the whole cluster leaves here
+    __syncthreads();
+    int flags = 0;
+    for (int i = 0; i < n_warps; ++i) {
+        tm = fmaxf(tm, w_tm[i]);
+        mt = fmaxf(mt, w_mt[i]);
+        flags |= w_flags[i];
+    }
+    if (!flags) {  // no weight or no list: the whole cluster leaves here
         if (kGrad) zero_slice<T>(v, out, a.vocab, same, sl.lo, sl.hi, tid, nt);
         if (rank == 0 && tid == 0) store_dead(a, row, !kGrad);
         return;
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, o));
-        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-    }
-    if (lane == 0) {
-        sh.tm[warp] = tm;
-        sh.mt[warp] = mt;
-    }
-    bad = __syncthreads_or(bad);
-    tm = mt = kNegInf;
-    for (int i = 0; i < n_warps; ++i) {
-        tm = fmaxf(tm, sh.tm[i]);
-        mt = fmaxf(mt, sh.mt[i]);
-    }
-    // ---- p before its normalisation, its sum, and the loss's sum over the list
+    // the other CTAs may write here from now on (they wait for it below)
+    if (C > 1) cluster_arrive();
+    // ---- the list's exponentials, its terms of the loss, and the bits of its columns
     const int j_base = sl.lo * kPer - v.off, j0 = max(j_base, 0), j1 = min(a.vocab, sl.hi * kPer - v.off);
     bool twice = false;
-    {
-        float hi = 0.0f, lo = 0.0f, sum = 0.0f;
-        for (int k = tid; k < K; k += nt) {
-            const int j = s_idx[k];
-            float e = 0.0f;
-            if (j >= 0) {
-                const float t = s_p[k], s = s_s[k];
-                e = teacher_exp(a, t, kFull ? lse : tm, kFull);
-                if (e != 0.0f)
-                    sum += s == kNegInf ? INFINITY
-                                        : e * fmaf(s, a.k2_slip, fmaf(t - s, a.inv_hi, (t - s) * a.inv_lo));
-                float err;
-                hi = two_sum_f32(hi, e, err);
-                lo += err;
-                if (j >= j0 && j < j1) {
-                    const uint32_t bit = static_cast<uint32_t>(j - j_base);
-                    twice |= (atomicOr(bits + (bit >> 5), 1u << (bit & 31u)) >> (bit & 31u) & 1u) != 0;
-                }
+    for (int k = tid; k < K; k += nt) {
+        const int j = s_idx[k];
+        float e = 0.0f, term = 0.0f;
+        if (j >= 0) {
+            const float t = s_p[k], s = s_s[k];
+            e = teacher_exp(a, t, kFull ? lse : tm, kFull);
+            if (e != 0.0f)
+                term = s == kNegInf ? INFINITY : e * fmaf(s, a.k2_slip, fmaf(t - s, a.inv_hi, (t - s) * a.inv_lo));
+            if (j >= j0 && j < j1) {
+                const uint32_t bit = static_cast<uint32_t>(j - j_base);
+                twice |= (atomicOr(bits + (bit >> 5), 1u << (bit & 31u)) >> (bit & 31u) & 1u) != 0;
             }
-            s_p[k] = e;
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const float h = __shfl_xor_sync(0xffffffffu, hi, o), q = __shfl_xor_sync(0xffffffffu, lo, o);
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            float e;
-            hi = two_sum_f32(hi, h, e);
-            lo += q + e;
-        }
-        if (lane == 0) {
-            sh.hi[warp] = hi;
-            sh.lo[warp] = lo;
-            sh.a[warp] = sum;
-        }
+        s_p[k] = e;
+        s_a[k] = term;
     }
     twice = __syncthreads_or(twice);
-    ListInfo info{bad, w, tm, mt, 0.0f, 0.0f, 1.0f, 0.0f, lse};
-    for (int i = 0; i < n_warps; ++i) {
+    // every warp takes the list's sums for itself
+    ListInfo info{(flags & 2) != 0, w, tm, mt, 0.0f, 0.0f, 1.0f, 0.0f, lse};
+    for (int k = lane; k < K; k += 32) {
         float e;
-        info.p_hi = two_sum_f32(info.p_hi, sh.hi[i], e);
-        info.p_lo += sh.lo[i] + e;
-        info.a += sh.a[i];
+        info.p_hi = two_sum_f32(info.p_hi, s_p[k], e);
+        info.p_lo += e;
+        info.a += s_a[k];
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float h = __shfl_xor_sync(0xffffffffu, info.p_hi, o), q = __shfl_xor_sync(0xffffffffu, info.p_lo, o);
+        info.a += __shfl_xor_sync(0xffffffffu, info.a, o);
+        float e;
+        info.p_hi = two_sum_f32(info.p_hi, h, e);
+        info.p_lo += q + e;
     }
     if (!kFull) info.p_inv = 1.0f / (info.p_hi + info.p_lo);
-    // a column's p at its first slot; the others, if it is listed more than
-    // once, stand back (-1)
+    // A column's p at its first slot; the others, if it is listed more than once,
+    // stand back.  The student's exponentials go to every CTA of the cluster.
     const float m2_top = mt * a.k2;
-    float sum_top = 0.0f, listed = 0.0f;
+    if (C > 1) cluster_wait();
     for (int k = tid; k < K; k += nt) {
         const int j = s_idx[k];
         if (j < j0 || j >= j1) continue;
@@ -717,30 +755,22 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const DistillAr
         }
         s_lead[k] = p < 0.0f ? p : p * info.p_inv;
         if (kFull && !(p < 0.0f)) {
-            sum_top += m2_top == kNegInf ? 0.0f : ex2(fmaf(s_s[k], a.k2, -m2_top));
-            listed += 1.0f;
+            const float e = m2_top == kNegInf ? 0.0f : ex2(fmaf(s_s[k], a.k2, -m2_top));
+            for (uint32_t r = 0; r < C; ++r) st_cluster_f32(mapa_shared(smem_u32(s_exp + k), r), e);
         }
     }
 
-    // ---- the sums of the slice; every warp's go to every CTA of the cluster
-    {
-        float m2, sum;
-        slice_sums<T, kFull, kGrad>(v, sl, a.vocab, a.k2, m2_top, m2, sum);
+    // ---- the sums of the slice's segments, which go to every CTA of the cluster
+    for (int g0 = sl.lo + warp * kSegment; g0 < sl.hi; g0 += n_warps * kSegment) {
+        const float2 q = segment<T, kFull, kGrad>(v, sl, a.vocab, g0, a.k2, m2_top);
         if (lane < static_cast<int>(C))
-            st_cluster_f32x2(mapa_shared(smem_u32(&sh.part[rank * n_warps + warp]), lane), m2, sum);
-        if (kFull) {
-            sum_top = warp_reduce(sum_top, AddOp());
-            listed = warp_reduce(listed, AddOp());
-            if (lane < static_cast<int>(C))
-                st_cluster_f32x2(mapa_shared(smem_u32(&sh.top[rank * n_warps + warp]), lane), sum_top, listed);
-        }
+            st_cluster_f32x2(mapa_shared(smem_u32(part + g0 / kSegment), lane), q.x, q.y);
     }
     if (C == 1)
         __syncthreads();
     else
         cluster_sync_all();
-    const int n_part = static_cast<int>(C) * n_warps;
-    const RowSums r = row_sums<kFull>(a, info, sh.part, sh.top, n_part);
+    const RowSums r = row_sums<kFull>(a, info, part, (v.n + kSegment - 1) / kSegment, s_exp);
     if (rank == 0 && warp == n_warps - 1) {
         const float loss = row_loss(a, info, r);
         if (lane == 0) {
@@ -977,18 +1007,26 @@ template <class T, bool kGrad>
 hess_status launch_typed(DistillArgs& a, int sms, cudaStream_t s) {
     constexpr int per = Elem<T>::kPer;
     const int granules = static_cast<int>((static_cast<int64_t>(a.vocab) + 2 * (per - 1)) / per);
-    // CTAs per row: one, unless the rows would leave SMs without two; then more,
-    // down to slices of 2 KB.
+    // CTAs per row.  With the gradient, as many as keep a slice at 128 KB: all the
+    // slices in flight (1,536 threads an SM) are then 58 MB, which L2 holds until
+    // they are read again (8,192 x 128,000 bf16, 512 threads: 689 us in slices of
+    // 125 KB, 872 in rows of 250 KB).  Without it one (342 against 455 us).  More
+    // than that when the rows would leave SMs without two CTAs, down to slices of
+    // 2 KB.
+    a.segments = (granules + kSegment - 1) / kSegment;
+    const auto slice_at = [&](int c) { return (a.segments + c - 1) / c * kSegment; };
     int C = 1;
-    while (C < kMaxCluster && ((a.rows * C < 2 * sms && granules >= 256 * C) ||
-                               dynamic_bytes((granules + C - 1) / C, a.top) > kMaxDynamic))
+    while (C < kMaxCluster && ((kGrad && granules > 8224 * C) || (a.rows * C < 2 * sms && granules >= 256 * C) ||
+                               dynamic_bytes(slice_at(C), a.segments, a.top) > kMaxDynamic))
         C *= 2;
-    a.slice = (granules + C - 1) / C;
-    const size_t smem = dynamic_bytes(a.slice, a.top);
-    if (smem > kMaxDynamic)
+    a.slice = slice_at(C);
+    const size_t smem = dynamic_bytes(a.slice, a.segments, a.top);
+    if (smem > kMaxDynamic)  // not reached: the widest vocabulary in f32, 8 CTAs and the longest list take 217 KB
         return ds_fail(HESS_ERR_UNSUPPORTED, "vocab %d is too wide for the bits of its columns", a.vocab);
-    // threads: about eight 16-byte loads each
-    const int threads = a.slice >= 4096 ? 512 : a.slice >= 2048 ? 256 : 128;
+    // Threads: about 16 loads each; without the gradient more, smaller CTAs, which
+    // hide each other's start (8,192 x 32,000: 95 us with 128 threads, 115 with 256;
+    // 8,192 x 128,000: 345 and 300 us, 328 with 512).
+    const int threads = kGrad ? (a.slice > 4112 ? 512 : a.slice > 2056 ? 256 : 128) : a.slice > 8224 ? 256 : 128;
     auto fn = a.lse ? distill_kernel<T, kGrad, true> : distill_kernel<T, kGrad, false>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows * C), 1, 1);

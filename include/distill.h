@@ -35,8 +35,10 @@
  *
  * Arithmetic: exponentials and their sums in fp32 (two references, one for the
  * listed columns and one for the others, so neither underflows next to the
- * other); the K-term loss in fp64; each output is rounded once.  Results do
- * not depend on timing: the same call gives the same bits.
+ * other); the loss's K terms with their rounding errors; each output is rounded
+ * once.  A row's bits depend on its own data (and where it starts in a 16-byte
+ * unit), not on timing or on the rows beside it, and distill_step gives the loss
+ * that distill_forward gives.
  *
  * Memory: nothing is allocated and no workspace is kept; calls are
  * asynchronous on `stream` and may run concurrently.  Every device pointer
