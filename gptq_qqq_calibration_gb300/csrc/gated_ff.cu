@@ -470,6 +470,235 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
+// ------------------------------------------------------------- few tokens
+//
+// Up to kFewTokens tokens the work is reading the weights once (4 d f bytes for
+// 4 n d f operations: memory-bound below some 280 tokens), so the roles turn:
+// weight rows are the MMA's rows (R of Wg and the same R of Wu in one operand),
+// tokens its columns (N = n rounded up to 16), and one CTA per SM streams its
+// rows through a ring of up to 192 KB.  R is any number up to 64, chosen so that
+// every SM gets the same number of rows (37 at f = 11,008: 298 tiles, two per
+// SM; tiles of 64 would be 172, one or two per SM), which needs no split of the
+// sums.  The operand's unused rows hold what they hold: an MMA row only reaches
+// its own tensor-memory lane.
+
+constexpr int kFewTokens = 128;
+constexpr uint32_t kFewRing = 192 * 1024;
+constexpr int kFewMaxStages = 16;
+constexpr int kFewThreads = 256;  // warps 0: copies, 1: MMAs, 4-7: epilogue
+constexpr int kFewNumBarriers = 2 * kFewMaxStages + 5;
+constexpr uint32_t kFewExchange = 2 * 16 * 64 * 4;  // two buffers of 16 tokens x 64 rows of u
+// an operand of few rows is still read as 128: the ring has room for it at its end
+constexpr uint32_t kFewTail = 128 * 128;
+constexpr size_t kFewSmem = 1024 + kFewRing + kFewTail + kFewExchange + 8 * kFewNumBarriers + 16;
+
+struct FewParams {
+    CUtensorMap maps[3];  // kMapX: n_cols-row boxes; kMapWg, kMapWu: R-row boxes
+    int32_t n, f, act;
+    int32_t n_cols;       // n rounded up to 16: the MMA's N
+    int32_t rows;         // R
+    int32_t rows8;        // R rounded up to 8: where Wu's rows begin in the operand
+    int32_t stages;
+    int32_t stage_bytes;
+    int32_t n_kb;         // boxes along d
+    int32_t n_tiles;      // ceil(f / R)
+    uint32_t fmt;
+    void* out;
+    uint32_t* status;
+    unsigned long long timeout_ns;
+};
+
+template <class T>
+__global__ void __launch_bounds__(kFewThreads, 1) gated_ff_few_kernel(const __grid_constant__ FewParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* const gbase = smem_raw + (base - raw);
+    constexpr uint32_t kAfter = kFewRing + kFewTail;
+    float* const exch = reinterpret_cast<float*>(gbase + kAfter);
+    const uint32_t bar0 = base + kAfter + kFewExchange;
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + kAfter + kFewExchange + 8 * kFewNumBarriers);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (kFewMaxStages + s); };
+    auto accf_bar = [&](int b) { return bar0 + 8u * (2 * kFewMaxStages + b); };
+    auto acce_bar = [&](int b) { return bar0 + 8u * (2 * kFewMaxStages + 2 + b); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * kFewMaxStages + 4);
+    __shared__ volatile int aborted;  // a wait of some role ran out
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // X's rows come first in a stage (n_cols of them), then Wg's, then Wu's
+    const uint32_t x_bytes = static_cast<uint32_t>(p.n_cols) * 128u;
+    const uint32_t u_at = x_bytes + static_cast<uint32_t>(p.rows8) * 128u;
+    const uint32_t stage_bytes = static_cast<uint32_t>(p.stage_bytes);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(accf_bar(b), 1);
+            mbar_init(acce_bar(b), 4);
+        }
+        mbar_init(drain_bar, 1);
+        aborted = 0;
+        fence_barrier_init();
+        for (int m = 0; m < 3; ++m) prefetch_tensormap(&p.maps[m]);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), 2 * kFewTokens);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    const unsigned long long limit = p.timeout_ns;
+
+    if (warp == 0 && lane == 0) {
+        // Set-up above, and the first ring of weights on its way to L2 (which
+        // later writes to them would update), may overlap the end of the
+        // stream's previous kernel; nothing is read before that has completed.
+        int kb0 = 0, t0 = blockIdx.x;
+        for (int s = 0; s < p.stages && t0 < p.n_tiles; ++s) {
+            tma_prefetch_2d(&p.maps[kMapWg], kb0 * kKB, t0 * p.rows);
+            tma_prefetch_2d(&p.maps[kMapWu], kb0 * kKB, t0 * p.rows);
+            if (++kb0 == p.n_kb) {
+                kb0 = 0;
+                t0 += gridDim.x;
+            }
+        }
+        griddep_wait();
+        griddep_launch_dependents();
+        bool ok = true;
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int t = blockIdx.x; ok && t < p.n_tiles; t += gridDim.x) {
+            for (int kb = 0; kb < p.n_kb; ++kb) {
+                if (!mbar_wait(empty_bar(stage), phase ^ 1u, limit)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t at = base + stage * stage_bytes;
+                mbar_arrive_expect_tx(full_bar(stage), x_bytes + 2u * 128u * static_cast<uint32_t>(p.rows));
+                tma_load_2d(at + x_bytes, &p.maps[kMapWg], full_bar(stage), kb * kKB, t * p.rows);
+                tma_load_2d(at + u_at, &p.maps[kMapWu], full_bar(stage), kb * kKB, t * p.rows);
+                tma_load_2d(at, &p.maps[kMapX], full_bar(stage), kb * kKB, 0);
+                if (++stage == p.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (!ok) {
+            atomicOr(p.status, kStatusTimeoutLoad);
+            aborted = 1;
+        }
+    } else if (warp == 1 && lane == 0) {
+        bool ok = true;
+        int stage = 0, ab = 0;
+        uint32_t phase = 0, aphase = 0;
+        const uint32_t idesc = (1u << 4) | (p.fmt << 7) | (p.fmt << 10) |
+                               ((static_cast<uint32_t>(p.n_cols) >> 3) << 17) | ((128u >> 4) << 24);
+        griddep_wait();
+        for (int t = blockIdx.x; ok && t < p.n_tiles; t += gridDim.x) {
+            if (!mbar_wait(acce_bar(ab), aphase ^ 1u, limit)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            for (int kb = 0; kb < p.n_kb; ++kb) {
+                if (!mbar_wait(full_bar(stage), phase, limit)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sB = base + stage * stage_bytes, sA = sB + x_bytes;
+#pragma unroll
+                for (int j = 0; j < kKB / 16; ++j)
+                    umma_f16(tmem + ab * kFewTokens, smem_desc_sw128(sA + j * 32u, 16u, 1024u),
+                             smem_desc_sw128(sB + j * 32u, 16u, 1024u), idesc, (kb | j) != 0 ? 1u : 0u);
+                tc_commit(empty_bar(stage));
+                if (++stage == p.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) break;
+            tc_commit(accf_bar(ab));
+            if (++ab == 2) {
+                ab = 0;
+                aphase ^= 1u;
+            }
+        }
+        if (!ok) {
+            atomicOr(p.status, kStatusTimeoutMma);
+            aborted = 1;
+        }
+        tc_commit(drain_bar);
+        if (!mbar_wait(drain_bar, 0, kDrainLimitNs)) atomicOr(p.status, kStatusTimeoutDrain);
+    } else if (warp >= 4) {
+        // Lanes r < R hold g of weight row r, lanes rows8 + r its u: the latter
+        // hand theirs over through shared memory, 16 tokens at a time.
+        griddep_wait();
+        const int q = warp - 4, l = q * 32 + lane, r = l - p.rows8;
+        int ab = 0, buf = 0;
+        uint32_t aphase = 0;
+        for (int t = blockIdx.x; t < p.n_tiles; t += gridDim.x) {
+            const bool ok = aborted == 0 && mbar_wait(accf_bar(ab), aphase, limit);
+            if (!ok && lane == 0) {
+                atomicOr(p.status, kStatusTimeoutEpilogue);
+                aborted = 1;
+            }
+            tc_fence_after();
+            const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(ab * kFewTokens);
+            const int row = t * p.rows + l;
+            const bool mine = ok && l < p.rows && row < p.f;
+            T* const out = static_cast<T*>(p.out) + row;
+            // every epilogue warp takes every turn: they meet at a barrier in each
+            for (int c = 0; c < p.n_cols; c += 16) {
+                uint32_t a[16];
+                tmem_ld16(acc + c, a);
+                tmem_wait16(a, a);
+                float* const ex = exch + buf * (16 * 64);
+                buf ^= 1;
+                if (r >= 0 && r < p.rows) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) ex[i * 64 + r] = __uint_as_float(a[i]);
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (mine) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (c + i >= p.n) break;
+                        float dz;
+                        const float g = __uint_as_float(a[i]);
+                        const uint32_t h = Half2<T>::pack(g * gate_sigmoid(g, p.act, dz) * ex[i * 64 + l], 0.0f);
+                        reinterpret_cast<uint16_t*>(out)[static_cast<int64_t>(c + i) * p.f] =
+                            static_cast<uint16_t>(h);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acce_bar(ab));
+            if (++ab == 2) {
+                ab = 0;
+                aphase ^= 1u;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (aborted != 0) {  // copies still in flight land before the memory goes
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < kAbortSettleNs) __nanosleep(1000);
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 2 * kFewTokens);
+    }
+}
+
 // ------------------------------------------------------------- host side
 
 hess_status ff_fail(hess_status s, const char* fmt, ...) {
@@ -511,15 +740,16 @@ EncodeTiledFn ff_encode_fn() {
     return fn;
 }
 
-// Row-major [rows, cols] of 16-bit elements, 64 x 64 boxes, zeros past the edges.
-hess_status ff_encode(CUtensorMap* m, const void* ptr, int32_t dtype, int64_t rows, int64_t cols) {
+// Row-major [rows, cols] of 16-bit elements, boxes of box_rows x 64, zeros past the edges.
+hess_status ff_encode(CUtensorMap* m, const void* ptr, int32_t dtype, int64_t rows, int64_t cols,
+                      uint32_t box_rows = 64) {
     EncodeTiledFn fn = ff_encode_fn();
     if (!fn) return ff_fail(HESS_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     if (ff_injected("encode"))
         return ff_fail(HESS_ERR_UNSUPPORTED, "injected tensor-map failure (HESS_FAULT=encode)");
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2u};
-    const cuuint32_t box[2] = {64u, 64u}, es[2] = {1u, 1u};
+    const cuuint32_t box[2] = {64u, box_rows}, es[2] = {1u, 1u};
     const CUresult r = fn(m, dtype == HESS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                           2, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -531,9 +761,9 @@ hess_status ff_encode(CUtensorMap* m, const void* ptr, int32_t dtype, int64_t ro
 }
 
 // Per-device set-up: shared-memory limits, and how many pairs stay resident.
-hess_status ff_prepare(int dev, int* pairs) {
+hess_status ff_prepare(int dev, int* pairs, int* sms_out) {
     static std::mutex mu;
-    static int count[128] = {};
+    static int count[128] = {}, sm_count[128] = {};
     std::lock_guard<std::mutex> lk(mu);
     if (dev < 0 || dev >= 128) return ff_fail(HESS_ERR_UNSUPPORTED, "device index %d", dev);
     if (!count[dev]) {
@@ -542,8 +772,11 @@ hess_status ff_prepare(int dev, int* pairs) {
                         gated_ff_kernel<__half, kActGrad>, gated_ff_kernel<__half, kGradients>})
             FF_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         static_cast<int>(kSmemBytes)));
+        for (auto fn : {gated_ff_few_kernel<__nv_bfloat16>, gated_ff_few_kernel<__half>})
+            FF_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kFewSmem)));
         int sms = 0;
         FF_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+        sm_count[dev] = sms;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(sms & ~1), 1, 1);
         cfg.blockDim = dim3(kThreads, 1, 1);
@@ -557,6 +790,7 @@ hess_status ff_prepare(int dev, int* pairs) {
         count[dev] = clusters;
     }
     *pairs = count[dev];
+    *sms_out = sm_count[dev];
     return HESS_OK;
 }
 
@@ -568,7 +802,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 struct gated_ff_ctx {
     std::mutex mu;
     int device = 0;
-    int pairs = 0;
+    int pairs = 0, sms = 0;
     int64_t d = 0, f = 0, train_tokens = 0;
     int32_t dtype = 0, act = 0;
     void* dg = nullptr;  // [train_tokens, f] each
@@ -626,6 +860,63 @@ hess_status ff_launch(const gated_ff_ctx* g, const FfParams& p, cudaStream_t s) 
     return HESS_OK;
 }
 
+// The handle's workspace has one user at a time.
+hess_status ff_begin(gated_ff_ctx* g, cudaStream_t s) {
+    if (g->used && g->last != s) FF_TRY(cudaStreamWaitEvent(s, g->ev, 0));
+    return HESS_OK;
+}
+hess_status ff_end(gated_ff_ctx* g, cudaStream_t s) {
+    FF_TRY(cudaEventRecord(g->ev, s));
+    g->last = s;
+    g->used = true;
+    return HESS_OK;
+}
+
+hess_status ff_forward_few(const gated_ff_ctx* g, const void* X, int64_t n, const void* Wg, const void* Wu, void* H,
+                           cudaStream_t s) {
+    FewParams p{};
+    p.n = static_cast<int32_t>(n);
+    p.f = static_cast<int32_t>(g->f);
+    p.act = g->act;
+    p.n_cols = static_cast<int32_t>(ceil_div(n, 16) * 16);
+    // the fewest rows on the SM that has most (counted as tiles of R), then the fewest tiles
+    int64_t best = 0;
+    for (int64_t R = 8; R <= 64; ++R) {
+        const int64_t most = ceil_div(ceil_div(g->f, R), g->sms) * R;
+        if (best == 0 || most <= best) {
+            best = most;
+            p.rows = static_cast<int32_t>(R);
+        }
+    }
+    p.rows8 = (p.rows + 7) / 8 * 8;
+    p.stage_bytes = 128 * p.n_cols + 256 * p.rows8;
+    p.stage_bytes = (p.stage_bytes + 1023) / 1024 * 1024;
+    const int fit = static_cast<int>(kFewRing) / p.stage_bytes;
+    p.stages = fit < kFewMaxStages ? fit : kFewMaxStages;
+    p.n_kb = static_cast<int32_t>(ceil_div(g->d, kKB));
+    p.n_tiles = static_cast<int32_t>(ceil_div(g->f, p.rows));
+    p.fmt = g->dtype == HESS_BF16 ? 1u : 0u;
+    p.out = H;
+    p.status = g->status;
+    p.timeout_ns = g->timeout_ns;
+    FF_CHECK(ff_encode(&p.maps[kMapX], X, g->dtype, n, g->d, static_cast<uint32_t>(p.n_cols)));
+    FF_CHECK(ff_encode(&p.maps[kMapWg], Wg, g->dtype, g->f, g->d, static_cast<uint32_t>(p.rows)));
+    FF_CHECK(ff_encode(&p.maps[kMapWu], Wu, g->dtype, g->f, g->d, static_cast<uint32_t>(p.rows)));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.n_tiles < g->sms ? p.n_tiles : g->sms), 1, 1);
+    cfg.blockDim = dim3(kFewThreads, 1, 1);
+    cfg.dynamicSmemBytes = kFewSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    FF_TRY(cudaLaunchKernelEx(
+        &cfg, g->dtype == HESS_BF16 ? gated_ff_few_kernel<__nv_bfloat16> : gated_ff_few_kernel<__half>, p));
+    return HESS_OK;
+}
+
 hess_status ff_tokens(int64_t n) {
     if (n < 0) return ff_fail(HESS_ERR_INVALID, "n_tokens < 0");
     if (n > (int64_t(1) << 26)) return ff_fail(HESS_ERR_UNSUPPORTED, "n_tokens > 2^26");
@@ -660,14 +951,15 @@ FF_EXPORT hess_status gated_ff_create(int64_t d, int64_t f, int64_t train_tokens
     if (act != GATED_FF_SILU && act != GATED_FF_GELU_TANH)
         return ff_fail(HESS_ERR_INVALID, "unknown activation %d", act);
     if (hk::ff_injected("alloc")) return ff_fail(HESS_ERR_OOM, "injected allocation failure (HESS_FAULT=alloc)");
-    int dev = 0, pairs = 0;
+    int dev = 0, pairs = 0, sms = 0;
     FF_TRY(cudaGetDevice(&dev));
     FF_TRY(hk::ensure_context());
-    FF_CHECK(hk::ff_prepare(dev, &pairs));
+    FF_CHECK(hk::ff_prepare(dev, &pairs, &sms));
     gated_ff_ctx* g = new (std::nothrow) gated_ff_ctx();
     if (!g) return ff_fail(HESS_ERR_OOM, "host allocation failed");
     g->device = dev;
     g->pairs = pairs;
+    g->sms = sms;
     g->d = d;
     g->f = f;
     g->train_tokens = train_tokens;
@@ -703,6 +995,8 @@ FF_EXPORT hess_status gated_ff_forward(gated_ff_t g, const void* X, int64_t n_to
     FF_CHECK(hk::ff_check(g, W_up, "W_up"));
     FF_CHECK(hk::ff_check(g, H_out, "H_out"));
     FF_TRY(hk::ensure_context());
+    if (n_tokens <= hk::kFewTokens)
+        return hk::ff_forward_few(g, X, n_tokens, W_gate, W_up, H_out, static_cast<cudaStream_t>(stream));
     hk::FfParams p{};
     hk::ff_params(p, g, n_tokens);
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapX], X, g->dtype, n_tokens, g->d));
@@ -756,7 +1050,7 @@ FF_EXPORT hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_t
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapWu], W_up, g->dtype, g->f, g->d));
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapDg], g->dg, g->dtype, n_tokens, g->f));
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapDu], g->du, g->dtype, n_tokens, g->f));
-    if (g->used && g->last != s) FF_TRY(cudaStreamWaitEvent(s, g->ev, 0));
+    FF_CHECK(hk::ff_begin(g, s));
     p.dh = dH;
     p.out0 = g->dg;
     p.out1 = g->du;
@@ -769,9 +1063,7 @@ FF_EXPORT hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_t
     p.tiles_w = want_w ? static_cast<int32_t>(ceil_div(g->f, 256) * ceil_div(g->d, 256)) : 0;
     p.n_units = p.tiles_x + 2 * p.tiles_w;
     const hess_status st = hk::ff_launch<hk::kGradients>(g, p, s);
-    FF_TRY(cudaEventRecord(g->ev, s));
-    g->last = s;
-    g->used = true;
+    FF_CHECK(hk::ff_end(g, s));
     return st;
 }
 

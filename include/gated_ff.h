@@ -61,8 +61,8 @@ hess_status gated_ff_create(int64_t d, int64_t f, int64_t train_tokens, int32_t 
  *   W_gate, W_up : [f, d] (output channel by input column).  The halves of
  *            one packed [2f, d] matrix will do.
  *   H_out  : [n_tokens, f].
- * Asynchronous on `stream`.  Calls without a shared output may run
- * concurrently on several streams. */
+ * Asynchronous on `stream`.  Forward calls may run concurrently on several
+ * streams. */
 hess_status gated_ff_forward(gated_ff_t g, const void* X, int64_t n_tokens, const void* W_gate,
                              const void* W_up, void* H_out, hess_stream_t stream);
 
@@ -79,7 +79,7 @@ hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_tokens, con
 
 /* Wait for `stream`; then HESS_ERR_TIMEOUT if a device-side wait of this
  * handle's kernels ran out since the last gated_ff_sync (their results are
- * invalid), else HESS_OK. */
+ * invalid, and the handle works again after this call), else HESS_OK. */
 hess_status gated_ff_sync(gated_ff_t g, hess_stream_t stream);
 
 /* Limit of every device-side wait, ns (default 2e9; 0 makes any wait that is

@@ -304,6 +304,31 @@ def test_timeout_is_reported_and_recovers():
     op.sync()
 
 
+def test_few_tokens_on_streams_and_after_a_timeout():
+    """Calls of few tokens share the handle's workspace: on several streams they
+    do not mix, and a call that gave up leaves nothing behind once it is
+    reported."""
+    from gptq_qqq_calibration_gb300 import GatedFF, HessError
+    from gptq_qqq_calibration_gb300.gated_ff import gated_ff_set_timeout
+    d, f = 2048, 3000
+    op = GatedFF(d, f)
+    sets = [[t.cuda() for t in make(n, d, f, torch.bfloat16, 70 + n)[:3]] for n in (1, 20, 90, 128)]
+    want = [op.forward(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [op.forward(*s, stream=st) for s, st in zip(sets, streams)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    op.sync()
+    gated_ff_set_timeout(op.handle, 0)
+    op.forward(*sets[1])
+    with pytest.raises(HessError, match="TIMEOUT"):
+        op.sync()
+    gated_ff_set_timeout(op.handle, 2_000_000_000)
+    assert all(torch.equal(op.forward(*s), w) for s, w in zip(sets, want))
+    op.sync()
+
+
 def test_refusals():
     from gptq_qqq_calibration_gb300 import GatedFF, HessError
     from gptq_qqq_calibration_gb300 import _lib
