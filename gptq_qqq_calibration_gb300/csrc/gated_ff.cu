@@ -323,6 +323,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
     const unsigned long long limit = p.timeout_ns;
+    // Set-up above may overlap the end of the stream's previous kernel; nothing
+    // is read or written before that has completed.
+    griddep_wait();
+    griddep_launch_dependents();
 
     if (warp == 0 && lane == 0) {
         bool ok = true;
@@ -487,7 +491,7 @@ constexpr uint32_t kFewRing = 192 * 1024;
 constexpr int kFewMaxStages = 16;
 constexpr int kFewThreads = 256;  // warps 0: copies, 1: MMAs, 4-7: epilogue
 constexpr int kFewNumBarriers = 2 * kFewMaxStages + 5;
-constexpr uint32_t kFewExchange = 2 * 16 * 64 * 4;  // two buffers of 16 tokens x 64 rows of u
+constexpr uint32_t kFewExchange = 2 * 2 * 16 * 64 * 4;  // two buffers of g and u: 16 tokens x 64 rows
 // an operand of few rows is still read as 128: the ring has room for it at its end
 constexpr uint32_t kFewTail = 128 * 128;
 constexpr size_t kFewSmem = 1024 + kFewRing + kFewTail + kFewExchange + 8 * kFewNumBarriers + 16;
@@ -637,10 +641,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) gated_ff_few_kernel(const __gr
         tc_commit(drain_bar);
         if (!mbar_wait(drain_bar, 0, kDrainLimitNs)) atomicOr(p.status, kStatusTimeoutDrain);
     } else if (warp >= 4) {
-        // Lanes r < R hold g of weight row r, lanes rows8 + r its u: the latter
-        // hand theirs over through shared memory, 16 tokens at a time.
+        // Lanes r < R hold g of weight row r, lanes rows8 + r its u.  They meet in
+        // shared memory, 16 tokens at a time; each thread then finishes one row
+        // of eight tokens.
         griddep_wait();
-        const int q = warp - 4, l = q * 32 + lane, r = l - p.rows8;
+        const int q = warp - 4, l = q * 32 + lane;
+        const int at = l < p.rows ? l : l >= p.rows8 && l < p.rows8 + p.rows ? 16 * 64 + l - p.rows8 : -1;
+        const int r = l & 63, c8 = (l >> 6) * 8;
         int ab = 0, buf = 0;
         uint32_t aphase = 0;
         for (int t = blockIdx.x; t < p.n_tiles; t += gridDim.x) {
@@ -651,31 +658,33 @@ __global__ void __launch_bounds__(kFewThreads, 1) gated_ff_few_kernel(const __gr
             }
             tc_fence_after();
             const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(ab * kFewTokens);
-            const int row = t * p.rows + l;
-            const bool mine = ok && l < p.rows && row < p.f;
-            T* const out = static_cast<T*>(p.out) + row;
+            const int row = t * p.rows + r;
+            const bool mine = ok && r < p.rows && row < p.f;
             // every epilogue warp takes every turn: they meet at a barrier in each
             for (int c = 0; c < p.n_cols; c += 16) {
                 uint32_t a[16];
                 tmem_ld16(acc + c, a);
                 tmem_wait16(a, a);
-                float* const ex = exch + buf * (16 * 64);
+                float* const ex = exch + buf * (2 * 16 * 64);
                 buf ^= 1;
-                if (r >= 0 && r < p.rows) {
+                if (at >= 0) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) ex[i * 64 + r] = __uint_as_float(a[i]);
+                    for (int i = 0; i < 16; ++i) ex[at + i * 64] = __uint_as_float(a[i]);
                 }
                 asm volatile("bar.sync 1, 128;" ::: "memory");
-                if (mine) {
+                if (mine && c + c8 < p.n) {
+                    uint16_t h[8];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (c + i >= p.n) break;
+                    for (int i = 0; i < 8; ++i) {
                         float dz;
-                        const float g = __uint_as_float(a[i]);
-                        const uint32_t h = Half2<T>::pack(g * gate_sigmoid(g, p.act, dz) * ex[i * 64 + l], 0.0f);
-                        reinterpret_cast<uint16_t*>(out)[static_cast<int64_t>(c + i) * p.f] =
-                            static_cast<uint16_t>(h);
+                        const float g = ex[(c8 + i) * 64 + r];
+                        h[i] = static_cast<uint16_t>(
+                            Half2<T>::pack(g * gate_sigmoid(g, p.act, dz) * ex[16 * 64 + (c8 + i) * 64 + r], 0.0f));
                     }
+                    uint16_t* const out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(c + c8) * p.f + row;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (c + c8 + i < p.n) out[static_cast<int64_t>(i) * p.f] = h[i];
                 }
             }
             tc_fence_before();
@@ -849,15 +858,29 @@ void ff_params(FfParams& p, const gated_ff_ctx* g, int64_t n) {
     p.timeout_ns = g->timeout_ns;
 }
 
-template <int kWhat>
-hess_status ff_launch(const gated_ff_ctx* g, const FfParams& p, cudaStream_t s) {
-    const int pairs = p.n_units < g->pairs ? p.n_units : g->pairs;
-    if (g->dtype == HESS_BF16)
-        gated_ff_kernel<__nv_bfloat16, kWhat><<<2 * pairs, kThreads, kSmemBytes, s>>>(p);
-    else
-        gated_ff_kernel<__half, kWhat><<<2 * pairs, kThreads, kSmemBytes, s>>>(p);
-    FF_TRY(cudaGetLastError());
+// Launches so that the kernel's set-up may run while the stream's previous
+// kernel ends (each kernel here waits for that one's completion by itself).
+template <class Kernel, class Params>
+hess_status ff_launch(Kernel kernel, const Params& p, int64_t grid, int threads, size_t smem, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    FF_TRY(cudaLaunchKernelEx(&cfg, kernel, p));
     return HESS_OK;
+}
+
+template <int kWhat>
+hess_status ff_launch_pairs(const gated_ff_ctx* g, const FfParams& p, cudaStream_t s) {
+    const int pairs = p.n_units < g->pairs ? p.n_units : g->pairs;
+    return ff_launch(g->dtype == HESS_BF16 ? gated_ff_kernel<__nv_bfloat16, kWhat> : gated_ff_kernel<__half, kWhat>, p,
+                     2 * pairs, kThreads, kSmemBytes, s);
 }
 
 // The handle's workspace has one user at a time.
@@ -902,19 +925,8 @@ hess_status ff_forward_few(const gated_ff_ctx* g, const void* X, int64_t n, cons
     FF_CHECK(ff_encode(&p.maps[kMapX], X, g->dtype, n, g->d, static_cast<uint32_t>(p.n_cols)));
     FF_CHECK(ff_encode(&p.maps[kMapWg], Wg, g->dtype, g->f, g->d, static_cast<uint32_t>(p.rows)));
     FF_CHECK(ff_encode(&p.maps[kMapWu], Wu, g->dtype, g->f, g->d, static_cast<uint32_t>(p.rows)));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.n_tiles < g->sms ? p.n_tiles : g->sms), 1, 1);
-    cfg.blockDim = dim3(kFewThreads, 1, 1);
-    cfg.dynamicSmemBytes = kFewSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    FF_TRY(cudaLaunchKernelEx(
-        &cfg, g->dtype == HESS_BF16 ? gated_ff_few_kernel<__nv_bfloat16> : gated_ff_few_kernel<__half>, p));
-    return HESS_OK;
+    return ff_launch(g->dtype == HESS_BF16 ? gated_ff_few_kernel<__nv_bfloat16> : gated_ff_few_kernel<__half>, p,
+                     p.n_tiles < g->sms ? p.n_tiles : g->sms, kFewThreads, kFewSmem, s);
 }
 
 hess_status ff_tokens(int64_t n) {
@@ -1004,7 +1016,7 @@ FF_EXPORT hess_status gated_ff_forward(gated_ff_t g, const void* X, int64_t n_to
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapWu], W_up, g->dtype, g->f, g->d));
     p.out0 = H_out;
     p.n_units = static_cast<int32_t>(hk::ceil_div(n_tokens, 256) * hk::ceil_div(g->f, 128));
-    return hk::ff_launch<hk::kForward>(g, p, static_cast<cudaStream_t>(stream));
+    return hk::ff_launch_pairs<hk::kForward>(g, p, static_cast<cudaStream_t>(stream));
 }
 
 FF_EXPORT hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_tokens, const void* W_gate,
@@ -1055,14 +1067,14 @@ FF_EXPORT hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_t
     p.out0 = g->dg;
     p.out1 = g->du;
     p.n_units = static_cast<int32_t>(ceil_div(n_tokens, 256) * ceil_div(g->f, 128));
-    FF_CHECK(hk::ff_launch<hk::kActGrad>(g, p, s));
+    FF_CHECK(hk::ff_launch_pairs<hk::kActGrad>(g, p, s));
     p.out0 = dX_out;
     p.out1 = dW_gate_out;
     p.out2 = dW_up_out;
     p.tiles_x = want_x ? static_cast<int32_t>(ceil_div(n_tokens, 256) * ceil_div(g->d, 256)) : 0;
     p.tiles_w = want_w ? static_cast<int32_t>(ceil_div(g->f, 256) * ceil_div(g->d, 256)) : 0;
     p.n_units = p.tiles_x + 2 * p.tiles_w;
-    const hess_status st = hk::ff_launch<hk::kGradients>(g, p, s);
+    const hess_status st = hk::ff_launch_pairs<hk::kGradients>(g, p, s);
     FF_CHECK(hk::ff_end(g, s));
     return st;
 }
