@@ -66,6 +66,7 @@ struct FfParams {
     int32_t tiles_x;  // kGradients: tiles of dX (first), then 2 * tiles_w tiles of dWg and dWu
     int32_t tiles_w;
     int32_t n_units;
+    int32_t skip;     // kGradients: turns of dW tiles that one tile of dX is worth
     uint32_t fmt;     // operand format of the instruction descriptor: 0 = f16, 1 = bf16
     void* out0;       // h | dg | dX
     void* out1;       // - | du | dWg
@@ -82,6 +83,23 @@ __host__ __device__ inline void tile_at(int u, int tm, int tn, int& m, int& n) {
     const int rows = tm - g * kGroupM < kGroupM ? tm - g * kGroupM : kGroupM;
     n = r / rows;
     m = g * kGroupM + (r - n * rows);
+}
+
+// The k-th unit of a pair, or -1.  Units go to the pairs in turn.  The tiles of
+// dX are long (their sums run over f twice), so some pairs have one more of them
+// than the others; those sit out the first p.skip turns of the tiles of dW.
+template <int kWhat>
+__device__ __forceinline__ int unit_of(const FfParams& p, int pair, int n_pairs, int k) {
+    int u = pair + k * n_pairs;
+    if constexpr (kWhat == kGradients) {
+        if (u >= p.tiles_x) {
+            const int more = p.tiles_x % n_pairs, mine = p.tiles_x / n_pairs + (pair < more ? 1 : 0);
+            const int turn = k - mine + (pair < more ? p.skip : 0);
+            u = p.tiles_x + (turn < p.skip ? turn * (n_pairs - more) + pair - more
+                                           : p.skip * (n_pairs - more) + (turn - p.skip) * n_pairs + pair);
+        }
+    }
+    return u < p.n_units ? u : -1;
 }
 
 struct Unit {
@@ -332,7 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         int stage = 0;
         uint32_t phase = 0;
-        for (int u = pair; ok && u < p.n_units; u += n_pairs) {
+        for (int i = 0, u; ok && (u = unit_of<kWhat>(p, pair, n_pairs, i)) >= 0; ++i) {
             const Unit un = unit_at<kWhat>(p, u);
             const int m = un.m0 + static_cast<int>(rank) * 128;
             const int n = un.kind == 0 ? un.n0 : un.n0 + static_cast<int>(rank) * 128;
@@ -383,7 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t phase = 0;
         int ab = 0;
         uint32_t aphase = 0;
-        for (int u = pair; ok && u < p.n_units; u += n_pairs) {
+        for (int i = 0, u; ok && (u = unit_of<kWhat>(p, pair, n_pairs, i)) >= 0; ++i) {
             const Unit un = unit_at<kWhat>(p, u);
             // K-major: 16 steps are 32 bytes of a row, 8-row groups are 1,024
             // bytes apart.  MN-major: 16 steps are 16 rows of 128 bytes, the
@@ -435,7 +453,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t aphase = 0;
         const int q = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
         const uint32_t acce0 = mapa_shared(acce_bar(0), 0);
-        for (int u = pair; u < p.n_units; u += n_pairs) {
+        for (int i = 0, u; (u = unit_of<kWhat>(p, pair, n_pairs, i)) >= 0; ++i) {
             const Unit un = unit_at<kWhat>(p, u);
             if (!mbar_wait_cluster(accf_bar(ab), aphase, limit)) {
                 ok = false;
@@ -1074,6 +1092,8 @@ FF_EXPORT hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_t
     p.tiles_x = want_x ? static_cast<int32_t>(ceil_div(n_tokens, 256) * ceil_div(g->d, 256)) : 0;
     p.tiles_w = want_w ? static_cast<int32_t>(ceil_div(g->f, 256) * ceil_div(g->d, 256)) : 0;
     p.n_units = p.tiles_x + 2 * p.tiles_w;
+    const int64_t kb_x = 2 * ceil_div(g->f, hk::kKB), kb_w = ceil_div(n_tokens, hk::kKB);
+    p.skip = want_x && want_w ? static_cast<int32_t>((kb_x + kb_w / 2) / kb_w) : 0;
     const hess_status st = hk::ff_launch_pairs<hk::kGradients>(g, p, s);
     FF_CHECK(hk::ff_end(g, s));
     return st;
