@@ -22,10 +22,11 @@ _DTYPES = {torch.bfloat16: HESS_BF16, torch.float16: HESS_F16, torch.float32: HE
 ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
 
 
-def _stream(stream) -> int:
+def _stream(stream, device: int) -> int:
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    # the raw handle of the device's current stream, without building a Stream object
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _empty(shape, like: torch.Tensor, stream) -> torch.Tensor:
@@ -52,19 +53,24 @@ def gated_ff_create(d: int, f: int, train_tokens: int, dtype: int, act: int) -> 
 
 
 def gated_ff_forward(g: int, X, n_tokens: int, W_gate, W_up, H_out, stream=None) -> None:
-    check(_lib.load().gated_ff_forward(g, X.data_ptr(), int(n_tokens), W_gate.data_ptr(), W_up.data_ptr(),
-                                       H_out.data_ptr(), _stream(stream)))
+    st = _lib.load().gated_ff_forward(g, X.data_ptr(), n_tokens, W_gate.data_ptr(), W_up.data_ptr(),
+                                      H_out.data_ptr(), _stream(stream, X.get_device()))
+    if st:
+        check(st)
 
 
 def gated_ff_backward(g: int, X, n_tokens: int, W_gate, W_up, dH, dX_out, dW_gate_out, dW_up_out,
                       stream=None) -> None:
-    check(_lib.load().gated_ff_backward(
-        g, X.data_ptr(), int(n_tokens), W_gate.data_ptr(), W_up.data_ptr(), dH.data_ptr(),
-        *(t.data_ptr() if t is not None else None for t in (dX_out, dW_gate_out, dW_up_out)), _stream(stream)))
+    st = _lib.load().gated_ff_backward(
+        g, X.data_ptr(), n_tokens, W_gate.data_ptr(), W_up.data_ptr(), dH.data_ptr(),
+        None if dX_out is None else dX_out.data_ptr(), None if dW_gate_out is None else dW_gate_out.data_ptr(),
+        None if dW_up_out is None else dW_up_out.data_ptr(), _stream(stream, X.get_device()))
+    if st:
+        check(st)
 
 
 def gated_ff_sync(g: int, stream=None) -> None:
-    check(_lib.load().gated_ff_sync(g, _stream(stream)))
+    check(_lib.load().gated_ff_sync(g, _stream(stream, torch.cuda.current_device())))
 
 
 def gated_ff_set_timeout(g: int, ns: int) -> None:
@@ -95,31 +101,28 @@ class GatedFF:
         self.d, self.f, self.dtype = int(d), int(f), dtype
         self.handle = gated_ff_create(d, f, train_tokens, _DTYPES[dtype], ACTIVATIONS[activation])
 
-    def _check(self, t: torch.Tensor, name: str, width: int, rows: Optional[int] = None) -> int:
+    def _rows(self, t: torch.Tensor, name: str, width: int) -> int:
+        if t.dtype is self.dtype and t.is_cuda and t.is_contiguous() and t.dim() and t.shape[-1] == width:
+            return t.numel() // width
+        if t.dtype is not self.dtype:
+            raise ValueError(f"{name} must be {self.dtype}, got {t.dtype}")
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA tensor")
-        if t.dtype != self.dtype:
-            raise ValueError(f"{name} must be {self.dtype}, got {t.dtype}")
-        if t.dim() == 0 or t.shape[-1] != width:
-            raise ValueError(f"{name} must have a last dimension of {width}")
-        n = t.numel() // width
-        if rows is not None and n != rows:
-            raise ValueError(f"{name} must have {rows} rows, got {n}")
-        return n
+        raise ValueError(f"{name} must have a last dimension of {width}")
 
     def _inputs(self, X, W_gate, W_up) -> int:
-        n = self._check(X, "X", self.d)
-        self._check(W_gate, "W_gate", self.d, self.f)
-        self._check(W_up, "W_up", self.d, self.f)
+        n = self._rows(X, "X", self.d)
+        if self._rows(W_gate, "W_gate", self.d) != self.f or self._rows(W_up, "W_up", self.d) != self.f:
+            raise ValueError(f"W_gate and W_up must be [{self.f}, {self.d}]")
         return n
 
     def forward(self, X: torch.Tensor, W_gate: torch.Tensor, W_up: torch.Tensor,
                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         n = self._inputs(X, W_gate, W_up)
         if out is None:
-            out = _empty((*X.shape[:-1], self.f), X, stream)
-        else:
-            self._check(out, "out", self.f, n)
+            out = _empty((n, self.f) if X.dim() == 2 else (*X.shape[:-1], self.f), X, stream)
+        elif self._rows(out, "out", self.f) != n:
+            raise ValueError(f"out must have {n} rows")
         gated_ff_forward(self.handle, X, n, W_gate, W_up, out, stream)
         _used_on(stream, X, W_gate, W_up, out)
         return out
@@ -129,7 +132,8 @@ class GatedFF:
                  ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], Optional[torch.Tensor]]:
         """(dX, dW_gate, dW_up); None for what is not wanted."""
         n = self._inputs(X, W_gate, W_up)
-        self._check(dH, "dH", self.f, n)
+        if self._rows(dH, "dH", self.f) != n:
+            raise ValueError(f"dH must have {n} rows")
         dx = _empty(X.shape, X, stream) if want_dx else None
         dwg = _empty(W_gate.shape, X, stream) if want_dw else None
         dwu = _empty(W_up.shape, X, stream) if want_dw else None
