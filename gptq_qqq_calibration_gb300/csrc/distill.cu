@@ -791,7 +791,9 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillAr
 }
 
 // Gradient from saved statistics: one CTA per slice of a row, no exchange.
-constexpr int kBwdThreads = 256;
+// A stream without reuse: 4,096 x 65,536 bf16 176 us, 83 % of a copy of its bytes
+// (186 us with 256 threads a CTA; 8,192 x 4,000: 43 against 72 us).
+constexpr int kBwdThreads = 128;
 constexpr int kInFlight = 4;                            // granules a thread loads at a time
 constexpr int kBwdSlice = kBwdThreads * kInFlight * 2;  // granules per CTA
 
@@ -819,6 +821,16 @@ __global__ void __launch_bounds__(kBwdThreads) distill_backward_kernel(const Dis
     }
     const float M2 = st0.x, inv_S = st0.y, ref_o = st0.z;
     const float gs = w * a.tau * (a.grad ? a.grad[row] : 1.0f), mul = gs * st0.w;
+    // the first loads are on their way while the list is read
+    uint4 b[kInFlight];
+    const auto load = [&](int g) {
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i) {
+            const int gg = g + i * kBwdThreads;
+            if (gg < g_hi && v.whole(gg, a.vocab)) b[i] = load_granule<false>(v.granule(gg));
+        }
+    };
+    load(g_lo + tid);
     // this slice's part of the list; the student's logits there are read
     // before any gradient is stored (dlogits may be logits)
     if (tid == 0) s_n = 0;
@@ -839,12 +851,7 @@ __global__ void __launch_bounds__(kBwdThreads) distill_backward_kernel(const Dis
     }
     __syncthreads();
     for (int g = g_lo + tid; g < g_hi; g += kBwdThreads * kInFlight) {
-        uint4 b[kInFlight];
-#pragma unroll
-        for (int i = 0; i < kInFlight; ++i) {
-            const int gg = g + i * kBwdThreads;
-            if (gg < g_hi && v.whole(gg, a.vocab)) b[i] = load_granule<false>(v.granule(gg));
-        }
+        if (g != g_lo + tid) load(g);
 #pragma unroll
         for (int i = 0; i < kInFlight; ++i) {
             const int gg = g + i * kBwdThreads;
@@ -1007,26 +1014,33 @@ template <class T, bool kGrad>
 hess_status launch_typed(DistillArgs& a, int sms, cudaStream_t s) {
     constexpr int per = Elem<T>::kPer;
     const int granules = static_cast<int>((static_cast<int64_t>(a.vocab) + 2 * (per - 1)) / per);
-    // CTAs per row.  With the gradient, as many as keep a slice at 128 KB: all the
-    // slices in flight (1,536 threads an SM) are then 58 MB, which L2 holds until
-    // they are read again (8,192 x 128,000 bf16, 512 threads: 689 us in slices of
-    // 125 KB, 872 in rows of 250 KB).  Without it one (342 against 455 us).  More
-    // than that when the rows would leave SMs without two CTAs, down to slices of
-    // 2 KB.
+    // CTAs per row and threads per CTA (an SM holds 1,536 threads; bf16 rows with
+    // an eighth without weight, in steady state).
+    // With the gradient a slice is at most 132 KB: what is in flight, 64 MB then, is
+    // still in L2 when it is read again (8,192 x 128,000: 730 us in 2 slices, 902 in
+    // one, 919 in 4).  About 16 loads a thread (8,192 x 32,000: 181 us with 256
+    // threads, 219 with 512, 240 with 128).
+    // Without it one CTA, and small ones, which hide each other's start (8,192 x
+    // 128,000: 273 us with 256 threads, 298 with 512, 315 with 128; 4,096 x 65,536:
+    // 74 us with 128, 79 with 256, 99 with 512).
     a.segments = (granules + kSegment - 1) / kSegment;
     const auto slice_at = [&](int c) { return (a.segments + c - 1) / c * kSegment; };
     int C = 1;
-    while (C < kMaxCluster && ((kGrad && granules > 8224 * C) || (a.rows * C < 2 * sms && granules >= 256 * C) ||
+    while (C < kMaxCluster && ((kGrad && slice_at(C) > 8448) ||
                                dynamic_bytes(slice_at(C), a.segments, a.top) > kMaxDynamic))
         C *= 2;
+    int threads = kGrad ? (slice_at(C) > 4224 ? 512 : slice_at(C) > 2112 ? 256 : 128) : slice_at(C) > 8448 ? 256 : 128;
+    // Few rows: more CTAs for each while half of the threads would be idle; smaller
+    // ones when they would come to between one wave and two (301 x 50,257 f32 with
+    // gradient: 34.9 us with 2 CTAs of 256 threads a row, 40.4 with 2 of 512).
+    const int64_t room = int64_t(1536) * sms;
+    while (C < kMaxCluster && 2 * a.rows * C * threads <= room && granules >= 512 * C) C *= 2;
+    if (threads > 128 && a.rows * C * threads > room && a.rows * C * threads <= 2 * room) threads /= 2;
+    if (dynamic_bytes(slice_at(C), a.segments, a.top) > kMaxDynamic)
+        // not reached: the widest vocabulary in f32, 8 CTAs and the longest list take 217 KB
+        return ds_fail(HESS_ERR_UNSUPPORTED, "vocab %d is too wide for the bits of its columns", a.vocab);
     a.slice = slice_at(C);
     const size_t smem = dynamic_bytes(a.slice, a.segments, a.top);
-    if (smem > kMaxDynamic)  // not reached: the widest vocabulary in f32, 8 CTAs and the longest list take 217 KB
-        return ds_fail(HESS_ERR_UNSUPPORTED, "vocab %d is too wide for the bits of its columns", a.vocab);
-    // Threads: about 16 loads each; without the gradient more, smaller CTAs, which
-    // hide each other's start (8,192 x 32,000: 95 us with 128 threads, 115 with 256;
-    // 8,192 x 128,000: 345 and 300 us, 328 with 512).
-    const int threads = kGrad ? (a.slice > 4112 ? 512 : a.slice > 2056 ? 256 : 128) : a.slice > 8224 ? 256 : 128;
     auto fn = a.lse ? distill_kernel<T, kGrad, true> : distill_kernel<T, kGrad, false>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows * C), 1, 1);
