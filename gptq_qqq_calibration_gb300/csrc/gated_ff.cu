@@ -19,6 +19,11 @@
 // memory holds two tiles, so one tile's epilogue runs under the next one's
 // products.
 //
+// Where the tiles do not fill the pairs (a small problem, or the last round of a
+// larger one) each is split along its sum: the pieces' fp32 sums go to memory
+// and the pair that comes last adds them, in the order of the pieces, and
+// finishes the tile.  Nobody waits for another pair.
+//
 // Every operand box is 64 x 64 elements with the 128-byte swizzle, whichever
 // way it is contiguous: boxes stacked in shared memory serve both the K-major
 // and the MN-major descriptors, and one tensor map per matrix is enough.
@@ -63,7 +68,9 @@ struct FfParams {
     CUtensorMap maps[kMaps];
     int32_t n, d, f;
     int32_t act;
-    int32_t tiles_x;  // kGradients: tiles of dX (first), then 2 * tiles_w tiles of dWg and dWu
+    int32_t whole;    // kForward, kActGrad: tiles that are not split; they come first
+    int32_t parts;    // units of each tile after them, or of each tile of dX
+    int32_t units_x;  // kGradients: units of dX (first), then 2 * tiles_w tiles of dWg and dWu
     int32_t tiles_w;
     int32_t n_units;
     int32_t skip;     // kGradients: turns of dW tiles that one tile of dX is worth
@@ -72,9 +79,12 @@ struct FfParams {
     void* out1;       // - | du | dWg
     void* out2;       // - | -  | dWu
     const void* dh;
+    float* pieces;      // 256 x 256 sums of every unit of a split tile
+    uint32_t* arrived;  // pieces of each split tile that have come, per CTA; zero between launches
     uint32_t* status;
     unsigned long long timeout_ns;
 };
+constexpr int kPieceFloats = 256 * 256;
 
 // Tile u of tm x tn, in groups of kGroupM row tiles walked column by column.
 __host__ __device__ inline void tile_at(int u, int tm, int tn, int& m, int& n) {
@@ -92,10 +102,10 @@ template <int kWhat>
 __device__ __forceinline__ int unit_of(const FfParams& p, int pair, int n_pairs, int k) {
     int u = pair + k * n_pairs;
     if constexpr (kWhat == kGradients) {
-        if (u >= p.tiles_x) {
-            const int more = p.tiles_x % n_pairs, mine = p.tiles_x / n_pairs + (pair < more ? 1 : 0);
+        if (u >= p.units_x) {
+            const int more = p.units_x % n_pairs, mine = p.units_x / n_pairs + (pair < more ? 1 : 0);
             const int turn = k - mine + (pair < more ? p.skip : 0);
-            u = p.tiles_x + (turn < p.skip ? turn * (n_pairs - more) + pair - more
+            u = p.units_x + (turn < p.skip ? turn * (n_pairs - more) + pair - more
                                            : p.skip * (n_pairs - more) + (turn - p.skip) * n_pairs + pair);
         }
     }
@@ -106,35 +116,50 @@ struct Unit {
     int kind;   // 0: X times weights, 1: dX, 2: dW
     int m0, n0;  // first row of A and of B (kind 0: of each weight)
     int which;  // kind 2: 0 = gate, 1 = up
-    int n_kb;
-    int split;  // kind 1: k-blocks of the gate half
+    int kb0, kb1;  // boxes of the sum
+    int half;   // kind 1: boxes of the gate half of the sum
+    int parts;  // units of this tile
+    int part;   // this one
+    int split;  // split tiles before this one
 };
 
 template <int kWhat>
 __device__ __forceinline__ Unit unit_at(const FfParams& p, int u) {
     Unit r{};
-    int m, n;
+    int m, n, n_kb;
+    r.parts = 1;
     if constexpr (kWhat != kGradients) {
+        if (u >= p.whole) {
+            r.parts = p.parts;
+            r.split = (u - p.whole) / p.parts;
+            r.part = (u - p.whole) - r.split * p.parts;
+            u = p.whole + r.split;
+        }
         tile_at(u, (p.n + 255) / 256, (p.f + 127) / 128, m, n);
         r.m0 = m * 256;
         r.n0 = n * 128;
-        r.n_kb = (p.d + kKB - 1) / kKB;
-    } else if (u < p.tiles_x) {
-        tile_at(u, (p.n + 255) / 256, (p.d + 255) / 256, m, n);
+        n_kb = (p.d + kKB - 1) / kKB;
+    } else if (u < p.units_x) {
+        r.parts = p.parts;
+        r.split = u / p.parts;
+        r.part = u - r.split * p.parts;
+        tile_at(r.split, (p.n + 255) / 256, (p.d + 255) / 256, m, n);
         r.kind = 1;
         r.m0 = m * 256;
         r.n0 = n * 256;
-        r.split = (p.f + kKB - 1) / kKB;
-        r.n_kb = 2 * r.split;
+        r.half = (p.f + kKB - 1) / kKB;
+        n_kb = 2 * r.half;
     } else {
-        u -= p.tiles_x;
+        u -= p.units_x;
         r.which = u >= p.tiles_w ? 1 : 0;
         tile_at(u - r.which * p.tiles_w, (p.f + 255) / 256, (p.d + 255) / 256, m, n);
         r.kind = 2;
         r.m0 = m * 256;
         r.n0 = n * 256;
-        r.n_kb = (p.n + kKB - 1) / kKB;
+        n_kb = (p.n + kKB - 1) / kKB;
     }
+    r.kb0 = n_kb * r.part / r.parts;
+    r.kb1 = n_kb * (r.part + 1) / r.parts;
     return r;
 }
 
@@ -206,6 +231,11 @@ __device__ __forceinline__ float gate_sigmoid(float g, int act, float& dz) {
     return __fdividef(1.0f, 1.0f + __expf(-z));
 }
 
+// The epilogue warps' own barrier.
+__device__ __forceinline__ void epi_barrier() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
+}
+
 // Eight consecutive values of one row.
 template <class T>
 __device__ __forceinline__ void store8(T* p, const float* x) {
@@ -218,24 +248,23 @@ __device__ __forceinline__ void store8(T* p, const float* x) {
 }
 
 // Epilogue of one tile by one warp: its 32 lanes are 32 rows of this CTA's 128
-// (lane quarter warp % 4), and it takes half of the columns, 16 at a time.
-template <class T, int kWhat>
-__device__ __forceinline__ void finish_tile(const FfParams& p, const Unit& un, uint32_t acc, int half, int64_t row) {
+// (lane quarter warp % 4), and it takes half of the columns, 16 at a time:
+// load(c, a, c2, b) gives the finished sums of columns c.. and c2...
+template <class T, int kWhat, class Load>
+__device__ __forceinline__ void finish_tile(const FfParams& p, const Unit& un, int half, int64_t row, Load load) {
     if constexpr (kWhat != kGradients) {
         const bool in = row < p.n;
 #pragma unroll 1
         for (int c = half * 64; c < half * 64 + 64; c += 16) {
             const int col = un.n0 + c;
-            uint32_t g[16], u[16];
-            tmem_ld16(acc + c, g);
-            tmem_ld16(acc + 128 + c, u);
             uint4 dv[2] = {};
             if constexpr (kWhat == kActGrad) {
                 const T* const dh = static_cast<const T*>(p.dh) + row * p.f + col;
                 if (in && col < p.f) dv[0] = *reinterpret_cast<const uint4*>(dh);
                 if (in && col + 8 < p.f) dv[1] = *reinterpret_cast<const uint4*>(dh + 8);
             }
-            tmem_wait16(g, u);
+            uint32_t g[16], u[16];
+            load(c, g, 128 + c, u);
             if constexpr (kWhat == kForward) {
                 float h[16];
 #pragma unroll
@@ -278,9 +307,7 @@ __device__ __forceinline__ void finish_tile(const FfParams& p, const Unit& un, u
 #pragma unroll 1
         for (int c = half * 128; c < half * 128 + 128; c += 32) {
             uint32_t a[16], b[16];
-            tmem_ld16(acc + c, a);
-            tmem_ld16(acc + c + 16, b);
-            tmem_wait16(a, b);
+            load(c, a, c + 16, b);
             float x[32];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -312,6 +339,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto acce_bar = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
     const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4);
     __shared__ int aborted;
+    __shared__ volatile int epi_failed, epi_last;  // of the epilogue warps
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -330,6 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         mbar_init(drain_bar, 1);
         aborted = 0;
+        epi_failed = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -354,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const Unit un = unit_at<kWhat>(p, u);
             const int m = un.m0 + static_cast<int>(rank) * 128;
             const int n = un.kind == 0 ? un.n0 : un.n0 + static_cast<int>(rank) * 128;
-            for (int kb = 0; kb < un.n_kb; ++kb) {
+            for (int kb = un.kb0; kb < un.kb1; ++kb) {
                 if (!mbar_wait_cluster(empty_bar(stage), phase ^ 1u, limit)) {
                     ok = false;
                     break;
@@ -370,10 +399,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tma_load_2d_pair(sB, w, fb, k, n);
                     tma_load_2d_pair(sB + kBoxBytes, w, fb, k, n + 64);
                 } else if (un.kind == 1) {
-                    const bool up = kb >= un.split;
+                    const bool up = kb >= un.half;
                     const CUtensorMap* const a = &p.maps[up ? kMapDu : kMapDg];
                     const CUtensorMap* const w = &p.maps[up ? kMapWu : kMapWg];
-                    if (up) k -= un.split * kKB;
+                    if (up) k -= un.half * kKB;
                     tma_load_2d_pair(sA, a, fb, k, m);
                     tma_load_2d_pair(sA + kBoxBytes, a, fb, k, m + 64);
                     tma_load_2d_pair(sB, w, fb, n, k);
@@ -416,7 +445,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const uint32_t acc = tmem + static_cast<uint32_t>(ab) * 256u;
-            for (int kb = 0; kb < un.n_kb; ++kb) {
+            for (int kb = un.kb0; kb < un.kb1; ++kb) {
                 if (!mbar_wait_cluster(full_bar(stage), phase, limit)) {
                     ok = false;
                     break;
@@ -426,7 +455,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < kKB / 16; ++j)
                     umma_f16_pair(acc, smem_desc_sw128(sA + j * a_step, a_lbo, 1024u),
-                                  smem_desc_sw128(sB + j * b_step, b_lbo, 1024u), idesc, (kb | j) != 0 ? 1u : 0u);
+                                  smem_desc_sw128(sB + j * b_step, b_lbo, 1024u), idesc,
+                                  kb != un.kb0 || j != 0 ? 1u : 0u);
                 tc_commit_pair_mc(empty_bar(stage), 0x3);
                 if (++stage == kStages) {
                     stage = 0;
@@ -448,21 +478,87 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_commit_pair_mc(drain_bar, 0x1);
         if (!mbar_wait(drain_bar, 0, kDrainLimitNs)) atomicOr(p.status, kStatusTimeoutDrain);
     } else if (warp >= kFirstEpiWarp) {
-        bool ok = true;
+        bool failed = false;
         int ab = 0;
         uint32_t aphase = 0;
         const int q = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
+        const int r128 = q * 32 + lane;  // row of this CTA's half of the tile
         const uint32_t acce0 = mapa_shared(acce_bar(0), 0);
         for (int i = 0, u; (u = unit_of<kWhat>(p, pair, n_pairs, i)) >= 0; ++i) {
             const Unit un = unit_at<kWhat>(p, u);
-            if (!mbar_wait_cluster(accf_bar(ab), aphase, limit)) {
-                ok = false;
-                break;
-            }
+            failed = failed || !mbar_wait_cluster(accf_bar(ab), aphase, limit);
             tc_fence_after();
-            const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(ab) * 256u;
-            const int64_t row = static_cast<int64_t>(un.m0) + static_cast<int>(rank) * 128 + q * 32 + lane;
-            finish_tile<T, kWhat>(p, un, acc, half, row);
+            const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(ab * 256);
+            const int64_t row = static_cast<int64_t>(un.m0) + static_cast<int>(rank) * 128 + r128;
+            const auto from_tmem = [&](int c, uint32_t (&a)[16], int c2, uint32_t (&b)[16]) {
+                tmem_ld16(acc + c, a);
+                tmem_ld16(acc + c2, b);
+                tmem_wait16(a, b);
+            };
+            if (un.parts == 1) {
+                if (!failed) finish_tile<T, kWhat>(p, un, half, row, from_tmem);
+            } else {
+                // Every epilogue warp passes the four barriers below for every split
+                // unit, whether its waits ran out or not.
+                if (failed) epi_failed = 1;
+                epi_barrier();
+                failed = epi_failed != 0;
+                // one piece after the other: this CTA's half of it in blocks of four
+                // columns, 128 rows of 16 bytes each
+                float* const piece0 = p.pieces + static_cast<int64_t>(un.split) * un.parts * kPieceFloats +
+                                      rank * (kPieceFloats / 2) + 4 * r128;
+                if (!failed) {
+                    float* const mine = piece0 + static_cast<int64_t>(un.part) * kPieceFloats;
+                    for (int c = half * 128; c < half * 128 + 128; c += 32) {
+                        uint32_t a[16], b[16];
+                        from_tmem(c, a, c + 16, b);
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4) {
+                            __stcg(reinterpret_cast<uint4*>(mine + (c + k) * 128),
+                                   make_uint4(a[k], a[k + 1], a[k + 2], a[k + 3]));
+                            __stcg(reinterpret_cast<uint4*>(mine + (c + 16 + k) * 128),
+                                   make_uint4(b[k], b[k + 1], b[k + 2], b[k + 3]));
+                        }
+                    }
+                    __threadfence();
+                }
+                epi_barrier();
+                if (warp == kFirstEpiWarp && lane == 0) {
+                    uint32_t* const count = p.arrived + 2 * un.split + rank;
+                    const bool last = !failed && atomicAdd(count, 1u) == static_cast<uint32_t>(un.parts - 1);
+                    if (last) *count = 0;
+                    epi_last = last;
+                }
+                epi_barrier();
+                if (epi_last) {
+                    __threadfence();
+                    finish_tile<T, kWhat>(p, un, half, row, [&](int c, uint32_t (&a)[16], int c2, uint32_t (&b)[16]) {
+                        float x[16] = {}, y[16] = {};
+                        for (int k = 0; k < un.parts; ++k) {
+                            const float* const piece = piece0 + static_cast<int64_t>(k) * kPieceFloats;
+                            float4 v[8];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                v[e] = __ldcg(reinterpret_cast<const float4*>(piece + (c + 4 * e) * 128));
+                                v[4 + e] = __ldcg(reinterpret_cast<const float4*>(piece + (c2 + 4 * e) * 128));
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                x[4 * e] += v[e].x, x[4 * e + 1] += v[e].y;
+                                x[4 * e + 2] += v[e].z, x[4 * e + 3] += v[e].w;
+                                y[4 * e] += v[4 + e].x, y[4 * e + 1] += v[4 + e].y;
+                                y[4 * e + 2] += v[4 + e].z, y[4 * e + 3] += v[4 + e].w;
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            a[e] = __float_as_uint(x[e]);
+                            b[e] = __float_as_uint(y[e]);
+                        }
+                    });
+                }
+                epi_barrier();  // epi_last may be written again
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster_relaxed(acce0 + 8u * ab);
@@ -471,7 +567,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 aphase ^= 1u;
             }
         }
-        if (!ok && lane == 0) {
+        if (failed && lane == 0) {
             atomicOr(p.status, kStatusTimeoutEpilogue);
             aborted = 1;
         }
@@ -823,6 +919,21 @@ hess_status ff_prepare(int dev, int* pairs, int* sms_out) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// The status word, then two arrival counts for every tile that may be split (at
+// most one per pair).
+size_t status_bytes(int pairs) { return (1 + 2 * static_cast<size_t>(pairs)) * sizeof(uint32_t); }
+
+// Units a tile of n_kb boxes is split in when `tiles` of them have `pairs` to
+// themselves.  A box takes 512 cycles at the tensor cores' rate, a piece about
+// 2,000 to be read again and 4,000 for the rest: n_kb / s * 512 + 2,000 s is least
+// at s = sqrt(n_kb) / 2, and below 16 boxes there is nothing to gain.
+int32_t parts_of(int64_t tiles, int64_t n_kb, int64_t pairs) {
+    if (tiles <= 0 || n_kb < 16) return 1;
+    int64_t s = 1;
+    while (4 * (s + 1) * (s + 1) <= n_kb + n_kb / 4 && tiles * (s + 1) <= pairs && s < 8) ++s;
+    return static_cast<int32_t>(s);
+}
+
 }  // namespace
 }  // namespace hk
 
@@ -832,6 +943,7 @@ struct gated_ff_ctx {
     int pairs = 0, sms = 0;
     int64_t d = 0, f = 0, train_tokens = 0;
     int32_t dtype = 0, act = 0;
+    float* pieces = nullptr;  // one per pair
     void* dg = nullptr;  // [train_tokens, f] each
     void* du = nullptr;
     uint32_t* status = nullptr;
@@ -872,8 +984,18 @@ void ff_params(FfParams& p, const gated_ff_ctx* g, int64_t n) {
     p.f = static_cast<int32_t>(g->f);
     p.act = g->act;
     p.fmt = g->dtype == HESS_BF16 ? 1u : 0u;
+    p.pieces = g->pieces;
+    p.arrived = g->status + 1;
     p.status = g->status;
     p.timeout_ns = g->timeout_ns;
+}
+
+// Units of X times the weights: whole rounds of tiles, then the rest, split.
+void ff_tiles(FfParams& p, const gated_ff_ctx* g) {
+    const int64_t tiles = ceil_div(p.n, 256) * ceil_div(g->f, 128), rest = tiles % g->pairs;
+    p.parts = parts_of(rest, ceil_div(g->d, kKB), g->pairs);
+    p.whole = static_cast<int32_t>(p.parts > 1 ? tiles - rest : tiles);
+    p.n_units = static_cast<int32_t>(p.parts > 1 ? p.whole + rest * p.parts : tiles);
 }
 
 // Launches so that the kernel's set-up may run while the stream's previous
@@ -956,6 +1078,7 @@ hess_status ff_tokens(int64_t n) {
 void ff_free(gated_ff_ctx* g) {
     cudaFree(g->dg);
     cudaFree(g->du);
+    cudaFree(g->pieces);
     cudaFree(g->status);
     if (g->ev) cudaEventDestroy(g->ev);
 }
@@ -996,8 +1119,10 @@ FF_EXPORT hess_status gated_ff_create(int64_t d, int64_t f, int64_t train_tokens
     g->dtype = dtype;
     g->act = act;
     const size_t bytes = static_cast<size_t>(train_tokens) * static_cast<size_t>(f) * 2;
-    cudaError_t e = cudaMalloc(&g->status, sizeof(uint32_t));
-    if (e == cudaSuccess) e = cudaMemset(g->status, 0, sizeof(uint32_t));
+    cudaError_t e = cudaMalloc(&g->status, hk::status_bytes(pairs));
+    if (e == cudaSuccess) e = cudaMemset(g->status, 0, hk::status_bytes(pairs));
+    if (e == cudaSuccess)
+        e = cudaMalloc(&g->pieces, static_cast<size_t>(pairs) * hk::kPieceFloats * sizeof(float));
     if (e == cudaSuccess && bytes) e = cudaMalloc(&g->dg, bytes);
     if (e == cudaSuccess && bytes) e = cudaMalloc(&g->du, bytes);
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&g->ev, cudaEventDisableTiming);
@@ -1033,8 +1158,12 @@ FF_EXPORT hess_status gated_ff_forward(gated_ff_t g, const void* X, int64_t n_to
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapWg], W_gate, g->dtype, g->f, g->d));
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapWu], W_up, g->dtype, g->f, g->d));
     p.out0 = H_out;
-    p.n_units = static_cast<int32_t>(hk::ceil_div(n_tokens, 256) * hk::ceil_div(g->f, 128));
-    return hk::ff_launch_pairs<hk::kForward>(g, p, static_cast<cudaStream_t>(stream));
+    hk::ff_tiles(p, g);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (p.parts == 1) return hk::ff_launch_pairs<hk::kForward>(g, p, s);
+    FF_CHECK(hk::ff_begin(g, s));
+    FF_CHECK(hk::ff_launch_pairs<hk::kForward>(g, p, s));
+    return hk::ff_end(g, s);
 }
 
 FF_EXPORT hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_tokens, const void* W_gate,
@@ -1084,16 +1213,23 @@ FF_EXPORT hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_t
     p.dh = dH;
     p.out0 = g->dg;
     p.out1 = g->du;
-    p.n_units = static_cast<int32_t>(ceil_div(n_tokens, 256) * ceil_div(g->f, 128));
+    hk::ff_tiles(p, g);
     FF_CHECK(hk::ff_launch_pairs<hk::kActGrad>(g, p, s));
     p.out0 = dX_out;
     p.out1 = dW_gate_out;
     p.out2 = dW_up_out;
-    p.tiles_x = want_x ? static_cast<int32_t>(ceil_div(n_tokens, 256) * ceil_div(g->d, 256)) : 0;
-    p.tiles_w = want_w ? static_cast<int32_t>(ceil_div(g->f, 256) * ceil_div(g->d, 256)) : 0;
-    p.n_units = p.tiles_x + 2 * p.tiles_w;
+    // A tile of dX is split when it is longer than a pair's share of the work.
+    const int64_t tiles_x = want_x ? ceil_div(n_tokens, 256) * ceil_div(g->d, 256) : 0;
+    const int64_t tiles_w = want_w ? ceil_div(g->f, 256) * ceil_div(g->d, 256) : 0;
     const int64_t kb_x = 2 * ceil_div(g->f, hk::kKB), kb_w = ceil_div(n_tokens, hk::kKB);
-    p.skip = want_x && want_w ? static_cast<int32_t>((kb_x + kb_w / 2) / kb_w) : 0;
+    const int64_t share = ceil_div(tiles_x * kb_x + 2 * tiles_w * kb_w, g->pairs);
+    p.parts = hk::parts_of(tiles_x, kb_x, g->pairs);
+    if (p.parts > ceil_div(kb_x, share)) p.parts = static_cast<int32_t>(ceil_div(kb_x, share));
+    p.units_x = static_cast<int32_t>(tiles_x * p.parts);
+    p.tiles_w = static_cast<int32_t>(tiles_w);
+    p.n_units = p.units_x + 2 * p.tiles_w;
+    const int64_t kb_unit = kb_x / p.parts;
+    p.skip = want_x && want_w ? static_cast<int32_t>((kb_unit + kb_w / 2) / kb_w) : 0;
     const hess_status st = hk::ff_launch_pairs<hk::kGradients>(g, p, s);
     FF_CHECK(hk::ff_end(g, s));
     return st;
@@ -1108,7 +1244,8 @@ FF_EXPORT hess_status gated_ff_sync(gated_ff_t g, hess_stream_t stream) {
     FF_TRY(cudaMemcpyAsync(&word, g->status, sizeof(word), cudaMemcpyDeviceToHost, s));
     FF_TRY(cudaStreamSynchronize(s));
     if (word == 0) return HESS_OK;
-    FF_TRY(cudaMemsetAsync(g->status, 0, sizeof(word), s));
+    // the arrival counts of an interrupted call go with it
+    FF_TRY(cudaMemsetAsync(g->status, 0, hk::status_bytes(g->pairs), s));
     return ff_fail(HESS_ERR_TIMEOUT, "a device-side wait ran out (status 0x%x); results are invalid", word);
 }
 

@@ -48,7 +48,7 @@ typedef enum {
  *                  multiple of 16 bytes), else HESS_ERR_UNSUPPORTED.
  *   train_tokens : the most tokens a backward call will have (0: forward
  *                  only).  The handle holds 4 * train_tokens * f bytes for dg
- *                  and du; forward needs no workspace.
+ *                  and du, and 19 MB for the sums of tiles that are split.
  *   dtype        : HESS_BF16 or HESS_F16 (HESS_F32: HESS_ERR_UNSUPPORTED).
  * Errors: INVALID, UNSUPPORTED, OOM, CUDA. */
 hess_status gated_ff_create(int64_t d, int64_t f, int64_t train_tokens, int32_t dtype, int32_t act,
@@ -61,8 +61,10 @@ hess_status gated_ff_create(int64_t d, int64_t f, int64_t train_tokens, int32_t 
  *   W_gate, W_up : [f, d] (output channel by input column).  The halves of
  *            one packed [2f, d] matrix will do.
  *   H_out  : [n_tokens, f].
- * Asynchronous on `stream`.  Forward calls may run concurrently on several
- * streams. */
+ * Asynchronous on `stream`.  Calls that split tiles use the handle's workspace
+ * (they have more than 128 tokens): such a call, or a backward call, on another
+ * stream waits for the one before it (an event; during stream capture, use one
+ * stream).  Other forward calls may run concurrently. */
 hess_status gated_ff_forward(gated_ff_t g, const void* X, int64_t n_tokens, const void* W_gate,
                              const void* W_up, void* H_out, hess_stream_t stream);
 
@@ -71,8 +73,7 @@ hess_status gated_ff_forward(gated_ff_t g, const void* X, int64_t n_tokens, cons
  *   dX_out      : [n_tokens, d], or NULL when it is not wanted.
  *   dW_gate_out, dW_up_out : [f, d], or both NULL.  Overwritten; zeros when
  *                 n_tokens is 0.
- * The workspace is the handle's: a call on another stream waits for the call
- * before it (an event; during stream capture, use one stream). */
+ * Uses the handle's workspace (see gated_ff_forward). */
 hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_tokens, const void* W_gate,
                               const void* W_up, const void* dH, void* dX_out, void* dW_gate_out,
                               void* dW_up_out, hess_stream_t stream);
