@@ -56,16 +56,18 @@ constexpr int kFirstEpiWarp = 4;
 constexpr int kThreads = (kFirstEpiWarp + kEpiWarps) * 32;
 constexpr uint32_t kTmemCols = 512;  // two 256-column tiles
 constexpr int kNumBarriers = 2 * kStages + 5;
-constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + 8 * kNumBarriers + 16;
+constexpr uint32_t kOutBytes = 128 * 128;  // 128 rows x 64 columns on their way out, for each half of the epilogue
+constexpr uint32_t kAfterRing = kStages * kStageBytes + 2 * kOutBytes;
+constexpr size_t kSmemBytes = 1024 + kAfterRing + 8 * kNumBarriers + 16;
 constexpr unsigned long long kDrainLimitNs = 1000000000ull;
 constexpr unsigned long long kAbortSettleNs = 2000000ull;
 constexpr int kGroupM = 8;  // row tiles that run side by side (their B boxes meet in L2)
 
-enum { kMapX, kMapWg, kMapWu, kMapDg, kMapDu, kMaps };
+enum { kMapX, kMapWg, kMapWu, kMapDg, kMapDu, kMapOut0, kMapOut1, kMapOut2, kMaps };
 enum { kForward, kActGrad, kGradients };  // what a launch computes
 
 struct FfParams {
-    CUtensorMap maps[kMaps];
+    CUtensorMap maps[kMaps];  // the last three are written: h | dg, du | dX, dWg, dWu
     int32_t n, d, f;
     int32_t act;
     int32_t whole;    // kForward, kActGrad: tiles that are not split; they come first
@@ -75,9 +77,6 @@ struct FfParams {
     int32_t n_units;
     int32_t skip;     // kGradients: turns of dW tiles that one tile of dX is worth
     uint32_t fmt;     // operand format of the instruction descriptor: 0 = f16, 1 = bf16
-    void* out0;       // h | dg | dX
-    void* out1;       // - | du | dWg
-    void* out2;       // - | -  | dWu
     const void* dh;
     float* pieces;      // 256 x 256 sums of every unit of a split tile
     uint32_t* arrived;  // pieces of each split tile that have come, per CTA; zero between launches
@@ -236,49 +235,75 @@ __device__ __forceinline__ void epi_barrier() {
     asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
 }
 
-// Eight consecutive values of one row.
+// 64 columns of 128 rows go out through shared memory and one TMA store, which
+// leaves out what lies past the matrix's edges (each thread storing its row's 16
+// bytes at a time half-fills 32-byte sectors, and a tile of dW with few tokens
+// takes longer to store than to compute).  The four warps of one half of the
+// epilogue share a buffer.
+struct OutBuffer {
+    uint32_t addr;
+    int barrier, row;  // this thread's row
+    bool leader;
+    __device__ void sync() const { asm volatile("bar.sync %0, 128;" ::"r"(barrier) : "memory"); }
+    // the buffer's former content has been read
+    __device__ void begin() const {
+        if (leader) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        sync();
+    }
+    // eight values from column 8 j on, two to a word, in the 128-byte swizzle
+    __device__ void put(int j, uint4 v) const { sts128(addr + row * 128 + ((j ^ (row & 7)) << 4), v); }
+    __device__ void end(const CUtensorMap* map, int x, int y, int cols, int rows) const {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        sync();
+        if (leader && x < cols && y < rows) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                             reinterpret_cast<uint64_t>(map)),
+                         "r"(addr), "r"(x), "r"(y)
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    }
+};
+
 template <class T>
-__device__ __forceinline__ void store8(T* p, const float* x) {
-    uint4 v;
-    v.x = Half2<T>::pack(x[0], x[1]);
-    v.y = Half2<T>::pack(x[2], x[3]);
-    v.z = Half2<T>::pack(x[4], x[5]);
-    v.w = Half2<T>::pack(x[6], x[7]);
-    *reinterpret_cast<uint4*>(p) = v;
+__device__ __forceinline__ uint4 pack8(const float* x) {
+    return make_uint4(Half2<T>::pack(x[0], x[1]), Half2<T>::pack(x[2], x[3]), Half2<T>::pack(x[4], x[5]),
+                      Half2<T>::pack(x[6], x[7]));
 }
 
-// Epilogue of one tile by one warp: its 32 lanes are 32 rows of this CTA's 128
-// (lane quarter warp % 4), and it takes half of the columns, 16 at a time:
-// load(c, a, c2, b) gives the finished sums of columns c.. and c2...
+// Epilogue of one tile by the four warps of one half: rows m.. of this CTA's
+// 128, half of the columns.  load(c, a, c2, b) gives the finished sums of the
+// tile's 16 columns from c on and from c2 on.
 template <class T, int kWhat, class Load>
-__device__ __forceinline__ void finish_tile(const FfParams& p, const Unit& un, int half, int64_t row, Load load) {
+__device__ __forceinline__ void finish_tile(const FfParams& p, const Unit& un, int half, int m, const OutBuffer& out,
+                                            Load load) {
     if constexpr (kWhat != kGradients) {
+        const int64_t row = static_cast<int64_t>(m) + out.row;
         const bool in = row < p.n;
-#pragma unroll 1
-        for (int c = half * 64; c < half * 64 + 64; c += 16) {
-            const int col = un.n0 + c;
+        const int n0 = un.n0 + half * 64;
+        uint4 later[kWhat == kActGrad ? 8 : 1];  // du, until dg has left the buffer
+        out.begin();
+#pragma unroll
+        for (int c = 0; c < 64; c += 16) {
             uint4 dv[2] = {};
             if constexpr (kWhat == kActGrad) {
-                const T* const dh = static_cast<const T*>(p.dh) + row * p.f + col;
-                if (in && col < p.f) dv[0] = *reinterpret_cast<const uint4*>(dh);
-                if (in && col + 8 < p.f) dv[1] = *reinterpret_cast<const uint4*>(dh + 8);
+                const T* const dh = static_cast<const T*>(p.dh) + row * p.f + n0 + c;
+                if (in && n0 + c < p.f) dv[0] = *reinterpret_cast<const uint4*>(dh);
+                if (in && n0 + c + 8 < p.f) dv[1] = *reinterpret_cast<const uint4*>(dh + 8);
             }
             uint32_t g[16], u[16];
-            load(c, g, 128 + c, u);
+            load(half * 64 + c, g, 128 + half * 64 + c, u);
+            float first[16];
             if constexpr (kWhat == kForward) {
-                float h[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     float dz;
                     const float gi = __uint_as_float(g[i]);
-                    h[i] = gi * gate_sigmoid(gi, p.act, dz) * __uint_as_float(u[i]);
+                    first[i] = gi * gate_sigmoid(gi, p.act, dz) * __uint_as_float(u[i]);
                 }
-                T* const out = static_cast<T*>(p.out0) + row * p.f + col;
-                if (in && col < p.f) store8(out, h);
-                if (in && col + 8 < p.f) store8(out + 8, h + 8);
             } else {
                 const uint32_t w[8] = {dv[0].x, dv[0].y, dv[0].z, dv[0].w, dv[1].x, dv[1].y, dv[1].z, dv[1].w};
-                float dg[16], du[16];
+                float du[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float2 d2 = Half2<T>::unpack(w[i / 2]);
@@ -287,36 +312,40 @@ __device__ __forceinline__ void finish_tile(const FfParams& p, const Unit& un, i
                     const float gi = __uint_as_float(g[i]);
                     const float s = gate_sigmoid(gi, p.act, dz);
                     du[i] = dh * (gi * s);
-                    dg[i] = dh * __uint_as_float(u[i]) * fmaf(gi * s * (1.0f - s), dz, s);
+                    first[i] = dh * __uint_as_float(u[i]) * fmaf(gi * s * (1.0f - s), dz, s);
                 }
-                T* const og = static_cast<T*>(p.out0) + row * p.f + col;
-                T* const ou = static_cast<T*>(p.out1) + row * p.f + col;
-                if (in && col < p.f) {
-                    store8(og, dg);
-                    store8(ou, du);
-                }
-                if (in && col + 8 < p.f) {
-                    store8(og + 8, dg + 8);
-                    store8(ou + 8, du + 8);
-                }
+                later[c / 8] = pack8<T>(du);
+                later[c / 8 + 1] = pack8<T>(du + 8);
             }
+            out.put(c / 8, pack8<T>(first));
+            out.put(c / 8 + 1, pack8<T>(first + 8));
+        }
+        out.end(&p.maps[kMapOut0], n0, m, p.f, p.n);
+        if constexpr (kWhat == kActGrad) {
+            out.begin();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) out.put(j, later[j]);
+            out.end(&p.maps[kMapOut1], n0, m, p.f, p.n);
         }
     } else {
-        const bool in = row < (un.kind == 1 ? p.n : p.f);
-        T* const out = static_cast<T*>(un.kind == 1 ? p.out0 : un.which ? p.out2 : p.out1) + row * p.d;
+        const CUtensorMap* const map = &p.maps[un.kind == 1 ? kMapOut0 : un.which ? kMapOut2 : kMapOut1];
 #pragma unroll 1
-        for (int c = half * 128; c < half * 128 + 128; c += 32) {
-            uint32_t a[16], b[16];
-            load(c, a, c + 16, b);
-            float x[32];
+        for (int n = half * 128; n < half * 128 + 128; n += 64) {
+            out.begin();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                x[i] = __uint_as_float(a[i]);
-                x[16 + i] = __uint_as_float(b[i]);
+            for (int c = 0; c < 64; c += 32) {
+                uint32_t a[16], b[16];
+                load(n + c, a, n + c + 16, b);
+                float x[32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    x[i] = __uint_as_float(a[i]);
+                    x[16 + i] = __uint_as_float(b[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) out.put(c / 8 + i, pack8<T>(x + 8 * i));
             }
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-                if (in && un.n0 + c + i < p.d) store8(out + un.n0 + c + i, x + i);
+            out.end(map, un.n0 + n, m, p.d, un.kind == 1 ? p.n : p.f);
         }
     }
 }
@@ -331,8 +360,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* const gbase = smem_raw + (base - raw);
-    const uint32_t bar0 = base + kStages * kStageBytes;
-    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + kStages * kStageBytes + 8 * kNumBarriers);
+    const uint32_t bar0 = base + kAfterRing;
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + kAfterRing + 8 * kNumBarriers);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
     auto accf_bar = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
@@ -483,26 +512,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t aphase = 0;
         const int q = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
         const int r128 = q * 32 + lane;  // row of this CTA's half of the tile
+        const OutBuffer out{base + kStages * kStageBytes + half * kOutBytes, 2 + half, r128, q == 0 && lane == 0};
         const uint32_t acce0 = mapa_shared(acce_bar(0), 0);
         for (int i = 0, u; (u = unit_of<kWhat>(p, pair, n_pairs, i)) >= 0; ++i) {
             const Unit un = unit_at<kWhat>(p, u);
-            failed = failed || !mbar_wait_cluster(accf_bar(ab), aphase, limit);
+            // The warps go on together: each passes every barrier below for every
+            // unit, whether its waits ran out or not.
+            if (failed || !mbar_wait_cluster(accf_bar(ab), aphase, limit)) epi_failed = 1;
+            epi_barrier();
+            failed = epi_failed != 0;
             tc_fence_after();
             const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(ab * 256);
-            const int64_t row = static_cast<int64_t>(un.m0) + static_cast<int>(rank) * 128 + r128;
+            const int m = un.m0 + static_cast<int>(rank) * 128;
             const auto from_tmem = [&](int c, uint32_t (&a)[16], int c2, uint32_t (&b)[16]) {
                 tmem_ld16(acc + c, a);
                 tmem_ld16(acc + c2, b);
                 tmem_wait16(a, b);
             };
             if (un.parts == 1) {
-                if (!failed) finish_tile<T, kWhat>(p, un, half, row, from_tmem);
+                if (!failed) finish_tile<T, kWhat>(p, un, half, m, out, from_tmem);
             } else {
-                // Every epilogue warp passes the four barriers below for every split
-                // unit, whether its waits ran out or not.
-                if (failed) epi_failed = 1;
-                epi_barrier();
-                failed = epi_failed != 0;
                 // one piece after the other: this CTA's half of it in blocks of four
                 // columns, 128 rows of 16 bytes each
                 float* const piece0 = p.pieces + static_cast<int64_t>(un.split) * un.parts * kPieceFloats +
@@ -532,7 +561,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 epi_barrier();
                 if (epi_last) {
                     __threadfence();
-                    finish_tile<T, kWhat>(p, un, half, row, [&](int c, uint32_t (&a)[16], int c2, uint32_t (&b)[16]) {
+                    finish_tile<T, kWhat>(p, un, half, m, out, [&](int c, uint32_t (&a)[16], int c2, uint32_t (&b)[16]) {
                         float x[16] = {}, y[16] = {};
                         for (int k = 0; k < un.parts; ++k) {
                             const float* const piece = piece0 + static_cast<int64_t>(k) * kPieceFloats;
@@ -567,6 +596,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 aphase ^= 1u;
             }
         }
+        if (out.leader) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (failed && lane == 0) {
             atomicOr(p.status, kStatusTimeoutEpilogue);
             aborted = 1;
@@ -923,15 +953,22 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // most one per pair).
 size_t status_bytes(int pairs) { return (1 + 2 * static_cast<size_t>(pairs)) * sizeof(uint32_t); }
 
-// Units a tile of n_kb boxes is split in when `tiles` of them have `pairs` to
-// themselves.  A box takes 512 cycles at the tensor cores' rate, a piece about
-// 2,000 to be read again and 4,000 for the rest: n_kb / s * 512 + 2,000 s is least
-// at s = sqrt(n_kb) / 2, and below 16 boxes there is nothing to gain.
-int32_t parts_of(int64_t tiles, int64_t n_kb, int64_t pairs) {
-    if (tiles <= 0 || n_kb < 16) return 1;
-    int64_t s = 1;
-    while (4 * (s + 1) * (s + 1) <= n_kb + n_kb / 4 && tiles * (s + 1) <= pairs && s < 8) ++s;
-    return static_cast<int32_t>(s);
+// Units to split a tile of n_kb boxes in, when `tiles` of them run side by side
+// and the pairs have `share` boxes of work each in all.  A box takes 512 cycles at
+// the tensor cores' rate; a split costs about as much as 8 boxes for the pieces'
+// way to memory and the pairs' meeting, and 4 for reading each piece again.  It
+// has to promise a fourteenth of the time (129 tokens at 4,096 x 11,008, backward:
+// 163 us unsplit, 129 with dX in 2, 145 in 3; 1,024 at 2,048 x 5,632: 94 unsplit,
+// 102 in 2; 203 at 520 x 1,400: 30.4 unsplit, 27.2 in 3).
+int32_t parts_of(int64_t tiles, int64_t n_kb, int64_t pairs, int64_t share) {
+    const auto cost = [&](int64_t s) {
+        const int64_t longest = ceil_div(n_kb, s);
+        return (longest > share ? longest : share) + (s > 1 ? 8 + 4 * s : 0);
+    };
+    int64_t best = 1;
+    for (int64_t s = 2; s <= 8 && tiles * s <= pairs; ++s)
+        if (14 * cost(s) < 13 * cost(1) && cost(s) < cost(best)) best = s;
+    return static_cast<int32_t>(best);
 }
 
 }  // namespace
@@ -993,7 +1030,7 @@ void ff_params(FfParams& p, const gated_ff_ctx* g, int64_t n) {
 // Units of X times the weights: whole rounds of tiles, then the rest, split.
 void ff_tiles(FfParams& p, const gated_ff_ctx* g) {
     const int64_t tiles = ceil_div(p.n, 256) * ceil_div(g->f, 128), rest = tiles % g->pairs;
-    p.parts = parts_of(rest, ceil_div(g->d, kKB), g->pairs);
+    p.parts = rest > 0 ? parts_of(rest, ceil_div(g->d, kKB), g->pairs, 0) : 1;
     p.whole = static_cast<int32_t>(p.parts > 1 ? tiles - rest : tiles);
     p.n_units = static_cast<int32_t>(p.parts > 1 ? p.whole + rest * p.parts : tiles);
 }
@@ -1157,7 +1194,7 @@ FF_EXPORT hess_status gated_ff_forward(gated_ff_t g, const void* X, int64_t n_to
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapX], X, g->dtype, n_tokens, g->d));
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapWg], W_gate, g->dtype, g->f, g->d));
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapWu], W_up, g->dtype, g->f, g->d));
-    p.out0 = H_out;
+    FF_CHECK(hk::ff_encode(&p.maps[hk::kMapOut0], H_out, g->dtype, n_tokens, g->f, 128));
     hk::ff_tiles(p, g);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p.parts == 1) return hk::ff_launch_pairs<hk::kForward>(g, p, s);
@@ -1209,28 +1246,30 @@ FF_EXPORT hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_t
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapWu], W_up, g->dtype, g->f, g->d));
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapDg], g->dg, g->dtype, n_tokens, g->f));
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapDu], g->du, g->dtype, n_tokens, g->f));
-    FF_CHECK(hk::ff_begin(g, s));
     p.dh = dH;
-    p.out0 = g->dg;
-    p.out1 = g->du;
+    FF_CHECK(hk::ff_encode(&p.maps[hk::kMapOut0], g->dg, g->dtype, n_tokens, g->f, 128));
+    FF_CHECK(hk::ff_encode(&p.maps[hk::kMapOut1], g->du, g->dtype, n_tokens, g->f, 128));
     hk::ff_tiles(p, g);
-    FF_CHECK(hk::ff_launch_pairs<hk::kActGrad>(g, p, s));
-    p.out0 = dX_out;
-    p.out1 = dW_gate_out;
-    p.out2 = dW_up_out;
-    // A tile of dX is split when it is longer than a pair's share of the work.
+    hk::FfParams q = p;  // of the second launch; nothing is enqueued before both are complete
+    if (want_x) FF_CHECK(hk::ff_encode(&q.maps[hk::kMapOut0], dX_out, g->dtype, n_tokens, g->d, 128));
+    if (want_w) {
+        FF_CHECK(hk::ff_encode(&q.maps[hk::kMapOut1], dW_gate_out, g->dtype, g->f, g->d, 128));
+        FF_CHECK(hk::ff_encode(&q.maps[hk::kMapOut2], dW_up_out, g->dtype, g->f, g->d, 128));
+    }
     const int64_t tiles_x = want_x ? ceil_div(n_tokens, 256) * ceil_div(g->d, 256) : 0;
     const int64_t tiles_w = want_w ? ceil_div(g->f, 256) * ceil_div(g->d, 256) : 0;
     const int64_t kb_x = 2 * ceil_div(g->f, hk::kKB), kb_w = ceil_div(n_tokens, hk::kKB);
-    const int64_t share = ceil_div(tiles_x * kb_x + 2 * tiles_w * kb_w, g->pairs);
-    p.parts = hk::parts_of(tiles_x, kb_x, g->pairs);
-    if (p.parts > ceil_div(kb_x, share)) p.parts = static_cast<int32_t>(ceil_div(kb_x, share));
-    p.units_x = static_cast<int32_t>(tiles_x * p.parts);
-    p.tiles_w = static_cast<int32_t>(tiles_w);
-    p.n_units = p.units_x + 2 * p.tiles_w;
-    const int64_t kb_unit = kb_x / p.parts;
-    p.skip = want_x && want_w ? static_cast<int32_t>((kb_unit + kb_w / 2) / kb_w) : 0;
-    const hess_status st = hk::ff_launch_pairs<hk::kGradients>(g, p, s);
+    // in the share of each pair a tile of dW counts at least its write-out, some 10 boxes
+    q.parts = hk::parts_of(tiles_x, kb_x, g->pairs,
+                           ceil_div(tiles_x * kb_x + 2 * tiles_w * (kb_w > 10 ? kb_w : 10), g->pairs));
+    q.units_x = static_cast<int32_t>(tiles_x * q.parts);
+    q.tiles_w = static_cast<int32_t>(tiles_w);
+    q.n_units = q.units_x + 2 * q.tiles_w;
+    const int64_t kb_unit = kb_x / q.parts;
+    q.skip = want_x && want_w ? static_cast<int32_t>((kb_unit + kb_w / 2) / kb_w) : 0;
+    FF_CHECK(hk::ff_begin(g, s));
+    FF_CHECK(hk::ff_launch_pairs<hk::kActGrad>(g, p, s));
+    const hess_status st = hk::ff_launch_pairs<hk::kGradients>(g, q, s);
     FF_CHECK(hk::ff_end(g, s));
     return st;
 }
