@@ -71,6 +71,7 @@ struct DistillArgs {
     int64_t ldd;
     int32_t slice;     // 16-byte granules of a row per CTA, a multiple of kSegment
     int32_t segments;  // of a row, at most
+    int32_t ahead;     // rows in work at a time, about
 };
 
 // ---------------------------------------------------------------- elements
@@ -115,12 +116,6 @@ struct Elem<__nv_bfloat16> {
         }
         return v;
     }
-    static __device__ float max_of(const uint4& v) {
-        __nv_bfloat162 h[4];
-        memcpy(h, &v, 16);
-        const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-        return fmaxf(__low2float(m), __high2float(m));
-    }
 };
 
 template <>
@@ -146,12 +141,6 @@ struct Elem<__half> {
         memcpy(&v, h, 16);
         return v;
     }
-    static __device__ float max_of(const uint4& v) {
-        __half2 h[4];
-        memcpy(h, &v, 16);
-        const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-        return fmaxf(__low2float(m), __high2float(m));
-    }
 };
 
 template <>
@@ -164,11 +153,6 @@ struct Elem<float> {
         uint4 v;
         memcpy(&v, x, 16);
         return v;
-    }
-    static __device__ float max_of(const uint4& v) {
-        float x[4];
-        memcpy(x, &v, 16);
-        return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
     }
 };
 
@@ -234,6 +218,7 @@ struct Pair {
 // 2^(a - b) with b >= a; 0 when a is -inf (whatever b is).
 __device__ __forceinline__ float rescale(float a, float b) { return a == kNegInf ? 0.0f : ex2(a - b); }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
@@ -602,7 +587,7 @@ __device__ __forceinline__ void write_slice(const DistillArgs& a, const RowView<
 
 // Dynamic shared memory: the bits of a slice's listed columns, the sums of the
 // whole row's segments, and kListArrays arrays of `top` words.
-constexpr int kListArrays = 6;
+constexpr int kListArrays = 5;
 __host__ __device__ constexpr size_t align16(size_t n) { return (n + 15) & ~size_t(15); }
 __host__ __device__ constexpr size_t bit_bytes(int slice) { return align16(static_cast<size_t>(slice)); }
 __host__ __device__ constexpr size_t part_bytes(int segments) { return align16(static_cast<size_t>(segments) * 8); }
@@ -618,6 +603,8 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillAr
     extern __shared__ uint4 dyn[];
     __shared__ float w_tm[kMaxWarps], w_mt[kMaxWarps];
     __shared__ int w_flags[kMaxWarps];
+    __shared__ int next_segment;
+    __shared__ ListInfo info;
     const int K = a.top, tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31, n_warps = nt >> 5;
     uint8_t* const base = reinterpret_cast<uint8_t*>(dyn);
     uint32_t* const bits = reinterpret_cast<uint32_t*>(base);
@@ -626,8 +613,7 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillAr
     int* const s_idx = reinterpret_cast<int*>(base + bit_bytes(a.slice) + part_bytes(a.segments));
     float* const s_p = reinterpret_cast<float*>(s_idx) + step;  // p before its normalisation
     float* const s_s = s_p + step;                              // the student's logit
-    float* const s_a = s_s + step;                              // the slot's term of the loss
-    float* const s_lead = s_a + step;                           // the column's p, or -1 where another slot has it
+    float* const s_lead = s_s + step;                           // the column's p, or -1 where another slot has it
     float* const s_exp = s_lead + step;                         // the student's exponential, or -1
 
     uint32_t C;
@@ -638,21 +624,33 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillAr
     const Slice<T> sl(v, a.vocab, static_cast<int>(rank), a.slice, reinterpret_cast<const uint8_t*>(bits));
     T* const out = kGrad ? static_cast<T*>(a.dlogits) + row * a.ldd : nullptr;
     const bool same = kGrad && ((reinterpret_cast<uintptr_t>(out) & 15u) / sizeof(T)) == static_cast<unsigned>(v.off);
-    // the row's scalars and the first entries of its list come together
+    // The row's scalars and the first entries of its list come together, and with
+    // them the list of a row that will be worked on when this one is done, which
+    // then finds it in L2 (loads of DRAM take 2 to 4 us while others stream).
     const float w = a.weights ? a.weights[row] : 1.0f;
     const float lse = kFull ? a.lse[row] : 0.0f;
     const int64_t j_first = tid < K ? load_index(a, row * K + tid) : -1;
     const float t_first = tid < K ? load_top(a, row * K + tid) : kNegInf;
+    const int64_t later = row + a.ahead;
+    uint32_t j_later = 0xffffffffu;
+    if (later < a.rows && tid < K) {
+        const int64_t i = later * K + tid;
+        j_later = static_cast<const uint32_t*>(a.top_index)[a.index_bytes == 8 ? 2 * i : i];
+        prefetch_l2(static_cast<const uint8_t*>(a.top_logits) + i * (a.top_dtype == HESS_F32 ? 4 : 2));
+    }
     for (int i = tid; i < static_cast<int>(bit_bytes(a.slice) / 16); i += nt) dyn[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) next_segment = 0;
+    __syncthreads();
 
-    // ---- the teacher's list, and the student's logits at its columns
+    // ---- the teacher's list, the bits of its columns, and the student's logits there
+    const int j_base = sl.lo * kPer - v.off, j0 = max(j_base, 0), j1 = min(a.vocab, sl.hi * kPer - v.off);
     float tm = kNegInf, mt = kNegInf;
     {
-        bool any = false, bad = false;
+        bool any = false, bad = false, twice = false;
         if (w != 0.0f) {
             // The slice sets out for L2 while the list is worked on (8,192 x
-            // 128,000 bf16: 744 -> 689 us; without the gradient it only gets in the
-            // way of the loads, 300 -> 367 us).
+            // 128,000 bf16: 772 -> 730 us; without the gradient it only gets in the
+            // way of the loads).
             if (kGrad && lane == 0) {
                 const int per = (sl.b - sl.a + n_warps - 1) / n_warps;
                 const int g0 = sl.a + warp * per, g1 = min(sl.b, g0 + per);
@@ -670,6 +668,10 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillAr
                 s_exp[k] = -1.0f;
                 if (in) {
                     const float s = Elem<T>::to_f(v.row[j]);
+                    if (j >= j0 && j < j1) {
+                        const uint32_t bit = static_cast<uint32_t>(static_cast<int>(j) - j_base);
+                        twice |= (atomicOr(bits + (bit >> 5), 1u << (bit & 31u)) >> (bit & 31u) & 1u) != 0;
+                    }
                     s_s[k] = s;
                     tm = fmaxf(tm, t);
                     mt = fmaxf(mt, s);
@@ -681,12 +683,11 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillAr
             tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, o));
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
         }
-        any = __any_sync(0xffffffffu, any);
-        bad = __any_sync(0xffffffffu, bad);
+        const int flags = __reduce_or_sync(0xffffffffu, (any ? 1u : 0u) | (bad ? 2u : 0u) | (twice ? 4u : 0u));
         if (lane == 0) {
             w_tm[warp] = tm;
             w_mt[warp] = mt;
-            w_flags[warp] = (any ? 1 : 0) | (bad ? 2 : 0);
+            w_flags[warp] = flags;
         }
     }
     __syncthreads();
@@ -703,69 +704,70 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillAr
     }
     // the other CTAs may write here from now on (they wait for it below)
     if (C > 1) cluster_arrive();
-    // ---- the list's exponentials, its terms of the loss, and the bits of its columns
-    const int j_base = sl.lo * kPer - v.off, j0 = max(j_base, 0), j1 = min(a.vocab, sl.hi * kPer - v.off);
-    bool twice = false;
-    for (int k = tid; k < K; k += nt) {
-        const int j = s_idx[k];
-        float e = 0.0f, term = 0.0f;
-        if (j >= 0) {
-            const float t = s_p[k], s = s_s[k];
-            e = teacher_exp(a, t, kFull ? lse : tm, kFull);
-            if (e != 0.0f)
-                term = s == kNegInf ? INFINITY : e * fmaf(s, a.k2_slip, fmaf(t - s, a.inv_hi, (t - s) * a.inv_lo));
-            if (j >= j0 && j < j1) {
-                const uint32_t bit = static_cast<uint32_t>(j - j_base);
-                twice |= (atomicOr(bits + (bit >> 5), 1u << (bit & 31u)) >> (bit & 31u) & 1u) != 0;
+    const float m2_top = mt * a.k2;
+    if (warp == n_warps - 1) {
+        // ---- the last warp: p, the list's sums, and the student's exponentials
+        // at the listed columns, while the others begin with the segments
+        ListInfo q{(flags & 2) != 0, w, tm, mt, 0.0f, 0.0f, 1.0f, 0.0f, lse};
+        for (int k = lane; k < K; k += 32) {
+            float e = 0.0f;
+            if (s_idx[k] >= 0) {
+                const float t = s_p[k], s = s_s[k];
+                e = teacher_exp(a, t, kFull ? lse : tm, kFull);
+                if (e != 0.0f)
+                    q.a += s == kNegInf ? INFINITY : e * fmaf(s, a.k2_slip, fmaf(t - s, a.inv_hi, (t - s) * a.inv_lo));
+                float err;
+                q.p_hi = two_sum_f32(q.p_hi, e, err);
+                q.p_lo += err;
+            }
+            s_p[k] = e;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const float h = __shfl_xor_sync(0xffffffffu, q.p_hi, o), l = __shfl_xor_sync(0xffffffffu, q.p_lo, o);
+            q.a += __shfl_xor_sync(0xffffffffu, q.a, o);
+            float e;
+            q.p_hi = two_sum_f32(q.p_hi, h, e);
+            q.p_lo += l + e;
+        }
+        if (!kFull) q.p_inv = 1.0f / (q.p_hi + q.p_lo);
+        if (lane == 0) info = q;
+        __syncwarp();
+    }
+    if (C > 1) cluster_wait();
+    if (warp == n_warps - 1) {
+        // A column's p at its first slot; the others, if it is listed more than
+        // once, stand back.  The exponentials go to every CTA of the cluster.
+        for (int k = lane; k < K; k += 32) {
+            const int j = s_idx[k];
+            if (j < j0 || j >= j1) continue;
+            float p = s_p[k];
+            if (flags & 4) {
+                p = 0.0f;
+                for (int l = 0; l < K && p >= 0.0f; ++l)
+                    if (s_idx[l] == j) p = l < k ? -1.0f : p + s_p[l];
+            }
+            s_lead[k] = p < 0.0f ? p : p * info.p_inv;
+            if (kFull && !(p < 0.0f)) {
+                const float e = m2_top == kNegInf ? 0.0f : ex2(fmaf(s_s[k], a.k2, -m2_top));
+                for (uint32_t r = 0; r < C; ++r) st_cluster_f32(mapa_shared(smem_u32(s_exp + k), r), e);
             }
         }
-        s_p[k] = e;
-        s_a[k] = term;
-    }
-    twice = __syncthreads_or(twice);
-    // every warp takes the list's sums for itself
-    ListInfo info{(flags & 2) != 0, w, tm, mt, 0.0f, 0.0f, 1.0f, 0.0f, lse};
-    for (int k = lane; k < K; k += 32) {
-        float e;
-        info.p_hi = two_sum_f32(info.p_hi, s_p[k], e);
-        info.p_lo += e;
-        info.a += s_a[k];
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const float h = __shfl_xor_sync(0xffffffffu, info.p_hi, o), q = __shfl_xor_sync(0xffffffffu, info.p_lo, o);
-        info.a += __shfl_xor_sync(0xffffffffu, info.a, o);
-        float e;
-        info.p_hi = two_sum_f32(info.p_hi, h, e);
-        info.p_lo += q + e;
-    }
-    if (!kFull) info.p_inv = 1.0f / (info.p_hi + info.p_lo);
-    // A column's p at its first slot; the others, if it is listed more than once,
-    // stand back.  The student's exponentials go to every CTA of the cluster.
-    const float m2_top = mt * a.k2;
-    if (C > 1) cluster_wait();
-    for (int k = tid; k < K; k += nt) {
-        const int j = s_idx[k];
-        if (j < j0 || j >= j1) continue;
-        float p = s_p[k];
-        if (twice) {
-            p = 0.0f;
-            for (int l = 0; l < K && p >= 0.0f; ++l)
-                if (s_idx[l] == j) p = l < k ? -1.0f : p + s_p[l];
-        }
-        s_lead[k] = p < 0.0f ? p : p * info.p_inv;
-        if (kFull && !(p < 0.0f)) {
-            const float e = m2_top == kNegInf ? 0.0f : ex2(fmaf(s_s[k], a.k2, -m2_top));
-            for (uint32_t r = 0; r < C; ++r) st_cluster_f32(mapa_shared(smem_u32(s_exp + k), r), e);
-        }
+        __syncwarp();
     }
 
     // ---- the sums of the slice's segments, which go to every CTA of the cluster
-    for (int g0 = sl.lo + warp * kSegment; g0 < sl.hi; g0 += n_warps * kSegment) {
+    for (;;) {
+        int i = 0;
+        if (lane == 0) i = atomicAdd(&next_segment, 1);
+        const int g0 = sl.lo + __shfl_sync(0xffffffffu, i, 0) * kSegment;
+        if (g0 >= sl.hi) break;
         const float2 q = segment<T, kFull, kGrad>(v, sl, a.vocab, g0, a.k2, m2_top);
         if (lane < static_cast<int>(C))
             st_cluster_f32x2(mapa_shared(smem_u32(part + g0 / kSegment), lane), q.x, q.y);
     }
+    if (j_later < static_cast<uint32_t>(a.vocab))
+        prefetch_l2(static_cast<const T*>(a.logits) + later * a.ld + j_later);
     if (C == 1)
         __syncthreads();
     else
@@ -1040,6 +1042,7 @@ hess_status launch_typed(DistillArgs& a, int sms, cudaStream_t s) {
         // not reached: the widest vocabulary in f32, 8 CTAs and the longest list take 217 KB
         return ds_fail(HESS_ERR_UNSUPPORTED, "vocab %d is too wide for the bits of its columns", a.vocab);
     a.slice = slice_at(C);
+    a.ahead = static_cast<int32_t>(room / (int64_t(C) * threads));
     const size_t smem = dynamic_bytes(a.slice, a.segments, a.top);
     auto fn = a.lse ? distill_kernel<T, kGrad, true> : distill_kernel<T, kGrad, false>;
     cudaLaunchConfig_t cfg = {};
