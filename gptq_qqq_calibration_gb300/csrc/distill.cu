@@ -1032,12 +1032,17 @@ hess_status launch_typed(DistillArgs& a, int sms, cudaStream_t s) {
                                dynamic_bytes(slice_at(C), a.segments, a.top) > kMaxDynamic))
         C *= 2;
     int threads = kGrad ? (slice_at(C) > 4224 ? 512 : slice_at(C) > 2112 ? 256 : 128) : slice_at(C) > 8448 ? 256 : 128;
-    // Few rows: more CTAs for each while half of the threads would be idle; smaller
-    // ones when they would come to between one wave and two (301 x 50,257 f32 with
-    // gradient: 34.9 us with 2 CTAs of 256 threads a row, 40.4 with 2 of 512).
+    // Few rows: more CTAs for each while half of the threads would be idle; and
+    // smaller ones where one wave of them then does for two (301 x 50,257 f32 with
+    // gradient, 2 CTAs a row: 29.6 us with 384 threads, 40 with 512; from three
+    // waves to two it is a loss, 512 x 128,000 bf16: 65 against 60 us).
     const int64_t room = int64_t(1536) * sms;
     while (C < kMaxCluster && 2 * a.rows * C * threads <= room && granules >= 512 * C) C *= 2;
-    if (threads > 128 && a.rows * C * threads > room && a.rows * C * threads <= 2 * room) threads /= 2;
+    const int64_t ctas = a.rows * C, slots = int64_t(1536 / threads) * sms;
+    if (ctas > slots && ctas <= 2 * slots) {
+        const int64_t t = 1536 / ((ctas + sms - 1) / sms) / 32 * 32;
+        if (t >= 128 && 2 * t >= threads) threads = static_cast<int>(t);
+    }
     if (dynamic_bytes(slice_at(C), a.segments, a.top) > kMaxDynamic)
         // not reached: the widest vocabulary in f32, 8 CTAs and the longest list take 217 KB
         return ds_fail(HESS_ERR_UNSUPPORTED, "vocab %d is too wide for the bits of its columns", a.vocab);
