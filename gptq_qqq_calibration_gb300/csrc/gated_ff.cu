@@ -623,22 +623,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // Up to kFewTokens tokens the work is reading the weights once (4 d f bytes for
 // 4 n d f operations: memory-bound below some 280 tokens), so the roles turn:
 // weight rows are the MMA's rows (R of Wg and the same R of Wu in one operand),
-// tokens its columns (N = n rounded up to 16), and one CTA per SM streams its
-// rows through a ring of up to 192 KB.  R is any number up to 64, chosen so that
-// every SM gets the same number of rows (37 at f = 11,008: 298 tiles, two per
-// SM; tiles of 64 would be 172, one or two per SM), which needs no split of the
-// sums.  The operand's unused rows hold what they hold: an MMA row only reaches
-// its own tensor-memory lane.
+// tokens its columns (N = n rounded up to 16), and each CTA streams its rows
+// through a ring of shared memory.  R is any number up to 64, chosen so that every
+// SM gets the same number of rows (37 at f = 11,008: 298 tiles; tiles of 64 would
+// be 172, one or two per SM), which needs no split of the sums.  The operand's
+// unused rows hold what they hold: an MMA row only reaches its own tensor-memory
+// lane.
+//
+// One CTA per SM with a ring of 192 KB, or two with 92 KB where that gives each
+// one tile instead of two: they fill each other's start and end, and the next
+// launch's first CTAs find room early (one token, 4,096 x 11,008: 33.4 us with one
+// CTA per SM, 29.1 with two, 92 % of the weights' bytes at the copy rate; 2,560 x
+// 6,912, one tile per SM either way: 14.3 and 14.9 us; 8,192 x 28,672: 137 and 155).
 
 constexpr int kFewTokens = 128;
-constexpr uint32_t kFewRing = 192 * 1024;
+constexpr uint32_t kFewRing = 192 * 1024, kFewRing2 = 92 * 1024;
 constexpr int kFewMaxStages = 16;
 constexpr int kFewThreads = 256;  // warps 0: copies, 1: MMAs, 4-7: epilogue
 constexpr int kFewNumBarriers = 2 * kFewMaxStages + 5;
-constexpr uint32_t kFewExchange = 2 * 2 * 16 * 64 * 4;  // two buffers of g and u: 16 tokens x 64 rows
-// an operand of few rows is still read as 128: the ring has room for it at its end
-constexpr uint32_t kFewTail = 128 * 128;
-constexpr size_t kFewSmem = 1024 + kFewRing + kFewTail + kFewExchange + 8 * kFewNumBarriers + 16;
+// two buffers of g and u: 16 tokens x 64 rows.  It follows the ring: an operand of
+// few rows at the ring's end, which is read as 128 rows all the same, ends in it.
+constexpr uint32_t kFewExchange = 2 * 2 * 16 * 64 * 4;
+static_assert(kFewExchange >= 128 * 128, "the last operand's 128 rows end in the exchange buffers");
+constexpr size_t few_smem(uint32_t ring) { return 1024 + ring + kFewExchange + 8 * kFewNumBarriers + 16; }
 
 struct FewParams {
     CUtensorMap maps[3];  // kMapX: n_cols-row boxes; kMapWg, kMapWu: R-row boxes
@@ -648,6 +655,7 @@ struct FewParams {
     int32_t rows8;        // R rounded up to 8: where Wu's rows begin in the operand
     int32_t stages;
     int32_t stage_bytes;
+    uint32_t ring;        // bytes
     int32_t n_kb;         // boxes along d
     int32_t n_tiles;      // ceil(f / R)
     uint32_t fmt;
@@ -657,15 +665,14 @@ struct FewParams {
 };
 
 template <class T>
-__global__ void __launch_bounds__(kFewThreads, 1) gated_ff_few_kernel(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(kFewThreads, 2) gated_ff_few_kernel(const __grid_constant__ FewParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* const gbase = smem_raw + (base - raw);
-    constexpr uint32_t kAfter = kFewRing + kFewTail;
-    float* const exch = reinterpret_cast<float*>(gbase + kAfter);
-    const uint32_t bar0 = base + kAfter + kFewExchange;
-    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + kAfter + kFewExchange + 8 * kFewNumBarriers);
+    float* const exch = reinterpret_cast<float*>(gbase + p.ring);
+    const uint32_t bar0 = base + p.ring + kFewExchange;
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + p.ring + kFewExchange + 8 * kFewNumBarriers);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (kFewMaxStages + s); };
     auto accf_bar = [&](int b) { return bar0 + 8u * (2 * kFewMaxStages + b); };
@@ -926,7 +933,7 @@ hess_status ff_prepare(int dev, int* pairs, int* sms_out) {
             FF_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         static_cast<int>(kSmemBytes)));
         for (auto fn : {gated_ff_few_kernel<__nv_bfloat16>, gated_ff_few_kernel<__half>})
-            FF_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kFewSmem)));
+            FF_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(few_smem(kFewRing))));
         int sms = 0;
         FF_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
         sm_count[dev] = sms;
@@ -980,8 +987,9 @@ struct gated_ff_ctx {
     int pairs = 0, sms = 0;
     int64_t d = 0, f = 0, train_tokens = 0;
     int32_t dtype = 0, act = 0;
+    void* memory = nullptr;   // holds the next four
     float* pieces = nullptr;  // one per pair
-    void* dg = nullptr;  // [train_tokens, f] each
+    void* dg = nullptr;       // [train_tokens, f] each
     void* du = nullptr;
     uint32_t* status = nullptr;
     cudaEvent_t ev = nullptr;  // the workspace's last user
@@ -1079,10 +1087,14 @@ hess_status ff_forward_few(const gated_ff_ctx* g, const void* X, int64_t n, cons
     p.f = static_cast<int32_t>(g->f);
     p.act = g->act;
     p.n_cols = static_cast<int32_t>(ceil_div(n, 16) * 16);
-    // the fewest rows on the SM that has most (counted as tiles of R), then the fewest tiles
+    // two CTAs per SM where one would have two tiles, and the ring still holds enough of them
+    const bool two = n <= 64 && g->f > int64_t(64) * g->sms && g->f <= int64_t(128) * g->sms;
+    const int64_t ctas = two ? 2 * g->sms : g->sms;
+    p.ring = two ? kFewRing2 : kFewRing;
+    // the fewest rows on the CTA that has most (counted as tiles of R), then the fewest tiles
     int64_t best = 0;
     for (int64_t R = 8; R <= 64; ++R) {
-        const int64_t most = ceil_div(ceil_div(g->f, R), g->sms) * R;
+        const int64_t most = ceil_div(ceil_div(g->f, R), ctas) * R;
         if (best == 0 || most <= best) {
             best = most;
             p.rows = static_cast<int32_t>(R);
@@ -1091,7 +1103,7 @@ hess_status ff_forward_few(const gated_ff_ctx* g, const void* X, int64_t n, cons
     p.rows8 = (p.rows + 7) / 8 * 8;
     p.stage_bytes = 128 * p.n_cols + 256 * p.rows8;
     p.stage_bytes = (p.stage_bytes + 1023) / 1024 * 1024;
-    const int fit = static_cast<int>(kFewRing) / p.stage_bytes;
+    const int fit = static_cast<int>(p.ring) / p.stage_bytes;
     p.stages = fit < kFewMaxStages ? fit : kFewMaxStages;
     p.n_kb = static_cast<int32_t>(ceil_div(g->d, kKB));
     p.n_tiles = static_cast<int32_t>(ceil_div(g->f, p.rows));
@@ -1103,7 +1115,7 @@ hess_status ff_forward_few(const gated_ff_ctx* g, const void* X, int64_t n, cons
     FF_CHECK(ff_encode(&p.maps[kMapWg], Wg, g->dtype, g->f, g->d, static_cast<uint32_t>(p.rows)));
     FF_CHECK(ff_encode(&p.maps[kMapWu], Wu, g->dtype, g->f, g->d, static_cast<uint32_t>(p.rows)));
     return ff_launch(g->dtype == HESS_BF16 ? gated_ff_few_kernel<__nv_bfloat16> : gated_ff_few_kernel<__half>, p,
-                     p.n_tiles < g->sms ? p.n_tiles : g->sms, kFewThreads, kFewSmem, s);
+                     p.n_tiles < ctas ? p.n_tiles : ctas, kFewThreads, few_smem(p.ring), s);
 }
 
 hess_status ff_tokens(int64_t n) {
@@ -1113,10 +1125,7 @@ hess_status ff_tokens(int64_t n) {
 }
 
 void ff_free(gated_ff_ctx* g) {
-    cudaFree(g->dg);
-    cudaFree(g->du);
-    cudaFree(g->pieces);
-    cudaFree(g->status);
+    cudaFree(g->memory);
     if (g->ev) cudaEventDestroy(g->ev);
 }
 
@@ -1155,13 +1164,18 @@ FF_EXPORT hess_status gated_ff_create(int64_t d, int64_t f, int64_t train_tokens
     g->train_tokens = train_tokens;
     g->dtype = dtype;
     g->act = act;
-    const size_t bytes = static_cast<size_t>(train_tokens) * static_cast<size_t>(f) * 2;
-    cudaError_t e = cudaMalloc(&g->status, hk::status_bytes(pairs));
-    if (e == cudaSuccess) e = cudaMemset(g->status, 0, hk::status_bytes(pairs));
-    if (e == cudaSuccess)
-        e = cudaMalloc(&g->pieces, static_cast<size_t>(pairs) * hk::kPieceFloats * sizeof(float));
-    if (e == cudaSuccess && bytes) e = cudaMalloc(&g->dg, bytes);
-    if (e == cudaSuccess && bytes) e = cudaMalloc(&g->du, bytes);
+    // one allocation: the split tiles' pieces, dg and du, the status word and the counts
+    const size_t pieces = static_cast<size_t>(pairs) * hk::kPieceFloats * sizeof(float);
+    const size_t half = (static_cast<size_t>(train_tokens) * static_cast<size_t>(f) * 2 + 255) / 256 * 256;
+    cudaError_t e = cudaMalloc(&g->memory, pieces + 2 * half + hk::status_bytes(pairs));
+    if (e == cudaSuccess) {
+        uint8_t* const m = static_cast<uint8_t*>(g->memory);
+        g->pieces = reinterpret_cast<float*>(m);
+        g->dg = m + pieces;
+        g->du = m + pieces + half;
+        g->status = reinterpret_cast<uint32_t*>(m + pieces + 2 * half);
+        e = cudaMemset(g->status, 0, hk::status_bytes(pairs));
+    }
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&g->ev, cudaEventDisableTiming);
     if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
     if (e != cudaSuccess) {

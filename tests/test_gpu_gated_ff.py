@@ -115,6 +115,17 @@ def test_few_tokens(n):
     op.sync()
 
 
+@pytest.mark.parametrize("n", [1, 17, 64, 65])
+def test_few_tokens_wide(n):
+    """A width that gives each SM two CTAs (up to 64 tokens), and one (above)."""
+    from gptq_qqq_calibration_gb300 import GatedFF
+    d, f = 136, 11008
+    x, wg, wu, dh = make(n, d, f, torch.bfloat16, 90 + n)
+    op = GatedFF(d, f)
+    check(op.forward(x.cuda(), wg.cuda(), wu.cuda()), reference(x, wg, wu, dh, "silu")["h"], torch.bfloat16)
+    op.sync()
+
+
 def test_many_tiles_and_repeatability():
     """More tiles than SM pairs in every contraction; the same bits each time."""
     from gptq_qqq_calibration_gb300 import GatedFF
