@@ -1016,22 +1016,32 @@ template <class T, bool kGrad>
 hess_status launch_typed(DistillArgs& a, int sms, cudaStream_t s) {
     constexpr int per = Elem<T>::kPer;
     const int granules = static_cast<int>((static_cast<int64_t>(a.vocab) + 2 * (per - 1)) / per);
-    // CTAs per row and threads per CTA (an SM holds 1,536 threads; bf16 rows with
-    // an eighth without weight, in steady state).
-    // With the gradient a slice is at most 132 KB: what is in flight, 64 MB then, is
-    // still in L2 when it is read again (8,192 x 128,000: 730 us in 2 slices, 902 in
-    // one, 919 in 4).  About 16 loads a thread (8,192 x 32,000: 181 us with 256
-    // threads, 219 with 512, 240 with 128).
+    // CTAs per row and threads per CTA (an SM holds 1,536 threads; figures: bf16
+    // rows with an eighth without weight, in steady state).
+    // With the gradient the slices in flight should fill L2 and no more, 72 MB: they
+    // are read again from there.  One CTA a row while its 512 threads keep to that,
+    // else twice the fewest that do, and as few threads as do (8,192 x 128,000: 687
+    // us with 4 CTAs of 256 threads a row, 707 with 2 of 512, 805 with 2 of 384,
+    // 902 with 1 of 512; 4,096 x 100,000: 290 us with 4 of 192, 318 with 2 of 512;
+    // 4,096 x 65,536: 184 us with 1 of 512, 198 with 2 of 256).
     // Without it one CTA, and small ones, which hide each other's start (8,192 x
     // 128,000: 273 us with 256 threads, 298 with 512, 315 with 128; 4,096 x 65,536:
     // 74 us with 128, 79 with 256, 99 with 512).
     a.segments = (granules + kSegment - 1) / kSegment;
     const auto slice_at = [&](int c) { return (a.segments + c - 1) / c * kSegment; };
-    int C = 1;
-    while (C < kMaxCluster && ((kGrad && slice_at(C) > 8448) ||
-                               dynamic_bytes(slice_at(C), a.segments, a.top) > kMaxDynamic))
-        C *= 2;
-    int threads = kGrad ? (slice_at(C) > 4224 ? 512 : slice_at(C) > 2112 ? 256 : 128) : slice_at(C) > 8448 ? 256 : 128;
+    const auto fits = [&](int c) { return dynamic_bytes(slice_at(c), a.segments, a.top) <= kMaxDynamic; };
+    const double in_flight = 72e6;
+    int C = 1, threads = slice_at(1) > 8448 ? 256 : 128;
+    if (kGrad) {
+        while (C < kMaxCluster && 3.0 * sms * 16.0 * slice_at(C) > in_flight) C *= 2;
+        if (C > 1 && C < kMaxCluster) C *= 2;
+        int per_sm = 12;  // CTAs of floor(1536 / per_sm) threads, where that is just how many fit
+        while (per_sm > 3 && (per_sm * (16.0 * sms) * slice_at(C) > in_flight ||
+                              1536 / (1536 / per_sm / 32 * 32) != per_sm))
+            --per_sm;
+        threads = 1536 / per_sm / 32 * 32;
+    }
+    while (C < kMaxCluster && !fits(C)) C *= 2;
     // Few rows: more CTAs for each while half of the threads would be idle; and
     // smaller ones where one wave of them then does for two (301 x 50,257 f32 with
     // gradient, 2 CTAs a row: 29.6 us with 384 threads, 40 with 512; from three
@@ -1043,8 +1053,8 @@ hess_status launch_typed(DistillArgs& a, int sms, cudaStream_t s) {
         const int64_t t = 1536 / ((ctas + sms - 1) / sms) / 32 * 32;
         if (t >= 128 && 2 * t >= threads) threads = static_cast<int>(t);
     }
-    if (dynamic_bytes(slice_at(C), a.segments, a.top) > kMaxDynamic)
-        // not reached: the widest vocabulary in f32, 8 CTAs and the longest list take 217 KB
+    // not reached: the widest vocabulary in f32, 8 CTAs and the longest list take 217 KB
+    if (!fits(C))
         return ds_fail(HESS_ERR_UNSUPPORTED, "vocab %d is too wide for the bits of its columns", a.vocab);
     a.slice = slice_at(C);
     a.ahead = static_cast<int32_t>(room / (int64_t(C) * threads));
