@@ -4,17 +4,19 @@
 // The work is a stream over the student's logits: read them once, write the
 // gradient once, a few operations per element.  The loss needs a row's sum of
 // exponentials before the first gradient can be written, so the logits are
-// needed twice: a CTA (a cluster of CTAs, when there are few rows) takes one
-// row, sums it straight from memory, and reads it again, from L2, for the
-// gradient.  The L2 holds what is in flight (58 MB: launch_typed) as long as
-// the gradient's stores leave it first, which they are marked to do.  What bounds
-// it is memory: 8,192 rows of 128,000 bf16 logits (an eighth without weight) take
-// 689 us for the loss and the gradient, 84 % of the rate of a copy of the bytes
-// it cannot do without, and 300 us for the loss alone, 90 %.  What is left are
-// the dependent loads at a row's start, 4 to 5 us that only other CTAs hide.
-// Keeping the rows in shared memory instead (a cluster per row, bulk copies, a
-// warp for each list) was built too: its phases wait for one another inside
-// each SM, and the same step took it 821 us.
+// needed twice: a CTA (or a cluster of CTAs) takes one row, sums it straight from
+// memory, and reads it again, from L2, for the gradient.  The L2 holds what is in
+// flight (launch_typed) as long as the gradient's stores leave it first, which
+// they are marked to do.
+//
+// Memory bounds it.  8,192 rows of 128,000 bf16 logits, an eighth of them without
+// weight: the loss alone takes 262 us, the rate of a copy of the bytes it reads;
+// loss and gradient 688 us, 83 % of that rate (ncu: 5.2 TB/s, a tenth of the
+// logits read twice); the gradient from saved statistics 604 us, 95 %.  What the
+// step lacks is the start of a row, two loads of DRAM one after the other, and the
+// meeting of its warps, which only other CTAs hide.  Keeping the rows in shared
+// memory instead (a cluster per row, bulk copies, a warp for each list) was built
+// too: its phases wait for one another inside each SM, and the step took 821 us.
 //
 // Exponentials are 2^(s k2 - M2) with k2 = log2(e) / tau and M2 = max(s) k2,
 // one FMA and one ex2 per element.  The listed columns are left out of the

@@ -28,6 +28,14 @@
 // way it is contiguous: boxes stacked in shared memory serve both the K-major
 // and the MN-major descriptors, and one tensor map per matrix is enough.
 // Edges cost nothing: the copies fill zeros past the end of a matrix.
+//
+// The tensor cores bound it, and under long loads the board's power: 8,192 tokens
+// at 4,096 x 11,008 forward take 844 us (1,750 TFLOP/s, 0.92 of the burst rate of a
+// library GEMM), the gradients of 4,096 tokens 1,310 to 1,350 us (1,640 to 1,690).
+// ncu (2,048 tokens): tensor pipe 85 % active forward, 94 % in the gradients'
+// kernel.  Below some 600 tokens the weights and their gradients are what takes
+// time (4 d f bytes each): 256 tokens forward 48 us for 28 us of bytes, as the 86
+// tiles of one row of tiles fill the 76 pairs once and an eighth.
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
