@@ -25,7 +25,11 @@
 // reference of its own.  With S_o, M2o of the other columns and S, M2 of the whole row:
 //     q_j = 2^(s_j k2 - M2) / S
 //     d loss / d s_j = w tau 2^(s_j k2 - M2o) (2^(M2o - M2) / S - p_r / S_o)
-// for columns outside the list, w tau (q_j - p_j) for those in it.
+// for columns outside the list, w tau (q_j - p_j) for those in it.  Where the list
+// holds at most half of either mass, P of the teacher's and Q of the student's, both
+// are nearly one outside it, and their roundings would outweigh what differs; there
+// the same is taken from the masses inside:
+//     log(p_r / q_r) = log1p(-P) - log1p(-Q),    1 / S - p_r / S_o = (P - Q) / S_o
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -442,6 +446,8 @@ struct RowSums {
     float m2o, s_o;       // of the columns outside the list (with kFull; else the same)
     float ref_o, B;       // gradient outside the list: w tau B 2^(s k2 - ref_o)
     float p_r;            // the teacher's mass outside its list
+    float Q;              // the student's mass inside the list
+    bool small;           // the list holds at most half of either mass
 };
 // part: (reference, sum) of every segment; s_exp, with kFull: the student's
 // exponential of every listed column, -1 for a slot that stands for none.
@@ -458,7 +464,8 @@ __device__ __forceinline__ RowSums row_sums(const DistillArgs& a, const ListInfo
     r.s_o = warp_reduce(r.s_o, AddOp());
     r.M2 = r.m2o;
     r.S = r.s_o;
-    r.p_r = 0.0f;
+    r.p_r = r.Q = 0.0f;
+    r.small = false;
     float f_o = 1.0f;
     if (kFull) {
         float s_t = 0.0f;
@@ -473,14 +480,20 @@ __device__ __forceinline__ RowSums row_sums(const DistillArgs& a, const ListInfo
         const float m2_top = info.m_top * a.k2;
         r.M2 = fmaxf(r.m2o, m2_top);
         f_o = rescale(r.m2o, r.M2);
-        r.S = r.s_o * f_o + s_t * rescale(m2_top, r.M2);
+        s_t *= rescale(m2_top, r.M2);
+        r.S = r.s_o * f_o + s_t;
+        r.Q = s_t / r.S;
         r.p_r = (1.0f - info.p_hi) - info.p_lo;
         // none where the list names every column
         if (r.p_r < 0.0f || listed >= a.vocab) r.p_r = 0.0f;
+        r.small = r.p_r >= 0.5f && r.Q <= 0.5f;
     }
     r.inv_S = info.bad ? NAN : 1.0f / r.S;
     r.B = f_o * r.inv_S;
-    if (r.p_r > 0.0f && r.s_o > 0.0f) r.B -= r.p_r / r.s_o;
+    if (r.small)
+        r.B = (info.p_hi - r.Q + info.p_lo) / r.s_o + (info.bad ? NAN : 0.0f);
+    else if (r.p_r > 0.0f && r.s_o > 0.0f)
+        r.B -= r.p_r / r.s_o;
     r.ref_o = r.m2o == kNegInf ? 0.0f : r.m2o;
     return r;
 }
@@ -509,7 +522,9 @@ __device__ __forceinline__ float row_loss(const DistillArgs& a, const ListInfo& 
         L.add(info.a);
         L.add_product(info.p_hi, d.hi);
         L.lo += info.p_hi * d.lo + info.p_lo * d.hi;
-        if (r.p_r != 0.0f) {
+        if (r.small) {
+            L.add(r.p_r * (log1pf(-(info.p_hi + info.p_lo)) - log1pf(-r.Q)));
+        } else if (r.p_r != 0.0f) {
             Pair g = ln_sum;
             g.add_ln2(-r.m2o);
             g.add_log(r.s_o, -1.0f);

@@ -146,6 +146,39 @@ def test_masked_rows_and_empty_slots(dtype):
             assert float(loss[r]) == 0.0 and not d[r].any() and not d2[r].any()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("rows,vocab,top,tau,scale", [(6, 62652, 7, 3.0, 0.5), (5, 33001, 3, 1.0, 0.3),
+                                                      (4, 9000, 40, 2.0, 1.0), (3, 140001, 16, 4.0, 2.0)])
+def test_little_mass_in_the_list(rows, vocab, top, tau, scale, dtype):
+    """Loss and gradients are small against the masses outside the list, which are
+    nearly one on both sides: they keep the accuracy of the masses P and Q in it.
+
+    Bounds, with eps as above: p and q of listed columns have relative errors of eps.
+    The loss is sum p log(p / q) + (1 - P) (log1p(-P) - log1p(-Q)), whose derivatives
+    by the listed p and q are at most |log(p / q)| + 1 + |log((1 - P) / (1 - Q))| and
+    p / q + 1 / (1 - Q): errors of eps (P (3 + max |log(p / q)|) + 2 Q).  Outside the
+    list the gradient is w tau (P - Q) q / q_rest: eps 2 (P + Q) q / q_rest.
+    """
+    s, v, i, t = make(rows, vocab, top, dtype, vocab + top, scale)
+    lse = torch.logsumexp(t / tau, 1).float()
+    loss, d1, d2 = run_all(s, v, i, tau, lse)
+    for r in range(rows):
+        o = distill_row(s[r].double().numpy(), v[r].double().numpy(), i[r].numpy(), tau, float(lse[r]))
+        inside = o["listed"]
+        P, Q = o["p"][inside].sum(), o["q"][inside].sum()
+        assert P < 0.5 and Q < 0.5
+        eps = 1e-6 * (2 + max(s[r].float().abs().max().item(), v[r].abs().max().item()) / tau)
+        ratio = np.abs(np.log(o["p"][inside] / o["q"][inside])).max()
+        tol = tau ** 2 * eps * (P * (3 + ratio) + 2 * Q) + 2.0 ** -22 * abs(o["loss"])
+        assert abs(float(loss[r]) - o["loss"]) <= tol, (r, float(loss[r]), o["loss"], tol)
+        ref = o["grad"]
+        tol = tau * eps * np.where(inside, o["q"] + o["p"], 2 * (P + Q) * o["q"] / o["q_rest"])
+        tol = tol + ULP[dtype] * np.abs(ref) * 1.01 + TINY[dtype]
+        for d in (d1, d2):
+            bad = ~(np.abs(d[r].double().numpy() - ref) <= tol)
+            assert not bad.any(), (r, np.flatnonzero(bad)[:5], d[r][torch.from_numpy(bad)][:5], ref[bad][:5], tol[bad][:5])
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_infinite_and_nan_logits(dtype):
     """-inf columns (a padded vocabulary) carry no probability; a column the
