@@ -1063,16 +1063,16 @@ hess_status launch_typed(DistillArgs& a, int sms, cudaStream_t s) {
     // smaller ones where one wave of them then does for two (301 x 50,257 f32 with
     // gradient, 2 CTAs a row: 29.6 us with 384 threads, 40 with 512; from three
     // waves to two it is a loss, 512 x 128,000 bf16: 65 against 60 us).  Not where
-    // a thread would walk more than 100 granules: the last rows then run alone on
-    // too few threads to keep HBM busy (loss; 83 granules, 1,200 x 128,000 bf16: 45
-    // us against 57 in two waves; but 184, 1,471 x 94,364 f32: 128 against 82; 123,
-    // 1,000 x 94,364 f32: 75 against 54; 125, 1,800 x 128,000 bf16: 78 against 69).
+    // a thread would walk more than 110 granules: too few loads are then in flight
+    // (the loss, one wave against two; 87 granules, 1,150 x 128,000 bf16: 45 and 55
+    // us; 104, 1,350 rows of it: 52 and 60; 100, 1,500 x 50,257 f32: 46 and 49; but
+    // 130, 1,700 x 128,000 bf16: 82 and 67; 124, 1,150 x 94,364 f32: 87 and 75).
     const int64_t room = int64_t(1536) * sms;
     while (C < kMaxCluster && 2 * a.rows * C * threads <= room && granules >= 512 * C) C *= 2;
     const int64_t ctas = a.rows * C, slots = int64_t(1536 / threads) * sms;
     if (ctas > slots && ctas <= 2 * slots) {
         const int64_t t = 1536 / ((ctas + sms - 1) / sms) / 32 * 32;
-        if (t >= 128 && 2 * t >= threads && slice_at(C) <= 100 * t) threads = static_cast<int>(t);
+        if (t >= 128 && 2 * t >= threads && slice_at(C) <= 110 * t) threads = static_cast<int>(t);
     }
     // not reached: the widest vocabulary in f32, 8 CTAs and the longest list take 217 KB
     if (!fits(C))
