@@ -50,6 +50,7 @@
 #include "gated_ff.h"
 #include "kernels.cuh"
 #include "ptx.cuh"
+#include "workspace_order.h"
 
 namespace hk {
 namespace {
@@ -1000,9 +1001,7 @@ struct gated_ff_ctx {
     void* dg = nullptr;       // [train_tokens, f] each
     void* du = nullptr;
     uint32_t* status = nullptr;
-    cudaEvent_t ev = nullptr;  // the workspace's last user
-    cudaStream_t last = nullptr;
-    bool used = false;
+    hk::WorkspaceOrder order;  // of the calls that use that memory
     unsigned long long timeout_ns = 2000000000ull;
 };
 
@@ -1078,13 +1077,11 @@ hess_status ff_launch_pairs(const gated_ff_ctx* g, const FfParams& p, cudaStream
 
 // The handle's workspace has one user at a time.
 hess_status ff_begin(gated_ff_ctx* g, cudaStream_t s) {
-    if (g->used && g->last != s) FF_TRY(cudaStreamWaitEvent(s, g->ev, 0));
+    FF_TRY(g->order.begin(s));
     return HESS_OK;
 }
 hess_status ff_end(gated_ff_ctx* g, cudaStream_t s) {
-    FF_TRY(cudaEventRecord(g->ev, s));
-    g->last = s;
-    g->used = true;
+    FF_TRY(g->order.end(s));
     return HESS_OK;
 }
 
@@ -1134,7 +1131,7 @@ hess_status ff_tokens(int64_t n) {
 
 void ff_free(gated_ff_ctx* g) {
     cudaFree(g->memory);
-    if (g->ev) cudaEventDestroy(g->ev);
+    g->order.destroy();
 }
 
 }  // namespace
@@ -1184,7 +1181,7 @@ FF_EXPORT hess_status gated_ff_create(int64_t d, int64_t f, int64_t train_tokens
         g->status = reinterpret_cast<uint32_t*>(m + pieces + 2 * half);
         e = cudaMemset(g->status, 0, hk::status_bytes(pairs));
     }
-    if (e == cudaSuccess) e = cudaEventCreateWithFlags(&g->ev, cudaEventDisableTiming);
+    if (e == cudaSuccess) e = g->order.create();
     if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
     if (e != cudaSuccess) {
         const hess_status s = e == cudaErrorMemoryAllocation ? HESS_ERR_OOM : HESS_ERR_CUDA;

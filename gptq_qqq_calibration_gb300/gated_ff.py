@@ -89,6 +89,10 @@ class GatedFF:
     serves every layer of these widths.  ``train_tokens`` is the most tokens a
     backward call will have (its workspace is 4 f bytes a token).  Called as a
     function, the object is a node of an autograd graph.
+
+    The object's calls may come on any streams, and may be captured into CUDA
+    graphs.  Replays of such graphs are the caller's to order, with each other
+    and with the object's other calls: they share its workspace.
     """
 
     def __init__(self, d: int, f: int, train_tokens: int = 0, dtype: torch.dtype = torch.bfloat16,

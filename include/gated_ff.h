@@ -63,8 +63,13 @@ hess_status gated_ff_create(int64_t d, int64_t f, int64_t train_tokens, int32_t 
  *   H_out  : [n_tokens, f].
  * Asynchronous on `stream`.  Calls that split tiles use the handle's workspace
  * (they have more than 128 tokens): such a call, or a backward call, on another
- * stream waits for the one before it (an event; during stream capture, use one
- * stream).  Other forward calls may run concurrently. */
+ * stream waits for the one before it (an event).  Other forward calls may run
+ * concurrently.
+ * Calls may be captured into a graph, on any stream; a captured call waits for
+ * the earlier ones of its capture.  A replay uses the workspace like the calls in
+ * it, but the library does not see it: the caller orders the replays of a
+ * handle's graphs with each other and with its other calls, and captures with
+ * one handle one after the other. */
 hess_status gated_ff_forward(gated_ff_t g, const void* X, int64_t n_tokens, const void* W_gate,
                              const void* W_up, void* H_out, hess_stream_t stream);
 

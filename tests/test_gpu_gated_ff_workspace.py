@@ -1,0 +1,79 @@
+"""How calls of one feed-forward handle share its workspace: stream captures,
+calls of several streams, tiles that are split, and what a timeout leaves.
+
+Values are compared with the same call made alone, bit for bit: the sums are
+taken in a fixed order."""
+
+import pytest
+import torch
+
+from test_gpu_gated_ff import make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from gptq_qqq_calibration_gb300 import build as b
+    b.build()
+
+
+def same(got, want):
+    return all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def cuda(n, d, f, seed):
+    return [t.cuda() for t in make(n, d, f, torch.bfloat16, seed)]
+
+
+def test_capture_after_calls_on_another_stream():
+    """The usual order of a program: calls on the current stream, a capture (on a
+    stream of its own), calls on yet another stream, replays.  The captured
+    calls do not wait for work outside the capture, and the later ones not for
+    work that only the capture knows."""
+    from gptq_qqq_calibration_gb300 import GatedFF
+    sets = [cuda(100, 256, 512, 30 + k) for k in range(2)]
+    op = GatedFF(256, 512, train_tokens=100)
+    want = [op.backward(*s) for s in sets]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = op.backward(*sets[0])
+    other = torch.cuda.Stream()
+    got = op.backward(*sets[1], stream=other)
+    torch.cuda.synchronize()
+    assert same(got, want[1])
+    for _ in range(2):
+        for t in captured:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(captured, want[0])
+    assert same(op.backward(*sets[1]), want[1])
+    op.sync()
+
+
+def test_two_streams_of_one_capture():
+    """Calls on two streams of one capture use the workspace one after the other."""
+    from gptq_qqq_calibration_gb300 import GatedFF
+    n, d, f = 1500, 512, 1024
+    sets = [cuda(n, d, f, 40 + k) for k in range(3)]
+    op = GatedFF(d, f, train_tokens=n)
+    want = [op.backward(*s) for s in sets]
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        first = op.backward(*sets[0])
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            second = op.backward(*sets[1])
+        third = op.backward(*sets[2])
+        main.wait_stream(side)
+    for _ in range(3):
+        for t in (*first, *second, *third):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(first, want[0]) and same(second, want[1]) and same(third, want[2])
+    op.sync()
