@@ -62,8 +62,8 @@ hess_status gated_ff_create(int64_t d, int64_t f, int64_t train_tokens, int32_t 
  *            one packed [2f, d] matrix will do.
  *   H_out  : [n_tokens, f].
  * Asynchronous on `stream`.  Calls that split tiles use the handle's workspace
- * (they have more than 128 tokens): such a call, or a backward call, on another
- * stream waits for the one before it (an event).  Other forward calls may run
+ * (they have more than 128 tokens): such a call, or a backward call, waits for
+ * the one before it, whatever its stream (an event).  Other forward calls may run
  * concurrently.
  * Calls may be captured into a graph, on any stream; a captured call waits for
  * the earlier ones of its capture.  A replay uses the workspace like the calls in

@@ -4,6 +4,8 @@ calls of several streams, tiles that are split, and what a timeout leaves.
 Values are compared with the same call made alone, bit for bit: the sums are
 taken in a fixed order."""
 
+import threading
+
 import pytest
 import torch
 
@@ -76,4 +78,34 @@ def test_two_streams_of_one_capture():
         graph.replay()
         torch.cuda.synchronize()
         assert same(first, want[0]) and same(second, want[1]) and same(third, want[2])
+    op.sync()
+
+
+def test_threads_default_streams():
+    """Each thread's own default stream has the same handle value: calls of two
+    threads follow one another all the same."""
+    from gptq_qqq_calibration_gb300 import GatedFF, _lib
+    n, d, f = 1500, 512, 1024
+    lib, per_thread = _lib.load(), 2  # cudaStreamPerThread
+    op = GatedFF(d, f, train_tokens=n)
+    sets = [cuda(n, d, f, 60 + k) for k in range(2)]
+    want = [op.backward(*s) for s in sets]
+    got = [[tuple(torch.zeros_like(t) for t in w) for _ in range(20)] for w in want]
+    torch.cuda.synchronize()
+    status = [[], []]
+
+    def work(k):
+        ptrs = [t.data_ptr() for t in sets[k]]
+        for out in got[k]:
+            status[k].append(lib.gated_ff_backward(op.handle, ptrs[0], n, *ptrs[1:], *(t.data_ptr() for t in out),
+                                                   per_thread))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert status == [[_lib.HESS_OK] * 20] * 2
+    assert all(same(out, want[k]) for k in range(2) for out in got[k])
     op.sync()

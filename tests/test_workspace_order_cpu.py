@@ -35,19 +35,43 @@ def test_calls_follow_one_another(tmp_path):
     assert rc == 0 and out.startswith("order ok"), out
 
 
-@pytest.mark.parametrize("old,new", [
-    # waits inside a capture for work outside it
-    ("if (in) return has_capture && capture == id ? cudaStreamWaitEvent(s, captured, 0) : cudaSuccess;\n", ""),
-    # the event of the calls outside recorded inside
-    ("cudaEventRecord(in ? captured : done, s)", "cudaEventRecord(done, s)"),
-    # the calls of an earlier capture waited for
-    ("has_capture && capture == id ?", "has_capture ?"),
-    # no order within a capture
-    ("has_capture && capture == id ? cudaStreamWaitEvent(s, captured, 0) : cudaSuccess", "cudaSuccess"),
-])
-def test_planted_mistakes_fail(tmp_path, old, new):
+def test_equal_handles_may_be_other_streams(tmp_path):
+    """Handle values that stand for one stream and later for another: a thread's
+    own default stream, or a new stream at a destroyed one's value."""
+    rc, out = run(tmp_path, HEADER, "aliases")
+    assert rc == 0 and out.startswith("order ok"), out
+
+
+def planted(tmp_path, old, new, *args):
     text = open(HEADER).read()
     assert text.count(old) == 1, old
     (tmp_path / "workspace_order.h").write_text(text.replace(old, new))
-    rc, out = run(tmp_path, str(tmp_path / "workspace_order.h"))
+    rc, out = run(tmp_path, str(tmp_path / "workspace_order.h"), *args)
     assert rc != 0, out
+
+
+@pytest.mark.parametrize("old,new", [
+    # waits inside a capture for work outside it, and outside for a capture's
+    ("const User& u = in ? inside : outside;", "const User& u = outside;"),
+    # an id asked for inside a capture
+    ("if (in || s ==", "if (s =="),
+    # the event of the calls outside recorded inside
+    ("cudaEventRecord(u.event, s)", "cudaEventRecord(outside.event, s)"),
+    # the calls of an earlier capture waited for
+    ("!u.some || u.capture != now.capture", "!u.some"),
+    # no order within a capture
+    ("!u.some || u.capture != now.capture", "!u.some || in"),
+    # no order outside
+    ("!u.some || u.capture != now.capture", "!u.some || u.capture != now.capture || !in"),
+])
+def test_planted_mistakes_fail(tmp_path, old, new):
+    planted(tmp_path, old, new)
+
+
+@pytest.mark.parametrize("old,new", [
+    ("if (in || s == cudaStreamPerThread)", "if (in)"),
+    ("return cudaStreamGetId(s, &now.stream);",
+     "return now.stream = reinterpret_cast<unsigned long long>(s), cudaSuccess;"),
+])
+def test_planted_mistakes_with_handles_fail(tmp_path, old, new):
+    planted(tmp_path, old, new, "aliases")

@@ -54,6 +54,13 @@ cudaError_t CUDARTAPI cudaStreamWaitEvent(cudaStream_t s, cudaEvent_t e, unsigne
     at(s).before.insert(at(e).before.begin(), at(e).before.end());
     return cudaSuccess;
 }
+// ids are given once, except to the stream that each thread has of its own: what
+// the model gives for that one is not to be gone by
+cudaError_t CUDARTAPI cudaStreamGetId(cudaStream_t s, unsigned long long* id) {
+    if (at(s).capture) return cudaErrorStreamCaptureUnsupported;
+    *id = s == cudaStreamPerThread ? 1000000ull : static_cast<unsigned long long>(by_handle.at(s)) + 1;
+    return cudaSuccess;
+}
 cudaError_t CUDARTAPI cudaStreamGetCaptureInfo(cudaStream_t s, cudaStreamCaptureStatus* status,
                                                unsigned long long* id, cudaGraph_t*, const cudaGraphNode_t**,
                                                const cudaGraphEdgeData**, size_t*) {
@@ -64,7 +71,10 @@ cudaError_t CUDARTAPI cudaStreamGetCaptureInfo(cudaStream_t s, cudaStreamCapture
 }
 
 int main(int argc, char** argv) {
-    const bool aliases = argc > 1;  // handles that stand for another stream than before
+    // handles that stand for another stream than before; of the streams that are
+    // never captured, the second has the handle of a thread's own
+    const bool aliases = argc > 1;
+    static_assert(sizeof(cudaStream_t) == sizeof(uintptr_t), "handles are values");
     std::mt19937 rng(7);
     const auto pick = [&](int n) { return static_cast<int>(rng() % static_cast<unsigned>(n)); };
     long calls = 0, captured_calls = 0;
