@@ -243,6 +243,19 @@ __device__ __forceinline__ float gate_sigmoid(float g, int act, float& dz) {
 __device__ __forceinline__ void epi_barrier() {
     asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
 }
+// The same, and whether any thread came with `x`: every thread gets the same answer.
+__device__ __forceinline__ bool epi_barrier_any(bool x) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(static_cast<uint32_t>(x)), "n"(kEpiWarps * 32)
+        : "memory");
+    return any != 0;
+}
 
 // 64 columns of 128 rows go out through shared memory and one TMA store, which
 // leaves out what lies past the matrix's edges (each thread storing its row's 16
@@ -377,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto acce_bar = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
     const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4);
     __shared__ int aborted;
-    __shared__ volatile int epi_failed, epi_last;  // of the epilogue warps
+    __shared__ volatile int epi_last;  // of the epilogue warps
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -396,7 +409,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         mbar_init(drain_bar, 1);
         aborted = 0;
-        epi_failed = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -525,11 +537,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t acce0 = mapa_shared(acce_bar(0), 0);
         for (int i = 0, u; (u = unit_of<kWhat>(p, pair, n_pairs, i)) >= 0; ++i) {
             const Unit un = unit_at<kWhat>(p, u);
-            // The warps go on together: each passes every barrier below for every
-            // unit, whether its waits ran out or not.
-            if (failed || !mbar_wait_cluster(accf_bar(ab), aphase, limit)) epi_failed = 1;
-            epi_barrier();
-            failed = epi_failed != 0;
+            // The warps go on together: they agree on whether a wait ran out (with the
+            // barrier itself: a flag read after it might already be the next unit's),
+            // so that all of them pass the same barriers below.
+            failed = epi_barrier_any(failed || !mbar_wait_cluster(accf_bar(ab), aphase, limit));
             tc_fence_after();
             const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(ab * 256);
             const int m = un.m0 + static_cast<int>(rank) * 128;

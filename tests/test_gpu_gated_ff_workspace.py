@@ -109,3 +109,29 @@ def test_threads_default_streams():
     assert status == [[_lib.HESS_OK] * 20] * 2
     assert all(same(out, want[k]) for k in range(2) for out in got[k])
     op.sync()
+
+
+@pytest.mark.parametrize("limit", [0, 300, 1000, 3000])
+def test_waits_that_run_out_end_the_kernel(limit):
+    """Several tiles a pair of SMs, with a limit that some waits keep and others do
+    not: the kernel ends, says so, and the handle works again."""
+    from gptq_qqq_calibration_gb300 import GatedFF, HessError
+    from gptq_qqq_calibration_gb300.gated_ff import gated_ff_set_timeout
+    n, d, f = 2000, 256, 4096  # 256 tiles
+    X, G, U, D = cuda(n, d, f, 70)
+    op = GatedFF(d, f, train_tokens=n)
+    want = (op.forward(X, G, U), *op.backward(X, G, U, D))
+    op.sync()
+    gated_ff_set_timeout(op.handle, limit)
+    timeouts = 0
+    for _ in range(10):
+        op.forward(X, G, U), op.backward(X, G, U, D)
+        try:
+            op.sync()
+        except HessError as e:
+            assert "TIMEOUT" in str(e)
+            timeouts += 1
+    gated_ff_set_timeout(op.handle, 2_000_000_000)
+    assert timeouts > 0 or limit > 0
+    assert same((op.forward(X, G, U), *op.backward(X, G, U, D)), want)
+    op.sync()
