@@ -1313,8 +1313,11 @@ FF_EXPORT hess_status gated_ff_sync(gated_ff_t g, hess_stream_t stream) {
     FF_TRY(cudaMemcpyAsync(&word, g->status, sizeof(word), cudaMemcpyDeviceToHost, s));
     FF_TRY(cudaStreamSynchronize(s));
     if (word == 0) return HESS_OK;
-    // the arrival counts of an interrupted call go with it
+    // the arrival counts of an interrupted call go with it, when no call on another
+    // stream is at them, and before the next call may be
+    FF_CHECK(hk::ff_begin(g, s));
     FF_TRY(cudaMemsetAsync(g->status, 0, hk::status_bytes(g->pairs), s));
+    FF_TRY(cudaStreamSynchronize(s));
     return ff_fail(HESS_ERR_TIMEOUT, "a device-side wait ran out (status 0x%x); results are invalid", word);
 }
 

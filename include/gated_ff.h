@@ -84,8 +84,11 @@ hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_tokens, con
                               void* dW_up_out, hess_stream_t stream);
 
 /* Wait for `stream`; then HESS_ERR_TIMEOUT if a device-side wait of this
- * handle's kernels ran out since the last gated_ff_sync (their results are
- * invalid, and the handle works again after this call), else HESS_OK. */
+ * handle's kernels ran out since the last gated_ff_sync, else HESS_OK.  After a
+ * timeout the results of every call of the handle since then are invalid (a
+ * later call may have counted what the interrupted one left behind); this call
+ * then also waits for the handle's calls on other streams that use its workspace,
+ * and the handle works again. */
 hess_status gated_ff_sync(gated_ff_t g, hess_stream_t stream);
 
 /* Limit of every device-side wait, ns (default 2e9; 0 makes any wait that is

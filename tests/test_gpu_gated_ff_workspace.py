@@ -135,3 +135,33 @@ def test_waits_that_run_out_end_the_kernel(limit):
     assert timeouts > 0 or limit > 0
     assert same((op.forward(X, G, U), *op.backward(X, G, U, D)), want)
     op.sync()
+
+
+@pytest.mark.parametrize("limit", [0, 500, 2000, 8000])
+def test_split_calls_on_another_stream_after_a_timeout(limit):
+    """A call of split tiles that gave up leaves pieces that no tile was finished
+    with.  Once it is reported, the next calls count from zero, on whatever
+    stream they come."""
+    from gptq_qqq_calibration_gb300 import GatedFF, HessError
+    from gptq_qqq_calibration_gb300.gated_ff import gated_ff_set_timeout
+    n, d, f = 300, 2568, 1096  # 18 tiles in 3 pieces each
+    first, second = (cuda(n, d, f, 80 + k)[:3] for k in range(2))
+    op = GatedFF(d, f)
+    want = op.forward(*second)
+    op.sync()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for k in range(6):
+        gated_ff_set_timeout(op.handle, limit)
+        op.forward(*first, stream=streams[0])
+        gated_ff_set_timeout(op.handle, 2_000_000_000)
+        late = op.forward(*first, stream=streams[1])  # may run while the first is reported
+        try:
+            op.sync(streams[0])
+        except HessError as e:
+            assert "TIMEOUT" in str(e)
+        got = [op.forward(*second, stream=streams[2]) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, want) for g in got)
+        del late
+    op.sync()
