@@ -88,6 +88,12 @@ def _common(logits, top_logits, top_index, temperature, teacher_lse, weights):
                   _vector(teacher_lse, rows, "teacher_lse"), _vector(weights, rows, "weights"), temperature)
 
 
+def _written(out: Optional[torch.Tensor]) -> None:
+    """Autograd learns that the caller's tensor was written, as after an in-place operation."""
+    if out is not None:
+        torch.autograd.graph.increment_version(out)
+
+
 def _output(out: Optional[torch.Tensor], logits: torch.Tensor, stream) -> Tuple[torch.Tensor, int]:
     if out is None:
         out = _empty(logits.shape, logits.dtype, logits, stream)
@@ -120,9 +126,11 @@ def distill_backward(logits: torch.Tensor, stats: torch.Tensor, top_logits: torc
     if not stats.is_cuda or stats.dtype != torch.float32 or not stats.is_contiguous() or \
             stats.numel() != rows * _STATS:
         raise ValueError("stats must be the tensor distill_forward returned for these logits")
+    given = out
     out, ldd = _output(out, logits, stream)
     check(_lib.load().distill_backward(*args, stats.data_ptr(), _vector(grad, rows, "grad"), out.data_ptr(), ldd,
                                        _stream(stream, logits.get_device())))
+    _written(given)
     _used_on(stream, logits, stats, top_logits, top_index, teacher_lse, weights, grad, out)
     return out
 
@@ -134,8 +142,10 @@ def distill_step(logits: torch.Tensor, top_logits: torch.Tensor, top_index: torc
     logits; ``out`` may be ``logits``."""
     rows, args = _common(logits, top_logits, top_index, temperature, teacher_lse, weights)
     loss = _empty(rows, torch.float32, logits, stream)
+    given = out
     out, ldd = _output(out, logits, stream)
     check(_lib.load().distill_step(*args, loss.data_ptr(), out.data_ptr(), ldd, _stream(stream, logits.get_device())))
+    _written(given)
     _used_on(stream, logits, top_logits, top_index, teacher_lse, weights, out)
     return loss, out
 

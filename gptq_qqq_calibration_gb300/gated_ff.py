@@ -52,21 +52,36 @@ def gated_ff_create(d: int, f: int, train_tokens: int, dtype: int, act: int) -> 
     return g.value
 
 
-def gated_ff_forward(g: int, X, n_tokens: int, W_gate, W_up, H_out, stream=None) -> None:
+def _written(*tensors) -> None:
+    """Autograd learns that a caller's tensors were written, as after an in-place operation."""
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
+def _forward(g: int, X, n_tokens: int, W_gate, W_up, H_out, stream) -> None:
     st = _lib.load().gated_ff_forward(g, X.data_ptr(), n_tokens, W_gate.data_ptr(), W_up.data_ptr(),
                                       H_out.data_ptr(), _stream(stream, X.get_device()))
     if st:
         check(st)
 
 
-def gated_ff_backward(g: int, X, n_tokens: int, W_gate, W_up, dH, dX_out, dW_gate_out, dW_up_out,
-                      stream=None) -> None:
+def gated_ff_forward(g: int, X, n_tokens: int, W_gate, W_up, H_out, stream=None) -> None:
+    _forward(g, X, n_tokens, W_gate, W_up, H_out, stream)
+    _written(H_out)
+
+
+def _backward(g: int, X, n_tokens: int, W_gate, W_up, dH, dX_out, dW_gate_out, dW_up_out, stream) -> None:
     st = _lib.load().gated_ff_backward(
         g, X.data_ptr(), n_tokens, W_gate.data_ptr(), W_up.data_ptr(), dH.data_ptr(),
         None if dX_out is None else dX_out.data_ptr(), None if dW_gate_out is None else dW_gate_out.data_ptr(),
         None if dW_up_out is None else dW_up_out.data_ptr(), _stream(stream, X.get_device()))
     if st:
         check(st)
+
+
+def gated_ff_backward(g: int, X, n_tokens: int, W_gate, W_up, dH, dX_out, dW_gate_out, dW_up_out,
+                      stream=None) -> None:
+    _backward(g, X, n_tokens, W_gate, W_up, dH, dX_out, dW_gate_out, dW_up_out, stream)
+    _written(dX_out, dW_gate_out, dW_up_out)
 
 
 def gated_ff_sync(g: int, stream=None) -> None:
@@ -125,9 +140,11 @@ class GatedFF:
         n = self._inputs(X, W_gate, W_up)
         if out is None:
             out = _empty((n, self.f) if X.dim() == 2 else (*X.shape[:-1], self.f), X, stream)
-        elif self._rows(out, "out", self.f) != n:
-            raise ValueError(f"out must have {n} rows")
-        gated_ff_forward(self.handle, X, n, W_gate, W_up, out, stream)
+            _forward(self.handle, X, n, W_gate, W_up, out, stream)
+        else:
+            if self._rows(out, "out", self.f) != n:
+                raise ValueError(f"out must have {n} rows")
+            gated_ff_forward(self.handle, X, n, W_gate, W_up, out, stream)
         _used_on(stream, X, W_gate, W_up, out)
         return out
 
@@ -141,7 +158,7 @@ class GatedFF:
         dx = _empty(X.shape, X, stream) if want_dx else None
         dwg = _empty(W_gate.shape, X, stream) if want_dw else None
         dwu = _empty(W_up.shape, X, stream) if want_dw else None
-        gated_ff_backward(self.handle, X, n, W_gate, W_up, dH, dx, dwg, dwu, stream)
+        _backward(self.handle, X, n, W_gate, W_up, dH, dx, dwg, dwu, stream)
         _used_on(stream, X, W_gate, W_up, dH)
         return dx, dwg, dwu
 
