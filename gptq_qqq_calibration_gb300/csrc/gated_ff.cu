@@ -1035,6 +1035,29 @@ hess_status ff_check(const gated_ff_ctx* g, const void* p, const char* name) {
     return HESS_OK;
 }
 
+struct FfBuffer {
+    const void* p;  // nullptr: not there
+    int64_t elements;
+    const char* name;
+};
+// Outputs share no memory with inputs or with each other: some CTAs read while
+// others write.
+template <size_t kIn, size_t kOut>
+hess_status ff_apart(const FfBuffer (&in)[kIn], const FfBuffer (&out)[kOut]) {
+    const auto meet = [](const FfBuffer& a, const FfBuffer& b) {
+        const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+        return a.p && b.p && a0 < b0 + 2 * static_cast<uintptr_t>(b.elements) &&
+               b0 < a0 + 2 * static_cast<uintptr_t>(a.elements);
+    };
+    for (size_t o = 0; o < kOut; ++o) {
+        for (size_t i = 0; i < kIn; ++i)
+            if (meet(out[o], in[i])) return ff_fail(HESS_ERR_INVALID, "%s overlaps %s", out[o].name, in[i].name);
+        for (size_t i = 0; i < o; ++i)
+            if (meet(out[o], out[i])) return ff_fail(HESS_ERR_INVALID, "%s overlaps %s", out[o].name, out[i].name);
+    }
+    return HESS_OK;
+}
+
 #define FF_CHECK(expr)                       \
     do {                                     \
         const hess_status st_ = (expr);      \
@@ -1216,6 +1239,9 @@ FF_EXPORT hess_status gated_ff_forward(gated_ff_t g, const void* X, int64_t n_to
     FF_CHECK(hk::ff_check(g, W_gate, "W_gate"));
     FF_CHECK(hk::ff_check(g, W_up, "W_up"));
     FF_CHECK(hk::ff_check(g, H_out, "H_out"));
+    const hk::FfBuffer in[] = {{X, n_tokens * g->d, "X"}, {W_gate, g->f * g->d, "W_gate"}, {W_up, g->f * g->d, "W_up"}};
+    const hk::FfBuffer result[] = {{H_out, n_tokens * g->f, "H_out"}};
+    FF_CHECK(hk::ff_apart(in, result));
     FF_TRY(hk::ensure_context());
     if (n_tokens <= hk::kFewTokens)
         return hk::ff_forward_few(g, X, n_tokens, W_gate, W_up, H_out, static_cast<cudaStream_t>(stream));
@@ -1258,6 +1284,12 @@ FF_EXPORT hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_t
         FF_CHECK(hk::ff_check(g, dW_gate_out, "dW_gate_out"));
         FF_CHECK(hk::ff_check(g, dW_up_out, "dW_up_out"));
     }
+    const int64_t weights = g->f * g->d;
+    const hk::FfBuffer in[] = {{X, n_tokens * g->d, "X"}, {W_gate, weights, "W_gate"}, {W_up, weights, "W_up"},
+                               {dH, n_tokens * g->f, "dH"}};
+    const hk::FfBuffer result[] = {{dX_out, n_tokens * g->d, "dX_out"}, {dW_gate_out, weights, "dW_gate_out"},
+                                   {dW_up_out, weights, "dW_up_out"}};
+    if (n_tokens > 0) FF_CHECK(hk::ff_apart(in, result));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (n_tokens == 0) {
         if (want_w) {

@@ -137,6 +137,7 @@ class GatedFF:
 
     def forward(self, X: torch.Tensor, W_gate: torch.Tensor, W_up: torch.Tensor,
                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """h of X [..., d]; ``out`` shares no memory with the inputs."""
         n = self._inputs(X, W_gate, W_up)
         if out is None:
             out = _empty((n, self.f) if X.dim() == 2 else (*X.shape[:-1], self.f), X, stream)

@@ -56,7 +56,8 @@ hess_status gated_ff_create(int64_t d, int64_t f, int64_t train_tokens, int32_t 
 
 /* h for n_tokens rows.  Every matrix is row-major and contiguous, 16-byte
  * aligned, of the handle's type, in device memory of the handle's device (or
- * managed memory); outputs must not overlap inputs.
+ * managed memory); outputs must not overlap inputs or each other
+ * (HESS_ERR_INVALID).
  *   X      : [n_tokens, d].  n_tokens 0 is a no-op; at most 2^26.
  *   W_gate, W_up : [f, d] (output channel by input column).  The halves of
  *            one packed [2f, d] matrix will do.
