@@ -193,6 +193,9 @@ class _GatedFF(torch.autograd.Function):
     def backward(ctx, dH):
         X, W_gate, W_up = ctx.saved_tensors
         want = ctx.needs_input_grad
-        dx, dwg, dwu = ctx.op.backward(X, W_gate, W_up, dH.contiguous(), want_dx=want[1],
+        dH = dH.contiguous()
+        if dH.data_ptr() % 16:  # a part of a buffer that starts anywhere
+            dH = dH.clone()
+        dx, dwg, dwu = ctx.op.backward(X, W_gate, W_up, dH, want_dx=want[1],
                                        want_dw=want[2] or want[3])
         return None, dx, dwg if want[2] else None, dwu if want[3] else None
