@@ -1019,8 +1019,12 @@ hess_status ds_output(const DistillArgs& a, int32_t dtype, bool want_grad) {
             const size_t es = elem_size(dtype);
             const uintptr_t s1 = s0 + ((a.rows - 1) * a.ld + a.vocab) * es;
             const uintptr_t d1 = d0 + ((a.rows - 1) * a.ldd + a.vocab) * es;
-            const bool in_place = s0 == d0 && a.ld == a.ldd;
-            if (!in_place && s0 < d1 && d0 < s1)
+            const bool in_place = s0 == d0 && (a.ld == a.ldd || a.rows == 1);
+            // rows of one stride may lie between each other, as columns of one buffer
+            const uintptr_t stride = a.ld * es, width = a.vocab * es;
+            const uintptr_t shift = (d0 > s0 ? d0 - s0 : stride - (s0 - d0) % stride) % stride;
+            const bool between = a.ld == a.ldd && shift >= width && shift + width <= stride;
+            if (!in_place && !between && s0 < d1 && d0 < s1)
                 return ds_fail(HESS_ERR_INVALID, "dlogits overlaps logits without being logits");
         }
     }

@@ -84,7 +84,8 @@ hess_status distill_forward(const void* logits, int64_t ld, int64_t rows, int64_
  *   grad    : [rows] fp32, the gradient of the row losses, or NULL (all 1).
  *   dlogits : [rows, vocab], element type `dtype`; row r starts at element
  *             r * ldd (ldd >= vocab).  May be `logits` itself (with ldd == ld);
- *             otherwise the two must not overlap. */
+ *             otherwise the two must not overlap (with ldd == ld, the rows of one
+ *             may lie between the rows of the other). */
 hess_status distill_backward(const void* logits, int64_t ld, int64_t rows, int64_t vocab, int32_t dtype,
                              const void* top_logits, int32_t top_dtype, const void* top_index,
                              int32_t index_bytes, int64_t top, const float* teacher_lse,

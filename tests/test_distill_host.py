@@ -52,3 +52,24 @@ def test_other_calls_refuse_float16(lib):
     from gptq_qqq_calibration_gb300._lib import HESS_ERR_INVALID, HESS_F16
     out = ctypes.c_void_p(16)
     assert lib.local_hess_compute_noalloc(P, 4, 64, 16, HESS_F16, out, None) == HESS_ERR_INVALID
+
+
+@pytest.mark.parametrize("dtype,size", [(0, 2), (1, 4)])
+def test_rows_between_rows_do_not_overlap(lib, dtype, size):
+    """Logits and gradient as columns of one buffer: refused exactly where an
+    element of one is an element of the other."""
+    rows, vocab, ld = 4, 100, 230
+    base = 1 << 20
+
+    def overlaps(shift, ldd=ld, rows=rows, ld=ld):
+        lib.distill_step(ctypes.c_void_p(base), ld, rows, vocab, dtype, P, 1, P, 4, 5, None, None, 1.0, P,
+                         ctypes.c_void_p(base + shift * size), ldd, None)
+        return b"overlaps" in lib.hess_last_error()
+
+    logits = {r * ld + j for r in range(rows) for j in range(vocab)}
+    for shift in (*range(-300, 301), 4 * ld - 1, 3 * ld + 99, 3 * ld + 100, -3 * ld - 99, -3 * ld - 100, -4 * ld):
+        out = {shift + r * ld + j for r in range(rows) for j in range(vocab)}
+        assert overlaps(shift) == (bool(logits & out) and shift != 0), shift
+    assert overlaps(105, ldd=ld + 1)  # other strides: by their ranges
+    assert not overlaps(0, ldd=100, rows=1)  # one row in place, whatever the strides
+    assert not overlaps(0) and not overlaps(4 * ld)
