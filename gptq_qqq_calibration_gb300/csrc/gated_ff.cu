@@ -48,6 +48,7 @@
 
 #include "device_ptr.h"
 #include "gated_ff.h"
+#include "gated_ff_schedule.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
 #include "workspace_order.h"
@@ -55,7 +56,8 @@
 namespace hk {
 namespace {
 
-constexpr int kKB = 64;                            // contraction steps of one stage
+using namespace ff;
+
 constexpr int kStages = 6;
 constexpr uint32_t kBoxBytes = 64 * 64 * 2;
 constexpr uint32_t kOperandBytes = 2 * kBoxBytes;  // 128 rows of A, or of B, per CTA
@@ -70,21 +72,12 @@ constexpr uint32_t kAfterRing = kStages * kStageBytes + 2 * kOutBytes;
 constexpr size_t kSmemBytes = 1024 + kAfterRing + 8 * kNumBarriers + 16;
 constexpr unsigned long long kDrainLimitNs = 1000000000ull;
 constexpr unsigned long long kAbortSettleNs = 2000000ull;
-constexpr int kGroupM = 8;  // row tiles that run side by side (their B boxes meet in L2)
 
 enum { kMapX, kMapWg, kMapWu, kMapDg, kMapDu, kMapOut0, kMapOut1, kMapOut2, kMaps };
-enum { kForward, kActGrad, kGradients };  // what a launch computes
 
-struct FfParams {
+struct FfParams : FfSchedule {
     CUtensorMap maps[kMaps];  // the last three are written: h | dg, du | dX, dWg, dWu
-    int32_t n, d, f;
     int32_t act;
-    int32_t whole;    // kForward, kActGrad: tiles that are not split; they come first
-    int32_t parts;    // units of each tile after them, or of each tile of dX
-    int32_t units_x;  // kGradients: units of dX (first), then 2 * tiles_w tiles of dWg and dWu
-    int32_t tiles_w;
-    int32_t n_units;
-    int32_t skip;     // kGradients: turns of dW tiles that one tile of dX is worth
     uint32_t fmt;     // operand format of the instruction descriptor: 0 = f16, 1 = bf16
     const void* dh;
     float* pieces;      // 256 x 256 sums of every unit of a split tile
@@ -93,83 +86,6 @@ struct FfParams {
     unsigned long long timeout_ns;
 };
 constexpr int kPieceFloats = 256 * 256;
-
-// Tile u of tm x tn, in groups of kGroupM row tiles walked column by column.
-__host__ __device__ inline void tile_at(int u, int tm, int tn, int& m, int& n) {
-    const int per = kGroupM * tn;
-    const int g = u / per, r = u - g * per;
-    const int rows = tm - g * kGroupM < kGroupM ? tm - g * kGroupM : kGroupM;
-    n = r / rows;
-    m = g * kGroupM + (r - n * rows);
-}
-
-// The k-th unit of a pair, or -1.  Units go to the pairs in turn.  The tiles of
-// dX are long (their sums run over f twice), so some pairs have one more of them
-// than the others; those sit out the first p.skip turns of the tiles of dW.
-template <int kWhat>
-__device__ __forceinline__ int unit_of(const FfParams& p, int pair, int n_pairs, int k) {
-    int u = pair + k * n_pairs;
-    if constexpr (kWhat == kGradients) {
-        if (u >= p.units_x) {
-            const int more = p.units_x % n_pairs, mine = p.units_x / n_pairs + (pair < more ? 1 : 0);
-            const int turn = k - mine + (pair < more ? p.skip : 0);
-            u = p.units_x + (turn < p.skip ? turn * (n_pairs - more) + pair - more
-                                           : p.skip * (n_pairs - more) + (turn - p.skip) * n_pairs + pair);
-        }
-    }
-    return u < p.n_units ? u : -1;
-}
-
-struct Unit {
-    int kind;   // 0: X times weights, 1: dX, 2: dW
-    int m0, n0;  // first row of A and of B (kind 0: of each weight)
-    int which;  // kind 2: 0 = gate, 1 = up
-    int kb0, kb1;  // boxes of the sum
-    int half;   // kind 1: boxes of the gate half of the sum
-    int parts;  // units of this tile
-    int part;   // this one
-    int split;  // split tiles before this one
-};
-
-template <int kWhat>
-__device__ __forceinline__ Unit unit_at(const FfParams& p, int u) {
-    Unit r{};
-    int m, n, n_kb;
-    r.parts = 1;
-    if constexpr (kWhat != kGradients) {
-        if (u >= p.whole) {
-            r.parts = p.parts;
-            r.split = (u - p.whole) / p.parts;
-            r.part = (u - p.whole) - r.split * p.parts;
-            u = p.whole + r.split;
-        }
-        tile_at(u, (p.n + 255) / 256, (p.f + 127) / 128, m, n);
-        r.m0 = m * 256;
-        r.n0 = n * 128;
-        n_kb = (p.d + kKB - 1) / kKB;
-    } else if (u < p.units_x) {
-        r.parts = p.parts;
-        r.split = u / p.parts;
-        r.part = u - r.split * p.parts;
-        tile_at(r.split, (p.n + 255) / 256, (p.d + 255) / 256, m, n);
-        r.kind = 1;
-        r.m0 = m * 256;
-        r.n0 = n * 256;
-        r.half = (p.f + kKB - 1) / kKB;
-        n_kb = 2 * r.half;
-    } else {
-        u -= p.units_x;
-        r.which = u >= p.tiles_w ? 1 : 0;
-        tile_at(u - r.which * p.tiles_w, (p.f + 255) / 256, (p.d + 255) / 256, m, n);
-        r.kind = 2;
-        r.m0 = m * 256;
-        r.n0 = n * 256;
-        n_kb = (p.n + kKB - 1) / kKB;
-    }
-    r.kb0 = n_kb * r.part / r.parts;
-    r.kb1 = n_kb * (r.part + 1) / r.parts;
-    return r;
-}
 
 __device__ __forceinline__ uint32_t instr_desc(uint32_t fmt, bool a_mn, bool b_mn) {
     return (1u << 4) | (fmt << 7) | (fmt << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
@@ -974,29 +890,9 @@ hess_status ff_prepare(int dev, int* pairs, int* sms_out) {
     return HESS_OK;
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 // The status word, then two arrival counts for every tile that may be split (at
 // most one per pair).
 size_t status_bytes(int pairs) { return (1 + 2 * static_cast<size_t>(pairs)) * sizeof(uint32_t); }
-
-// Units to split a tile of n_kb boxes in, when `tiles` of them run side by side
-// and the pairs have `share` boxes of work each in all.  A box takes 512 cycles at
-// the tensor cores' rate; a split costs about as much as 8 boxes for the pieces'
-// way to memory and the pairs' meeting, and 4 for reading each piece again.  It
-// has to promise a fourteenth of the time (129 tokens at 4,096 x 11,008, backward:
-// 163 us unsplit, 129 with dX in 2, 145 in 3; 1,024 at 2,048 x 5,632: 94 unsplit,
-// 102 in 2; 203 at 520 x 1,400: 30.4 unsplit, 27.2 in 3).
-int32_t parts_of(int64_t tiles, int64_t n_kb, int64_t pairs, int64_t share) {
-    const auto cost = [&](int64_t s) {
-        const int64_t longest = ceil_div(n_kb, s);
-        return (longest > share ? longest : share) + (s > 1 ? 8 + 4 * s : 0);
-    };
-    int64_t best = 1;
-    for (int64_t s = 2; s <= 8 && tiles * s <= pairs; ++s)
-        if (14 * cost(s) < 13 * cost(1) && cost(s) < cost(best)) best = s;
-    return static_cast<int32_t>(best);
-}
 
 }  // namespace
 }  // namespace hk
@@ -1074,14 +970,6 @@ void ff_params(FfParams& p, const gated_ff_ctx* g, int64_t n) {
     p.arrived = g->status + 1;
     p.status = g->status;
     p.timeout_ns = g->timeout_ns;
-}
-
-// Units of X times the weights: whole rounds of tiles, then the rest, split.
-void ff_tiles(FfParams& p, const gated_ff_ctx* g) {
-    const int64_t tiles = ceil_div(p.n, 256) * ceil_div(g->f, 128), rest = tiles % g->pairs;
-    p.parts = rest > 0 ? parts_of(rest, ceil_div(g->d, kKB), g->pairs, 0) : 1;
-    p.whole = static_cast<int32_t>(p.parts > 1 ? tiles - rest : tiles);
-    p.n_units = static_cast<int32_t>(p.parts > 1 ? p.whole + rest * p.parts : tiles);
 }
 
 // Launches so that the kernel's set-up may run while the stream's previous
@@ -1251,7 +1139,7 @@ FF_EXPORT hess_status gated_ff_forward(gated_ff_t g, const void* X, int64_t n_to
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapWg], W_gate, g->dtype, g->f, g->d));
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapWu], W_up, g->dtype, g->f, g->d));
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapOut0], H_out, g->dtype, n_tokens, g->f, 128));
-    hk::ff_tiles(p, g);
+    hk::plan_projections(p, g->pairs);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p.parts == 1) return hk::ff_launch_pairs<hk::kForward>(g, p, s);
     FF_CHECK(hk::ff_begin(g, s));
@@ -1262,7 +1150,6 @@ FF_EXPORT hess_status gated_ff_forward(gated_ff_t g, const void* X, int64_t n_to
 FF_EXPORT hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_tokens, const void* W_gate,
                                         const void* W_up, const void* dH, void* dX_out, void* dW_gate_out,
                                         void* dW_up_out, hess_stream_t stream) {
-    using hk::ceil_div;
     if (!g) return ff_fail(HESS_ERR_INVALID, "handle is NULL");
     FF_CHECK(hk::ff_tokens(n_tokens));
     if ((dW_gate_out == nullptr) != (dW_up_out == nullptr))
@@ -1311,24 +1198,14 @@ FF_EXPORT hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_t
     p.dh = dH;
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapOut0], g->dg, g->dtype, n_tokens, g->f, 128));
     FF_CHECK(hk::ff_encode(&p.maps[hk::kMapOut1], g->du, g->dtype, n_tokens, g->f, 128));
-    hk::ff_tiles(p, g);
+    hk::plan_projections(p, g->pairs);
     hk::FfParams q = p;  // of the second launch; nothing is enqueued before both are complete
     if (want_x) FF_CHECK(hk::ff_encode(&q.maps[hk::kMapOut0], dX_out, g->dtype, n_tokens, g->d, 128));
     if (want_w) {
         FF_CHECK(hk::ff_encode(&q.maps[hk::kMapOut1], dW_gate_out, g->dtype, g->f, g->d, 128));
         FF_CHECK(hk::ff_encode(&q.maps[hk::kMapOut2], dW_up_out, g->dtype, g->f, g->d, 128));
     }
-    const int64_t tiles_x = want_x ? ceil_div(n_tokens, 256) * ceil_div(g->d, 256) : 0;
-    const int64_t tiles_w = want_w ? ceil_div(g->f, 256) * ceil_div(g->d, 256) : 0;
-    const int64_t kb_x = 2 * ceil_div(g->f, hk::kKB), kb_w = ceil_div(n_tokens, hk::kKB);
-    // in the share of each pair a tile of dW counts at least its write-out, some 10 boxes
-    q.parts = hk::parts_of(tiles_x, kb_x, g->pairs,
-                           ceil_div(tiles_x * kb_x + 2 * tiles_w * (kb_w > 10 ? kb_w : 10), g->pairs));
-    q.units_x = static_cast<int32_t>(tiles_x * q.parts);
-    q.tiles_w = static_cast<int32_t>(tiles_w);
-    q.n_units = q.units_x + 2 * q.tiles_w;
-    const int64_t kb_unit = kb_x / q.parts;
-    q.skip = want_x && want_w ? static_cast<int32_t>((kb_unit + kb_w / 2) / kb_w) : 0;
+    hk::plan_gradients(q, g->pairs, want_x, want_w);
     FF_CHECK(hk::ff_begin(g, s));
     FF_CHECK(hk::ff_launch_pairs<hk::kActGrad>(g, p, s));
     const hess_status st = hk::ff_launch_pairs<hk::kGradients>(g, q, s);
