@@ -73,3 +73,12 @@ def test_rows_between_rows_do_not_overlap(lib, dtype, size):
     assert overlaps(105, ldd=ld + 1)  # other strides: by their ranges
     assert not overlaps(0, ldd=100, rows=1)  # one row in place, whatever the strides
     assert not overlaps(0) and not overlaps(4 * ld)
+
+
+def test_vocabulary_limit(lib):
+    """One column past the widest row is refused; the widest is not, here."""
+    from gptq_qqq_calibration_gb300._lib import HESS_ERR_UNSUPPORTED
+    assert fwd(lib, vocab=(1 << 22) + 1, ld=1 << 23) == HESS_ERR_UNSUPPORTED
+    assert b"vocab" in lib.hess_last_error()
+    fwd(lib, vocab=1 << 22, ld=1 << 22)
+    assert b"vocab" not in lib.hess_last_error()
