@@ -10,7 +10,7 @@
 // they are marked to do.
 //
 // Memory bounds it.  8,192 rows of 128,000 bf16 logits, an eighth of them without
-// weight: the loss alone takes 262 us, the rate of a copy of the bytes it reads;
+// weight: the loss alone takes 266 us, the rate of a copy of the bytes it reads;
 // loss and gradient 688 us, 83 % of that rate (ncu: 5.2 TB/s, a tenth of the
 // logits read twice); the gradient from saved statistics 604 us, 95 %.  What the
 // step lacks is the start of a row, two loads of DRAM one after the other, and the
@@ -1037,8 +1037,8 @@ template <class T, bool kGrad>
 hess_status launch_typed(DistillArgs& a, int sms, cudaStream_t s) {
     constexpr int per = Elem<T>::kPer;
     const int granules = static_cast<int>((static_cast<int64_t>(a.vocab) + 2 * (per - 1)) / per);
-    // CTAs per row and threads per CTA (an SM holds 1,536 threads; figures: bf16
-    // rows with an eighth without weight, in steady state).
+    // CTAs per row and threads per CTA (the kernels' registers leave an SM 1,536
+    // threads; figures: bf16 rows with an eighth without weight, in steady state).
     // With the gradient the slices in flight should fill L2 and no more, 72 MB: they
     // are read again from there.  One CTA a row while its 512 threads keep to that,
     // else twice the fewest that do, and as few threads as do (8,192 x 128,000: 687
@@ -1046,8 +1046,11 @@ hess_status launch_typed(DistillArgs& a, int sms, cudaStream_t s) {
     // 902 with 1 of 512; 4,096 x 100,000: 290 us with 4 of 192, 318 with 2 of 512;
     // 4,096 x 65,536: 184 us with 1 of 512, 198 with 2 of 256).
     // Without it one CTA, and small ones, which hide each other's start (8,192 x
-    // 128,000: 273 us with 256 threads, 298 with 512, 315 with 128; 4,096 x 65,536:
-    // 74 us with 128, 79 with 256, 99 with 512).
+    // 128,000: 266 us with 256 threads, 291 with 512, 313 with 128; 4,096 x 65,536:
+    // 72 us with 128, 76 with 256, 98 with 512).  Rows between those two widths go
+    // with the wider ones: 128 threads are 7 % faster there for many of them (8,192 x
+    // 96,000: 201 against 214) up to some 12,000 granules (8,192 x 112,000: 286
+    // against 244), but slower where 256 make one wave (904 x 96,000: 42 against 29).
     a.segments = (granules + kSegment - 1) / kSegment;
     const auto slice_at = [&](int c) { return (a.segments + c - 1) / c * kSegment; };
     const auto fits = [&](int c) { return dynamic_bytes(slice_at(c), a.segments, a.top) <= kMaxDynamic; };
@@ -1078,7 +1081,7 @@ hess_status launch_typed(DistillArgs& a, int sms, cudaStream_t s) {
         const int64_t t = 1536 / ((ctas + sms - 1) / sms) / 32 * 32;
         if (t >= 128 && 2 * t >= threads && slice_at(C) <= 110 * t) threads = static_cast<int>(t);
     }
-    // not reached: the widest vocabulary in f32, 8 CTAs and the longest list take 217 KB
+    // not reached: the widest vocabulary in f32, 8 CTAs and the longest list take 185 KB
     if (!fits(C))
         return ds_fail(HESS_ERR_UNSUPPORTED, "vocab %d is too wide for the bits of its columns", a.vocab);
     a.slice = slice_at(C);

@@ -2,8 +2,9 @@
 
 Argument marshalling only: tensors become device pointers, sizes and row
 strides; the loss and its gradient run in the library's CUDA kernels.  The
-functions carry the C names and allocate their outputs; ``distill_loss`` is
-the same loss as a node of an autograd graph.
+functions carry the C names and allocate their outputs; a gradient written
+into a caller's tensor (``out``) is an in-place change of it for autograd.
+``distill_loss`` is the same loss as a node of an autograd graph.
 """
 
 from __future__ import annotations

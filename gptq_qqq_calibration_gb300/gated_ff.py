@@ -102,8 +102,9 @@ class GatedFF:
     ``forward`` and ``backward`` take [..., d] and [..., f] tensors of the
     object's type; weights are [f, d] and belong to the caller, so one object
     serves every layer of these widths.  ``train_tokens`` is the most tokens a
-    backward call will have (its workspace is 4 f bytes a token).  Called as a
-    function, the object is a node of an autograd graph.
+    backward call will have (its workspace is 4 f bytes a token); a backward of
+    more is refused, a forward is not.  Called as a function, the object is a node
+    of an autograd graph.
 
     The object's calls may come on any streams, and may be captured into CUDA
     graphs.  Replays of such graphs are the caller's to order, with each other

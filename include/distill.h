@@ -29,9 +29,15 @@
  *   - An index >= V is an error of the caller that only the device can see:
  *     the row's loss and gradient are NaN, and nothing is accessed there.
  *   - An index that occurs twice in a row counts with the sum of its p.
- *   - Logits of -inf (masked columns) have q = 0 and gradient 0; if the teacher
- *     gives such a column p > 0 the loss is +inf.  A NaN or +inf logit makes
- *     its row NaN, and no other row.
+ *   - Student logits of -inf (masked columns) have q = 0, and gradient 0 outside
+ *     the list; if the teacher gives such a column, or columns outside the list
+ *     that are all -inf, a mass p > 0, the loss is +inf and a listed column's
+ *     gradient still -w tau p.  A NaN or +inf logit of the student makes its row
+ *     NaN, and no other row.  Finite logits with |s| log2(e) / tau past the range of
+ *     fp32 (masks of bfloat16's or float32's lowest value) count as infinite; in the
+ *     list the loss may be very large instead.
+ *   - A NaN among the teacher's values makes its row's loss NaN, and the gradient
+ *     NaN at least in the listed columns.
  *
  * Arithmetic: exponentials and their sums in fp32 (two references, one for the
  * listed columns and one for the others, so neither underflows next to the

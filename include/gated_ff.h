@@ -24,8 +24,9 @@
  * g, u, act and its derivative stay in fp32.  h, dX, dW_gate and dW_up are
  * rounded once, to the input type.  dg and du are rounded to the input type
  * between the two backward kernels, because the tensor cores take 16-bit
- * operands there; each is the fp32 value rounded once.  No atomics: the same
- * call gives the same bits.
+ * operands there; each is the fp32 value rounded once (beyond 65,504 it is
+ * infinite in float16: scale dH down where that may happen).  Sums are taken in a
+ * fixed order, by no atomics: the same call gives the same bits.
  */
 #ifndef GPTQ_QQQ_GATED_FF_H
 #define GPTQ_QQQ_GATED_FF_H

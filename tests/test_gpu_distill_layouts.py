@@ -37,3 +37,45 @@ def test_columns_of_one_buffer(rows, vocab, gap, first, dtype):
     distill_backward(S, stats, out=out, **kw)
     assert torch.equal(out, want_backward) and torch.equal(S, s.cuda())
     assert (buf[:, vocab:vocab + gap] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("mask", ["-inf", "lowest"])
+def test_everything_outside_the_list_masked(dtype, mask):
+    """The teacher has a mass where the student has none: an infinite loss, no
+    gradient outside the list, q - p inside it."""
+    from gptq_qqq_calibration_gb300 import distill_backward, distill_forward, distill_step
+    s, v, i, t = make(3, 3000, 10, dtype, 5)
+    low = -float("inf") if mask == "-inf" else torch.finfo(dtype).min
+    keep = torch.zeros(3, 3000, dtype=torch.bool)
+    keep.scatter_(1, i.long(), True)
+    s[:2] = torch.where(keep[:2], s[:2], torch.tensor(low, dtype=dtype))
+    lse = torch.logsumexp(t, 1).float() + 0.2
+    kw = dict(top_logits=v.cuda(), top_index=i.cuda(), teacher_lse=lse.cuda())
+    loss, d = distill_step(s.cuda(), **kw)
+    loss2, stats = distill_forward(s.cuda(), **kw)
+    d2 = distill_backward(s.cuda(), stats, **kw)
+    assert torch.isinf(loss[:2]).all() and (loss[:2] > 0).all() and torch.equal(loss, loss2)
+    for g in (d.cpu(), d2.cpu()):
+        assert not g[:2][~keep[:2]].any()
+        check(s[2:], v[2:], i[2:], loss.cpu()[2:], g[2:], 1.0, lse[2:])
+        check(torch.where(keep, s, torch.tensor(-float("inf"), dtype=dtype))[:2], v[:2], i[:2], None, g[:2], 1.0,
+              lse[:2])
+
+
+def test_nan_of_the_teacher():
+    from gptq_qqq_calibration_gb300 import distill_step
+    s, v, i, t = make(3, 500, 6, torch.float32, 6)
+    lse = torch.logsumexp(t, 1).float()
+    v[0, 2] = float("nan")
+    for l in (None, lse.clone()):
+        if l is not None:
+            l[1] = float("nan")
+        loss, d = distill_step(s.cuda(), v.cuda(), i.cuda(), teacher_lse=None if l is None else l.cuda())
+        bad = [0] if l is None else [0, 1]
+        for r in range(3):
+            assert bool(torch.isnan(loss[r])) == (r in bad)
+        assert torch.isnan(d[0, i[0, 2].long()])
+        if l is not None:
+            assert torch.isnan(d[1, i[1].long().cuda()]).all()
+        check(s[2:], v[2:], i[2:], loss.cpu()[2:], d.cpu()[2:], 1.0, None if l is None else l[2:])
