@@ -108,7 +108,8 @@ class GatedFF:
 
     The object's calls may come on any streams, and may be captured into CUDA
     graphs.  Replays of such graphs are the caller's to order, with each other
-    and with the object's other calls: they share its workspace.
+    and with the object's other calls: they share its workspace, and need the
+    object to stay alive.
     """
 
     def __init__(self, d: int, f: int, train_tokens: int = 0, dtype: torch.dtype = torch.bfloat16,

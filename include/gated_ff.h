@@ -97,7 +97,8 @@ hess_status gated_ff_sync(gated_ff_t g, hess_stream_t stream);
  * not already satisfied give up). */
 hess_status gated_ff_set_timeout(gated_ff_t g, int64_t ns);
 
-/* Free the handle (waits for the device).  NULL is a no-op. */
+/* Free the handle (waits for the device).  Graphs that captured calls of it must
+ * not be replayed afterwards: its workspace is gone.  NULL is a no-op. */
 hess_status gated_ff_destroy(gated_ff_t g);
 
 #ifdef __cplusplus
