@@ -66,6 +66,8 @@ PROTOTYPES = {
     "gated_ff_create": (_i32, [_i64, _i64, _i64, _i32, _i32, ctypes.POINTER(_vp)]),
     "gated_ff_forward": (_i32, [_vp, _vp, _i64, _vp, _vp, _vp, _vp]),
     "gated_ff_backward": (_i32, [_vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "gated_ff_reserve_rows8": (_i32, [_vp]),
+    "gated_ff_backward_rows8": (_i32, [_vp, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "gated_ff_sync": (_i32, [_vp, _vp]),
     "gated_ff_set_timeout": (_i32, [_vp, _i64]),
     "gated_ff_destroy": (_i32, [_vp]),
@@ -75,6 +77,15 @@ PROTOTYPES = {
                                 _vp, _i64, _vp]),
     "distill_step": (_i32, [_vp, _i64, _i64, _i64, _i32, _vp, _i32, _vp, _i32, _i64, _vp, _vp, _f64, _vp, _vp, _i64,
                             _vp]),
+    "rows8_quantize": (_i32, [_vp, _i64, _i64, _i64, _i32, _i32, _vp, _i64, _vp, _vp]),
+    "rows8_restore": (_i32, [_vp, _i64, _vp, _i64, _i64, _i32, _vp, _i64, _i32, _vp]),
+    "int8_linear_create": (_i32, [_i64, _i64, _i64, _i64, _i32, ctypes.POINTER(_vp)]),
+    "int8_linear_forward": (_i32, [_vp, _vp, _i64, _vp, _vp, _vp, _vp]),
+    "int8_linear_forward_rows8": (_i32, [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp]),
+    "int8_linear_backward": (_i32, [_vp, _vp, _i64, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "int8_linear_sync": (_i32, [_vp, _vp]),
+    "int8_linear_set_timeout": (_i32, [_vp, _i64]),
+    "int8_linear_destroy": (_i32, [_vp]),
     "hess_last_error": (ctypes.c_char_p, []),
     "hess_abi_version": (_i32, []),
 }

@@ -49,8 +49,10 @@
 #include "device_ptr.h"
 #include "gated_ff.h"
 #include "gated_ff_schedule.cuh"
+#include "int8_linear.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
+#include "rows8.cuh"
 #include "workspace_order.h"
 
 namespace hk {
@@ -908,6 +910,7 @@ struct gated_ff_ctx {
     void* dg = nullptr;       // [train_tokens, f] each
     void* du = nullptr;
     uint32_t* status = nullptr;
+    void* restored = nullptr;  // X^ [train_tokens, d] of gated_ff_backward_rows8, once it is reserved
     hk::WorkspaceOrder order;  // of the calls that use that memory
     unsigned long long timeout_ns = 2000000000ull;
 };
@@ -991,10 +994,14 @@ hess_status ff_launch(Kernel kernel, const Params& p, int64_t grid, int threads,
 }
 
 template <int kWhat>
-hess_status ff_launch_pairs(const gated_ff_ctx* g, const FfParams& p, cudaStream_t s) {
-    const int pairs = p.n_units < g->pairs ? p.n_units : g->pairs;
-    return ff_launch(g->dtype == HESS_BF16 ? gated_ff_kernel<__nv_bfloat16, kWhat> : gated_ff_kernel<__half, kWhat>, p,
+hess_status ff_launch_resident(int resident, int32_t dtype, const FfParams& p, cudaStream_t s) {
+    const int pairs = p.n_units < resident ? p.n_units : resident;
+    return ff_launch(dtype == HESS_BF16 ? gated_ff_kernel<__nv_bfloat16, kWhat> : gated_ff_kernel<__half, kWhat>, p,
                      2 * pairs, kThreads, kSmemBytes, s);
+}
+template <int kWhat>
+hess_status ff_launch_pairs(const gated_ff_ctx* g, const FfParams& p, cudaStream_t s) {
+    return ff_launch_resident<kWhat>(g->pairs, g->dtype, p, s);
 }
 
 // The handle's workspace has one user at a time.
@@ -1053,10 +1060,38 @@ hess_status ff_tokens(int64_t n) {
 
 void ff_free(gated_ff_ctx* g) {
     cudaFree(g->memory);
+    cudaFree(g->restored);
     g->order.destroy();
 }
 
 }  // namespace
+
+hess_status ff_resident_pairs(int dev, int* pairs, int* sms) { return ff_prepare(dev, pairs, sms); }
+
+hess_status ff_gradients_single(const FfSingle& a, cudaStream_t s) {
+    FfParams p{};
+    p.n = static_cast<int32_t>(a.n);
+    p.d = static_cast<int32_t>(a.d);
+    p.f = static_cast<int32_t>(a.f);
+    p.single = 1;
+    p.fmt = a.dtype == HESS_BF16 ? 1u : 0u;
+    p.pieces = a.pieces;
+    p.arrived = a.arrived;
+    p.status = a.status;
+    p.timeout_ns = a.timeout_ns;
+    FF_CHECK(ff_encode(&p.maps[kMapDg], a.dY, a.dtype, a.n, a.f));
+    if (a.dX) {
+        FF_CHECK(ff_encode(&p.maps[kMapWg], a.W, a.dtype, a.f, a.d));
+        FF_CHECK(ff_encode(&p.maps[kMapOut0], a.dX, a.dtype, a.n, a.d, 128));
+    }
+    if (a.dW) {
+        FF_CHECK(ff_encode(&p.maps[kMapX], a.X, a.dtype, a.n, a.d));
+        FF_CHECK(ff_encode(&p.maps[kMapOut1], a.dW, a.dtype, a.f, a.d, 128));
+    }
+    plan_gradients(p, a.pairs, a.dX != nullptr, a.dW != nullptr);
+    return ff_launch_resident<kGradients>(a.pairs, a.dtype, p, s);
+}
+
 }  // namespace hk
 
 using hk::ff_fail;
@@ -1147,11 +1182,20 @@ FF_EXPORT hess_status gated_ff_forward(gated_ff_t g, const void* X, int64_t n_to
     return hk::ff_end(g, s);
 }
 
-FF_EXPORT hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_tokens, const void* W_gate,
-                                        const void* W_up, const void* dH, void* dX_out, void* dW_gate_out,
-                                        void* dW_up_out, hess_stream_t stream) {
+// 8-bit rows in the place of X.
+struct FfKept {
+    const int8_t* codes;
+    const float* scale;
+    int32_t group;
+};
+
+static hess_status ff_backward(gated_ff_t g, const void* X, const FfKept* kept, int64_t n_tokens, const void* W_gate,
+                               const void* W_up, const void* dH, void* dX_out, void* dW_gate_out, void* dW_up_out,
+                               hess_stream_t stream) {
     if (!g) return ff_fail(HESS_ERR_INVALID, "handle is NULL");
     FF_CHECK(hk::ff_tokens(n_tokens));
+    if (kept && kept->group != 0 && kept->group != 32 && kept->group != 64 && kept->group != 128 && kept->group != 256)
+        return ff_fail(HESS_ERR_UNSUPPORTED, "group must be 0, 32, 64, 128 or 256, got %d", kept->group);
     if ((dW_gate_out == nullptr) != (dW_up_out == nullptr))
         return ff_fail(HESS_ERR_INVALID, "dW_gate_out and dW_up_out must both be given or both be NULL");
     std::lock_guard<std::mutex> lk(g->mu);
@@ -1159,9 +1203,23 @@ FF_EXPORT hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_t
         return ff_fail(HESS_ERR_INVALID, "n_tokens %lld exceeds the handle's train_tokens %lld",
                            static_cast<long long>(n_tokens), static_cast<long long>(g->train_tokens));
     FF_CHECK(hk::ff_check_device(g));
+    if (kept) {
+        if (!g->restored) return ff_fail(HESS_ERR_INVALID, "gated_ff_reserve_rows8 has not been called");
+        if (n_tokens > 0) {
+            char why[128];
+            if (!kept->codes || !kept->scale) return ff_fail(HESS_ERR_INVALID, "X_codes or X_scale is NULL");
+            if (reinterpret_cast<uintptr_t>(kept->scale) % 4)
+                return ff_fail(HESS_ERR_INVALID, "X_scale is not aligned to its element");
+            if (const char* w = hk::device_ptr_problem(kept->codes, g->device, why))
+                return ff_fail(HESS_ERR_INVALID, "X_codes %s", w);
+            if (const char* w = hk::device_ptr_problem(kept->scale, g->device, why))
+                return ff_fail(HESS_ERR_INVALID, "X_scale %s", w);
+        }
+        X = g->restored;
+    }
     const bool want_x = dX_out != nullptr && n_tokens > 0, want_w = dW_gate_out != nullptr;
     if (n_tokens > 0) {
-        FF_CHECK(hk::ff_check(g, X, "X"));
+        if (!kept) FF_CHECK(hk::ff_check(g, X, "X"));
         FF_CHECK(hk::ff_check(g, W_gate, "W_gate"));
         FF_CHECK(hk::ff_check(g, W_up, "W_up"));
         FF_CHECK(hk::ff_check(g, dH, "dH"));
@@ -1172,8 +1230,13 @@ FF_EXPORT hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_t
         FF_CHECK(hk::ff_check(g, dW_up_out, "dW_up_out"));
     }
     const int64_t weights = g->f * g->d;
-    const hk::FfBuffer in[] = {{X, n_tokens * g->d, "X"}, {W_gate, weights, "W_gate"}, {W_up, weights, "W_up"},
-                               {dH, n_tokens * g->f, "dH"}};
+    // sizes in elements of two bytes
+    const int64_t groups = kept && kept->group ? (g->d + kept->group - 1) / kept->group : 1;
+    const void* const x_in = kept ? kept->codes : X;
+    const void* const scale_in = kept ? kept->scale : nullptr;
+    const int64_t x_size = kept ? (n_tokens * g->d + 1) / 2 : n_tokens * g->d;
+    const hk::FfBuffer in[] = {{x_in, x_size, kept ? "X_codes" : "X"}, {scale_in, 2 * n_tokens * groups, "X_scale"},
+                               {W_gate, weights, "W_gate"}, {W_up, weights, "W_up"}, {dH, n_tokens * g->f, "dH"}};
     const hk::FfBuffer result[] = {{dX_out, n_tokens * g->d, "dX_out"}, {dW_gate_out, weights, "dW_gate_out"},
                                    {dW_up_out, weights, "dW_up_out"}};
     if (n_tokens > 0) FF_CHECK(hk::ff_apart(in, result));
@@ -1207,10 +1270,42 @@ FF_EXPORT hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_t
     }
     hk::plan_gradients(q, g->pairs, want_x, want_w);
     FF_CHECK(hk::ff_begin(g, s));
+    if (kept)
+        FF_TRY(hk::rows8_restore_launch(kept->codes, g->d, kept->scale, n_tokens, g->d, kept->group, g->restored, g->d,
+                                        g->dtype, s));
     FF_CHECK(hk::ff_launch_pairs<hk::kActGrad>(g, p, s));
     const hess_status st = hk::ff_launch_pairs<hk::kGradients>(g, q, s);
     FF_CHECK(hk::ff_end(g, s));
     return st;
+}
+
+FF_EXPORT hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_tokens, const void* W_gate,
+                                        const void* W_up, const void* dH, void* dX_out, void* dW_gate_out,
+                                        void* dW_up_out, hess_stream_t stream) {
+    return ff_backward(g, X, nullptr, n_tokens, W_gate, W_up, dH, dX_out, dW_gate_out, dW_up_out, stream);
+}
+
+FF_EXPORT hess_status gated_ff_reserve_rows8(gated_ff_t g) {
+    if (!g) return ff_fail(HESS_ERR_INVALID, "handle is NULL");
+    std::lock_guard<std::mutex> lk(g->mu);
+    FF_CHECK(hk::ff_check_device(g));
+    if (g->restored) return HESS_OK;
+    if (g->train_tokens == 0) return ff_fail(HESS_ERR_INVALID, "the handle's train_tokens is 0");
+    if (hk::ff_injected("alloc")) return ff_fail(HESS_ERR_OOM, "injected allocation failure (HESS_FAULT=alloc)");
+    const cudaError_t e = cudaMalloc(&g->restored, static_cast<size_t>(g->train_tokens) * static_cast<size_t>(g->d) * 2);
+    if (e == cudaSuccess) return HESS_OK;
+    g->restored = nullptr;
+    if (e == cudaErrorMemoryAllocation) cudaGetLastError();
+    return ff_fail(e == cudaErrorMemoryAllocation ? HESS_ERR_OOM : HESS_ERR_CUDA, "gated_ff_reserve_rows8: %s",
+                   cudaGetErrorString(e));
+}
+
+FF_EXPORT hess_status gated_ff_backward_rows8(gated_ff_t g, const int8_t* X_codes, const float* X_scale, int32_t group,
+                                              int64_t n_tokens, const void* W_gate, const void* W_up, const void* dH,
+                                              void* dX_out, void* dW_gate_out, void* dW_up_out,
+                                              hess_stream_t stream) {
+    const FfKept kept{X_codes, X_scale, group};
+    return ff_backward(g, nullptr, &kept, n_tokens, W_gate, W_up, dH, dX_out, dW_gate_out, dW_up_out, stream);
 }
 
 FF_EXPORT hess_status gated_ff_sync(gated_ff_t g, hess_stream_t stream) {

@@ -20,10 +20,11 @@ struct FfSchedule {
     int32_t n, d, f;
     int32_t whole;    // kForward, kActGrad: tiles that are not split; they come first
     int32_t parts;    // units of each tile after them, or of each tile of dX
-    int32_t units_x;  // kGradients: units of dX (first), then 2 * tiles_w tiles of dWg and dWu
+    int32_t units_x;  // kGradients: units of dX (first), then tiles_w tiles of dWg, and as many of dWu
     int32_t tiles_w;
     int32_t n_units;
     int32_t skip;     // kGradients: turns of dW tiles that one tile of dX is worth
+    int32_t single;   // kGradients: 1 where there is one weight (dX = dg Wg, dW = dg^T X), 0 for the pair
 };
 
 // Tile u of tm x tn, in groups of kGroupM row tiles walked column by column.
@@ -88,7 +89,7 @@ __host__ __device__ inline Unit unit_at(const FfSchedule& p, int u) {
         r.m0 = m * 256;
         r.n0 = n * 256;
         r.half = (p.f + kKB - 1) / kKB;
-        n_kb = 2 * r.half;
+        n_kb = p.single ? r.half : 2 * r.half;
     } else {
         u -= p.units_x;
         r.which = u >= p.tiles_w ? 1 : 0;
@@ -131,17 +132,18 @@ inline void plan_projections(FfSchedule& p, int64_t pairs) {
     p.n_units = static_cast<int32_t>(p.parts > 1 ? p.whole + rest * p.parts : tiles);
 }
 
-// Units of dX, and of both weight gradients.
+// Units of dX, and of the weight gradients (p.single is set).
 inline void plan_gradients(FfSchedule& p, int64_t pairs, bool want_x, bool want_w) {
     const int64_t tiles_x = want_x ? ceil_div(p.n, 256) * ceil_div(p.d, 256) : 0;
     const int64_t tiles_w = want_w ? ceil_div(p.f, 256) * ceil_div(p.d, 256) : 0;
-    const int64_t kb_x = 2 * ceil_div(p.f, kKB), kb_w = ceil_div(p.n, kKB);
+    const int64_t weights = p.single ? 1 : 2;
+    const int64_t kb_x = weights * ceil_div(p.f, kKB), kb_w = ceil_div(p.n, kKB);
     // in the share of each pair a tile of dW counts at least its write-out, some 10 boxes
     p.parts = parts_of(tiles_x, kb_x, pairs,
-                       ceil_div(tiles_x * kb_x + 2 * tiles_w * (kb_w > 10 ? kb_w : 10), pairs));
+                       ceil_div(tiles_x * kb_x + weights * tiles_w * (kb_w > 10 ? kb_w : 10), pairs));
     p.units_x = static_cast<int32_t>(tiles_x * p.parts);
     p.tiles_w = static_cast<int32_t>(tiles_w);
-    p.n_units = p.units_x + 2 * p.tiles_w;
+    p.n_units = p.units_x + static_cast<int32_t>(weights) * p.tiles_w;
     const int64_t kb_unit = kb_x / p.parts;
     p.skip = want_x && want_w ? static_cast<int32_t>((kb_unit + kb_w / 2) / kb_w) : 0;
 }

@@ -1,0 +1,1140 @@
+// The 8-bit integer linear layer (formulas and conventions: include/int8_linear.h).
+//
+// GB300's int8 tensor rate is a small fraction of its float16 rate, but int8 values
+// are float16 numbers, their products (at most 2^14) are exact in float32, and so is a
+// sum of 1,024 of them (at most 2^24).  So the products run on tcgen05 kind::f16, and
+// every 1,024 steps of the contraction the tile's float32 sums, whole numbers, are
+// added to int32 registers: the result is the exact integer, whatever the codes.
+//
+// Weights stay int8 in memory and on the way to the SM.  They are the MMA's rows (Y^T =
+// Wq Xq^T): converter warps read a row's bytes from shared memory, turn them into
+// float16 in registers and put them into tensor memory, from where tcgen05.mma takes
+// its A operand.  A byte becomes a float16 by a byte permutation (0x6400 | b is 1024 + b)
+// and one subtraction for two.  Shared memory then carries, per 64 steps of a 128 x 192
+// tile per CTA, 8 KB of bytes twice and 12 KB of tokens twice; with the weights as an
+// operand in shared memory it would be 56 KB, more than its rate allows in the MMAs' time.
+// The tokens are quantized to float16 whole numbers by a kernel in front (2 n d bytes).
+//
+// Tile: 256 weight rows x up to 192 tokens on a pair of SMs (cta_group::2).  Tensor
+// memory: two 192-column sums, so that one is drained under the other's products, and
+// four slots of 64 steps of A.
+//
+// Few tokens (the weights no longer pay for the trip through tensor memory): one pass
+// over the weights with dp4a, the tokens' codes in registers.
+#include <cstdarg>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <mutex>
+#include <new>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "device_ptr.h"
+#include "int8_linear.cuh"
+#include "int8_linear.h"
+#include "int8_schedule.cuh"
+#include "kernels.cuh"
+#include "ptx.cuh"
+#include "rows8.cuh"
+#include "workspace_order.h"
+
+namespace hk {
+namespace {
+
+using namespace i8;
+
+constexpr int kMaxStages = 12;
+constexpr uint32_t kRing = 208 * 1024;
+constexpr int kSlots = 4;             // of 64 steps of A in tensor memory, 32 columns each
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSlotCol = 2 * kMaxTok;
+static_assert(kSlotCol + kSlots * 32 <= kTmemCols, "tensor memory");
+constexpr int kNumBarriers = 4 * kMaxStages + 2 * kSlots + 5;
+constexpr size_t kSmemBytes = 1024 + kRing + 8 * kNumBarriers + 16;
+constexpr int kThreads = 512;  // warp 0: weights, 1: MMAs, 2: tokens, 4-11: converters, 12-15: epilogue
+constexpr unsigned long long kDrainLimitNs = 1000000000ull;
+constexpr unsigned long long kAbortSettleNs = 2000000ull;
+constexpr int64_t kPieceInts = 2 * kMaxTok * kMaxRows;  // both CTAs' sums of one unit
+
+struct PairParams : Schedule {
+    CUtensorMap x, w;  // float16 codes [n, d], boxes of tok/2 rows x 64; weights [f, d], boxes of rows x 128
+    int32_t stages;
+    uint32_t w_bytes, stage_bytes;  // of a stage; the tokens' two boxes follow the weights
+    const float *x_scale, *w_scale;
+    void* out;
+    int32_t* pieces;    // sums of every unit of a split tile
+    uint32_t* arrived;  // units of each split tile that have come, per CTA; zero between launches
+    uint32_t* status;
+    unsigned long long timeout_ns;
+};
+
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// D (M = 256 across the pair) (+)= A[tensor memory] * B[shared memory], f16, issued by the even CTA.
+__device__ __forceinline__ void umma_f16_pair_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                                 uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t (&a)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
+          "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15])
+        : "r"(t)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t (&a)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(t),
+        "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(a[4]), "r"(a[5]), "r"(a[6]), "r"(a[7]), "r"(a[8]), "r"(a[9]),
+        "r"(a[10]), "r"(a[11]), "r"(a[12]), "r"(a[13]), "r"(a[14]), "r"(a[15]), "r"(a[16]), "r"(a[17]), "r"(a[18]),
+        "r"(a[19]), "r"(a[20]), "r"(a[21]), "r"(a[22]), "r"(a[23]), "r"(a[24]), "r"(a[25]), "r"(a[26]), "r"(a[27]),
+        "r"(a[28]), "r"(a[29]), "r"(a[30]), "r"(a[31])
+        : "memory");
+}
+
+// Four int8 as two words of two float16: 1024 + (q + 128), less 1152.
+__device__ __forceinline__ void widen4(uint32_t q, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = q ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 k = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    __half2 x, y;
+    memcpy(&x, &a, 4);
+    memcpy(&y, &b, 4);
+    x = __hsub2(x, k);
+    y = __hsub2(y, k);
+    memcpy(&lo, &x, 4);
+    memcpy(&hi, &y, 4);
+}
+
+template <class T>
+__device__ __forceinline__ T rounded(float x);
+template <>
+__device__ __forceinline__ __half rounded<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// The epilogue warps' barrier, and whether any thread came with `x`.
+__device__ __forceinline__ bool epi_barrier_any(bool x) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(static_cast<uint32_t>(x))
+        : "memory");
+    return any != 0;
+}
+
+// Every wait is bounded.  The launch before this one is the kernel that writes the
+// tokens' codes and scales; it waits for all work before it and only then lets this
+// one start, so that only what it writes itself has to be waited for here.
+template <class T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    int8_pair_kernel(const __grid_constant__ PairParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* const gbase = smem_raw + (base - raw);
+    const uint32_t bar0 = base + kRing;
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + kRing + 8 * kNumBarriers);
+    auto wfull_bar = [&](int s) { return bar0 + 8u * s; };                      // this CTA's weights have landed
+    auto wempty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };      // its converters have read them
+    auto xfull_bar = [&](int s) { return bar0 + 8u * (2 * kMaxStages + s); };   // even CTA: the pair's tokens
+    auto xempty_bar = [&](int s) { return bar0 + 8u * (3 * kMaxStages + s); };  // MMAs have read them
+    auto afull_bar = [&](int s) { return bar0 + 8u * (4 * kMaxStages + s); };   // even CTA: the pair's slot of A
+    auto aempty_bar = [&](int s) { return bar0 + 8u * (4 * kMaxStages + kSlots + s); };
+    auto accf_bar = [&](int b) { return bar0 + 8u * (4 * kMaxStages + 2 * kSlots + b); };
+    auto acce_bar = [&](int b) { return bar0 + 8u * (4 * kMaxStages + 2 * kSlots + 2 + b); };
+    const uint32_t drain_bar = bar0 + 8u * (4 * kMaxStages + 2 * kSlots + 4);
+    __shared__ volatile int aborted;
+    __shared__ volatile int epi_last;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+    const unsigned long long limit = p.timeout_ns;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(wfull_bar(s), 1);
+            mbar_init(wempty_bar(s), 8);
+            mbar_init(xfull_bar(s), 1);
+            mbar_init(xempty_bar(s), 1);
+        }
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(afull_bar(s), 8);  // four converter warps of each CTA
+            mbar_init(aempty_bar(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(accf_bar(b), 1);
+            mbar_init(acce_bar(b), 8);  // four epilogue warps of each CTA
+        }
+        mbar_init(drain_bar, 1);
+        aborted = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&p.w);
+        prefetch_tensormap(&p.x);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+
+    if (warp < 4) {
+        setmaxnreg_dec<48>();
+        if (warp == 0 && lane == 0) {
+            bool ok = true;
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int u = pair; ok && u < p.n_units; u += n_pairs) {
+                const Unit un = unit_at(p, u);
+                const int row = un.f0 + static_cast<int>(rank) * p.rows;
+                for (int kb = un.kb0; kb < un.kb1; ++kb) {
+                    if (!mbar_wait(wempty_bar(stage), phase ^ 1u, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(wfull_bar(stage), static_cast<uint32_t>(p.rows) * kKB);
+                    tma_load_2d(base + stage * p.stage_bytes, &p.w, wfull_bar(stage), kb * kKB, row);
+                    if (++stage == p.stages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                atomicOr(p.status, kStatusTimeoutLoad);
+                aborted = 1;
+            }
+        } else if (warp == 2 && lane == 0) {
+            griddep_wait();
+            griddep_launch_dependents();
+            bool ok = true;
+            int stage = 0;
+            uint32_t phase = 0;
+            const uint32_t box = static_cast<uint32_t>(p.tok) * 64u;  // tok / 2 rows of 128 bytes
+            for (int u = pair; ok && u < p.n_units; u += n_pairs) {
+                const Unit un = unit_at(p, u);
+                const int row = un.t0 + static_cast<int>(rank) * (p.tok / 2);
+                for (int kb = un.kb0; kb < un.kb1; ++kb) {
+                    if (!mbar_wait_cluster(xempty_bar(stage), phase ^ 1u, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t at = base + stage * p.stage_bytes + p.w_bytes;
+                    const uint32_t fb = mapa_shared(xfull_bar(stage), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(xfull_bar(stage), 4 * box);
+                    tma_load_2d_pair(at, &p.x, fb, kb * kKB, row);
+                    tma_load_2d_pair(at + box, &p.x, fb, kb * kKB + 64, row);
+                    if (++stage == p.stages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                atomicOr(p.status, kStatusTimeoutLoad);
+                aborted = 1;
+            }
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            bool ok = true;
+            int stage = 0, slot = 0, ab = 0;
+            uint32_t phase = 0, sphase = 0, aphase = 0;
+            const uint32_t box = static_cast<uint32_t>(p.tok) * 64u;
+            // float32 sums, float16 operands, both contiguous along the contraction
+            const uint32_t idesc = (1u << 4) | ((static_cast<uint32_t>(p.tok) >> 3) << 17) | ((256u >> 4) << 24);
+            for (int u = pair; ok && u < p.n_units; u += n_pairs) {
+                const Unit un = unit_at(p, u);
+                for (int c0 = un.kb0; ok && c0 < un.kb1; c0 += kChunk) {
+                    if (!mbar_wait_cluster(acce_bar(ab), aphase ^ 1u, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t acc = tmem + static_cast<uint32_t>(ab * kMaxTok);
+                    const int c1 = c0 + kChunk < un.kb1 ? c0 + kChunk : un.kb1;
+                    for (int kb = c0; ok && kb < c1; ++kb) {
+                        if (!mbar_wait_cluster(xfull_bar(stage), phase, limit)) {
+                            ok = false;
+                            break;
+                        }
+                        for (int h = 0; h < 2; ++h) {
+                            if (!mbar_wait_cluster(afull_bar(slot), sphase, limit)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const uint32_t sB = base + stage * p.stage_bytes + p.w_bytes + h * box;
+                            const uint32_t a = tmem + kSlotCol + static_cast<uint32_t>(slot) * 32u;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                umma_f16_pair_ta(acc, a + j * 8u, smem_desc_sw128(sB + j * 32u, 16u, 1024u), idesc,
+                                                 kb != c0 || h != 0 || j != 0 ? 1u : 0u);
+                            tc_commit_pair_mc(aempty_bar(slot), 0x3);
+                            if (++slot == kSlots) {
+                                slot = 0;
+                                sphase ^= 1u;
+                            }
+                        }
+                        if (!ok) break;
+                        tc_commit_pair_mc(xempty_bar(stage), 0x3);
+                        if (++stage == p.stages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    tc_commit_pair_mc(accf_bar(ab), 0x3);
+                    if (++ab == 2) {
+                        ab = 0;
+                        aphase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                atomicOr(p.status, kStatusTimeoutMma);
+                aborted = 1;
+            }
+            // every MMA issued has completed before the pair's memories are released
+            tc_commit_pair_mc(drain_bar, 0x1);
+            if (!mbar_wait(drain_bar, 0, kDrainLimitNs)) atomicOr(p.status, kStatusTimeoutDrain);
+        }
+    } else if (warp < 12) {
+        // Converters: the first four warps take the first 64 steps of each stage, the
+        // others the rest.  A thread owns one weight row.
+        setmaxnreg_dec<96>();
+        const int h = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const bool some = (warp & 3) * 32 < p.rows, mine = row < p.rows;
+        const uint32_t afull0 = mapa_shared(afull_bar(0), 0);
+        bool ok = true;
+        int stage = 0, slot = h;
+        uint32_t phase = 0, sphase = 0;
+        for (int u = pair; ok && u < p.n_units; u += n_pairs) {
+            const Unit un = unit_at(p, u);
+            for (int kb = un.kb0; kb < un.kb1; ++kb) {
+                if (!mbar_wait(wfull_bar(stage), phase, limit)) {
+                    ok = false;
+                    break;
+                }
+                uint32_t a[32];
+                const uint32_t src = base + stage * p.stage_bytes + row * 128u;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 v = mine ? lds128(src + (((h * 4 + j) ^ (row & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+                    widen4(v.x, a[8 * j], a[8 * j + 1]);
+                    widen4(v.y, a[8 * j + 2], a[8 * j + 3]);
+                    widen4(v.z, a[8 * j + 4], a[8 * j + 5]);
+                    widen4(v.w, a[8 * j + 6], a[8 * j + 7]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(wempty_bar(stage));
+                if (!mbar_wait_cluster(aempty_bar(slot), sphase ^ 1u, limit)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (some) tmem_st32(tmem + lanes + kSlotCol + static_cast<uint32_t>(slot) * 32u, a);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(afull0 + 8u * slot);
+                slot ^= 2;
+                if (slot == h) sphase ^= 1u;
+                if (++stage == p.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            atomicOr(p.status, kStatusTimeoutLoad);
+            aborted = 1;
+        }
+    } else {
+        // Epilogue: a thread owns one weight row (an output channel) of up to 192 tokens.
+        setmaxnreg_inc<240>();
+        griddep_wait();
+        const int q = warp & 3, row = q * 32 + lane;
+        const uint32_t acce0 = mapa_shared(acce_bar(0), 0);
+        bool failed = false;
+        int ab = 0;
+        uint32_t aphase = 0;
+        int32_t sum[kMaxTok];
+        for (int u = pair; u < p.n_units; u += n_pairs) {
+            const Unit un = unit_at(p, u);
+#pragma unroll
+            for (int c = 0; c < kMaxTok; ++c) sum[c] = 0;
+            for (int c0 = un.kb0; c0 < un.kb1; c0 += kChunk) {
+                // the warps agree on whether a wait ran out, so that all of them pass the
+                // same barriers
+                failed = epi_barrier_any(failed || !mbar_wait_cluster(accf_bar(ab), aphase, limit));
+                tc_fence_after();
+                if (!failed) {
+                    const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(ab * kMaxTok);
+#pragma unroll
+                    for (int c = 0; c < kMaxTok; c += 16) {
+                        if (c < p.tok) {
+                            uint32_t v[16];
+                            tmem_ld16(acc + c, v);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) sum[c + i] += __float2int_rn(__uint_as_float(v[i]));
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(acce0 + 8u * ab);
+                if (++ab == 2) {
+                    ab = 0;
+                    aphase ^= 1u;
+                }
+            }
+            bool finish = !failed;
+            if (un.parts > 1) {
+                // pieces: [token][row], so that a warp moves 128 bytes at a time
+                int32_t* const piece0 = p.pieces + static_cast<int64_t>(un.split) * un.parts * kPieceInts +
+                                        rank * (kPieceInts / 2) + row;
+                if (!failed) {
+                    int32_t* const out = piece0 + un.part * kPieceInts;
+#pragma unroll
+                    for (int c = 0; c < kMaxTok; ++c)
+                        if (c < p.tok) __stcg(out + c * kMaxRows, sum[c]);
+                    __threadfence();
+                }
+                epi_barrier_any(false);
+                if (warp == 12 && lane == 0) {
+                    uint32_t* const count = p.arrived + 2 * un.split + rank;
+                    const bool last = !failed && atomicAdd(count, 1u) == static_cast<uint32_t>(un.parts - 1);
+                    if (last) *count = 0;
+                    epi_last = last;
+                }
+                epi_barrier_any(false);
+                finish = epi_last != 0;
+                if (finish) {
+                    __threadfence();
+                    for (int k = 0; k < un.parts; ++k) {
+                        if (k == un.part) continue;
+                        const int32_t* const in = piece0 + k * kPieceInts;
+#pragma unroll
+                        for (int c = 0; c < kMaxTok; c += 16) {
+                            if (c < p.tok) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) sum[c + i] += __ldcg(in + (c + i) * kMaxRows);
+                            }
+                        }
+                    }
+                }
+                epi_barrier_any(false);  // epi_last may be written again
+            }
+            const int ch = un.f0 + static_cast<int>(rank) * p.rows + row;
+            if (finish && row < p.rows && ch < p.f) {
+                const float sw = p.w_scale[ch];
+                T* const out = static_cast<T*>(p.out) + static_cast<int64_t>(un.t0) * p.f + ch;
+                const int n = p.n - un.t0;  // tokens of this tile
+#pragma unroll
+                for (int c = 0; c < kMaxTok; ++c)
+                    if (c < p.tok && c < n)
+                        out[static_cast<int64_t>(c) * p.f] =
+                            rounded<T>(__fmul_rn(__int2float_rn(sum[c]), __fmul_rn(p.x_scale[un.t0 + c], sw)));
+            }
+        }
+        if (failed && lane == 0) {
+            atomicOr(p.status, kStatusTimeoutEpilogue);
+            aborted = 1;
+        }
+    }
+
+    // After a timeout copies still in flight (a CTA cannot watch all of its own: the
+    // tokens' count on the even CTA's barrier) get time to land before the memory goes.
+    __syncthreads();
+    if (aborted != 0) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < kAbortSettleNs) __nanosleep(1000);
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------- few tokens
+//
+// Reading the weights once is what takes time, so a CTA takes the same number of weight
+// rows on every SM and streams them straight into registers.  A thread owns kGran
+// granules of 16 columns and keeps their codes of all kTok tokens in registers; `wr` warps
+// cover a row, and the CTA's warps cover `rp` rows side by side.  Four dp4a a granule
+// and token, one warp reduction a row and token, integer adds in shared memory across
+// warps: exact and independent of the order.
+
+constexpr int kFewMaxThreads = 512;
+
+struct FewParams {
+    const void* x;          // 16-bit activations, or NULL:
+    const int8_t* x_codes;  // 8-bit rows
+    const float* x_scale;
+    const int8_t* w;
+    const float* w_scale;
+    void* out;
+    int32_t n, d, f;
+    int32_t wr, rp;      // warps of a row, rows side by side
+    int32_t rows;        // rows of a CTA
+};
+
+// As rows8_quantize: rint of the exact quotient x / s (see rows8.cu).
+__device__ __forceinline__ int few_code(float x, float s, float r) {
+    const float t = fminf(fmaxf(__fmul_rn(x, r), -127.0f), 127.0f);
+    float q = rintf(t);
+    if (fabsf(__fsub_rn(t, q)) > 0.5f - 1.0f / 32768.0f) {
+        const float lo = floorf(t), half = __fadd_rn(lo, 0.5f);
+        const float e = __fmaf_rn(-half, s, x);
+        q = e > 0.0f ? __fadd_rn(lo, 1.0f) : e < 0.0f ? lo : rintf(half);
+    }
+    return static_cast<int>(q);
+}
+
+template <class T>
+__device__ __forceinline__ float2 unpack2f(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2f<__nv_bfloat16>(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 unpack2f<__half>(uint32_t w) {
+    __half2 h;
+    memcpy(&h, &w, 4);
+    return __half22float2(h);
+}
+
+template <class T, int kTok, int kGran>
+__global__ void __launch_bounds__(kFewMaxThreads, 1) int8_few_kernel(const __grid_constant__ FewParams p) {
+    constexpr int kBatch = (kTok == 8 ? 4 : 8) / kGran;  // rows a thread has in flight
+    extern __shared__ int32_t sums[];  // [rows][kTok]
+    __shared__ uint32_t tops[kTok][16];
+    __shared__ float scales[kTok];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warps = blockDim.x >> 5;
+    const int row0 = blockIdx.x * p.rows;
+    const int rows = p.f - row0 < p.rows ? p.f - row0 : p.rows;
+    const int at = warp / p.wr;                                  // which of the rows side by side
+    const int g0 = (warp - at * p.wr) * 32 + lane;               // first granule
+    const int gs = p.wr * 32, granules = p.d >> 4;
+    for (int i = threadIdx.x; i < rows * kTok; i += blockDim.x) sums[i] = 0;
+    griddep_wait();
+    griddep_launch_dependents();
+
+    const int8_t* const w = p.w + static_cast<int64_t>(row0) * p.d;
+    uint4 v[kBatch][kGran];
+    const auto fetch = [&](int r0) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int j = 0; j < kGran; ++j) {
+                const int r = r0 + b * p.rp, g = g0 + j * gs;
+                v[b][j] = r < rows && g < granules
+                              ? __ldcg(reinterpret_cast<const uint4*>(w + static_cast<int64_t>(r) * p.d) + g)
+                              : make_uint4(0, 0, 0, 0);
+            }
+    };
+    fetch(at);
+
+    uint32_t code[kTok][kGran][4];
+    if (p.x_codes) {
+#pragma unroll
+        for (int t = 0; t < kTok; ++t)
+#pragma unroll
+            for (int j = 0; j < kGran; ++j) {
+                const int g = g0 + j * gs;
+                uint4 c = make_uint4(0, 0, 0, 0);
+                if (t < p.n && g < granules)
+                    c = *(reinterpret_cast<const uint4*>(p.x_codes + static_cast<int64_t>(t) * p.d) + g);
+                code[t][j][0] = c.x, code[t][j][1] = c.y, code[t][j][2] = c.z, code[t][j][3] = c.w;
+            }
+        if (threadIdx.x < kTok && threadIdx.x < p.n) scales[threadIdx.x] = p.x_scale[threadIdx.x];
+        __syncthreads();
+    } else {
+        const T* const x = static_cast<const T*>(p.x);
+        const auto value = [&](int t, int j, uint32_t (&raw)[8]) {
+            const int g = g0 + j * gs;
+            uint4 a = make_uint4(0, 0, 0, 0), b = a;
+            if (t < p.n && g < granules) {
+                const uint4* const src = reinterpret_cast<const uint4*>(x + static_cast<int64_t>(t) * p.d) + 2 * g;
+                a = src[0];
+                b = src[1];
+            }
+            raw[0] = a.x, raw[1] = a.y, raw[2] = a.z, raw[3] = a.w;
+            raw[4] = b.x, raw[5] = b.y, raw[6] = b.z, raw[7] = b.w;
+        };
+#pragma unroll
+        for (int t = 0; t < kTok; ++t) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < kGran; ++j) {
+                uint32_t raw[8];
+                value(t, j, raw);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 f = unpack2f<T>(raw[i]);
+                    top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
+                }
+            }
+            top = __reduce_max_sync(~0u, top);
+            if (lane == 0) tops[t][warp] = top;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < kTok; ++t) {
+            uint32_t top = lane < warps ? tops[t][lane] : 0u;
+            top = __reduce_max_sync(~0u, top);
+            const bool finite = top < 0x7f800000u;
+            float s = finite ? __fdiv_rn(__uint_as_float(top), 127.0f) : 0.0f;
+            if (threadIdx.x == 0) scales[t] = finite ? s : __uint_as_float(0x7fffffffu);
+            // a subnormal scale and its values are both taken 2^64 times (exactly)
+            const float up = s < 1.17549435e-38f ? 18446744073709551616.0f : 1.0f;
+            s = __fmul_rn(s, up);
+            const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < kGran; ++j) {
+                uint32_t raw[8];
+                value(t, j, raw);  // from L1 this time
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 a = unpack2f<T>(raw[2 * i]), b = unpack2f<T>(raw[2 * i + 1]);
+                    const int q0 = few_code(__fmul_rn(a.x, up), s, r), q1 = few_code(__fmul_rn(a.y, up), s, r);
+                    const int q2 = few_code(__fmul_rn(b.x, up), s, r), q3 = few_code(__fmul_rn(b.y, up), s, r);
+                    const uint32_t c = __byte_perm(__byte_perm(q0, q1, 0x0040), __byte_perm(q2, q3, 0x0040), 0x5410);
+                    code[t][j][i] = s > 0.0f ? c : 0u;
+                }
+            }
+        }
+    }
+
+    for (int r0 = at; r0 < rows; r0 += kBatch * p.rp) {
+        int32_t acc[kBatch][kTok];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int t = 0; t < kTok; ++t) {
+                int32_t a = 0;
+#pragma unroll
+                for (int j = 0; j < kGran; ++j) {
+                    a = __dp4a(static_cast<int>(v[b][j].x), static_cast<int>(code[t][j][0]), a);
+                    a = __dp4a(static_cast<int>(v[b][j].y), static_cast<int>(code[t][j][1]), a);
+                    a = __dp4a(static_cast<int>(v[b][j].z), static_cast<int>(code[t][j][2]), a);
+                    a = __dp4a(static_cast<int>(v[b][j].w), static_cast<int>(code[t][j][3]), a);
+                }
+                acc[b][t] = a;
+            }
+        if (r0 + kBatch * p.rp < rows) fetch(r0 + kBatch * p.rp);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int r = r0 + b * p.rp;
+            int32_t mine = 0;  // lane t keeps token t's sum
+#pragma unroll
+            for (int t = 0; t < kTok; ++t) {
+                const int32_t a = __reduce_add_sync(~0u, acc[b][t]);
+                if (lane == t) mine = a;
+            }
+            if (lane < kTok && r < rows) atomicAdd(&sums[r * kTok + lane], mine);
+        }
+    }
+    __syncthreads();
+    // channel by channel, so that a warp writes side by side
+    for (int i = threadIdx.x; i < rows * kTok; i += blockDim.x) {
+        const int t = i / rows, r = i - t * rows;
+        if (t < p.n)
+            static_cast<T*>(p.out)[static_cast<int64_t>(t) * p.f + row0 + r] =
+                rounded<T>(__fmul_rn(__int2float_rn(sums[r * kTok + t]), __fmul_rn(scales[t], p.w_scale[row0 + r])));
+    }
+}
+
+// ------------------------------------------------------------- host side
+
+hess_status il_fail(hess_status s, const char* fmt, ...) {
+    char buf[384];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    set_last_error(buf);
+    return s;
+}
+
+#define IL_TRY(call)                                                                           \
+    do {                                                                                       \
+        cudaError_t e_ = (call);                                                               \
+        if (e_ != cudaSuccess)                                                                 \
+            return il_fail(HESS_ERR_CUDA, "%s failed: %s", #call, cudaGetErrorString(e_));     \
+    } while (0)
+#define IL_CHECK(expr)                       \
+    do {                                     \
+        const hess_status st_ = (expr);      \
+        if (st_ != HESS_OK) return st_;      \
+    } while (0)
+
+bool il_injected(const char* what) {
+    const char* f = std::getenv("HESS_FAULT");
+    return f && std::strcmp(f, what) == 0;
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Row-major [rows, cols], boxes of box_rows x 128 bytes in the 128-byte swizzle, zeros past the edges.
+hess_status il_encode(CUtensorMap* m, const void* ptr, bool bytes, int64_t rows, int64_t cols, int64_t box_rows) {
+    static const EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<EncodeTiledFn>(p);
+        return static_cast<EncodeTiledFn>(nullptr);
+    }();
+    if (!fn) return il_fail(HESS_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    if (il_injected("encode"))
+        return il_fail(HESS_ERR_UNSUPPORTED, "injected tensor-map failure (HESS_FAULT=encode)");
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * (bytes ? 1u : 2u)};
+    const cuuint32_t box[2] = {bytes ? 128u : 64u, static_cast<cuuint32_t>(box_rows)}, es[2] = {1u, 1u};
+    const CUresult r = fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                          const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return il_fail(HESS_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled failed (%d) for [%lld, %lld]",
+                       static_cast<int>(r), static_cast<long long>(rows), static_cast<long long>(cols));
+    return HESS_OK;
+}
+
+template <class T>
+auto few_kernel(int tok, int gran) -> void (*)(FewParams) {
+    switch (tok * 16 + gran) {
+        case 1 * 16 + 1: return int8_few_kernel<T, 1, 1>;
+        case 1 * 16 + 2: return int8_few_kernel<T, 1, 2>;
+        case 1 * 16 + 4: return int8_few_kernel<T, 1, 4>;
+        case 1 * 16 + 8: return int8_few_kernel<T, 1, 8>;
+        case 2 * 16 + 1: return int8_few_kernel<T, 2, 1>;
+        case 2 * 16 + 2: return int8_few_kernel<T, 2, 2>;
+        case 2 * 16 + 4: return int8_few_kernel<T, 2, 4>;
+        case 4 * 16 + 1: return int8_few_kernel<T, 4, 1>;
+        case 4 * 16 + 2: return int8_few_kernel<T, 4, 2>;
+        case 8 * 16 + 1: return int8_few_kernel<T, 8, 1>;
+    }
+    return nullptr;
+}
+
+// Per-device set-up: shared-memory limits, and how many pairs stay resident.
+hess_status il_prepare(int dev, int* pairs, int* sms_out) {
+    static std::mutex mu;
+    static int count[128] = {}, sm_count[128] = {};
+    std::lock_guard<std::mutex> lk(mu);
+    if (dev < 0 || dev >= 128) return il_fail(HESS_ERR_UNSUPPORTED, "device index %d", dev);
+    if (!count[dev]) {
+        for (auto fn : {int8_pair_kernel<__nv_bfloat16>, int8_pair_kernel<__half>})
+            IL_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)));
+        int sms = 0;
+        IL_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+        sm_count[dev] = sms;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(sms & ~1), 1, 1);
+        cfg.blockDim = dim3(kThreads, 1, 1);
+        cfg.dynamicSmemBytes = kSmemBytes;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, int8_pair_kernel<__nv_bfloat16>, &cfg) != cudaSuccess ||
+            clusters <= 0) {
+            cudaGetLastError();
+            clusters = sms / 2;
+        }
+        count[dev] = clusters;
+    }
+    *pairs = count[dev];
+    *sms_out = sm_count[dev];
+    return HESS_OK;
+}
+
+}  // namespace
+}  // namespace hk
+
+struct int8_linear_ctx {
+    std::mutex mu;
+    int device = 0;
+    int pairs = 0, ff_pairs = 0, sms = 0;
+    int64_t d = 0, f = 0, tokens = 0, train_tokens = 0;
+    int32_t dtype = 0;
+    void* memory = nullptr;  // holds what follows
+    uint16_t* wide = nullptr;       // [tokens, d] float16 codes
+    float* x_scale = nullptr;       // [tokens]
+    int32_t* pieces = nullptr;      // one per pair
+    void* w_restored = nullptr;     // [f, d]
+    void* x_restored = nullptr;     // [train_tokens, d]
+    float* ff_pieces = nullptr;
+    uint32_t* status = nullptr;     // the status word, then the arrival counts
+    size_t status_bytes = 0;
+    hk::WorkspaceOrder order;  // of the calls that use that memory
+    unsigned long long timeout_ns = 2000000000ull;
+};
+
+namespace hk {
+namespace {
+
+hess_status il_check_device(const int8_linear_ctx* g) {
+    int cur = -1;
+    IL_TRY(cudaGetDevice(&cur));
+    if (cur != g->device)
+        return il_fail(HESS_ERR_INVALID, "handle belongs to device %d but device %d is current", g->device, cur);
+    return HESS_OK;
+}
+
+hess_status il_check(const int8_linear_ctx* g, const void* p, const char* name, int align = 16) {
+    if (!p) return il_fail(HESS_ERR_INVALID, "%s is NULL", name);
+    if (reinterpret_cast<uintptr_t>(p) % align)
+        return il_fail(HESS_ERR_INVALID, "%s is not %d-byte aligned", name, align);
+    char why[128];
+    if (const char* w = device_ptr_problem(p, g->device, why)) return il_fail(HESS_ERR_INVALID, "%s %s", name, w);
+    return HESS_OK;
+}
+
+struct IlBuffer {
+    const void* p;  // NULL: not there
+    int64_t bytes;
+    const char* name;
+};
+hess_status il_apart(const IlBuffer& out, const IlBuffer& in) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(out.p), b = reinterpret_cast<uintptr_t>(in.p);
+    if (out.p && in.p && a < b + static_cast<uintptr_t>(in.bytes) && b < a + static_cast<uintptr_t>(out.bytes))
+        return il_fail(HESS_ERR_INVALID, "%s overlaps %s", out.name, in.name);
+    return HESS_OK;
+}
+
+hess_status il_tokens(int64_t n, int64_t most, const char* what) {
+    if (n < 0) return il_fail(HESS_ERR_INVALID, "n_tokens < 0");
+    if (n > most)
+        return il_fail(HESS_ERR_INVALID, "n_tokens %lld exceeds the handle's %s %lld", static_cast<long long>(n), what,
+                       static_cast<long long>(most));
+    return HESS_OK;
+}
+
+template <class Kernel, class Params>
+hess_status il_launch(Kernel kernel, const Params& p, int64_t grid, int threads, size_t smem, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    IL_TRY(cudaLaunchKernelEx(&cfg, kernel, p));
+    return HESS_OK;
+}
+
+// Granules of 16 columns a thread of the few-token kernel takes.
+int few_granules(int64_t d) {
+    int g = 1;
+    while (static_cast<int64_t>(g) * kFewMaxThreads * 16 < d) g *= 2;
+    return g;
+}
+int few_tokens(int64_t n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : 8; }
+// The codes of all tokens stay in registers: 4 words a token and granule.
+bool is_few(int64_t n, int64_t d) { return n <= 8 && few_tokens(n) * few_granules(d) <= 8; }
+
+hess_status forward_few(const int8_linear_ctx* g, const void* X, const int8_t* codes, const float* scale, int64_t n,
+                        const int8_t* W, const float* W_scale, void* Y, cudaStream_t s) {
+    FewParams p{};
+    p.x = X;
+    p.x_codes = codes;
+    p.x_scale = scale;
+    p.w = W;
+    p.w_scale = W_scale;
+    p.out = Y;
+    p.n = static_cast<int32_t>(n);
+    p.d = static_cast<int32_t>(g->d);
+    p.f = static_cast<int32_t>(g->f);
+    const int gran = few_granules(g->d), tok = few_tokens(n);
+    p.wr = static_cast<int32_t>(ceil_div(g->d, static_cast<int64_t>(gran) * 512));
+    p.rp = kFewMaxThreads / 32 / p.wr;
+    const int64_t ctas = g->f < g->sms ? g->f : g->sms;
+    p.rows = static_cast<int32_t>(ceil_div(g->f, ctas));
+    const int64_t grid = ceil_div(g->f, p.rows);
+    const auto kernel = g->dtype == HESS_BF16 ? few_kernel<__nv_bfloat16>(tok, gran) : few_kernel<__half>(tok, gran);
+    if (!kernel) return il_fail(HESS_ERR_INTERNAL, "no kernel for %d tokens and %d granules", tok, gran);
+    return il_launch(kernel, p, grid, p.wr * p.rp * 32, static_cast<size_t>(p.rows) * tok * 4, s);
+}
+
+// X in 16 bits, or codes and scale.
+hess_status forward(int8_linear_ctx* g, const void* X, const int8_t* codes, const float* scale, int64_t n,
+                    const int8_t* W, const float* W_scale, void* Y, cudaStream_t s) {
+    IL_TRY(ensure_context());
+    if (is_few(n, g->d)) return forward_few(g, X, codes, scale, n, W, W_scale, Y, s);
+    PairParams p{};
+    p.n = static_cast<int32_t>(n);
+    p.d = static_cast<int32_t>(g->d);
+    p.f = static_cast<int32_t>(g->f);
+    plan(p, g->pairs);
+    p.w_bytes = static_cast<uint32_t>((p.rows + 7) / 8 * 8) * kKB;
+    p.stage_bytes = p.w_bytes + static_cast<uint32_t>(p.tok) * 128u;
+    const int fit = static_cast<int>(kRing / p.stage_bytes);
+    p.stages = fit < kMaxStages ? fit : kMaxStages;
+    p.x_scale = X ? g->x_scale : scale;
+    p.w_scale = W_scale;
+    p.out = Y;
+    p.pieces = g->pieces;
+    p.arrived = g->status + 1;
+    p.status = g->status;
+    p.timeout_ns = g->timeout_ns;
+    IL_CHECK(il_encode(&p.x, g->wide, false, n, g->d, p.tok / 2));
+    IL_CHECK(il_encode(&p.w, W, true, g->f, g->d, p.rows));
+    IL_TRY(g->order.begin(s));
+    if (X)
+        IL_TRY(rows8_quantize_launch(X, g->d, n, g->d, g->dtype, 0, nullptr, 0, g->wide, g->d, g->x_scale, s));
+    else
+        IL_TRY(rows8_restore_launch(codes, g->d, nullptr, n, g->d, 0, g->wide, g->d, HESS_F16, s));
+    const int pairs = p.n_units < g->pairs ? p.n_units : g->pairs;
+    const hess_status st = il_launch(
+        g->dtype == HESS_BF16 ? int8_pair_kernel<__nv_bfloat16> : int8_pair_kernel<__half>, p, 2 * pairs, kThreads,
+        kSmemBytes, s);
+    IL_TRY(g->order.end(s));
+    return st;
+}
+
+void il_free(int8_linear_ctx* g) {
+    cudaFree(g->memory);
+    g->order.destroy();
+}
+
+}  // namespace
+}  // namespace hk
+
+using hk::il_fail;
+
+#define IL_EXPORT extern "C" __attribute__((visibility("default")))
+
+IL_EXPORT hess_status int8_linear_create(int64_t d, int64_t f, int64_t tokens, int64_t train_tokens, int32_t dtype,
+                                         int8_linear_t* out) {
+    if (!out) return il_fail(HESS_ERR_INVALID, "out is NULL");
+    *out = nullptr;
+    if (d <= 0 || f <= 0) return il_fail(HESS_ERR_INVALID, "d and f must be positive");
+    if (tokens < 0 || train_tokens < 0) return il_fail(HESS_ERR_INVALID, "tokens or train_tokens < 0");
+    if (d % 16 || f % 8) return il_fail(HESS_ERR_UNSUPPORTED, "d must be a multiple of 16 and f a multiple of 8");
+    if (d > 65536 || f > 65536) return il_fail(HESS_ERR_UNSUPPORTED, "d or f exceeds 65536");
+    if (tokens > (int64_t(1) << 26) || train_tokens > (int64_t(1) << 26))
+        return il_fail(HESS_ERR_UNSUPPORTED, "tokens or train_tokens > 2^26");
+    if (dtype == HESS_F32) return il_fail(HESS_ERR_UNSUPPORTED, "int8_linear takes bf16 or f16");
+    if (dtype != HESS_BF16 && dtype != HESS_F16) return il_fail(HESS_ERR_INVALID, "unknown dtype %d", dtype);
+    if (hk::il_injected("alloc")) return il_fail(HESS_ERR_OOM, "injected allocation failure (HESS_FAULT=alloc)");
+    int dev = 0, pairs = 0, sms = 0, ff_pairs = 0, ff_sms = 0;
+    IL_TRY(cudaGetDevice(&dev));
+    IL_TRY(hk::ensure_context());
+    IL_CHECK(hk::il_prepare(dev, &pairs, &sms));
+    if (train_tokens > 0) IL_CHECK(hk::ff_resident_pairs(dev, &ff_pairs, &ff_sms));
+    int8_linear_ctx* g = new (std::nothrow) int8_linear_ctx();
+    if (!g) return il_fail(HESS_ERR_OOM, "host allocation failed");
+    g->device = dev;
+    g->pairs = pairs;
+    g->ff_pairs = ff_pairs;
+    g->sms = sms;
+    g->d = d;
+    g->f = f;
+    g->tokens = tokens;
+    g->train_tokens = train_tokens;
+    g->dtype = dtype;
+    const auto round = [](size_t b) { return (b + 255) / 256 * 256; };
+    const size_t wide = round(static_cast<size_t>(tokens) * d * 2), x_scale = round(static_cast<size_t>(tokens) * 4);
+    const size_t pieces = tokens > 0 ? static_cast<size_t>(pairs) * hk::kPieceInts * 4 : 0;
+    const size_t w_restored = train_tokens > 0 ? round(static_cast<size_t>(f) * d * 2) : 0;
+    const size_t x_restored = round(static_cast<size_t>(train_tokens) * d * 2);
+    const size_t ff_pieces = static_cast<size_t>(ff_pairs) * hk::kFfPieceBytes;
+    g->status_bytes = (1 + 2 * static_cast<size_t>(pairs) + 2 * static_cast<size_t>(ff_pairs)) * 4;
+    cudaError_t e = cudaMalloc(&g->memory, wide + x_scale + pieces + w_restored + x_restored + ff_pieces + g->status_bytes);
+    if (e == cudaSuccess) {
+        uint8_t* m = static_cast<uint8_t*>(g->memory);
+        g->wide = reinterpret_cast<uint16_t*>(m);
+        g->x_scale = reinterpret_cast<float*>(m += wide);
+        g->pieces = reinterpret_cast<int32_t*>(m += x_scale);
+        g->w_restored = m += pieces;
+        g->x_restored = m += w_restored;
+        g->ff_pieces = reinterpret_cast<float*>(m += x_restored);
+        g->status = reinterpret_cast<uint32_t*>(m += ff_pieces);
+        e = cudaMemset(g->status, 0, g->status_bytes);
+    }
+    if (e == cudaSuccess) e = g->order.create();
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+    if (e != cudaSuccess) {
+        const hess_status s = e == cudaErrorMemoryAllocation ? HESS_ERR_OOM : HESS_ERR_CUDA;
+        if (s == HESS_ERR_OOM) cudaGetLastError();
+        hk::il_free(g);
+        delete g;
+        return il_fail(s, "int8_linear_create: %s", cudaGetErrorString(e));
+    }
+    *out = g;
+    return HESS_OK;
+}
+
+static hess_status il_forward(int8_linear_t g, const void* X, const int8_t* X_codes, const float* X_scale,
+                              bool rows8, int64_t n, const int8_t* W_codes, const float* W_scale, void* Y_out,
+                              hess_stream_t stream) {
+    if (!g) return il_fail(HESS_ERR_INVALID, "handle is NULL");
+    IL_CHECK(hk::il_tokens(n, g->tokens, "tokens"));
+    if (n == 0) return HESS_OK;
+    std::lock_guard<std::mutex> lk(g->mu);
+    IL_CHECK(hk::il_check_device(g));
+    if (rows8) {
+        IL_CHECK(hk::il_check(g, X_codes, "X_codes"));
+        IL_CHECK(hk::il_check(g, X_scale, "X_scale", 4));
+    } else {
+        IL_CHECK(hk::il_check(g, X, "X"));
+    }
+    IL_CHECK(hk::il_check(g, W_codes, "W_codes"));
+    IL_CHECK(hk::il_check(g, W_scale, "W_scale", 4));
+    IL_CHECK(hk::il_check(g, Y_out, "Y_out"));
+    const hk::IlBuffer y{Y_out, 2 * n * g->f, "Y_out"};
+    IL_CHECK(hk::il_apart(y, {X, 2 * n * g->d, "X"}));
+    IL_CHECK(hk::il_apart(y, {X_codes, n * g->d, "X_codes"}));
+    IL_CHECK(hk::il_apart(y, {X_scale, 4 * n, "X_scale"}));
+    IL_CHECK(hk::il_apart(y, {W_codes, g->f * g->d, "W_codes"}));
+    IL_CHECK(hk::il_apart(y, {W_scale, 4 * g->f, "W_scale"}));
+    return hk::forward(g, X, X_codes, X_scale, n, W_codes, W_scale, Y_out, static_cast<cudaStream_t>(stream));
+}
+
+IL_EXPORT hess_status int8_linear_forward(int8_linear_t g, const void* X, int64_t n_tokens, const int8_t* W_codes,
+                                          const float* W_scale, void* Y_out, hess_stream_t stream) {
+    return il_forward(g, X, nullptr, nullptr, false, n_tokens, W_codes, W_scale, Y_out, stream);
+}
+
+IL_EXPORT hess_status int8_linear_forward_rows8(int8_linear_t g, const int8_t* X_codes, const float* X_scale,
+                                                int64_t n_tokens, const int8_t* W_codes, const float* W_scale,
+                                                void* Y_out, hess_stream_t stream) {
+    return il_forward(g, nullptr, X_codes, X_scale, true, n_tokens, W_codes, W_scale, Y_out, stream);
+}
+
+IL_EXPORT hess_status int8_linear_backward(int8_linear_t g, const void* dY, int64_t n_tokens, const int8_t* X_codes,
+                                           const float* X_scale, int32_t group, const int8_t* W_codes,
+                                           const float* W_scale, void* dX_out, void* dW_out, hess_stream_t stream) {
+    if (!g) return il_fail(HESS_ERR_INVALID, "handle is NULL");
+    IL_CHECK(hk::il_tokens(n_tokens, g->train_tokens, "train_tokens"));
+    if (group != 0 && group != 32 && group != 64 && group != 128 && group != 256)
+        return il_fail(HESS_ERR_UNSUPPORTED, "group must be 0, 32, 64, 128 or 256, got %d", group);
+    const int64_t n = n_tokens, groups = group ? (g->d + group - 1) / group : 1;
+    const bool want_x = dX_out != nullptr && n > 0, want_w = dW_out != nullptr;
+    std::lock_guard<std::mutex> lk(g->mu);
+    IL_CHECK(hk::il_check_device(g));
+    if (want_w && g->train_tokens == 0) return il_fail(HESS_ERR_INVALID, "the handle's train_tokens is 0");
+    if (want_x) {
+        IL_CHECK(hk::il_check(g, W_codes, "W_codes", 1));
+        IL_CHECK(hk::il_check(g, W_scale, "W_scale", 4));
+        IL_CHECK(hk::il_check(g, dX_out, "dX_out"));
+    }
+    if (want_w) {
+        if (n > 0) {
+            IL_CHECK(hk::il_check(g, X_codes, "X_codes", 1));
+            IL_CHECK(hk::il_check(g, X_scale, "X_scale", 4));
+        }
+        IL_CHECK(hk::il_check(g, dW_out, "dW_out"));
+    }
+    if (n > 0 && (want_x || want_w)) {
+        IL_CHECK(hk::il_check(g, dY, "dY"));
+        const hk::IlBuffer out[] = {{dX_out, 2 * n * g->d, "dX_out"}, {dW_out, 2 * g->f * g->d, "dW_out"}};
+        for (const hk::IlBuffer& o : out) {
+            IL_CHECK(hk::il_apart(o, {dY, 2 * n * g->f, "dY"}));
+            IL_CHECK(hk::il_apart(o, {X_codes, n * g->d, "X_codes"}));
+            IL_CHECK(hk::il_apart(o, {X_scale, 4 * n * groups, "X_scale"}));
+            IL_CHECK(hk::il_apart(o, {W_codes, g->f * g->d, "W_codes"}));
+            IL_CHECK(hk::il_apart(o, {W_scale, 4 * g->f, "W_scale"}));
+        }
+        IL_CHECK(hk::il_apart(out[1], out[0]));
+    }
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (n == 0) {
+        if (want_w) IL_TRY(cudaMemsetAsync(dW_out, 0, static_cast<size_t>(g->f) * g->d * 2, s));
+        return HESS_OK;
+    }
+    if (!want_x && !want_w) return HESS_OK;
+    IL_TRY(hk::ensure_context());
+    hk::FfSingle a{};
+    a.dY = dY;
+    a.W = g->w_restored;
+    a.X = g->x_restored;
+    a.dX = dX_out;
+    a.dW = dW_out;
+    a.n = n;
+    a.d = g->d;
+    a.f = g->f;
+    a.dtype = g->dtype;
+    a.pairs = g->ff_pairs;
+    a.pieces = g->ff_pieces;
+    a.arrived = g->status + 1 + 2 * g->pairs;
+    a.status = g->status;
+    a.timeout_ns = g->timeout_ns;
+    IL_TRY(g->order.begin(s));
+    if (want_x)
+        IL_TRY(hk::rows8_restore_launch(W_codes, g->d, W_scale, g->f, g->d, 0, g->w_restored, g->d, g->dtype, s));
+    if (want_w)
+        IL_TRY(hk::rows8_restore_launch(X_codes, g->d, X_scale, n, g->d, group, g->x_restored, g->d, g->dtype, s));
+    const hess_status st = hk::ff_gradients_single(a, s);
+    IL_TRY(g->order.end(s));
+    return st;
+}
+
+IL_EXPORT hess_status int8_linear_sync(int8_linear_t g, hess_stream_t stream) {
+    if (!g) return il_fail(HESS_ERR_INVALID, "handle is NULL");
+    std::lock_guard<std::mutex> lk(g->mu);
+    IL_CHECK(hk::il_check_device(g));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint32_t word = 0;
+    IL_TRY(cudaMemcpyAsync(&word, g->status, sizeof(word), cudaMemcpyDeviceToHost, s));
+    IL_TRY(cudaStreamSynchronize(s));
+    if (word == 0) return HESS_OK;
+    // the arrival counts of an interrupted call go with it, when no call on another
+    // stream is at them, and before the next call may be
+    IL_TRY(g->order.begin(s));
+    IL_TRY(cudaMemsetAsync(g->status, 0, g->status_bytes, s));
+    IL_TRY(cudaStreamSynchronize(s));
+    return il_fail(HESS_ERR_TIMEOUT, "a device-side wait ran out (status 0x%x); results are invalid", word);
+}
+
+IL_EXPORT hess_status int8_linear_set_timeout(int8_linear_t g, int64_t ns) {
+    if (!g) return il_fail(HESS_ERR_INVALID, "handle is NULL");
+    if (ns < 0) return il_fail(HESS_ERR_INVALID, "the limit must not be negative");
+    std::lock_guard<std::mutex> lk(g->mu);
+    g->timeout_ns = static_cast<unsigned long long>(ns);
+    return HESS_OK;
+}
+
+IL_EXPORT hess_status int8_linear_destroy(int8_linear_t g) {
+    if (!g) return HESS_OK;
+    int cur = 0;
+    IL_TRY(cudaGetDevice(&cur));
+    IL_TRY(cudaSetDevice(g->device));
+    const cudaError_t e = cudaDeviceSynchronize();
+    hk::il_free(g);
+    cudaSetDevice(cur);
+    delete g;
+    if (e != cudaSuccess) return il_fail(HESS_ERR_CUDA, "int8_linear_destroy: %s", cudaGetErrorString(e));
+    return HESS_OK;
+}

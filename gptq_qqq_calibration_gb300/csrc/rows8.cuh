@@ -1,0 +1,20 @@
+// Launchers of the 8-bit row kernels that other parts of the library call (no
+// argument checks; conventions: include/rows8.h).  They return at once.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+namespace hk {
+
+// Codes go to `codes` as int8, or, when that is NULL, to `wide` as float16 whole
+// numbers (for the tensor cores, which take no int8 on this GPU at speed).
+cudaError_t rows8_quantize_launch(const void* X, int64_t ldx, int64_t n, int64_t d, int32_t dtype, int32_t group,
+                                  int8_t* codes, int64_t ldc, uint16_t* wide, int64_t ldw, float* scale,
+                                  cudaStream_t s);
+// scale == NULL: every scale is 1.
+cudaError_t rows8_restore_launch(const int8_t* codes, int64_t ldc, const float* scale, int64_t n, int64_t d,
+                                 int32_t group, void* X, int64_t ldx, int32_t dtype, cudaStream_t s);
+
+}  // namespace hk

@@ -8,15 +8,16 @@ wraps a handle and can be called as a node of an autograd graph.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Tuple
+from typing import Optional, Tuple, Union
 
 import torch
 
 from . import _lib
 from ._lib import HESS_BF16, HESS_F16, HESS_F32, check
+from .rows8 import Rows8, _scale, quantize_rows
 
-__all__ = ["gated_ff_create", "gated_ff_forward", "gated_ff_backward", "gated_ff_sync", "gated_ff_set_timeout",
-           "gated_ff_destroy", "GatedFF"]
+__all__ = ["gated_ff_create", "gated_ff_forward", "gated_ff_backward", "gated_ff_reserve_rows8",
+           "gated_ff_backward_rows8", "gated_ff_sync", "gated_ff_set_timeout", "gated_ff_destroy", "GatedFF"]
 
 _DTYPES = {torch.bfloat16: HESS_BF16, torch.float16: HESS_F16, torch.float32: HESS_F32}
 ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
@@ -84,6 +85,26 @@ def gated_ff_backward(g: int, X, n_tokens: int, W_gate, W_up, dH, dX_out, dW_gat
     _written(dX_out, dW_gate_out, dW_up_out)
 
 
+def gated_ff_reserve_rows8(g: int) -> None:
+    check(_lib.load().gated_ff_reserve_rows8(g))
+
+
+def _backward_rows8(g: int, X_codes, X_scale, group, n_tokens, W_gate, W_up, dH, dX_out, dW_gate_out, dW_up_out,
+                    stream) -> None:
+    st = _lib.load().gated_ff_backward_rows8(
+        g, X_codes.data_ptr(), X_scale.data_ptr(), group, n_tokens, W_gate.data_ptr(), W_up.data_ptr(), dH.data_ptr(),
+        None if dX_out is None else dX_out.data_ptr(), None if dW_gate_out is None else dW_gate_out.data_ptr(),
+        None if dW_up_out is None else dW_up_out.data_ptr(), _stream(stream, dH.get_device()))
+    if st:
+        check(st)
+
+
+def gated_ff_backward_rows8(g: int, X_codes, X_scale, group: int, n_tokens: int, W_gate, W_up, dH, dX_out,
+                            dW_gate_out, dW_up_out, stream=None) -> None:
+    _backward_rows8(g, X_codes, X_scale, group, n_tokens, W_gate, W_up, dH, dX_out, dW_gate_out, dW_up_out, stream)
+    _written(dX_out, dW_gate_out, dW_up_out)
+
+
 def gated_ff_sync(g: int, stream=None) -> None:
     check(_lib.load().gated_ff_sync(g, _stream(stream, torch.cuda.current_device())))
 
@@ -104,7 +125,9 @@ class GatedFF:
     serves every layer of these widths.  ``train_tokens`` is the most tokens a
     backward call will have (its workspace is 4 f bytes a token); a backward of
     more is refused, a forward is not.  Called as a function, the object is a node
-    of an autograd graph.
+    of an autograd graph.  With ``rows8`` the object can take 8-bit rows in the place of
+    X in ``backward`` (2 d bytes of workspace a token of ``train_tokens``), and the node keeps X
+    in that form, with a scale per 128 columns: 1.03 bytes a value instead of 2.
 
     The object's calls may come on any streams, and may be captured into CUDA
     graphs.  Replays of such graphs are the caller's to order, with each other
@@ -113,7 +136,7 @@ class GatedFF:
     """
 
     def __init__(self, d: int, f: int, train_tokens: int = 0, dtype: torch.dtype = torch.bfloat16,
-                 activation: str = "silu"):
+                 activation: str = "silu", rows8: bool = False):
         self.handle = None
         if dtype not in _DTYPES:
             raise ValueError(f"dtype must be bfloat16 or float16, got {dtype}")
@@ -121,6 +144,9 @@ class GatedFF:
             raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
         self.d, self.f, self.dtype = int(d), int(f), dtype
         self.handle = gated_ff_create(d, f, train_tokens, _DTYPES[dtype], ACTIVATIONS[activation])
+        self.rows8 = bool(rows8)
+        if rows8:
+            gated_ff_reserve_rows8(self.handle)
 
     def _rows(self, t: torch.Tensor, name: str, width: int) -> int:
         if t.dtype is self.dtype and t.is_cuda and t.is_contiguous() and t.dim() and t.shape[-1] == width:
@@ -131,8 +157,17 @@ class GatedFF:
             raise ValueError(f"{name} must be a contiguous CUDA tensor")
         raise ValueError(f"{name} must have a last dimension of {width}")
 
+    def _kept(self, X: Rows8) -> int:
+        codes = X.codes
+        if codes.dtype is not torch.int8 or not codes.is_cuda or not codes.is_contiguous() or not codes.dim() or \
+                codes.shape[-1] != self.d:
+            raise ValueError(f"X.codes must be a contiguous int8 CUDA tensor with a last dimension of {self.d}")
+        n = codes.numel() // self.d
+        _scale(X.scale, n, self.d, X.group, "X.scale")
+        return n
+
     def _inputs(self, X, W_gate, W_up) -> int:
-        n = self._rows(X, "X", self.d)
+        n = self._kept(X) if isinstance(X, Rows8) else self._rows(X, "X", self.d)
         if self._rows(W_gate, "W_gate", self.d) != self.f or self._rows(W_up, "W_up", self.d) != self.f:
             raise ValueError(f"W_gate and W_up must be [{self.f}, {self.d}]")
         return n
@@ -151,18 +186,24 @@ class GatedFF:
         _used_on(stream, X, W_gate, W_up, out)
         return out
 
-    def backward(self, X: torch.Tensor, W_gate: torch.Tensor, W_up: torch.Tensor, dH: torch.Tensor,
+    def backward(self, X: Union[torch.Tensor, Rows8], W_gate: torch.Tensor, W_up: torch.Tensor, dH: torch.Tensor,
                  want_dx: bool = True, want_dw: bool = True, stream=None
                  ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], Optional[torch.Tensor]]:
-        """(dX, dW_gate, dW_up); None for what is not wanted."""
+        """(dX, dW_gate, dW_up); None for what is not wanted.  X may be an 8-bit
+        checkpoint of the input (an object with ``rows8``)."""
         n = self._inputs(X, W_gate, W_up)
+        kept = isinstance(X, Rows8)
         if self._rows(dH, "dH", self.f) != n:
             raise ValueError(f"dH must have {n} rows")
-        dx = _empty(X.shape, X, stream) if want_dx else None
-        dwg = _empty(W_gate.shape, X, stream) if want_dw else None
-        dwu = _empty(W_up.shape, X, stream) if want_dw else None
-        _backward(self.handle, X, n, W_gate, W_up, dH, dx, dwg, dwu, stream)
-        _used_on(stream, X, W_gate, W_up, dH)
+        dx = _empty(X.codes.shape if kept else X.shape, dH, stream) if want_dx else None
+        dwg = _empty(W_gate.shape, dH, stream) if want_dw else None
+        dwu = _empty(W_up.shape, dH, stream) if want_dw else None
+        if kept:
+            _backward_rows8(self.handle, X.codes, X.scale, int(X.group), n, W_gate, W_up, dH, dx, dwg, dwu, stream)
+            _used_on(stream, X.codes, X.scale, W_gate, W_up, dH)
+        else:
+            _backward(self.handle, X, n, W_gate, W_up, dH, dx, dwg, dwu, stream)
+            _used_on(stream, X, W_gate, W_up, dH)
         return dx, dwg, dwu
 
     def __call__(self, X: torch.Tensor, W_gate: torch.Tensor, W_up: torch.Tensor) -> torch.Tensor:
@@ -187,13 +228,17 @@ class _GatedFF(torch.autograd.Function):
     @staticmethod
     def forward(ctx, op, X, W_gate, W_up):
         ctx.op = op
-        ctx.save_for_backward(X, W_gate, W_up)
+        if op.rows8:
+            ctx.save_for_backward(*quantize_rows(X, group=128)[:2], W_gate, W_up)
+        else:
+            ctx.save_for_backward(X, W_gate, W_up)
         return op.forward(X, W_gate, W_up)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dH):
-        X, W_gate, W_up = ctx.saved_tensors
+        *X, W_gate, W_up = ctx.saved_tensors
+        X = Rows8(*X, 128) if ctx.op.rows8 else X[0]
         want = ctx.needs_input_grad
         dH = dH.contiguous()
         if dH.data_ptr() % 16:  # a part of a buffer that starts anywhere

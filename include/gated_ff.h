@@ -85,6 +85,20 @@ hess_status gated_ff_backward(gated_ff_t g, const void* X, int64_t n_tokens, con
                               const void* W_up, const void* dH, void* dX_out, void* dW_gate_out,
                               void* dW_up_out, hess_stream_t stream);
 
+/* Room for gated_ff_backward_rows8: 2 * train_tokens * d bytes more.  A second call does
+ * nothing.  Not during a capture (it allocates). */
+hess_status gated_ff_reserve_rows8(gated_ff_t g);
+
+/* gated_ff_backward with an 8-bit checkpoint in the place of X (rows8.h):
+ *   X_codes : int8 [n_tokens, d], contiguous, any alignment;
+ *   X_scale : float32 [n_tokens] (group 0) or [n_tokens, ceil(d / group)].
+ * The values that X_codes and X_scale stand for are rounded to the handle's type and take
+ * X's place: the result is that of gated_ff_backward on rows8_restore's output, bit for
+ * bit.  Needs gated_ff_reserve_rows8 (HESS_ERR_INVALID without it). */
+hess_status gated_ff_backward_rows8(gated_ff_t g, const int8_t* X_codes, const float* X_scale, int32_t group,
+                                    int64_t n_tokens, const void* W_gate, const void* W_up, const void* dH,
+                                    void* dX_out, void* dW_gate_out, void* dW_up_out, hess_stream_t stream);
+
 /* Wait for `stream`; then HESS_ERR_TIMEOUT if a device-side wait of this
  * handle's kernels ran out since the last gated_ff_sync, else HESS_OK.  After a
  * timeout the results of every call of the handle since then are invalid (a
