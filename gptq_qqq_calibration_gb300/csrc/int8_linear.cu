@@ -70,8 +70,15 @@ struct PairParams : Schedule {
     unsigned long long timeout_ns;
 };
 
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// True in one lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 
 // D (M = 256 across the pair) (+)= A[tensor memory] * B[shared memory], f16, issued by the even CTA.
@@ -257,67 +264,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 atomicOr(p.status, kStatusTimeoutLoad);
                 aborted = 1;
             }
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && rank == 0) {
+            // The whole warp takes every turn and one elected lane issues: the operands then
+            // stay in uniform registers (one lane alone: 74 cycles an MMA, this way 40).
             bool ok = true;
-            int stage = 0, slot = 0, ab = 0;
-            uint32_t phase = 0, sphase = 0, aphase = 0;
-            const uint32_t box = static_cast<uint32_t>(p.tok) * 64u;
+            int stage = 0, ab = 0;
+            uint32_t slot = 0, phase = 0, sphase = 0, aphase = 0;
             // float32 sums, float16 operands, both contiguous along the contraction
             const uint32_t idesc = (1u << 4) | ((static_cast<uint32_t>(p.tok) >> 3) << 17) | ((256u >> 4) << 24);
+            // descriptors count 16 bytes
+            const uint64_t first = smem_desc_sw128(base + p.w_bytes, 16u, 1024u);
+            const uint64_t next = p.stage_bytes >> 4, half = static_cast<uint64_t>(p.tok) * 4u;
+            uint64_t b = first;
             for (int u = pair; ok && u < p.n_units; u += n_pairs) {
                 const Unit un = unit_at(p, u);
                 for (int c0 = un.kb0; ok && c0 < un.kb1; c0 += kChunk) {
-                    if (!mbar_wait_cluster(acce_bar(ab), aphase ^ 1u, limit)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = __all_sync(~0u, mbar_wait_cluster(acce_bar(ab), aphase ^ 1u, limit));
+                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t acc = tmem + static_cast<uint32_t>(ab * kMaxTok);
                     const int c1 = c0 + kChunk < un.kb1 ? c0 + kChunk : un.kb1;
-                    for (int kb = c0; ok && kb < c1; ++kb) {
-                        if (!mbar_wait_cluster(xfull_bar(stage), phase, limit)) {
-                            ok = false;
-                            break;
-                        }
-                        for (int h = 0; h < 2; ++h) {
-                            if (!mbar_wait_cluster(afull_bar(slot), sphase, limit)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            const uint32_t sB = base + stage * p.stage_bytes + p.w_bytes + h * box;
-                            const uint32_t a = tmem + kSlotCol + static_cast<uint32_t>(slot) * 32u;
+                    for (int kb = c0; kb < c1; ++kb) {
+                        ok = __all_sync(~0u, mbar_wait_cluster(xfull_bar(stage), phase, limit));
+                        if (!ok) break;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                umma_f16_pair_ta(acc, a + j * 8u, smem_desc_sw128(sB + j * 32u, 16u, 1024u), idesc,
-                                                 kb != c0 || h != 0 || j != 0 ? 1u : 0u);
-                            tc_commit_pair_mc(aempty_bar(slot), 0x3);
+                        for (int h = 0; h < 2; ++h) {
+                            ok = __all_sync(~0u, mbar_wait_cluster(afull_bar(slot), sphase, limit));
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t a = tmem + kSlotCol + slot * 32u;
+                            const uint64_t bh = h ? b + half : b;
+                            if (elect_one()) {
+                                umma_f16_pair_ta(acc, a, bh, idesc, h != 0 || kb != c0 ? 1u : 0u);
+                                umma_f16_pair_ta(acc, a + 8u, bh + 2u, idesc, 1u);
+                                umma_f16_pair_ta(acc, a + 16u, bh + 4u, idesc, 1u);
+                                umma_f16_pair_ta(acc, a + 24u, bh + 6u, idesc, 1u);
+                                tc_commit_pair_mc(aempty_bar(slot), 0x3);
+                                if (h) tc_commit_pair_mc(xempty_bar(stage), 0x3);
+                            }
+                            __syncwarp();
                             if (++slot == kSlots) {
                                 slot = 0;
                                 sphase ^= 1u;
                             }
                         }
                         if (!ok) break;
-                        tc_commit_pair_mc(xempty_bar(stage), 0x3);
+                        b += next;
                         if (++stage == p.stages) {
                             stage = 0;
                             phase ^= 1u;
+                            b = first;
                         }
                     }
                     if (!ok) break;
-                    tc_commit_pair_mc(accf_bar(ab), 0x3);
+                    if (elect_one()) tc_commit_pair_mc(accf_bar(ab), 0x3);
+                    __syncwarp();
                     if (++ab == 2) {
                         ab = 0;
                         aphase ^= 1u;
                     }
                 }
             }
-            if (!ok) {
+            if (!ok && lane == 0) {
                 atomicOr(p.status, kStatusTimeoutMma);
                 aborted = 1;
             }
             // every MMA issued has completed before the pair's memories are released
-            tc_commit_pair_mc(drain_bar, 0x1);
+            if (elect_one()) tc_commit_pair_mc(drain_bar, 0x1);
+            __syncwarp();
             if (!mbar_wait(drain_bar, 0, kDrainLimitNs)) atomicOr(p.status, kStatusTimeoutDrain);
         }
     } else if (warp < 12) {
@@ -358,7 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (some) tmem_st32(tmem + lanes + kSlotCol + static_cast<uint32_t>(slot) * 32u, a);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(afull0 + 8u * slot);
+                if (lane == 0) mbar_arrive_cluster_relaxed(afull0 + 8u * slot);
                 slot ^= 2;
                 if (slot == h) sphase ^= 1u;
                 if (++stage == p.stages) {
@@ -452,11 +466,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const float sw = p.w_scale[ch];
                 T* const out = static_cast<T*>(p.out) + static_cast<int64_t>(un.t0) * p.f + ch;
                 const int n = p.n - un.t0;  // tokens of this tile
+                const float* const sx = p.x_scale + un.t0;
 #pragma unroll
-                for (int c = 0; c < kMaxTok; ++c)
-                    if (c < p.tok && c < n)
-                        out[static_cast<int64_t>(c) * p.f] =
-                            rounded<T>(__fmul_rn(__int2float_rn(sum[c]), __fmul_rn(p.x_scale[un.t0 + c], sw)));
+                for (int c = 0; c < kMaxTok; c += 16) {
+                    if (c < p.tok && c < n) {
+                        // sixteen scales on their way at once, before the stores
+                        float k[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) k[i] = sx[c + i < n ? c + i : n - 1];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c + i < n)
+                                out[static_cast<int64_t>(c + i) * p.f] =
+                                    rounded<T>(__fmul_rn(__int2float_rn(sum[c + i]), __fmul_rn(k[i], sw)));
+                    }
+                }
             }
         }
         if (failed && lane == 0) {
