@@ -47,13 +47,14 @@ using namespace i8;
 
 constexpr int kMaxStages = 12;
 constexpr uint32_t kRing = 208 * 1024;
-constexpr int kSlots = 4;             // of 64 steps of A in tensor memory, 32 columns each
+constexpr int kMaxSlots = 12;         // of 64 steps of A in tensor memory, 32 columns each
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSlotCol = 2 * kMaxTok;
-static_assert(kSlotCol + kSlots * 32 <= kTmemCols, "tensor memory");
-constexpr int kNumBarriers = 4 * kMaxStages + 2 * kSlots + 5;
+static_assert(2 * kMaxTok + 4 * 32 <= kTmemCols, "two sums and four slots");
+constexpr int kNumBarriers = 4 * kMaxStages + 2 * kMaxSlots + 5;
 constexpr size_t kSmemBytes = 1024 + kRing + 8 * kNumBarriers + 16;
-constexpr int kThreads = 512;  // warp 0: weights, 1: MMAs, 2: tokens, 4-11: converters, 12-15: epilogue
+constexpr int kThreads = 640;  // warp 0: weights, 1: MMAs, 2: tokens, 4-11: converters, 12-19: epilogue
+constexpr int kFirstEpiWarp = 12, kEpiWarps = 8;
+constexpr int kCols = kMaxTok / 2;  // tokens of an epilogue thread
 constexpr unsigned long long kDrainLimitNs = 1000000000ull;
 constexpr unsigned long long kAbortSettleNs = 2000000ull;
 constexpr int64_t kPieceInts = 2 * kMaxTok * kMaxRows;  // both CTAs' sums of one unit
@@ -61,6 +62,8 @@ constexpr int64_t kPieceInts = 2 * kMaxTok * kMaxRows;  // both CTAs' sums of on
 struct PairParams : Schedule {
     CUtensorMap x, w;  // float16 codes [n, d], boxes of tok/2 rows x 64; weights [f, d], boxes of rows x 128
     int32_t stages;
+    int32_t slots;       // of A in tensor memory, an even number
+    uint32_t acc_cols;   // columns of one sum in tensor memory; the slots follow the second
     uint32_t w_bytes, stage_bytes;  // of a stage; the tokens' two boxes follow the weights
     const float *x_scale, *w_scale;
     void* out;
@@ -141,10 +144,10 @@ __device__ __forceinline__ bool epi_barrier_any(bool x) {
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, 1, 128, p;\n\t"
+        "bar.red.or.pred q, 1, %2, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(any)
-        : "r"(static_cast<uint32_t>(x))
+        : "r"(static_cast<uint32_t>(x)), "n"(kEpiWarps * 32)
         : "memory");
     return any != 0;
 }
@@ -166,10 +169,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto xfull_bar = [&](int s) { return bar0 + 8u * (2 * kMaxStages + s); };   // even CTA: the pair's tokens
     auto xempty_bar = [&](int s) { return bar0 + 8u * (3 * kMaxStages + s); };  // MMAs have read them
     auto afull_bar = [&](int s) { return bar0 + 8u * (4 * kMaxStages + s); };   // even CTA: the pair's slot of A
-    auto aempty_bar = [&](int s) { return bar0 + 8u * (4 * kMaxStages + kSlots + s); };
-    auto accf_bar = [&](int b) { return bar0 + 8u * (4 * kMaxStages + 2 * kSlots + b); };
-    auto acce_bar = [&](int b) { return bar0 + 8u * (4 * kMaxStages + 2 * kSlots + 2 + b); };
-    const uint32_t drain_bar = bar0 + 8u * (4 * kMaxStages + 2 * kSlots + 4);
+    auto aempty_bar = [&](int s) { return bar0 + 8u * (4 * kMaxStages + kMaxSlots + s); };
+    auto accf_bar = [&](int b) { return bar0 + 8u * (4 * kMaxStages + 2 * kMaxSlots + b); };
+    auto acce_bar = [&](int b) { return bar0 + 8u * (4 * kMaxStages + 2 * kMaxSlots + 2 + b); };
+    const uint32_t drain_bar = bar0 + 8u * (4 * kMaxStages + 2 * kMaxSlots + 4);
     __shared__ volatile int aborted;
     __shared__ volatile int epi_last;
 
@@ -185,13 +188,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(xfull_bar(s), 1);
             mbar_init(xempty_bar(s), 1);
         }
-        for (int s = 0; s < kSlots; ++s) {
+        for (int s = 0; s < p.slots; ++s) {
             mbar_init(afull_bar(s), 8);  // four converter warps of each CTA
             mbar_init(aempty_bar(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf_bar(b), 1);
-            mbar_init(acce_bar(b), 8);  // four epilogue warps of each CTA
+            mbar_init(acce_bar(b), 2 * kEpiWarps);
         }
         mbar_init(drain_bar, 1);
         aborted = 0;
@@ -245,7 +248,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const Unit un = unit_at(p, u);
                 const int row = un.t0 + static_cast<int>(rank) * (p.tok / 2);
                 for (int kb = un.kb0; kb < un.kb1; ++kb) {
-                    if (!mbar_wait_cluster(xempty_bar(stage), phase ^ 1u, limit)) {
+                    if (!mbar_wait(xempty_bar(stage), phase ^ 1u, limit)) {
                         ok = false;
                         break;
                     }
@@ -279,20 +282,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int u = pair; ok && u < p.n_units; u += n_pairs) {
                 const Unit un = unit_at(p, u);
                 for (int c0 = un.kb0; ok && c0 < un.kb1; c0 += kChunk) {
-                    ok = __all_sync(~0u, mbar_wait_cluster(acce_bar(ab), aphase ^ 1u, limit));
+                    ok = __all_sync(~0u, mbar_wait(acce_bar(ab), aphase ^ 1u, limit));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t acc = tmem + static_cast<uint32_t>(ab * kMaxTok);
+                    const uint32_t acc = tmem + static_cast<uint32_t>(ab) * p.acc_cols;
                     const int c1 = c0 + kChunk < un.kb1 ? c0 + kChunk : un.kb1;
                     for (int kb = c0; kb < c1; ++kb) {
-                        ok = __all_sync(~0u, mbar_wait_cluster(xfull_bar(stage), phase, limit));
+                        ok = __all_sync(~0u, mbar_wait(xfull_bar(stage), phase, limit));
                         if (!ok) break;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            ok = __all_sync(~0u, mbar_wait_cluster(afull_bar(slot), sphase, limit));
+                            ok = __all_sync(~0u, mbar_wait(afull_bar(slot), sphase, limit));
                             if (!ok) break;
                             tc_fence_after();
-                            const uint32_t a = tmem + kSlotCol + slot * 32u;
+                            const uint32_t a = tmem + 2 * p.acc_cols + slot * 32u;
                             const uint64_t bh = h ? b + half : b;
                             if (elect_one()) {
                                 umma_f16_pair_ta(acc, a, bh, idesc, h != 0 || kb != c0 ? 1u : 0u);
@@ -303,7 +306,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                 if (h) tc_commit_pair_mc(xempty_bar(stage), 0x3);
                             }
                             __syncwarp();
-                            if (++slot == kSlots) {
+                            if (++slot == static_cast<uint32_t>(p.slots)) {
                                 slot = 0;
                                 sphase ^= 1u;
                             }
@@ -337,7 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp < 12) {
         // Converters: the first four warps take the first 64 steps of each stage, the
         // others the rest.  A thread owns one weight row.
-        setmaxnreg_dec<96>();
+        setmaxnreg_dec<80>();
         const int h = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const bool some = (warp & 3) * 32 < p.rows, mine = row < p.rows;
@@ -364,17 +367,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(wempty_bar(stage));
-                if (!mbar_wait_cluster(aempty_bar(slot), sphase ^ 1u, limit)) {
+                if (!mbar_wait(aempty_bar(slot), sphase ^ 1u, limit)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (some) tmem_st32(tmem + lanes + kSlotCol + static_cast<uint32_t>(slot) * 32u, a);
+                if (some) tmem_st32(tmem + lanes + 2 * p.acc_cols + static_cast<uint32_t>(slot) * 32u, a);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster_relaxed(afull0 + 8u * slot);
-                slot ^= 2;
-                if (slot == h) sphase ^= 1u;
+                slot += 2;
+                if (slot >= p.slots) {
+                    slot = h;
+                    sphase ^= 1u;
+                }
                 if (++stage == p.stages) {
                     stage = 0;
                     phase ^= 1u;
@@ -386,31 +392,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             aborted = 1;
         }
     } else {
-        // Epilogue: a thread owns one weight row (an output channel) of up to 192 tokens.
-        setmaxnreg_inc<240>();
+        // Epilogue: a thread owns one weight row (an output channel) and every other
+        // sixteen tokens: of the first four warps the even ones, of the others the odd.
+        setmaxnreg_inc<136>();
         griddep_wait();
         const int q = warp & 3, row = q * 32 + lane;
+        const int first = ((warp - kFirstEpiWarp) >> 2) * 16;
         const uint32_t acce0 = mapa_shared(acce_bar(0), 0);
         bool failed = false;
         int ab = 0;
         uint32_t aphase = 0;
-        int32_t sum[kMaxTok];
+        int32_t sum[kCols];
         for (int u = pair; u < p.n_units; u += n_pairs) {
             const Unit un = unit_at(p, u);
 #pragma unroll
-            for (int c = 0; c < kMaxTok; ++c) sum[c] = 0;
+            for (int c = 0; c < kCols; ++c) sum[c] = 0;
             for (int c0 = un.kb0; c0 < un.kb1; c0 += kChunk) {
                 // the warps agree on whether a wait ran out, so that all of them pass the
                 // same barriers
-                failed = epi_barrier_any(failed || !mbar_wait_cluster(accf_bar(ab), aphase, limit));
+                failed = epi_barrier_any(failed || !mbar_wait(accf_bar(ab), aphase, limit));
                 tc_fence_after();
                 if (!failed) {
-                    const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(ab * kMaxTok);
+                    const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(ab) * p.acc_cols;
 #pragma unroll
-                    for (int c = 0; c < kMaxTok; c += 16) {
-                        if (c < p.tok) {
+                    for (int c = 0; c < kCols; c += 16) {
+                        const int at = first + 2 * c;
+                        if (at < p.tok) {
                             uint32_t v[16];
-                            tmem_ld16(acc + c, v);
+                            tmem_ld16(acc + at, v);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) sum[c + i] += __float2int_rn(__uint_as_float(v[i]));
                         }
@@ -432,12 +441,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!failed) {
                     int32_t* const out = piece0 + un.part * kPieceInts;
 #pragma unroll
-                    for (int c = 0; c < kMaxTok; ++c)
-                        if (c < p.tok) __stcg(out + c * kMaxRows, sum[c]);
+                    for (int c = 0; c < kCols; c += 16) {
+                        const int at = first + 2 * c;
+                        if (at < p.tok) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) __stcg(out + (at + i) * kMaxRows, sum[c + i]);
+                        }
+                    }
                     __threadfence();
                 }
                 epi_barrier_any(false);
-                if (warp == 12 && lane == 0) {
+                if (warp == kFirstEpiWarp && lane == 0) {
                     uint32_t* const count = p.arrived + 2 * un.split + rank;
                     const bool last = !failed && atomicAdd(count, 1u) == static_cast<uint32_t>(un.parts - 1);
                     if (last) *count = 0;
@@ -451,10 +465,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (k == un.part) continue;
                         const int32_t* const in = piece0 + k * kPieceInts;
 #pragma unroll
-                        for (int c = 0; c < kMaxTok; c += 16) {
-                            if (c < p.tok) {
+                        for (int c = 0; c < kCols; c += 16) {
+                            const int at = first + 2 * c;
+                            if (at < p.tok) {
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) sum[c + i] += __ldcg(in + (c + i) * kMaxRows);
+                                for (int i = 0; i < 16; ++i) sum[c + i] += __ldcg(in + (at + i) * kMaxRows);
                             }
                         }
                     }
@@ -468,16 +483,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int n = p.n - un.t0;  // tokens of this tile
                 const float* const sx = p.x_scale + un.t0;
 #pragma unroll
-                for (int c = 0; c < kMaxTok; c += 16) {
-                    if (c < p.tok && c < n) {
+                for (int c = 0; c < kCols; c += 16) {
+                    const int at = first + 2 * c;
+                    if (at < p.tok && at < n) {
                         // sixteen scales on their way at once, before the stores
                         float k[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) k[i] = sx[c + i < n ? c + i : n - 1];
+                        for (int i = 0; i < 16; ++i) k[i] = sx[at + i < n ? at + i : n - 1];
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            if (c + i < n)
-                                out[static_cast<int64_t>(c + i) * p.f] =
+                            if (at + i < n)
+                                out[static_cast<int64_t>(at + i) * p.f] =
                                     rounded<T>(__fmul_rn(__int2float_rn(sum[c + i]), __fmul_rn(k[i], sw)));
                     }
                 }
@@ -925,6 +941,9 @@ hess_status forward(int8_linear_ctx* g, const void* X, const int8_t* codes, cons
     p.stage_bytes = p.w_bytes + static_cast<uint32_t>(p.tok) * 128u;
     const int fit = static_cast<int>(kRing / p.stage_bytes);
     p.stages = fit < kMaxStages ? fit : kMaxStages;
+    p.acc_cols = static_cast<uint32_t>((p.tok + 31) / 32 * 32);
+    const int slots = static_cast<int>((kTmemCols - 2 * p.acc_cols) / 32) & ~1;
+    p.slots = slots < kMaxSlots ? slots : kMaxSlots;
     p.x_scale = X ? g->x_scale : scale;
     p.w_scale = W_scale;
     p.out = Y;
