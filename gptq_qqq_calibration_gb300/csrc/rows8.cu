@@ -5,14 +5,17 @@
 // A group of 32 .. 256 columns lies inside a segment, so its maximum is a few
 // shuffles; a whole row's segments are held in the registers of one CTA and its
 // maximum meets in shared memory, so that the values are read once either way.
-// Where rows start on 16 bytes and d is a multiple of 8 a lane owns eight columns
-// side by side (16-byte accesses); otherwise it owns columns 32 apart, which keeps a
+// A lane's columns come in runs of V side by side, 32 V columns apart: V is 8 where
+// rows are multiples of 16 bytes, 4 where they are of half that, else 1, which keeps a
 // warp's accesses contiguous at any alignment.
 //
-// The whole number nearest to the exact quotient x / s is wanted.  x (1/s) differs from
-// the quotient by less than 2^-15 for |x / s| <= 127.5, so both round to the same whole
-// number unless the product lies that close to a half: only then is it looked at more
-// closely (1 value in 10^4), and the kernel stays at the memory's pace.
+// The whole number nearest to the exact quotient x / s is wanted, and the memory's pace
+// leaves some ten instructions a value.  So the value is multiplied by a number a little
+// below 1/s and by one a little above it, each product rounded to a whole number by the
+// multiply-add that adds 1.5 * 2^23.  The quotient lies between the products: where both
+// round alike that is the code, and where they do not the exact sign of the remainder at
+// the half between them decides (16-bit values meet that in 1 of 400: half of a row's
+// maximum is 63.5 s, up to the rounding of s).
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -32,154 +35,230 @@ namespace {
 constexpr int kSegment = 256;
 constexpr int kItemSegments = 4;  // segments one warp has in flight
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 template <class T>
-__device__ __forceinline__ T from_f32(float x);
+__device__ __forceinline__ float2 pair_f32(uint32_t w);  // two 16-bit values
 template <>
-__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+__device__ __forceinline__ float2 pair_f32<__nv_bfloat16>(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
 template <>
-__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-
-// Column of a lane's element e within a segment.
-template <bool kVec>
-__device__ __forceinline__ int column(int lane, int e) {
-    return kVec ? lane * 8 + e : e * 32 + lane;
+__device__ __forceinline__ float2 pair_f32<__half>(uint32_t w) {
+    __half2 h;
+    memcpy(&h, &w, 4);
+    return __half22float2(h);
 }
 
-// A lane's eight values of the segment that begins at column c0; zeros past d.
-template <class T, bool kVec>
+// Column of a lane's element e within a segment.
+template <int V>
+__device__ __forceinline__ int column(int lane, int e) {
+    return (e / V) * (32 * V) + lane * V + e % V;
+}
+
+// V elements of 16 or 32 bits from an address aligned to all of them (or, beyond 16
+// bytes, to 16), as words.
+template <int kBytes>
+__device__ __forceinline__ void load_words(const void* p, uint32_t* w) {
+    if constexpr (kBytes >= 16) {
+#pragma unroll
+        for (int i = 0; i < kBytes / 16; ++i) {
+            const uint4 v = __ldcs(static_cast<const uint4*>(p) + i);
+            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        }
+    } else if constexpr (kBytes == 8) {
+        const uint2 v = __ldcs(static_cast<const uint2*>(p));
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        w[0] = __ldcs(static_cast<const uint32_t*>(p));
+    }
+}
+
+// A lane's eight values of a segment: words of two 16-bit values or of one of 32 bits;
+// zeros past the row's end.
+template <class T, int V>
 struct Raw {
-    union {
-        uint4 q[sizeof(T) / 2];
-        T v[8];
-    };
-    __device__ Raw() {}
-    __device__ __forceinline__ void load(const T* row, int64_t c0, int64_t d, int lane) {
-        if constexpr (kVec) {
-            const int64_t c = c0 + lane * 8;
-            if (c < d) {
+    static constexpr int kWords = 2 * sizeof(T);
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const T* row, int c0, int d, int lane) {
 #pragma unroll
-                for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-                    q[i] = __ldcs(reinterpret_cast<const uint4*>(row + c) + i);
-            } else {
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
 #pragma unroll
-                for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) q[i] = make_uint4(0, 0, 0, 0);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int64_t c = c0 + column<false>(lane, e);
-                v[e] = c < d ? row[c] : from_f32<T>(0.0f);
+        for (int e = 0; e < 8; e += V) {
+            const int c = c0 + column<V>(lane, e);
+            if (c < d) {  // d is a multiple of V
+                if constexpr (V > 1) {
+                    load_words<V * sizeof(T)>(row + c, w + e * sizeof(T) / 4);
+                } else if constexpr (sizeof(T) == 4) {
+                    w[e] = __float_as_uint(__ldcs(reinterpret_cast<const float*>(row) + c));
+                } else {
+                    const uint32_t h = __ldcs(reinterpret_cast<const unsigned short*>(row) + c);
+                    w[e / 2] |= e & 1 ? h << 16 : h;
+                }
             }
         }
     }
+    __device__ __forceinline__ float value(int e) const {
+        if constexpr (sizeof(T) == 4) {
+            return __uint_as_float(w[e]);
+        } else {
+            const float2 f = pair_f32<T>(w[e / 2]);
+            return e & 1 ? f.y : f.x;
+        }
+    }
+    // The largest magnitude of the values of run r, as float32 bits.  Bits without the sign
+    // are ordered like the values, infinity and NaN above all of them.
+    __device__ __forceinline__ uint32_t top(int r) const {
+        uint32_t t = 0;
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int e = r * V; e < r * V + V; ++e) t = max(t, w[e] & 0x7fffffffu);
+        } else {
+            if constexpr (V > 1) {
+#pragma unroll
+                for (int i = r * V / 2; i < (r + 1) * V / 2; ++i) t = __vmaxu2(t, w[i] & 0x7fff7fffu);
+                t = max(t >> 16, t & 0xffffu);
+            } else {
+                t = (r & 1 ? w[r / 2] >> 16 : w[r / 2]) & 0x7fffu;
+            }
+            t = __float_as_uint(pair_f32<T>(t).x);
+        }
+        return t;
+    }
 };
 
-// |x| as bits: ordered like the values, infinity and NaN above all of them.
-__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
+// The scale of a maximum, and the two multipliers around 1/s.
 struct Scale {
-    float s;     // as it is stored
-    float t, r;  // what the values are divided by, and its reciprocal
-    int how;     // 0: codes are 0, 1: s is a normal number, 2: s is subnormal
+    float s, lo, hi;
+    bool plain;  // codes by the multipliers; otherwise by `code_of`
 };
+constexpr float kTwo64 = 18446744073709551616.0f;
+
 __device__ __forceinline__ Scale scale_of(uint32_t top) {
     Scale k;
-    k.t = k.r = 1.0f;
-    k.how = 0;
-    if (top >= 0x7f800000u) {
-        k.s = __uint_as_float(0x7fffffffu);
+    const float t = __uint_as_float(top);
+    // From 2^-100 on no step is subnormal, and t c, corrected by its remainder, is
+    // t / 127 correctly rounded (checked for every significand).
+    if (top - 0x0d800000u < 0x7f800000u - 0x0d800000u) {
+        const float c = 1.0f / 127.0f;
+        const float q = __fmul_rn(t, c);
+        k.s = __fmaf_rn(__fmaf_rn(-127.0f, q, t), c, q);
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(k.s));  // within 2^-23
+        k.lo = __fmul_rn(r, 1.0f - 1.0f / 2097152.0f);           // within 2^-20 below 1/s,
+        k.hi = __fmul_rn(r, 1.0f + 1.0f / 2097152.0f);           // and above
+        k.plain = true;
         return k;
     }
-    k.s = __fdiv_rn(__uint_as_float(top), 127.0f);
-    if (k.s == 0.0f) return k;
-    // a subnormal scale and its values are both taken 2^64 times (exactly)
-    k.how = k.s < 1.17549435e-38f ? 2 : 1;
-    k.t = k.how == 2 ? __fmul_rn(k.s, 18446744073709551616.0f) : k.s;
-    k.r = __frcp_rn(k.t);
+    k.s = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : __fdiv_rn(t, 127.0f);
+    k.lo = k.hi = 0.0f;
+    k.plain = top == 0;
     return k;
 }
 
-constexpr float kNearHalf = 0.5f - 1.0f / 32768.0f;
-
 // rint(x / s) of the exact quotient.  Near a half the sign of x - (half) s, which a
-// fused multiply-add gives exactly, says on which side of it the quotient lies.
-__device__ __forceinline__ int encode1(float x, const Scale& k) {
-    if (k.how == 0) return 0;
-    if (k.how == 2) x = __fmul_rn(x, 18446744073709551616.0f);
-    const float t = fminf(fmaxf(__fmul_rn(x, k.r), -127.0f), 127.0f);
+// fused multiply-add gives exactly, says on which side of it the quotient lies.  A
+// subnormal scale and its values are both taken 2^64 times (exactly).
+__device__ __forceinline__ int code_of(float x, float s) {
+    if (!(s > 0.0f)) return 0;  // 0 or NaN
+    if (s < 1.17549435e-38f) {
+        s = __fmul_rn(s, kTwo64);
+        x = __fmul_rn(x, kTwo64);
+    }
+    const float t = fminf(fmaxf(__fdiv_rn(x, s), -127.0f), 127.0f);
     float q = rintf(t);
-    if (fabsf(__fsub_rn(t, q)) > kNearHalf) {
-        const float lo = floorf(t);
-        const float e = __fmaf_rn(-__fadd_rn(lo, 0.5f), k.t, x);
-        if (e != 0.0f) q = e > 0.0f ? __fadd_rn(lo, 1.0f) : lo;
-        else q = rintf(__fadd_rn(lo, 0.5f));
+    if (fabsf(__fsub_rn(t, q)) > 0.5f - 1.0f / 32768.0f) {
+        const float below = floorf(t), half = __fadd_rn(below, 0.5f);
+        const float e = __fmaf_rn(-half, s, x);
+        q = e > 0.0f ? __fadd_rn(below, 1.0f) : e < 0.0f ? below : rintf(half);
     }
     return static_cast<int>(q);
 }
 
-// Eight codes in the low bytes of eight words.
-__device__ __forceinline__ void encode8(const float (&x)[8], const Scale& k, int (&q)[8]) {
-    constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number, half to even
-    if (k.how == 1) {
-        float far = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float t = __fmul_rn(x[e], k.r);
-            const float y = __fadd_rn(t, kMagic);
-            far = fmaxf(far, fabsf(__fsub_rn(t, __fsub_rn(y, kMagic))));
-            q[e] = __float_as_int(y);
-        }
-        if (far <= kNearHalf) return;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = encode1(x[e], k);
-}
-
-__device__ __forceinline__ uint32_t pack_bytes(int a, int b, int c, int d) {
+__device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// The low bytes of two words as float16 whole numbers: 1024 + (q + 128) has the
-// byte q ^ 0x80 at its low end.
-__device__ __forceinline__ uint32_t wide2(int a, int b) {
-    const uint32_t w = __byte_perm(a, b, 0x3430) & 0x00ff00ffu;  // a's and b's low byte, 16 bits each
-    const uint32_t biased = w ^ 0x64806480u;
-    __half2 h;
-    memcpy(&h, &biased, 4);
-    h = __hsub2(h, __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
-    uint32_t out;
-    memcpy(&out, &h, 4);
-    return out;
+constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number
+
+// The code of x where its two products round to a and z, neighbours (as bits of kMagic + q).
+__device__ __forceinline__ uint32_t between(float x, float s, uint32_t a, uint32_t z) {
+    const float fa = __fsub_rn(__uint_as_float(a), kMagic), fz = __fsub_rn(__uint_as_float(z), kMagic);
+    const float e = __fmaf_rn(-0.5f * __fadd_rn(fa, fz), s, x);  // exact in sign
+    if (e == 0.0f) return a & 1 ? z : a;
+    return e > 0.0f ? max(a, z) : min(a, z);
 }
 
-// Codes as bytes, or as float16 whole numbers.
-template <bool kVec>
-__device__ __forceinline__ void store8(int8_t* codes, __half* wide, int64_t c0, int64_t d, int lane, const int (&q)[8]) {
-    if constexpr (kVec) {
-        const int64_t c = c0 + lane * 8;
-        if (c >= d) return;
-        if (codes) {
-            const uint2 w = make_uint2(pack_bytes(q[0], q[1], q[2], q[3]), pack_bytes(q[4], q[5], q[6], q[7]));
-            *reinterpret_cast<uint2*>(codes + c) = w;
-        } else {
-            uint32_t w[4];
+// The codes of run r, in order, as bytes of `out` (V / 4 words, or one for V = 1).
+template <class T, int V>
+__device__ __forceinline__ void encode(const Raw<T, V>& raw, int r, const Scale& k, uint32_t* out) {
+    uint32_t a[V], z[V], differ = 0;
+    if constexpr (V > 1) {
+        const uint64_t lo = pack2(__float_as_uint(k.lo), __float_as_uint(k.lo));
+        const uint64_t hi = pack2(__float_as_uint(k.hi), __float_as_uint(k.hi));
+        const uint64_t m = pack2(__float_as_uint(kMagic), __float_as_uint(kMagic));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = wide2(q[2 * i], q[2 * i + 1]);
-            *reinterpret_cast<uint4*>(wide + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int e = 0; e < V; e += 2) {  // two multiply-adds at a time
+            const uint64_t x = pack2(__float_as_uint(raw.value(r * V + e)), __float_as_uint(raw.value(r * V + e + 1)));
+            uint64_t y;
+            asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(x), "l"(lo), "l"(m));
+            a[e] = static_cast<uint32_t>(y), a[e + 1] = static_cast<uint32_t>(y >> 32);
+            asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(x), "l"(hi), "l"(m));
+            z[e] = static_cast<uint32_t>(y), z[e + 1] = static_cast<uint32_t>(y >> 32);
+            differ |= (a[e] ^ z[e]) | (a[e + 1] ^ z[e + 1]);
         }
     } else {
+        const float x = raw.value(r);
+        a[0] = __float_as_uint(__fmaf_rn(x, k.lo, kMagic));
+        z[0] = __float_as_uint(__fmaf_rn(x, k.hi, kMagic));
+        differ = a[0] ^ z[0];
+    }
+    if (differ != 0) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int64_t c = c0 + column<false>(lane, e);
-            if (c < d) {
-                if (codes) codes[c] = static_cast<int8_t>(q[e]);
-                else wide[c] = __ushort_as_half(static_cast<unsigned short>(wide2(q[e], 0)));
-            }
+        for (int e = 0; e < V; ++e)
+            if (a[e] != z[e]) a[e] = between(raw.value(r * V + e), k.s, a[e], z[e]);
+    }
+    if (!k.plain) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) a[e] = static_cast<uint32_t>(code_of(raw.value(r * V + e), k.s));
+    }
+    if constexpr (V == 1) {
+        out[0] = a[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) out[i] = pack_bytes(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+    }
+}
+
+// Four codes as two words of two float16 whole numbers: 1024 + (q + 128) has the byte
+// q ^ 0x80 at its low end.
+__device__ __forceinline__ uint2 wide4(uint32_t q) {
+    const uint32_t u = q ^ 0x80808080u;
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 k = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    __half2 x, y;
+    memcpy(&x, &a, 4);
+    memcpy(&y, &b, 4);
+    x = __hsub2(x, k);
+    y = __hsub2(y, k);
+    memcpy(&a, &x, 4);
+    memcpy(&b, &y, 4);
+    return make_uint2(a, b);
+}
+
+// The codes of one run at column c, as bytes or as float16 whole numbers.
+template <int V>
+__device__ __forceinline__ void store(int8_t* codes, __half* wide, int c, const uint32_t* q) {
+    if constexpr (V == 1) {
+        if (codes) codes[c] = static_cast<int8_t>(q[0]);
+        else wide[c] = __int2half_rn(static_cast<int8_t>(q[0]));
+    } else if constexpr (V == 4) {
+        if (codes) *reinterpret_cast<uint32_t*>(codes + c) = q[0];
+        else *reinterpret_cast<uint2*>(wide + c) = wide4(q[0]);
+    } else {
+        if (codes) {
+            *reinterpret_cast<uint2*>(codes + c) = make_uint2(q[0], q[1]);
+        } else {
+            const uint2 a = wide4(q[0]), b = wide4(q[1]);
+            *reinterpret_cast<uint4*>(wide + c) = make_uint4(a.x, a.y, b.x, b.y);
         }
     }
 }
@@ -192,7 +271,8 @@ __device__ __forceinline__ int64_t row_of(int64_t item, int32_t items) {
 
 struct QuantizeParams {
     const void* x;
-    int64_t ldx, n, d, ldc, ldw;
+    int64_t ldx, n, ldc, ldw;
+    int32_t d;
     int32_t group;    // group kernel: 32 .. 256, or 256 for whole rows of at most 256 columns
     int32_t shift;    // its logarithm
     int64_t groups;   // scales of a row
@@ -204,64 +284,67 @@ struct QuantizeParams {
 };
 
 // Scales per group: one warp takes kItemSegments segments of a row.
-template <class T, bool kVec>
-__global__ void __launch_bounds__(256) rows8_group_kernel(const __grid_constant__ QuantizeParams p) {
+template <class T, int V>
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 5) rows8_group_kernel(const __grid_constant__ QuantizeParams p) {
+    constexpr int kRuns = 8 / V;
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int64_t r = row_of(item, p.items);
     if (r >= p.n) return;
-    const int64_t c00 = (item - r * p.items) * (kItemSegments * kSegment);
+    const int c00 = static_cast<int>(item - r * p.items) * (kItemSegments * kSegment);
     const T* const row = static_cast<const T*>(p.x) + r * p.ldx;
-    Raw<T, kVec> raw[kItemSegments];
+    int8_t* const codes = p.codes ? p.codes + r * p.ldc : nullptr;
+    __half* const wide = p.codes ? nullptr : p.wide + r * p.ldw;
+    float* const scale = p.scale + r * p.groups;
+    Raw<T, V> raw[kItemSegments];
 #pragma unroll
     for (int i = 0; i < kItemSegments; ++i) raw[i].load(row, c00 + i * kSegment, p.d, lane);
 #pragma unroll
     for (int i = 0; i < kItemSegments; ++i) {
-        const int64_t c0 = c00 + i * kSegment;
+        const int c0 = c00 + i * kSegment;
         if (c0 >= p.d) return;
-        float x[8];
-        int q[8];
-        int8_t* const codes = p.codes ? p.codes + r * p.ldc : nullptr;
-        __half* const wide = p.codes ? nullptr : p.wide + r * p.ldw;
+        // within a run a group is group / V lanes; beyond 32 lanes it is several runs
+        uint32_t top[kRuns];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = to_f32(raw[i].v[e]);
-        if constexpr (kVec) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = max(top, magnitude(x[e]));
-            for (int o = p.group >> 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
-            const Scale k = scale_of(top);
-            const int64_t c = c0 + lane * 8;
-            if (c < p.d && (lane & ((p.group >> 3) - 1)) == 0) p.scale[r * p.groups + (c >> p.shift)] = k.s;
-            encode8(x, k, q);
-        } else {
-            // a group is group / 32 elements of every lane
-            const int each = p.group >> 5;
-            uint32_t top[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top[e] = __reduce_max_sync(~0u, magnitude(x[e]));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                uint32_t t = 0;
-#pragma unroll
-                for (int o = 0; o < 8; ++o)
-                    if (o / each == e / each) t = max(t, top[o]);
-                const Scale k = scale_of(t);
-                const int64_t c = c0 + e * 32;
-                if (lane == 0 && e % each == 0 && c < p.d) p.scale[r * p.groups + (c >> p.shift)] = k.s;
-                q[e] = encode1(x[e], k);
+        for (int k = 0; k < kRuns; ++k) {
+            top[k] = raw[i].top(k);
+            if constexpr (V == 1) {
+                top[k] = __reduce_max_sync(~0u, top[k]);
+            } else {
+                for (int o = min(p.group / V, 32) >> 1; o > 0; o >>= 1)
+                    top[k] = max(top[k], __shfl_xor_sync(~0u, top[k], o));
             }
         }
-        store8<kVec>(codes, wide, c0, p.d, lane, q);
+        if constexpr (kRuns > 1) {
+#pragma unroll
+            for (int span = 1; span < kRuns; span *= 2)
+                if (p.group > 32 * V * span) {
+#pragma unroll
+                    for (int k = 0; k < kRuns; ++k)
+                        if (!(k & span)) top[k] = top[k ^ span] = max(top[k], top[k ^ span]);
+                }
+        }
+#pragma unroll
+        for (int k = 0; k < kRuns; ++k) {
+            const int c = c0 + column<V>(lane, k * V);
+            if (c < p.d) {
+                const Scale s = scale_of(top[k]);
+                if ((c & (p.group - 1)) == 0) scale[c >> p.shift] = s.s;
+                uint32_t q[V > 4 ? 2 : 1];
+                encode<T, V>(raw[i], k, s, q);
+                store<V>(codes, wide, c, q);
+            }
+        }
     }
 }
 
 // One scale per row: a CTA takes one row, kHeld segments per warp in registers.
 // Rows longer than that are read twice (the second time mostly from L2).
-template <class T, bool kVec, int kHeld>
-__global__ void __launch_bounds__(512) rows8_row_kernel(const __grid_constant__ QuantizeParams p) {
+template <class T, int V, int kHeld>
+__global__ void __launch_bounds__(512, 2) rows8_row_kernel(const __grid_constant__ QuantizeParams p) {
+    constexpr int kRuns = 8 / V;
     griddep_wait();
     griddep_launch_dependents();
     __shared__ uint32_t tops[16];
@@ -270,47 +353,48 @@ __global__ void __launch_bounds__(512) rows8_row_kernel(const __grid_constant__ 
     const T* const row = static_cast<const T*>(p.x) + r * p.ldx;
     int8_t* const codes = p.codes ? p.codes + r * p.ldc : nullptr;
     __half* const wide = p.codes ? nullptr : p.wide + r * p.ldw;
-    Raw<T, kVec> raw[kHeld];
+    Raw<T, V> raw[kHeld];
     uint32_t top = 0;
-    for (int64_t c00 = warp * (kHeld * kSegment); c00 < p.d; c00 += p.held) {
+    for (int c00 = warp * (kHeld * kSegment); c00 < p.d; c00 += p.held) {
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) raw[i].load(row, c00 + i * kSegment, p.d, lane);
 #pragma unroll
         for (int i = 0; i < kHeld; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top = max(top, magnitude(to_f32(raw[i].v[e])));
+            for (int k = 0; k < kRuns; ++k) top = max(top, raw[i].top(k));
     }
     top = __reduce_max_sync(~0u, top);
     if (lane == 0) tops[warp] = top;
     __syncthreads();
     top = lane < static_cast<int>(blockDim.x >> 5) ? tops[lane] : 0u;
     top = __reduce_max_sync(~0u, top);
-    const Scale k = scale_of(top);
-    if (threadIdx.x == 0) p.scale[r] = k.s;
-    for (int64_t c00 = warp * (kHeld * kSegment); c00 < p.d; c00 += p.held) {
+    const Scale s = scale_of(top);
+    if (threadIdx.x == 0) p.scale[r] = s.s;
+    for (int c00 = warp * (kHeld * kSegment); c00 < p.d; c00 += p.held) {
         if (p.held < p.d) {
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) raw[i].load(row, c00 + i * kSegment, p.d, lane);
         }
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const int64_t c0 = c00 + i * kSegment;
-            if (c0 >= p.d) break;
-            float x[8];
-            int q[8];
+        for (int i = 0; i < kHeld; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = to_f32(raw[i].v[e]);
-            encode8(x, k, q);
-            store8<kVec>(codes, wide, c0, p.d, lane, q);
-        }
+            for (int k = 0; k < kRuns; ++k) {
+                const int c = c00 + i * kSegment + column<V>(lane, k * V);
+                if (c < p.d) {
+                    uint32_t q[V > 4 ? 2 : 1];
+                    encode<T, V>(raw[i], k, s, q);
+                    store<V>(codes, wide, c, q);
+                }
+            }
     }
 }
 
 struct RestoreParams {
     const int8_t* codes;
     const float* scale;  // NULL: 1
-    int64_t ldc, n, d, ldx;
-    int32_t shift;   // log2(group); whole rows: 63
+    int64_t ldc, n, ldx;
+    int32_t d;
+    int32_t shift;   // log2(group); whole rows: 31
     int64_t groups;  // scales of a row
     int32_t items;   // items of kItemSegments segments in a row
     void* x;
@@ -321,63 +405,90 @@ __device__ __forceinline__ float byte_to_f32(uint32_t biased, uint32_t which) {
     return __fsub_rn(__uint_as_float(__byte_perm(biased, 0x4b000000u, 0x7440 + which)), 8388736.0f);
 }
 
-template <class T, bool kVec>
+template <class T>
+__device__ __forceinline__ uint32_t two_of(float a, float b);  // as 16-bit values
+template <>
+__device__ __forceinline__ uint32_t two_of<__half>(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    uint32_t w;
+    memcpy(&w, &h, 4);
+    return w;
+}
+template <>
+__device__ __forceinline__ uint32_t two_of<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    uint32_t w;
+    memcpy(&w, &h, 4);
+    return w;
+}
+
+// V values of one run at `out`.
+template <class T, int V>
+__device__ __forceinline__ void put(T* out, const float (&x)[V]) {
+    if constexpr (sizeof(T) == 4) {
+        if constexpr (V == 1) {
+            *reinterpret_cast<float*>(out) = x[0];
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i += 4)
+                *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + i) =
+                    make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        }
+    } else if constexpr (V == 1) {
+        *reinterpret_cast<unsigned short*>(out) = static_cast<unsigned short>(two_of<T>(x[0], 0.0f));
+    } else {
+        uint32_t w[V / 2];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) w[i] = two_of<T>(x[2 * i], x[2 * i + 1]);
+        if constexpr (V == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+template <class T, int V>
 __global__ void __launch_bounds__(256) rows8_restore_kernel(const __grid_constant__ RestoreParams p) {
+    constexpr int kRuns = 8 / V;
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int64_t r = row_of(item, p.items);
     if (r >= p.n) return;
-    const int64_t c00 = (item - r * p.items) * (kItemSegments * kSegment);
+    const int c00 = static_cast<int>(item - r * p.items) * (kItemSegments * kSegment);
     const int8_t* const codes = p.codes + r * p.ldc;
     const float* const scale = p.scale ? p.scale + r * p.groups : nullptr;
     T* const out = static_cast<T*>(p.x) + r * p.ldx;
-    if constexpr (kVec) {
-        uint2 w[kItemSegments];
-        float s[kItemSegments];
+    uint32_t w[kItemSegments][kRuns][V > 4 ? 2 : 1];
+    float s[kItemSegments][kRuns];
 #pragma unroll
-        for (int i = 0; i < kItemSegments; ++i) {
-            const int64_t c = c00 + i * kSegment + lane * 8;
+    for (int i = 0; i < kItemSegments; ++i)
+#pragma unroll
+        for (int k = 0; k < kRuns; ++k) {
+            const int c = c00 + i * kSegment + column<V>(lane, k * V);
             const bool in = c < p.d;
-            w[i] = in ? __ldcs(reinterpret_cast<const uint2*>(codes + c)) : make_uint2(0, 0);
-            s[i] = in && scale ? scale[c >> p.shift] : 1.0f;
+            if constexpr (V == 8) {
+                const uint2 v = in ? __ldcs(reinterpret_cast<const uint2*>(codes + c)) : make_uint2(0, 0);
+                w[i][k][0] = v.x, w[i][k][1] = v.y;
+            } else if constexpr (V == 4) {
+                w[i][k][0] = in ? __ldcs(reinterpret_cast<const uint32_t*>(codes + c)) : 0u;
+            } else {
+                w[i][k][0] = in ? __ldcs(reinterpret_cast<const unsigned char*>(codes + c)) : 0u;
+            }
+            s[i][k] = in && scale ? scale[c >> p.shift] : 1.0f;
         }
 #pragma unroll
-        for (int i = 0; i < kItemSegments; ++i) {
-            const int64_t c = c00 + i * kSegment + lane * 8;
-            if (c >= p.d) return;
-            const uint32_t a = w[i].x ^ 0x80808080u, b = w[i].y ^ 0x80808080u;
-            union {
-                uint4 q[sizeof(T) / 2];
-                T v[8];
-            } y;
+    for (int i = 0; i < kItemSegments; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                y.v[e] = from_f32<T>(__fmul_rn(byte_to_f32(a, e), s[i]));
-                y.v[4 + e] = from_f32<T>(__fmul_rn(byte_to_f32(b, e), s[i]));
-            }
+        for (int k = 0; k < kRuns; ++k) {
+            const int c = c00 + i * kSegment + column<V>(lane, k * V);
+            if (c < p.d) {
+                float x[V];
 #pragma unroll
-            for (int j = 0; j < static_cast<int>(sizeof(T)) / 2; ++j) reinterpret_cast<uint4*>(out + c)[j] = y.q[j];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kItemSegments; ++i) {
-            int8_t q[8];
-            float s[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int64_t c = c00 + i * kSegment + column<false>(lane, e);
-                q[e] = c < p.d ? codes[c] : int8_t(0);
-                s[e] = c < p.d && scale ? scale[c >> p.shift] : 1.0f;
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int64_t c = c00 + i * kSegment + column<false>(lane, e);
-                if (c < p.d) out[c] = from_f32<T>(__fmul_rn(static_cast<float>(q[e]), s[e]));
+                for (int e = 0; e < V; ++e)
+                    x[e] = __fmul_rn(byte_to_f32(w[i][k][e / 4] ^ 0x80808080u, e % 4), s[i][k]);
+                put<T, V>(out + c, x);
             }
         }
-    }
 }
 
 int log2_of(int32_t group) {
@@ -404,40 +515,47 @@ bool aligned(const void* p, int64_t stride_bytes, int to) {
     return reinterpret_cast<uintptr_t>(p) % to == 0 && stride_bytes % to == 0;
 }
 
-template <class T, bool kVec>
+template <class T, int V>
 cudaError_t quantize_as(QuantizeParams& p, cudaStream_t s) {
     if (p.group != 0 || p.d <= kSegment) {
         if (p.group == 0) p.group = kSegment;
         p.shift = log2_of(p.group);
-        p.items = static_cast<int32_t>((p.d + kItemSegments * kSegment - 1) / (kItemSegments * kSegment));
-        return rows_launch(rows8_group_kernel<T, kVec>, p, (p.n * p.items + 7) / 8, 256, s);
+        p.items = (p.d + kItemSegments * kSegment - 1) / (kItemSegments * kSegment);
+        return rows_launch(rows8_group_kernel<T, V>, p, (p.n * p.items + 7) / 8, 256, s);
     }
     // Few rows are spread over more warps each, so that a row takes one round trip to
     // memory and little work after it; many rows get smaller CTAs.
-    const int64_t segments = (p.d + kSegment - 1) / kSegment;
-    const int64_t held = p.n <= 512 ? (segments + 15) / 16 : 4;
-    const int h = held <= 1 ? 1 : held <= 2 ? 2 : 4;
-    int64_t warps = (segments + h - 1) / h;
+    const int segments = (p.d + kSegment - 1) / kSegment;
+    const int h = p.n <= 512 && segments <= 16 ? 1 : 4;
+    int warps = (segments + h - 1) / h;
     if (warps > 16) warps = 16;
-    p.held = static_cast<int32_t>(warps * h * kSegment);
-    const auto kernel = h == 1 ? rows8_row_kernel<T, kVec, 1> : h == 2 ? rows8_row_kernel<T, kVec, 2>
-                                                                       : rows8_row_kernel<T, kVec, 4>;
-    return rows_launch(kernel, p, p.n, static_cast<int>(warps) * 32, s);
+    p.held = warps * h * kSegment;
+    return rows_launch(h == 1 ? rows8_row_kernel<T, V, 1> : rows8_row_kernel<T, V, 4>, p, p.n, warps * 32, s);
+}
+
+// The widest run that rows of both matrices allow.
+int run_of(int32_t d, const void* x, int64_t x_row, int x_item, const void* q, int64_t q_row, int q_item) {
+    for (int v : {8, 4})
+        if (d % v == 0 && aligned(x, x_row * x_item, v * x_item < 16 ? v * x_item : 16) &&
+            aligned(q, q_row * q_item, v * q_item < 16 ? v * q_item : 16))
+            return v;
+    return 1;
 }
 
 template <class T>
 cudaError_t quantize_of(QuantizeParams& p, cudaStream_t s) {
-    const bool vec = p.d % 8 == 0 && aligned(p.x, p.ldx * static_cast<int64_t>(sizeof(T)), 16) &&
-                     (p.codes ? aligned(p.codes, p.ldc, 8) : aligned(p.wide, p.ldw * 2, 16));
-    return vec ? quantize_as<T, true>(p, s) : quantize_as<T, false>(p, s);
+    const int v = p.codes ? run_of(p.d, p.x, p.ldx, sizeof(T), p.codes, p.ldc, 1)
+                          : run_of(p.d, p.x, p.ldx, sizeof(T), p.wide, p.ldw, 2);
+    return v == 8 ? quantize_as<T, 8>(p, s) : v == 4 ? quantize_as<T, 4>(p, s) : quantize_as<T, 1>(p, s);
 }
 
 template <class T>
 cudaError_t restore_of(RestoreParams& p, cudaStream_t s) {
-    const bool vec = p.d % 8 == 0 && aligned(p.codes, p.ldc, 8) &&
-                     aligned(p.x, p.ldx * static_cast<int64_t>(sizeof(T)), 16);
-    return rows_launch(vec ? rows8_restore_kernel<T, true> : rows8_restore_kernel<T, false>, p,
-                       (p.n * p.items + 7) / 8, 256, s);
+    const int v = run_of(p.d, p.x, p.ldx, sizeof(T), p.codes, p.ldc, 1);
+    return rows_launch(v == 8   ? rows8_restore_kernel<T, 8>
+                       : v == 4 ? rows8_restore_kernel<T, 4>
+                                : rows8_restore_kernel<T, 1>,
+                       p, (p.n * p.items + 7) / 8, 256, s);
 }
 
 hess_status rows_fail(hess_status s, const char* fmt, ...) {
@@ -508,7 +626,7 @@ cudaError_t rows8_quantize_launch(const void* X, int64_t ldx, int64_t n, int64_t
     p.x = X;
     p.ldx = ldx;
     p.n = n;
-    p.d = d;
+    p.d = static_cast<int32_t>(d);
     p.ldc = ldc;
     p.ldw = ldw;
     p.group = group;
@@ -529,9 +647,9 @@ cudaError_t rows8_restore_launch(const int8_t* codes, int64_t ldc, const float* 
     p.scale = scale;
     p.ldc = ldc;
     p.n = n;
-    p.d = d;
+    p.d = static_cast<int32_t>(d);
     p.ldx = ldx;
-    p.shift = group ? log2_of(group) : 63;
+    p.shift = group ? log2_of(group) : 31;
     p.groups = group ? (d + group - 1) / group : 1;
     p.items = static_cast<int32_t>((d + kItemSegments * kSegment - 1) / (kItemSegments * kSegment));
     p.x = X;
