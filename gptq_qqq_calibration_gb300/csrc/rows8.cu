@@ -1,24 +1,30 @@
 // 8-bit rows: int8 codes with a scale per row or per group of columns
 // (formulas and conventions: include/rows8.h).
 //
-// The unit of work is a segment: 256 columns of one row, eight per lane of a warp.
-// A group of 32 .. 256 columns lies inside a segment, so its maximum is a few
-// shuffles; a whole row's segments are held in the registers of one CTA and its
-// maximum meets in shared memory, so that the values are read once either way.
-// A lane's columns come in runs of V side by side, 32 V columns apart: V is 8 where
-// rows are multiples of 16 bytes, 4 where they are of half that, else 1, which keeps a
-// warp's accesses contiguous at any alignment.
+// The unit of work is a segment: 256 columns of one row, eight per lane of a warp (512
+// and sixteen where rows allow it).  A group of 32 .. 256 columns lies inside a segment,
+// so its maximum is a few shuffles; a whole row is held by one CTA, in registers or, where
+// there are many rows, in shared memory, and its maximum meets in shared memory, so
+// that the values are read once either way.  A lane's columns come in runs of V side by
+// side, 32 V columns apart: V is 16 or 8 where rows are multiples of 16 bytes, 4 where they
+// are of half that, else 1, which keeps a warp's accesses contiguous at any alignment.
 //
 // The whole number nearest to the exact quotient x / s is wanted, and the memory's pace
-// leaves some ten instructions a value.  So the value is multiplied by a number a little
-// below 1/s and by one a little above it, each product rounded to a whole number by the
-// multiply-add that adds 1.5 * 2^23.  The quotient lies between the products: where both
-// round alike that is the code, and where they do not the exact sign of the remainder at
-// the half between them decides (16-bit values meet that in 1 of 400: half of a row's
-// maximum is 63.5 s, up to the rounding of s).
+// leaves some ten instructions a value.  A multiply-add that adds 1.5 * 2^23 rounds a
+// product to a whole number.  What it must not do is put a quotient near a half on the
+// wrong side:
+//   * 16-bit values.  With p significant bits in x and a, 127 x / a is a half itself or
+//     1 / (254 * 2^p) >= 2^-19 of itself away from one.  So only halves matter, where x / s lies
+//     above or below by the rounding of s = a / 127: the multiplier is taken 2^-21 above
+//     or below 1/s, to the side of that rounding (a row whose s needs none and is no
+//     power of two is divided value by value).
+//   * 32-bit values.  One multiplier below 1/s and one above it: where both products round
+//     alike that is the code, and where they do not (1 value in 10^5) the exact sign of
+//     the remainder at the half between them decides.
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <mutex>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -33,6 +39,9 @@ namespace hk {
 namespace {
 
 constexpr int kSegment = 256;
+// Values of a lane in a segment, and columns of a segment, for runs of V.
+__host__ __device__ constexpr int lane_values(int v) { return v > 8 ? v : 8; }
+__host__ __device__ constexpr int segment_columns(int v) { return 32 * lane_values(v); }
 constexpr int kItemSegments = 4;  // segments one warp has in flight
 
 template <class T>
@@ -72,17 +81,17 @@ __device__ __forceinline__ void load_words(const void* p, uint32_t* w) {
     }
 }
 
-// A lane's eight values of a segment: words of two 16-bit values or of one of 32 bits;
-// zeros past the row's end.
+// A lane's values of a segment: words of two 16-bit values or of one of 32 bits; zeros
+// past the row's end.
 template <class T, int V>
 struct Raw {
-    static constexpr int kWords = 2 * sizeof(T);
+    static constexpr int kWords = lane_values(V) * sizeof(T) / 4;
     uint32_t w[kWords];
     __device__ __forceinline__ void load(const T* row, int c0, int d, int lane) {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) w[i] = 0;
 #pragma unroll
-        for (int e = 0; e < 8; e += V) {
+        for (int e = 0; e < lane_values(V); e += V) {
             const int c = c0 + column<V>(lane, e);
             if (c < d) {  // d is a multiple of V
                 if constexpr (V > 1) {
@@ -114,7 +123,7 @@ struct Raw {
         } else {
             if constexpr (V > 1) {
 #pragma unroll
-                for (int i = r * V / 2; i < (r + 1) * V / 2; ++i) t = __vmaxu2(t, w[i] & 0x7fff7fffu);
+                for (int i = r * V / 2; i < (r + 1) * V / 2; ++i) asm("max.u16x2 %0, %1, %2;" : "=r"(t) : "r"(t), "r"(w[i] & 0x7fff7fffu));
                 t = max(t >> 16, t & 0xffffu);
             } else {
                 t = (r & 1 ? w[r / 2] >> 16 : w[r / 2]) & 0x7fffu;
@@ -125,13 +134,14 @@ struct Raw {
     }
 };
 
-// The scale of a maximum, and the two multipliers around 1/s.
+// The scale of a maximum, and what the values are multiplied by.
 struct Scale {
-    float s, lo, hi;
-    bool plain;  // codes by the multipliers; otherwise by `code_of`
+    float s, lo, hi;  // 16-bit values: lo alone
+    bool plain;       // codes by the multipliers; otherwise by `code_of`
 };
 constexpr float kTwo64 = 18446744073709551616.0f;
 
+template <class T>
 __device__ __forceinline__ Scale scale_of(uint32_t top) {
     Scale k;
     const float t = __uint_as_float(top);
@@ -139,13 +149,25 @@ __device__ __forceinline__ Scale scale_of(uint32_t top) {
     // t / 127 correctly rounded (checked for every significand).
     if (top - 0x0d800000u < 0x7f800000u - 0x0d800000u) {
         const float c = 1.0f / 127.0f;
+        constexpr float kBelow = 1.0f - 1.0f / 2097152.0f, kAbove = 1.0f + 1.0f / 2097152.0f;
         const float q = __fmul_rn(t, c);
         k.s = __fmaf_rn(__fmaf_rn(-127.0f, q, t), c, q);
         float r;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(k.s));  // within 2^-23
-        k.lo = __fmul_rn(r, 1.0f - 1.0f / 2097152.0f);           // within 2^-20 below 1/s,
-        k.hi = __fmul_rn(r, 1.0f + 1.0f / 2097152.0f);           // and above
         k.plain = true;
+        if constexpr (sizeof(T) == 4) {
+            k.lo = __fmul_rn(r, kBelow);  // within 2^-20 below 1/s,
+            k.hi = __fmul_rn(r, kAbove);  // and above
+        } else {
+            const float left = __fmaf_rn(-127.0f, k.s, t);  // exact
+            k.lo = __fmul_rn(r, left > 0.0f ? kAbove : kBelow);
+            k.hi = 0.0f;
+            if (left == 0.0f) {
+                // s is t / 127 itself, and halves go to the even code: right where 1/s is exact
+                k.lo = __uint_as_float(0x7f000000u - __float_as_uint(k.s));
+                k.plain = (__float_as_uint(k.s) & 0x7fffffu) == 0;
+            }
+        }
         return k;
     }
     k.s = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : __fdiv_rn(t, 127.0f);
@@ -190,31 +212,38 @@ __device__ __forceinline__ uint32_t between(float x, float s, uint32_t a, uint32
 // The codes of run r, in order, as bytes of `out` (V / 4 words, or one for V = 1).
 template <class T, int V>
 __device__ __forceinline__ void encode(const Raw<T, V>& raw, int r, const Scale& k, uint32_t* out) {
-    uint32_t a[V], z[V], differ = 0;
+    uint32_t a[V];
     if constexpr (V > 1) {
         const uint64_t lo = pack2(__float_as_uint(k.lo), __float_as_uint(k.lo));
         const uint64_t hi = pack2(__float_as_uint(k.hi), __float_as_uint(k.hi));
         const uint64_t m = pack2(__float_as_uint(kMagic), __float_as_uint(kMagic));
+        uint32_t z[V], differ = 0;
 #pragma unroll
         for (int e = 0; e < V; e += 2) {  // two multiply-adds at a time
             const uint64_t x = pack2(__float_as_uint(raw.value(r * V + e)), __float_as_uint(raw.value(r * V + e + 1)));
             uint64_t y;
             asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(x), "l"(lo), "l"(m));
             a[e] = static_cast<uint32_t>(y), a[e + 1] = static_cast<uint32_t>(y >> 32);
-            asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(x), "l"(hi), "l"(m));
-            z[e] = static_cast<uint32_t>(y), z[e + 1] = static_cast<uint32_t>(y >> 32);
-            differ |= (a[e] ^ z[e]) | (a[e + 1] ^ z[e + 1]);
+            if constexpr (sizeof(T) == 4) {
+                asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(x), "l"(hi), "l"(m));
+                z[e] = static_cast<uint32_t>(y), z[e + 1] = static_cast<uint32_t>(y >> 32);
+                differ |= (a[e] ^ z[e]) | (a[e + 1] ^ z[e + 1]);
+            }
+        }
+        if constexpr (sizeof(T) == 4) {
+            if (differ != 0) {
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    if (a[e] != z[e]) a[e] = between(raw.value(r * V + e), k.s, a[e], z[e]);
+            }
         }
     } else {
         const float x = raw.value(r);
         a[0] = __float_as_uint(__fmaf_rn(x, k.lo, kMagic));
-        z[0] = __float_as_uint(__fmaf_rn(x, k.hi, kMagic));
-        differ = a[0] ^ z[0];
-    }
-    if (differ != 0) {
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-            if (a[e] != z[e]) a[e] = between(raw.value(r * V + e), k.s, a[e], z[e]);
+        if constexpr (sizeof(T) == 4) {
+            const uint32_t z = __float_as_uint(__fmaf_rn(x, k.hi, kMagic));
+            if (a[0] != z) a[0] = between(x, k.s, a[0], z);
+        }
     }
     if (!k.plain) {
 #pragma unroll
@@ -253,6 +282,16 @@ __device__ __forceinline__ void store(int8_t* codes, __half* wide, int c, const 
     } else if constexpr (V == 4) {
         if (codes) *reinterpret_cast<uint32_t*>(codes + c) = q[0];
         else *reinterpret_cast<uint2*>(wide + c) = wide4(q[0]);
+    } else if constexpr (V == 16) {
+        if (codes) {
+            *reinterpret_cast<uint4*>(codes + c) = make_uint4(q[0], q[1], q[2], q[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint2 a = wide4(q[2 * i]), b = wide4(q[2 * i + 1]);
+                reinterpret_cast<uint4*>(wide + c)[i] = make_uint4(a.x, a.y, b.x, b.y);
+            }
+        }
     } else {
         if (codes) {
             *reinterpret_cast<uint2*>(codes + c) = make_uint2(q[0], q[1]);
@@ -276,78 +315,118 @@ struct QuantizeParams {
     int32_t group;    // group kernel: 32 .. 256, or 256 for whole rows of at most 256 columns
     int32_t shift;    // its logarithm
     int64_t groups;   // scales of a row
-    int32_t items;    // group kernel: items of kItemSegments segments in a row
+    int32_t items;    // group kernel: segments of a row
     int32_t held;     // row kernel: columns that a pass of the CTA covers
     int8_t* codes;
     __half* wide;
     float* scale;
 };
 
-// Scales per group: one warp takes kItemSegments segments of a row.
-template <class T, int V>
-__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 5) rows8_group_kernel(const __grid_constant__ QuantizeParams p) {
-    constexpr int kRuns = 8 / V;
-    griddep_wait();
-    griddep_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t r = row_of(item, p.items);
-    if (r >= p.n) return;
-    const int c00 = static_cast<int>(item - r * p.items) * (kItemSegments * kSegment);
-    const T* const row = static_cast<const T*>(p.x) + r * p.ldx;
+// Scales per group.  Warps walk the segments of all rows, with the next one on its way
+// from memory under the one at work.
+template <class T, int V, int kGroup>
+__device__ __forceinline__ void encode_segment(const QuantizeParams& p, const Raw<T, V>& raw, int64_t r, int c0, int lane) {
+    constexpr int kRuns = lane_values(V) / V;
+    const int group = kGroup ? kGroup : p.group;
+    // within a run a group is group / V lanes; beyond 32 lanes it is several runs
+    uint32_t top[kRuns];
+#pragma unroll
+    for (int k = 0; k < kRuns; ++k) {
+        top[k] = raw.top(k);
+        if constexpr (V == 1) {
+            top[k] = __reduce_max_sync(~0u, top[k]);
+        } else {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                if (o < group / V) top[k] = max(top[k], __shfl_xor_sync(~0u, top[k], o));
+        }
+    }
+    if constexpr (kRuns > 1) {
+#pragma unroll
+        for (int span = 1; span < kRuns; span *= 2)
+            if (group > 32 * V * span) {
+#pragma unroll
+                for (int k = 0; k < kRuns; ++k)
+                    if (!(k & span)) top[k] = top[k ^ span] = max(top[k], top[k ^ span]);
+            }
+    }
     int8_t* const codes = p.codes ? p.codes + r * p.ldc : nullptr;
     __half* const wide = p.codes ? nullptr : p.wide + r * p.ldw;
     float* const scale = p.scale + r * p.groups;
-    Raw<T, V> raw[kItemSegments];
+    Scale s;
 #pragma unroll
-    for (int i = 0; i < kItemSegments; ++i) raw[i].load(row, c00 + i * kSegment, p.d, lane);
-#pragma unroll
-    for (int i = 0; i < kItemSegments; ++i) {
-        const int c0 = c00 + i * kSegment;
-        if (c0 >= p.d) return;
-        // within a run a group is group / V lanes; beyond 32 lanes it is several runs
-        uint32_t top[kRuns];
-#pragma unroll
-        for (int k = 0; k < kRuns; ++k) {
-            top[k] = raw[i].top(k);
-            if constexpr (V == 1) {
-                top[k] = __reduce_max_sync(~0u, top[k]);
-            } else {
-                for (int o = min(p.group / V, 32) >> 1; o > 0; o >>= 1)
-                    top[k] = max(top[k], __shfl_xor_sync(~0u, top[k], o));
-            }
-        }
-        if constexpr (kRuns > 1) {
-#pragma unroll
-            for (int span = 1; span < kRuns; span *= 2)
-                if (p.group > 32 * V * span) {
-#pragma unroll
-                    for (int k = 0; k < kRuns; ++k)
-                        if (!(k & span)) top[k] = top[k ^ span] = max(top[k], top[k ^ span]);
-                }
-        }
-#pragma unroll
-        for (int k = 0; k < kRuns; ++k) {
-            const int c = c0 + column<V>(lane, k * V);
-            if (c < p.d) {
-                const Scale s = scale_of(top[k]);
-                if ((c & (p.group - 1)) == 0) scale[c >> p.shift] = s.s;
-                uint32_t q[V > 4 ? 2 : 1];
-                encode<T, V>(raw[i], k, s, q);
-                store<V>(codes, wide, c, q);
-            }
+    for (int k = 0; k < kRuns; ++k) {
+        const int c = c0 + column<V>(lane, k * V);
+        if (kRuns == 1 || ((32 * V * k) & (group - 1)) == 0) s = scale_of<T>(top[k]);  // a group's first run
+        if (c < p.d) {
+            if ((c & (group - 1)) == 0) scale[c >> p.shift] = s.s;
+            uint32_t q[V > 4 ? V / 4 : 1];
+            encode<T, V>(raw, k, s, q);
+            store<V>(codes, wide, c, q);
         }
     }
 }
 
+// Segment `index` of all rows, walked by `step` segments at a time.
+struct Walk {
+    int64_t r;
+    int32_t c;  // segment of the row
+    __device__ __forceinline__ Walk(int64_t index, int32_t segments) {
+        r = row_of(index, segments);
+        c = static_cast<int32_t>(index - r * segments);
+    }
+    __device__ __forceinline__ void add(const Walk& step, int32_t segments) {
+        r += step.r;
+        c += step.c;
+        if (c >= segments) {
+            c -= segments;
+            ++r;
+        }
+    }
+};
+
+constexpr int kGroupWarps = 8, kGroupCtas = 4;
+
+template <class T, int V, int kGroup>
+__global__ void __launch_bounds__(kGroupWarps * 32, kGroupCtas)
+    rows8_group_kernel(const __grid_constant__ QuantizeParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t warp = static_cast<int64_t>(blockIdx.x) * kGroupWarps + (threadIdx.x >> 5);
+    const Walk step(static_cast<int64_t>(gridDim.x) * kGroupWarps, p.items);
+    Walk at(warp, p.items);
+    const auto fetch = [&](Raw<T, V>& raw, const Walk& w) {
+        if (w.r < p.n) raw.load(static_cast<const T*>(p.x) + w.r * p.ldx, w.c * segment_columns(V), p.d, lane);
+    };
+    Walk next = at;
+    Raw<T, V> a, b;
+    fetch(a, at);
+    // two segments a turn, each fetched while the other is at work
+#pragma unroll 1
+    while (at.r < p.n) {
+        next.add(step, p.items);
+        fetch(b, next);
+        encode_segment<T, V, kGroup>(p, a, at.r, at.c * segment_columns(V), lane);
+        at = next;
+        if (at.r >= p.n) return;
+        next.add(step, p.items);
+        fetch(a, next);
+        encode_segment<T, V, kGroup>(p, b, at.r, at.c * segment_columns(V), lane);
+        at = next;
+    }
+}
+
 // One scale per row: a CTA takes one row, kHeld segments per warp in registers.
-// Rows longer than that are read twice (the second time mostly from L2).
+// Rows longer than that are read twice (the second time mostly from L2).  Two large
+// CTAs per SM, so that one loads while the other works.
+constexpr int kRowWarps = 24;
 template <class T, int V, int kHeld>
-__global__ void __launch_bounds__(512, 2) rows8_row_kernel(const __grid_constant__ QuantizeParams p) {
+__global__ void __launch_bounds__(kRowWarps * 32, 2) rows8_row_kernel(const __grid_constant__ QuantizeParams p) {
     constexpr int kRuns = 8 / V;
     griddep_wait();
     griddep_launch_dependents();
-    __shared__ uint32_t tops[16];
+    __shared__ uint32_t tops[kRowWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t r = blockIdx.x;
     const T* const row = static_cast<const T*>(p.x) + r * p.ldx;
@@ -368,7 +447,7 @@ __global__ void __launch_bounds__(512, 2) rows8_row_kernel(const __grid_constant
     __syncthreads();
     top = lane < static_cast<int>(blockDim.x >> 5) ? tops[lane] : 0u;
     top = __reduce_max_sync(~0u, top);
-    const Scale s = scale_of(top);
+    const Scale s = scale_of<T>(top);
     if (threadIdx.x == 0) p.scale[r] = s.s;
     for (int c00 = warp * (kHeld * kSegment); c00 < p.d; c00 += p.held) {
         if (p.held < p.d) {
@@ -386,6 +465,102 @@ __global__ void __launch_bounds__(512, 2) rows8_row_kernel(const __grid_constant
                     store<V>(codes, wide, c, q);
                 }
             }
+    }
+}
+
+// One scale per row, rows of at most kShort segments: a warp holds one.
+constexpr int kShort = 4;
+
+template <class T, int V>
+__global__ void __launch_bounds__(kGroupWarps * 32, 3) rows8_short_kernel(const __grid_constant__ QuantizeParams p) {
+    constexpr int kRuns = lane_values(V) / V;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kGroupWarps;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kGroupWarps + (threadIdx.x >> 5); r < p.n; r += step) {
+        const T* const row = static_cast<const T*>(p.x) + r * p.ldx;
+        Raw<T, V> raw[kShort];
+#pragma unroll
+        for (int i = 0; i < kShort; ++i) raw[i].load(row, i * segment_columns(V), p.d, lane);
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < kShort; ++i)
+#pragma unroll
+            for (int k = 0; k < kRuns; ++k) top = max(top, raw[i].top(k));
+        const Scale s = scale_of<T>(__reduce_max_sync(~0u, top));
+        if (lane == 0) p.scale[r] = s.s;
+        int8_t* const codes = p.codes ? p.codes + r * p.ldc : nullptr;
+        __half* const wide = p.codes ? nullptr : p.wide + r * p.ldw;
+#pragma unroll
+        for (int i = 0; i < kShort; ++i)
+#pragma unroll
+            for (int k = 0; k < kRuns; ++k) {
+                const int c = i * segment_columns(V) + column<V>(lane, k * V);
+                if (c < p.d) {
+                    uint32_t q[V > 4 ? V / 4 : 1];
+                    encode<T, V>(raw[i], k, s, q);
+                    store<V>(codes, wide, c, q);
+                }
+            }
+    }
+}
+
+// One scale per row, many rows of 16-bit values: a CTA walks rows, with the next one on
+// its way into shared memory under the one at work.  A thread copies, and later reads,
+// the same granules of eight values, so only the maxima have to meet.  (Rows in
+// registers cost every warp its start and its scale for two segments of a row: 124 us
+// against 90 for 16,384 x 11,008 bf16.)
+constexpr int kStreamThreads = 128;
+
+template <class T>
+__global__ void __launch_bounds__(kStreamThreads) rows8_stream_kernel(const __grid_constant__ QuantizeParams p) {
+    extern __shared__ uint4 buffers[];  // two rows
+    __shared__ uint32_t tops[2][kStreamThreads / 32];
+    const int granules = p.d >> 3;
+    griddep_wait();
+    griddep_launch_dependents();
+    const auto fetch = [&](int64_t r, int b) {
+        if (r < p.n) {
+            const uint4* const src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + r * p.ldx);
+            const uint32_t dst = smem_u32(buffers + b * granules);
+            for (int g = threadIdx.x; g < granules; g += kStreamThreads)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * g), "l"(src + g) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(blockIdx.x, 0);
+    int b = 0;
+#pragma unroll 1
+    for (int64_t r = blockIdx.x; r < p.n; r += gridDim.x, b ^= 1) {
+        fetch(r + gridDim.x, b ^ 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        const uint4* const row = buffers + b * granules;
+        Raw<T, 8> raw;
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int g = threadIdx.x; g < granules; g += kStreamThreads) {
+            const uint4 v = row[g];
+            raw.w[0] = v.x, raw.w[1] = v.y, raw.w[2] = v.z, raw.w[3] = v.w;
+            top = max(top, raw.top(0));
+        }
+        top = __reduce_max_sync(~0u, top);
+        if ((threadIdx.x & 31) == 0) tops[b][threadIdx.x >> 5] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kStreamThreads / 32; ++i) top = max(top, tops[b][i]);
+        const Scale s = scale_of<T>(top);
+        if (threadIdx.x == 0) p.scale[r] = s.s;
+        int8_t* const codes = p.codes ? p.codes + r * p.ldc : nullptr;
+        __half* const wide = p.codes ? nullptr : p.wide + r * p.ldw;
+#pragma unroll 2
+        for (int g = threadIdx.x; g < granules; g += kStreamThreads) {
+            const uint4 v = row[g];
+            raw.w[0] = v.x, raw.w[1] = v.y, raw.w[2] = v.z, raw.w[3] = v.w;
+            uint32_t q[2];
+            encode<T, 8>(raw, 0, s, q);
+            store<8>(codes, wide, 8 * g, q);
+        }
     }
 }
 
@@ -498,10 +673,11 @@ int log2_of(int32_t group) {
 }
 
 template <class Kernel, class Params>
-cudaError_t rows_launch(Kernel kernel, const Params& p, int64_t grid, int threads, cudaStream_t s) {
+cudaError_t rows_launch(Kernel kernel, const Params& p, int64_t grid, int threads, cudaStream_t s, size_t smem = 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -515,28 +691,98 @@ bool aligned(const void* p, int64_t stride_bytes, int to) {
     return reinterpret_cast<uintptr_t>(p) % to == 0 && stride_bytes % to == 0;
 }
 
+constexpr int kStreamSmem = 100 * 1024;  // two rows of at most 25,600 values
+
+// The current device's SMs, after its first call also with the stream kernels' shared memory.
+cudaError_t prepare(int* sms) {
+    static std::mutex mu;
+    static int count[128] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lk(mu);
+    if (!count[dev]) {
+        for (auto fn : {rows8_stream_kernel<__nv_bfloat16>, rows8_stream_kernel<__half>})
+            if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem)) != cudaSuccess)
+                return e;
+        if ((e = cudaDeviceGetAttribute(&count[dev], cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    }
+    *sms = count[dev];
+    return cudaSuccess;
+}
+
+template <class T, int V, int kGroup>
+cudaError_t quantize_groups(const QuantizeParams& p, cudaStream_t s) {
+    int sms = 0;
+    const cudaError_t e = prepare(&sms);
+    if (e != cudaSuccess) return e;
+    const int64_t all = (p.n * p.items + kGroupWarps - 1) / kGroupWarps;
+    const int64_t fit = static_cast<int64_t>(sms) * kGroupCtas;
+    return rows_launch(rows8_group_kernel<T, V, kGroup>, p, all < fit ? all : fit, kGroupWarps * 32, s);
+}
+
+// A scale for every row of more than 256 values.  Few rows are spread over more warps
+// each, so that a row takes one round trip to memory and little work after it.
+template <class T, int V>
+cudaError_t quantize_rows(QuantizeParams& p, cudaStream_t s) {
+    if (p.d <= kShort * kSegment && p.n > 512) {
+        int sms = 0;
+        const cudaError_t e = prepare(&sms);
+        if (e != cudaSuccess) return e;
+        const int64_t all = (p.n + kGroupWarps - 1) / kGroupWarps, fit = static_cast<int64_t>(sms) * 6;
+        return rows_launch(rows8_short_kernel<T, V>, p, all < fit ? all : fit, kGroupWarps * 32, s);
+    }
+    if constexpr (V == 8 && sizeof(T) == 2) {
+        const size_t smem = 4 * static_cast<size_t>(p.d);
+        if (p.n > 512 && smem <= kStreamSmem) {
+            int sms = 0, per_sm = 0;
+            cudaError_t e = prepare(&sms);
+            if (e == cudaSuccess)
+                e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, rows8_stream_kernel<T>, kStreamThreads, smem);
+            if (e != cudaSuccess) return e;
+            const int64_t fit = static_cast<int64_t>(sms) * (per_sm < 1 ? 1 : per_sm);
+            return rows_launch(rows8_stream_kernel<T>, p, p.n < fit ? p.n : fit, kStreamThreads, s, smem);
+        }
+    }
+    const int segments = (p.d + kSegment - 1) / kSegment;
+    const int h = p.n <= 512 && segments <= kRowWarps ? 1 : segments <= 2 * kRowWarps || sizeof(T) == 4 ? 2 : 4;
+    int warps = (segments + h - 1) / h;
+    if (warps > kRowWarps) warps = kRowWarps;
+    p.held = warps * h * kSegment;
+    if (h == 1) return rows_launch(rows8_row_kernel<T, V, 1>, p, p.n, warps * 32, s);
+    if constexpr (sizeof(T) == 2) {
+        if (h == 4) return rows_launch(rows8_row_kernel<T, V, 4>, p, p.n, warps * 32, s);
+    }
+    return rows_launch(rows8_row_kernel<T, V, 2>, p, p.n, warps * 32, s);
+}
+
 template <class T, int V>
 cudaError_t quantize_as(QuantizeParams& p, cudaStream_t s) {
     if (p.group != 0 || p.d <= kSegment) {
         if (p.group == 0) p.group = kSegment;
         p.shift = log2_of(p.group);
-        p.items = (p.d + kItemSegments * kSegment - 1) / (kItemSegments * kSegment);
-        return rows_launch(rows8_group_kernel<T, V>, p, (p.n * p.items + 7) / 8, 256, s);
+        p.items = (p.d + segment_columns(V) - 1) / segment_columns(V);
+        if constexpr (V >= 8) {
+            return p.group == 32    ? quantize_groups<T, V, 32>(p, s)
+                   : p.group == 64  ? quantize_groups<T, V, 64>(p, s)
+                   : p.group == 128 ? quantize_groups<T, V, 128>(p, s)
+                                    : quantize_groups<T, V, 256>(p, s);
+        } else {
+            return quantize_groups<T, V, 0>(p, s);
+        }
     }
-    // Few rows are spread over more warps each, so that a row takes one round trip to
-    // memory and little work after it; many rows get smaller CTAs.
-    const int segments = (p.d + kSegment - 1) / kSegment;
-    const int h = p.n <= 512 && segments <= 16 ? 1 : 4;
-    int warps = (segments + h - 1) / h;
-    if (warps > 16) warps = 16;
-    p.held = warps * h * kSegment;
-    return rows_launch(h == 1 ? rows8_row_kernel<T, V, 1> : rows8_row_kernel<T, V, 4>, p, p.n, warps * 32, s);
+    if constexpr (V == 16) {
+        return quantize_as<T, 8>(p, s);
+    } else {
+        return quantize_rows<T, V>(p, s);
+    }
 }
 
-// The widest run that rows of both matrices allow.
-int run_of(int32_t d, const void* x, int64_t x_row, int x_item, const void* q, int64_t q_row, int q_item) {
-    for (int v : {8, 4})
-        if (d % v == 0 && aligned(x, x_row * x_item, v * x_item < 16 ? v * x_item : 16) &&
+// The widest run that rows of both matrices allow, and that gives every lane one.
+int run_of(int most, int32_t d, const void* x, int64_t x_row, int x_item, const void* q, int64_t q_row, int q_item) {
+    for (int v : {16, 8, 4})
+        if (v <= most && (v == 4 || 32 * v <= d) && d % v == 0 && aligned(x, x_row * x_item, v * x_item < 16 ? v * x_item : 16) &&
             aligned(q, q_row * q_item, v * q_item < 16 ? v * q_item : 16))
             return v;
     return 1;
@@ -544,14 +790,22 @@ int run_of(int32_t d, const void* x, int64_t x_row, int x_item, const void* q, i
 
 template <class T>
 cudaError_t quantize_of(QuantizeParams& p, cudaStream_t s) {
-    const int v = p.codes ? run_of(p.d, p.x, p.ldx, sizeof(T), p.codes, p.ldc, 1)
-                          : run_of(p.d, p.x, p.ldx, sizeof(T), p.wide, p.ldw, 2);
+    const int most = sizeof(T) == 2 ? 16 : 8;
+    const int v = p.codes ? run_of(most, p.d, p.x, p.ldx, sizeof(T), p.codes, p.ldc, 1)
+                          : run_of(most, p.d, p.x, p.ldx, sizeof(T), p.wide, p.ldw, 2);
+    if constexpr (sizeof(T) == 2) {
+        if (v == 16) return quantize_as<T, 16>(p, s);
+    }
     return v == 8 ? quantize_as<T, 8>(p, s) : v == 4 ? quantize_as<T, 4>(p, s) : quantize_as<T, 1>(p, s);
 }
 
 template <class T>
 cudaError_t restore_of(RestoreParams& p, cudaStream_t s) {
-    const int v = run_of(p.d, p.x, p.ldx, sizeof(T), p.codes, p.ldc, 1);
+    // 16 bytes of output a lane
+    const int v = run_of(sizeof(T) == 2 ? 8 : 4, p.d, p.x, p.ldx, sizeof(T), p.codes, p.ldc, 1);
+    if constexpr (sizeof(T) == 4)
+        return rows_launch(v == 4 ? rows8_restore_kernel<T, 4> : rows8_restore_kernel<T, 1>, p, (p.n * p.items + 7) / 8,
+                           256, s);
     return rows_launch(v == 8   ? rows8_restore_kernel<T, 8>
                        : v == 4 ? rows8_restore_kernel<T, 4>
                                 : rows8_restore_kernel<T, 1>,
