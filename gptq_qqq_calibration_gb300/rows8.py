@@ -104,11 +104,13 @@ def _same_device(first: torch.Tensor, *others: torch.Tensor) -> int:
 
 def _on(dev: int, call, args) -> None:
     """The call with the tensors' device current."""
-    if torch.cuda.current_device() == dev:
-        check(call(*args))
-        return
-    with torch.cuda.device(dev):
-        check(call(*args))
+    if torch._C._cuda_getDevice() == dev:
+        st = call(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = call(*args)
+    if st:
+        check(st)
 
 
 def _quantize(X, group, codes, scale, stream) -> None:
@@ -117,9 +119,9 @@ def _quantize(X, group, codes, scale, stream) -> None:
     if (n2, d2) != (n, d):
         raise ValueError(f"codes must be {n} rows of {d}")
     dev = _same_device(X, codes, scale)
-    args = (X.data_ptr(), ldx, n, d, _DTYPES[X.dtype], int(group), codes.data_ptr(), ldc,
-            _scale(scale, n, d, group, "scale"), _stream(stream, dev))
-    _on(dev, _lib.load().rows8_quantize, args)
+    _on(dev, _lib.load().rows8_quantize,
+        (X.data_ptr(), ldx, n, d, _DTYPES[X.dtype], int(group), codes.data_ptr(), ldc,
+         _scale(scale, n, d, group, "scale"), _stream(stream, dev)))
 
 
 def rows8_quantize(X: torch.Tensor, group: int, codes_out: torch.Tensor, scale_out: torch.Tensor, stream=None) -> None:
@@ -135,9 +137,9 @@ def _restore(rows: Rows8, X, stream) -> None:
     if (n2, d2) != (n, d):
         raise ValueError(f"X_out must be {n} rows of {d}")
     dev = _same_device(rows.codes, rows.scale, X)
-    args = (rows.codes.data_ptr(), ldc, _scale(rows.scale, n, d, rows.group, "scale"), n, d, int(rows.group),
-            X.data_ptr(), ldx, _DTYPES[X.dtype], _stream(stream, dev))
-    _on(dev, _lib.load().rows8_restore, args)
+    _on(dev, _lib.load().rows8_restore,
+        (rows.codes.data_ptr(), ldc, _scale(rows.scale, n, d, rows.group, "scale"), n, d, int(rows.group),
+         X.data_ptr(), ldx, _DTYPES[X.dtype], _stream(stream, dev)))
 
 
 def rows8_restore(rows: Rows8, X_out: torch.Tensor, stream=None) -> None:
@@ -150,11 +152,16 @@ def rows8_restore(rows: Rows8, X_out: torch.Tensor, stream=None) -> None:
 def quantize_rows(X: torch.Tensor, group: int = 0, stream=None) -> Rows8:
     """8-bit rows of X [..., d]: one scale per row (group 0), or per ``group``
     (32, 64, 128 or 256) consecutive columns of a row."""
-    n, d, _ = _float_rows(X, "X")
-    codes = _empty(X.shape, torch.int8, X, stream)
-    scale = _empty((*X.shape[:-1], _groups(d, group)) if group else X.shape[:-1], torch.float32, X, stream)
-    _quantize(X, group, codes, scale, stream)
-    _used_on(stream, X)
+    n, d, ldx = _float_rows(X, "X")
+    shape = X.shape
+    codes = _empty(shape, torch.int8, X, stream)
+    scale = _empty((*shape[:-1], _groups(d, group)) if group else shape[:-1], torch.float32, X, stream)
+    dev = X.get_device()
+    _on(dev, _lib.load().rows8_quantize,
+        (X.data_ptr(), ldx, n, d, _DTYPES[X.dtype], int(group), codes.data_ptr(), d, scale.data_ptr(),
+         _stream(stream, dev)))
+    if stream is not None:
+        _used_on(stream, X)
     return Rows8(codes, scale, int(group))
 
 
@@ -166,7 +173,13 @@ def restore_rows(rows: Rows8, dtype: torch.dtype = torch.bfloat16, out: Optional
         return out
     if dtype not in _DTYPES:
         raise ValueError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
-    out = _empty(rows.codes.shape, dtype, rows.codes, stream)
-    _restore(rows, out, stream)
-    _used_on(stream, rows.codes, rows.scale)
+    codes, scale, group = rows
+    n, d, ldc = _code_rows(codes, "codes")
+    dev = _same_device(codes, scale)
+    s = _scale(scale, n, d, group, "scale")
+    out = _empty(codes.shape, dtype, codes, stream)
+    _on(dev, _lib.load().rows8_restore,
+        (codes.data_ptr(), ldc, s, n, d, int(group), out.data_ptr(), d, _DTYPES[dtype], _stream(stream, dev)))
+    if stream is not None:
+        _used_on(stream, codes, scale)
     return out
