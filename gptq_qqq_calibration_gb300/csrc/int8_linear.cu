@@ -522,14 +522,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------- few tokens
 //
-// Reading the weights once is what takes time, so a CTA takes the same number of weight
-// rows on every SM and streams them straight into registers.  A thread owns kGran
-// granules of 16 columns and keeps their codes of all kTok tokens in registers; `wr` warps
+// Reading the weights once is what takes time, so every SM takes the same number of weight
+// rows and streams them straight into registers, in the order of memory; the part that
+// does not fit there is on its way to L2 while the tokens are quantized.  A thread owns
+// kGran granules of 16 columns and keeps their codes of all kTok tokens in registers; `wr` warps
 // cover a row, and the CTA's warps cover `rp` rows side by side.  Four dp4a a granule
-// and token, one warp reduction a row and token, integer adds in shared memory across
-// warps: exact and independent of the order.
+// and token, one warp reduction a row and token (the more granules, the fewer), integer
+// adds in shared memory across warps: exact and independent of the order.
 
-constexpr int kFewMaxThreads = 512;
+constexpr int64_t kFewTokens = 8;
+constexpr int kFewThreads = 512, kFewWarps = kFewThreads / 32;
+constexpr int kFewAhead = 256 * 1024;  // bytes a CTA asks into L2
 
 struct FewParams {
     const void* x;          // 16-bit activations, or NULL:
@@ -568,24 +571,82 @@ __device__ __forceinline__ float2 unpack2f<__half>(uint32_t w) {
     return __half22float2(h);
 }
 
+// The codes of the tokens into shared memory, [kTok][d], by all warps: kFewWarps / kTok of
+// them take a token.
+template <class T, int kTok>
+__device__ __forceinline__ void few_quantize(const FewParams& p, int8_t* codes, uint32_t (&tops)[kFewWarps],
+                                             float (&scales)[kTok]) {
+    constexpr int kEach = kFewWarps / kTok;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int token = warp / kEach, first = (warp - token * kEach) * 32 + lane, granules = p.d >> 3;
+    const bool some = token < p.n;
+    const uint4* const row = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + static_cast<int64_t>(some ? token : 0) * p.d);
+    uint32_t top = 0;
+    if (some) {
+        for (int g = first; g < granules; g += kEach * 32) {
+            const uint4 v = row[g];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack2f<T>(w[i] & 0x7fff7fffu);
+                top = max(top, max(__float_as_uint(f.x), __float_as_uint(f.y)));
+            }
+        }
+    }
+    top = __reduce_max_sync(~0u, top);
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+    if (!some) return;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) top = max(top, tops[token * kEach + i]);
+    const bool finite = top < 0x7f800000u;
+    float s = finite ? __fdiv_rn(__uint_as_float(top), 127.0f) : 0.0f;
+    if (first == 0) scales[token] = finite ? s : __uint_as_float(0x7fffffffu);
+    // a subnormal scale and its values are both taken 2^64 times (exactly)
+    const float up = s < 1.17549435e-38f ? 18446744073709551616.0f : 1.0f;
+    s = __fmul_rn(s, up);
+    const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
+    for (int g = first; g < granules; g += kEach * 32) {
+        const uint4 v = row[g];  // from L1 this time
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t out[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 a = unpack2f<T>(w[2 * i]), b = unpack2f<T>(w[2 * i + 1]);
+            const int q0 = few_code(__fmul_rn(a.x, up), s, r), q1 = few_code(__fmul_rn(a.y, up), s, r);
+            const int q2 = few_code(__fmul_rn(b.x, up), s, r), q3 = few_code(__fmul_rn(b.y, up), s, r);
+            const uint32_t c = __byte_perm(__byte_perm(q0, q1, 0x0040), __byte_perm(q2, q3, 0x0040), 0x5410);
+            out[i] = s > 0.0f ? c : 0u;
+        }
+        *reinterpret_cast<uint2*>(codes + static_cast<int64_t>(token) * p.d + 8 * g) = make_uint2(out[0], out[1]);
+    }
+}
+
 template <class T, int kTok, int kGran>
-__global__ void __launch_bounds__(kFewMaxThreads, 1) int8_few_kernel(const __grid_constant__ FewParams p) {
-    constexpr int kBatch = (kTok == 8 ? 4 : 8) / kGran;  // rows a thread has in flight
-    extern __shared__ int32_t sums[];  // [rows][kTok]
-    __shared__ uint32_t tops[kTok][16];
+__global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const __grid_constant__ FewParams p) {
+    constexpr int kBatch = 8 / kGran;  // rows a thread has in flight
+    extern __shared__ uint4 few_smem[];
+    int32_t* const sums = reinterpret_cast<int32_t*>(few_smem);  // [rows][kTok], then the tokens' codes
+    int8_t* const codes = reinterpret_cast<int8_t*>(few_smem + (p.rows * kTok + 3) / 4);
+    __shared__ uint32_t tops[kFewWarps];
     __shared__ float scales[kTok];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int warps = blockDim.x >> 5;
     const int row0 = blockIdx.x * p.rows;
     const int rows = p.f - row0 < p.rows ? p.f - row0 : p.rows;
     const int at = warp / p.wr;                                  // which of the rows side by side
     const int g0 = (warp - at * p.wr) * 32 + lane;               // first granule
     const int gs = p.wr * 32, granules = p.d >> 4;
-    for (int i = threadIdx.x; i < rows * kTok; i += blockDim.x) sums[i] = 0;
+    const int8_t* const w = p.w + static_cast<int64_t>(row0) * p.d;
+    {
+        // (may run under the end of the stream's previous kernel: nothing is read by it)
+        const int64_t bytes = static_cast<int64_t>(rows) * p.d, from = static_cast<int64_t>(threadIdx.x) * 8192;
+        const int64_t to = bytes < kFewAhead ? bytes : kFewAhead;
+        if (from < to) prefetch_l2_bulk(w + from, static_cast<uint32_t>(to - from < 8192 ? to - from : 8192));
+    }
+    for (int i = threadIdx.x; i < rows * kTok; i += kFewThreads) sums[i] = 0;
     griddep_wait();
     griddep_launch_dependents();
 
-    const int8_t* const w = p.w + static_cast<int64_t>(row0) * p.d;
     uint4 v[kBatch][kGran];
     const auto fetch = [&](int r0) {
 #pragma unroll
@@ -593,116 +654,63 @@ __global__ void __launch_bounds__(kFewMaxThreads, 1) int8_few_kernel(const __gri
 #pragma unroll
             for (int j = 0; j < kGran; ++j) {
                 const int r = r0 + b * p.rp, g = g0 + j * gs;
-                v[b][j] = r < rows && g < granules
+                v[b][j] = at < p.rp && r < rows && g < granules
                               ? __ldcg(reinterpret_cast<const uint4*>(w + static_cast<int64_t>(r) * p.d) + g)
                               : make_uint4(0, 0, 0, 0);
             }
     };
     fetch(at);
 
-    uint32_t code[kTok][kGran][4];
     if (p.x_codes) {
-#pragma unroll
-        for (int t = 0; t < kTok; ++t)
-#pragma unroll
-            for (int j = 0; j < kGran; ++j) {
-                const int g = g0 + j * gs;
-                uint4 c = make_uint4(0, 0, 0, 0);
-                if (t < p.n && g < granules)
-                    c = *(reinterpret_cast<const uint4*>(p.x_codes + static_cast<int64_t>(t) * p.d) + g);
-                code[t][j][0] = c.x, code[t][j][1] = c.y, code[t][j][2] = c.z, code[t][j][3] = c.w;
-            }
         if (threadIdx.x < kTok && threadIdx.x < p.n) scales[threadIdx.x] = p.x_scale[threadIdx.x];
-        __syncthreads();
     } else {
-        const T* const x = static_cast<const T*>(p.x);
-        const auto value = [&](int t, int j, uint32_t (&raw)[8]) {
-            const int g = g0 + j * gs;
-            uint4 a = make_uint4(0, 0, 0, 0), b = a;
-            if (t < p.n && g < granules) {
-                const uint4* const src = reinterpret_cast<const uint4*>(x + static_cast<int64_t>(t) * p.d) + 2 * g;
-                a = src[0];
-                b = src[1];
-            }
-            raw[0] = a.x, raw[1] = a.y, raw[2] = a.z, raw[3] = a.w;
-            raw[4] = b.x, raw[5] = b.y, raw[6] = b.z, raw[7] = b.w;
-        };
-#pragma unroll
-        for (int t = 0; t < kTok; ++t) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int j = 0; j < kGran; ++j) {
-                uint32_t raw[8];
-                value(t, j, raw);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 f = unpack2f<T>(raw[i]);
-                    top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
-                }
-            }
-            top = __reduce_max_sync(~0u, top);
-            if (lane == 0) tops[t][warp] = top;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int t = 0; t < kTok; ++t) {
-            uint32_t top = lane < warps ? tops[t][lane] : 0u;
-            top = __reduce_max_sync(~0u, top);
-            const bool finite = top < 0x7f800000u;
-            float s = finite ? __fdiv_rn(__uint_as_float(top), 127.0f) : 0.0f;
-            if (threadIdx.x == 0) scales[t] = finite ? s : __uint_as_float(0x7fffffffu);
-            // a subnormal scale and its values are both taken 2^64 times (exactly)
-            const float up = s < 1.17549435e-38f ? 18446744073709551616.0f : 1.0f;
-            s = __fmul_rn(s, up);
-            const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
-#pragma unroll
-            for (int j = 0; j < kGran; ++j) {
-                uint32_t raw[8];
-                value(t, j, raw);  // from L1 this time
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 a = unpack2f<T>(raw[2 * i]), b = unpack2f<T>(raw[2 * i + 1]);
-                    const int q0 = few_code(__fmul_rn(a.x, up), s, r), q1 = few_code(__fmul_rn(a.y, up), s, r);
-                    const int q2 = few_code(__fmul_rn(b.x, up), s, r), q3 = few_code(__fmul_rn(b.y, up), s, r);
-                    const uint32_t c = __byte_perm(__byte_perm(q0, q1, 0x0040), __byte_perm(q2, q3, 0x0040), 0x5410);
-                    code[t][j][i] = s > 0.0f ? c : 0u;
-                }
-            }
-        }
+        few_quantize<T, kTok>(p, codes, tops, scales);
     }
+    __syncthreads();
+    uint4 code[kTok][kGran];
+#pragma unroll
+    for (int t = 0; t < kTok; ++t)
+#pragma unroll
+        for (int j = 0; j < kGran; ++j) {
+            const int g = g0 + j * gs;
+            const int8_t* const from = (p.x_codes ? p.x_codes : codes) + static_cast<int64_t>(t) * p.d;
+            code[t][j] = t < p.n && g < granules ? reinterpret_cast<const uint4*>(from)[g] : make_uint4(0, 0, 0, 0);
+        }
 
-    for (int r0 = at; r0 < rows; r0 += kBatch * p.rp) {
-        int32_t acc[kBatch][kTok];
+    if (at < p.rp) {
+        for (int r0 = at; r0 < rows; r0 += kBatch * p.rp) {
+            int32_t acc[kBatch][kTok];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b)
+            for (int b = 0; b < kBatch; ++b)
 #pragma unroll
-            for (int t = 0; t < kTok; ++t) {
-                int32_t a = 0;
+                for (int t = 0; t < kTok; ++t) {
+                    int32_t a = 0;
 #pragma unroll
-                for (int j = 0; j < kGran; ++j) {
-                    a = __dp4a(static_cast<int>(v[b][j].x), static_cast<int>(code[t][j][0]), a);
-                    a = __dp4a(static_cast<int>(v[b][j].y), static_cast<int>(code[t][j][1]), a);
-                    a = __dp4a(static_cast<int>(v[b][j].z), static_cast<int>(code[t][j][2]), a);
-                    a = __dp4a(static_cast<int>(v[b][j].w), static_cast<int>(code[t][j][3]), a);
+                    for (int j = 0; j < kGran; ++j) {
+                        a = __dp4a(static_cast<int>(v[b][j].x), static_cast<int>(code[t][j].x), a);
+                        a = __dp4a(static_cast<int>(v[b][j].y), static_cast<int>(code[t][j].y), a);
+                        a = __dp4a(static_cast<int>(v[b][j].z), static_cast<int>(code[t][j].z), a);
+                        a = __dp4a(static_cast<int>(v[b][j].w), static_cast<int>(code[t][j].w), a);
+                    }
+                    acc[b][t] = a;
                 }
-                acc[b][t] = a;
-            }
-        if (r0 + kBatch * p.rp < rows) fetch(r0 + kBatch * p.rp);
+            if (r0 + kBatch * p.rp < rows) fetch(r0 + kBatch * p.rp);
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int r = r0 + b * p.rp;
-            int32_t mine = 0;  // lane t keeps token t's sum
+            for (int b = 0; b < kBatch; ++b) {
+                const int r = r0 + b * p.rp;
+                int32_t mine = 0;  // lane t keeps token t's sum
 #pragma unroll
-            for (int t = 0; t < kTok; ++t) {
-                const int32_t a = __reduce_add_sync(~0u, acc[b][t]);
-                if (lane == t) mine = a;
+                for (int t = 0; t < kTok; ++t) {
+                    const int32_t a = __reduce_add_sync(~0u, acc[b][t]);
+                    if (lane == t) mine = a;
+                }
+                if (lane < kTok && r < rows) atomicAdd(&sums[r * kTok + lane], mine);
             }
-            if (lane < kTok && r < rows) atomicAdd(&sums[r * kTok + lane], mine);
         }
     }
     __syncthreads();
     // channel by channel, so that a warp writes side by side
-    for (int i = threadIdx.x; i < rows * kTok; i += blockDim.x) {
+    for (int i = threadIdx.x; i < rows * kTok; i += kFewThreads) {
         const int t = i / rows, r = i - t * rows;
         if (t < p.n)
             static_cast<T*>(p.out)[static_cast<int64_t>(t) * p.f + row0 + r] =
@@ -770,6 +778,8 @@ hess_status il_encode(CUtensorMap* m, const void* ptr, bool bytes, int64_t rows,
     return HESS_OK;
 }
 
+constexpr size_t kFewSmem = 128 * 1024;
+
 template <class T>
 auto few_kernel(int tok, int gran) -> void (*)(FewParams) {
     switch (tok * 16 + gran) {
@@ -780,9 +790,12 @@ auto few_kernel(int tok, int gran) -> void (*)(FewParams) {
         case 2 * 16 + 1: return int8_few_kernel<T, 2, 1>;
         case 2 * 16 + 2: return int8_few_kernel<T, 2, 2>;
         case 2 * 16 + 4: return int8_few_kernel<T, 2, 4>;
+        case 2 * 16 + 8: return int8_few_kernel<T, 2, 8>;
         case 4 * 16 + 1: return int8_few_kernel<T, 4, 1>;
         case 4 * 16 + 2: return int8_few_kernel<T, 4, 2>;
+        case 4 * 16 + 4: return int8_few_kernel<T, 4, 4>;
         case 8 * 16 + 1: return int8_few_kernel<T, 8, 1>;
+        case 8 * 16 + 2: return int8_few_kernel<T, 8, 2>;
     }
     return nullptr;
 }
@@ -794,6 +807,12 @@ hess_status il_prepare(int dev, int* pairs, int* sms_out) {
     std::lock_guard<std::mutex> lk(mu);
     if (dev < 0 || dev >= 128) return il_fail(HESS_ERR_UNSUPPORTED, "device index %d", dev);
     if (!count[dev]) {
+        for (int tok : {1, 2, 4, 8})
+            for (int gran : {1, 2, 4, 8})
+                for (auto fn : {few_kernel<__nv_bfloat16>(tok, gran), few_kernel<__half>(tok, gran)})
+                    if (fn)
+                        IL_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                    static_cast<int>(kFewSmem)));
         for (auto fn : {int8_pair_kernel<__nv_bfloat16>, int8_pair_kernel<__half>})
             IL_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)));
         int sms = 0;
@@ -894,15 +913,29 @@ hess_status il_launch(Kernel kernel, const Params& p, int64_t grid, int threads,
     return HESS_OK;
 }
 
-// Granules of 16 columns a thread of the few-token kernel takes.
-int few_granules(int64_t d) {
-    int g = 1;
-    while (static_cast<int64_t>(g) * kFewMaxThreads * 16 < d) g *= 2;
-    return g;
-}
 int few_tokens(int64_t n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : 8; }
-// The codes of all tokens stay in registers: 4 words a token and granule.
-bool is_few(int64_t n, int64_t d) { return n <= 8 && few_tokens(n) * few_granules(d) <= 8; }
+
+// Granules of 16 columns a thread of the few-token kernel takes: the most that the codes'
+// registers allow (4 words a token and granule) without leaving many threads idle; 0
+// where a row does not fit at all.
+int few_granules(int64_t n, int64_t d) {
+    const int64_t granules = d / 16;
+    int best = 0;
+    double most = 0.0;
+    for (int g = 1; g <= 8 && g * few_tokens(n) <= 16; g *= 2) {
+        const int64_t wr = (granules + 32 * g - 1) / (32 * g);
+        if (wr > kFewWarps) continue;
+        const double used = static_cast<double>(granules) * (kFewWarps / wr) / (32.0 * g * kFewWarps);
+        if (used >= 0.85 * most) {
+            best = g;
+            if (used > most) most = used;
+        }
+    }
+    return best;
+}
+bool is_few(int64_t n, int64_t d) {
+    return n <= kFewTokens && few_granules(n, d) > 0 && few_tokens(n) * d <= int64_t(64) * 1024;
+}
 
 hess_status forward_few(const int8_linear_ctx* g, const void* X, const int8_t* codes, const float* scale, int64_t n,
                         const int8_t* W, const float* W_scale, void* Y, cudaStream_t s) {
@@ -916,15 +949,16 @@ hess_status forward_few(const int8_linear_ctx* g, const void* X, const int8_t* c
     p.n = static_cast<int32_t>(n);
     p.d = static_cast<int32_t>(g->d);
     p.f = static_cast<int32_t>(g->f);
-    const int gran = few_granules(g->d), tok = few_tokens(n);
+    const int gran = few_granules(n, g->d), tok = few_tokens(n);
     p.wr = static_cast<int32_t>(ceil_div(g->d, static_cast<int64_t>(gran) * 512));
-    p.rp = kFewMaxThreads / 32 / p.wr;
+    p.rp = kFewWarps / p.wr;
     const int64_t ctas = g->f < g->sms ? g->f : g->sms;
     p.rows = static_cast<int32_t>(ceil_div(g->f, ctas));
     const int64_t grid = ceil_div(g->f, p.rows);
+    const size_t smem = static_cast<size_t>(ceil_div(static_cast<int64_t>(p.rows) * tok, 4)) * 16 + (X ? tok * g->d : 0);
     const auto kernel = g->dtype == HESS_BF16 ? few_kernel<__nv_bfloat16>(tok, gran) : few_kernel<__half>(tok, gran);
-    if (!kernel) return il_fail(HESS_ERR_INTERNAL, "no kernel for %d tokens and %d granules", tok, gran);
-    return il_launch(kernel, p, grid, p.wr * p.rp * 32, static_cast<size_t>(p.rows) * tok * 4, s);
+    if (!kernel || smem > kFewSmem) return il_fail(HESS_ERR_INTERNAL, "no kernel for %d tokens and %d granules", tok, gran);
+    return il_launch(kernel, p, grid, kFewThreads, smem, s);
 }
 
 // X in 16 bits, or codes and scale.
