@@ -17,7 +17,7 @@
 //
 // Tile: 256 weight rows x up to 192 tokens on a pair of SMs (cta_group::2).  Tensor
 // memory: two 192-column sums, so that one is drained under the other's products, and
-// four slots of 64 steps of A.
+// two slots of 128 steps of A (more where the tile has fewer tokens).
 //
 // Few tokens (the weights no longer pay for the trip through tensor memory): one pass
 // over the weights with dp4a, the tokens' codes in registers.
@@ -47,9 +47,12 @@ using namespace i8;
 
 constexpr int kMaxStages = 12;
 constexpr uint32_t kRing = 208 * 1024;
-constexpr int kMaxSlots = 12;         // of 64 steps of A in tensor memory, 32 columns each
+// Slots of A in tensor memory hold a stage (64 columns), or half of one where the
+// sums leave room for no more than three of those.
+constexpr int kMaxSlots = 6;
+constexpr int kCoarseTok = 128;  // the most tokens of a tile with whole stages in slots
 constexpr uint32_t kTmemCols = 512;
-static_assert(2 * kMaxTok + 4 * 32 <= kTmemCols, "two sums and four slots");
+static_assert(2 * kMaxTok + 4 * (kKB / 4) <= kTmemCols, "two sums and four halves of a stage");
 constexpr int kNumBarriers = 4 * kMaxStages + 2 * kMaxSlots + 5;
 constexpr size_t kSmemBytes = 1024 + kRing + 8 * kNumBarriers + 16;
 constexpr int kThreads = 640;  // warp 0: weights, 1: MMAs, 2: tokens, 4-11: converters, 12-19: epilogue
@@ -57,18 +60,18 @@ constexpr int kFirstEpiWarp = 12, kEpiWarps = 8;
 constexpr int kCols = kMaxTok / 2;  // tokens of an epilogue thread
 constexpr unsigned long long kDrainLimitNs = 1000000000ull;
 constexpr unsigned long long kAbortSettleNs = 2000000ull;
-constexpr int64_t kPieceInts = 2 * kMaxTok * kMaxRows;  // both CTAs' sums of one unit
+constexpr int64_t kTileInts = kMaxTok * kMaxRows;  // one CTA's sums of a split tile
 
 struct PairParams : Schedule {
     CUtensorMap x, w;  // float16 codes [n, d], boxes of tok/2 rows x 64; weights [f, d], boxes of rows x 128
     int32_t stages;
-    int32_t slots;       // of A in tensor memory, an even number
+    int32_t slots;       // of A in tensor memory
     uint32_t acc_cols;   // columns of one sum in tensor memory; the slots follow the second
     uint32_t w_bytes, stage_bytes;  // of a stage; the tokens' two boxes follow the weights
     const float *x_scale, *w_scale;
     void* out;
-    int32_t* pieces;    // sums of every unit of a split tile
-    uint32_t* arrived;  // units of each split tile that have come, per CTA; zero between launches
+    int32_t* sums;      // of the tiles that are split, per CTA; zero between launches
+    uint32_t* arrived;  // units of each of them that have come, per CTA; zero between launches
     uint32_t* status;
     unsigned long long timeout_ns;
 };
@@ -155,9 +158,10 @@ __device__ __forceinline__ bool epi_barrier_any(bool x) {
 // Every wait is bounded.  The launch before this one is the kernel that writes the
 // tokens' codes and scales; it waits for all work before it and only then lets this
 // one start, so that only what it writes itself has to be waited for here.
-template <class T>
+template <class T, bool kHalves>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int8_pair_kernel(const __grid_constant__ PairParams p) {
+    constexpr uint32_t kSlotCols = kHalves ? kKB / 4 : kKB / 2;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -189,7 +193,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(xempty_bar(s), 1);
         }
         for (int s = 0; s < p.slots; ++s) {
-            mbar_init(afull_bar(s), 8);  // four converter warps of each CTA
+            mbar_init(afull_bar(s), kHalves ? 8 : 16);  // four or eight converter warps of each CTA
             mbar_init(aempty_bar(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -217,8 +221,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             int stage = 0;
             uint32_t phase = 0;
-            for (int u = pair; ok && u < p.n_units; u += n_pairs) {
-                const Unit un = unit_at(p, u);
+            Unit un;
+            for (int i = 0; ok && unit_of(p, pair, n_pairs, i, un); ++i) {
                 const int row = un.f0 + static_cast<int>(rank) * p.rows;
                 for (int kb = un.kb0; kb < un.kb1; ++kb) {
                     if (!mbar_wait(wempty_bar(stage), phase ^ 1u, limit)) {
@@ -244,8 +248,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int stage = 0;
             uint32_t phase = 0;
             const uint32_t box = static_cast<uint32_t>(p.tok) * 64u;  // tok / 2 rows of 128 bytes
-            for (int u = pair; ok && u < p.n_units; u += n_pairs) {
-                const Unit un = unit_at(p, u);
+            Unit un;
+            for (int i = 0; ok && unit_of(p, pair, n_pairs, i, un); ++i) {
                 const int row = un.t0 + static_cast<int>(rank) * (p.tok / 2);
                 for (int kb = un.kb0; kb < un.kb1; ++kb) {
                     if (!mbar_wait(xempty_bar(stage), phase ^ 1u, limit)) {
@@ -268,8 +272,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 aborted = 1;
             }
         } else if (warp == 1 && rank == 0) {
-            // The whole warp takes every turn and one elected lane issues: the operands then
-            // stay in uniform registers (one lane alone: 74 cycles an MMA, this way 40).
+            // The whole warp takes every turn, waits and agrees on the outcome, and one
+            // elected lane issues: control flow and operands then stay uniform (an MMA
+            // every 40 cycles; 74 from code of one lane).
             bool ok = true;
             int stage = 0, ab = 0;
             uint32_t slot = 0, phase = 0, sphase = 0, aphase = 0;
@@ -279,39 +284,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint64_t first = smem_desc_sw128(base + p.w_bytes, 16u, 1024u);
             const uint64_t next = p.stage_bytes >> 4, half = static_cast<uint64_t>(p.tok) * 4u;
             uint64_t b = first;
-            for (int u = pair; ok && u < p.n_units; u += n_pairs) {
-                const Unit un = unit_at(p, u);
+            Unit un;
+            for (int i = 0; ok && unit_of(p, pair, n_pairs, i, un); ++i) {
                 for (int c0 = un.kb0; ok && c0 < un.kb1; c0 += kChunk) {
                     ok = __all_sync(~0u, mbar_wait(acce_bar(ab), aphase ^ 1u, limit));
                     if (!ok) break;
-                    tc_fence_after();
                     const uint32_t acc = tmem + static_cast<uint32_t>(ab) * p.acc_cols;
                     const int c1 = c0 + kChunk < un.kb1 ? c0 + kChunk : un.kb1;
                     for (int kb = c0; kb < c1; ++kb) {
-                        ok = __all_sync(~0u, mbar_wait(xfull_bar(stage), phase, limit));
-                        if (!ok) break;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            ok = __all_sync(~0u, mbar_wait(afull_bar(slot), sphase, limit));
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint32_t a = tmem + 2 * p.acc_cols + slot * 32u;
-                            const uint64_t bh = h ? b + half : b;
-                            if (elect_one()) {
-                                umma_f16_pair_ta(acc, a, bh, idesc, h != 0 || kb != c0 ? 1u : 0u);
-                                umma_f16_pair_ta(acc, a + 8u, bh + 2u, idesc, 1u);
-                                umma_f16_pair_ta(acc, a + 16u, bh + 4u, idesc, 1u);
-                                umma_f16_pair_ta(acc, a + 24u, bh + 6u, idesc, 1u);
-                                tc_commit_pair_mc(aempty_bar(slot), 0x3);
-                                if (h) tc_commit_pair_mc(xempty_bar(stage), 0x3);
-                            }
-                            __syncwarp();
+                        const auto four = [&](uint32_t a, uint64_t at, uint32_t add) {
+                            umma_f16_pair_ta(acc, a, at, idesc, add);
+                            umma_f16_pair_ta(acc, a + 8u, at + 2u, idesc, 1u);
+                            umma_f16_pair_ta(acc, a + 16u, at + 4u, idesc, 1u);
+                            umma_f16_pair_ta(acc, a + 24u, at + 6u, idesc, 1u);
+                        };
+                        const auto turn = [&] {
                             if (++slot == static_cast<uint32_t>(p.slots)) {
                                 slot = 0;
                                 sphase ^= 1u;
                             }
-                        }
+                        };
+                        const uint32_t slot0 = tmem + 2 * p.acc_cols;
+                        ok = __all_sync(~0u, mbar_wait(xfull_bar(stage), phase, limit) &&
+                                                 mbar_wait(afull_bar(slot), sphase, limit));
                         if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            four(slot0 + slot * kSlotCols, b, kb != c0 ? 1u : 0u);
+                            if constexpr (!kHalves) four(slot0 + slot * kSlotCols + 32u, b + half, 1u);
+                            tc_commit_pair_mc(aempty_bar(slot), 0x3);
+                            if constexpr (!kHalves) tc_commit_pair_mc(xempty_bar(stage), 0x3);
+                        }
+                        __syncwarp();
+                        turn();
+                        if constexpr (kHalves) {
+                            ok = __all_sync(~0u, mbar_wait(afull_bar(slot), sphase, limit));
+                            if (!ok) break;
+                            tc_fence_after();
+                            if (elect_one()) {
+                                four(slot0 + slot * kSlotCols, b + half, 1u);
+                                tc_commit_pair_mc(aempty_bar(slot), 0x3);
+                                tc_commit_pair_mc(xempty_bar(stage), 0x3);
+                            }
+                            __syncwarp();
+                            turn();
+                        }
                         b += next;
                         if (++stage == p.stages) {
                             stage = 0;
@@ -328,14 +345,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (!ok && lane == 0) {
-                atomicOr(p.status, kStatusTimeoutMma);
-                aborted = 1;
+            if (elect_one()) {
+                if (!ok) {
+                    atomicOr(p.status, kStatusTimeoutMma);
+                    aborted = 1;
+                }
+                // every MMA issued has completed before the pair's memories are released
+                tc_commit_pair_mc(drain_bar, 0x1);
+                if (!mbar_wait(drain_bar, 0, kDrainLimitNs)) atomicOr(p.status, kStatusTimeoutDrain);
             }
-            // every MMA issued has completed before the pair's memories are released
-            if (elect_one()) tc_commit_pair_mc(drain_bar, 0x1);
             __syncwarp();
-            if (!mbar_wait(drain_bar, 0, kDrainLimitNs)) atomicOr(p.status, kStatusTimeoutDrain);
         }
     } else if (warp < 12) {
         // Converters: the first four warps take the first 64 steps of each stage, the
@@ -346,10 +365,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool some = (warp & 3) * 32 < p.rows, mine = row < p.rows;
         const uint32_t afull0 = mapa_shared(afull_bar(0), 0);
         bool ok = true;
-        int stage = 0, slot = h;
+        int stage = 0, slot = kHalves ? h : 0;
         uint32_t phase = 0, sphase = 0;
-        for (int u = pair; ok && u < p.n_units; u += n_pairs) {
-            const Unit un = unit_at(p, u);
+        Unit un;
+        for (int i = 0; ok && unit_of(p, pair, n_pairs, i, un); ++i) {
             for (int kb = un.kb0; kb < un.kb1; ++kb) {
                 if (!mbar_wait(wfull_bar(stage), phase, limit)) {
                     ok = false;
@@ -372,13 +391,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                if (some) tmem_st32(tmem + lanes + 2 * p.acc_cols + static_cast<uint32_t>(slot) * 32u, a);
+                if (some) tmem_st32(tmem + lanes + 2 * p.acc_cols + static_cast<uint32_t>(slot) * kSlotCols + (kHalves ? 0u : h * 32u), a);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster_relaxed(afull0 + 8u * slot);
-                slot += 2;
+                slot += kHalves ? 2 : 1;
                 if (slot >= p.slots) {
-                    slot = h;
+                    slot = kHalves ? h : 0;
                     sphase ^= 1u;
                 }
                 if (++stage == p.stages) {
@@ -403,8 +422,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int ab = 0;
         uint32_t aphase = 0;
         int32_t sum[kCols];
-        for (int u = pair; u < p.n_units; u += n_pairs) {
-            const Unit un = unit_at(p, u);
+        Unit un;
+        for (int i = 0; unit_of(p, pair, n_pairs, i, un); ++i) {
 #pragma unroll
             for (int c = 0; c < kCols; ++c) sum[c] = 0;
             for (int c0 = un.kb0; c0 < un.kb1; c0 += kChunk) {
@@ -435,17 +454,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             bool finish = !failed;
             if (un.parts > 1) {
-                // pieces: [token][row], so that a warp moves 128 bytes at a time
-                int32_t* const piece0 = p.pieces + static_cast<int64_t>(un.split) * un.parts * kPieceInts +
-                                        rank * (kPieceInts / 2) + row;
+                // Integers: whoever adds first.  [token][row], so that a warp adds to 128 bytes.
+                int32_t* const all = p.sums + (2 * static_cast<int64_t>(un.split) + rank) * kTileInts + row;
                 if (!failed) {
-                    int32_t* const out = piece0 + un.part * kPieceInts;
 #pragma unroll
                     for (int c = 0; c < kCols; c += 16) {
                         const int at = first + 2 * c;
-                        if (at < p.tok) {
+                        if (at < p.tok && row < p.rows) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) __stcg(out + (at + i) * kMaxRows, sum[c + i]);
+                            for (int i = 0; i < 16; ++i) atomicAdd(all + (at + i) * kMaxRows, sum[c + i]);
                         }
                     }
                     __threadfence();
@@ -460,17 +477,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 epi_barrier_any(false);
                 finish = epi_last != 0;
                 if (finish) {
+                    // all parts' sums, and zeros in their place for the next launch
                     __threadfence();
-                    for (int k = 0; k < un.parts; ++k) {
-                        if (k == un.part) continue;
-                        const int32_t* const in = piece0 + k * kPieceInts;
 #pragma unroll
-                        for (int c = 0; c < kCols; c += 16) {
-                            const int at = first + 2 * c;
-                            if (at < p.tok) {
+                    for (int c = 0; c < kCols; c += 16) {
+                        const int at = first + 2 * c;
+                        if (at < p.tok && row < p.rows) {
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) sum[c + i] += __ldcg(in + (at + i) * kMaxRows);
-                            }
+                            for (int i = 0; i < 16; ++i) sum[c + i] = __ldcg(all + (at + i) * kMaxRows);
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 16) {
+                        const int at = first + 2 * c;
+                        if (at < p.tok && row < p.rows) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) __stcg(all + (at + i) * kMaxRows, 0);
                         }
                     }
                 }
@@ -813,7 +835,8 @@ hess_status il_prepare(int dev, int* pairs, int* sms_out) {
                     if (fn)
                         IL_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                     static_cast<int>(kFewSmem)));
-        for (auto fn : {int8_pair_kernel<__nv_bfloat16>, int8_pair_kernel<__half>})
+        for (auto fn : {int8_pair_kernel<__nv_bfloat16, true>, int8_pair_kernel<__nv_bfloat16, false>,
+                        int8_pair_kernel<__half, true>, int8_pair_kernel<__half, false>})
             IL_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)));
         int sms = 0;
         IL_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
@@ -823,7 +846,7 @@ hess_status il_prepare(int dev, int* pairs, int* sms_out) {
         cfg.blockDim = dim3(kThreads, 1, 1);
         cfg.dynamicSmemBytes = kSmemBytes;
         int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, int8_pair_kernel<__nv_bfloat16>, &cfg) != cudaSuccess ||
+        if (cudaOccupancyMaxActiveClusters(&clusters, int8_pair_kernel<__nv_bfloat16, true>, &cfg) != cudaSuccess ||
             clusters <= 0) {
             cudaGetLastError();
             clusters = sms / 2;
@@ -847,7 +870,7 @@ struct int8_linear_ctx {
     void* memory = nullptr;  // holds what follows
     uint16_t* wide = nullptr;       // [tokens, d] float16 codes
     float* x_scale = nullptr;       // [tokens]
-    int32_t* pieces = nullptr;      // one per pair
+    int32_t* sums = nullptr;        // of split tiles, two CTAs' per pair, zero between calls
     void* w_restored = nullptr;     // [f, d]
     void* x_restored = nullptr;     // [train_tokens, d]
     float* ff_pieces = nullptr;
@@ -976,12 +999,13 @@ hess_status forward(int8_linear_ctx* g, const void* X, const int8_t* codes, cons
     const int fit = static_cast<int>(kRing / p.stage_bytes);
     p.stages = fit < kMaxStages ? fit : kMaxStages;
     p.acc_cols = static_cast<uint32_t>((p.tok + 31) / 32 * 32);
-    const int slots = static_cast<int>((kTmemCols - 2 * p.acc_cols) / 32) & ~1;
+    const bool halves = p.tok > kCoarseTok;
+    const int slots = static_cast<int>((kTmemCols - 2 * p.acc_cols) / (halves ? kKB / 4 : kKB / 2)) & (halves ? ~1 : ~0);
     p.slots = slots < kMaxSlots ? slots : kMaxSlots;
     p.x_scale = X ? g->x_scale : scale;
     p.w_scale = W_scale;
     p.out = Y;
-    p.pieces = g->pieces;
+    p.sums = g->sums;
     p.arrived = g->status + 1;
     p.status = g->status;
     p.timeout_ns = g->timeout_ns;
@@ -992,10 +1016,11 @@ hess_status forward(int8_linear_ctx* g, const void* X, const int8_t* codes, cons
         IL_TRY(rows8_quantize_launch(X, g->d, n, g->d, g->dtype, 0, nullptr, 0, g->wide, g->d, g->x_scale, s));
     else
         IL_TRY(rows8_restore_launch(codes, g->d, nullptr, n, g->d, 0, g->wide, g->d, HESS_F16, s));
-    const int pairs = p.n_units < g->pairs ? p.n_units : g->pairs;
+    const int pairs = pairs_of(p, g->pairs);
     const hess_status st = il_launch(
-        g->dtype == HESS_BF16 ? int8_pair_kernel<__nv_bfloat16> : int8_pair_kernel<__half>, p, 2 * pairs, kThreads,
-        kSmemBytes, s);
+        g->dtype == HESS_BF16 ? (halves ? int8_pair_kernel<__nv_bfloat16, true> : int8_pair_kernel<__nv_bfloat16, false>)
+                              : (halves ? int8_pair_kernel<__half, true> : int8_pair_kernel<__half, false>),
+        p, 2 * pairs, kThreads, kSmemBytes, s);
     IL_TRY(g->order.end(s));
     return st;
 }
@@ -1043,22 +1068,23 @@ IL_EXPORT hess_status int8_linear_create(int64_t d, int64_t f, int64_t tokens, i
     g->dtype = dtype;
     const auto round = [](size_t b) { return (b + 255) / 256 * 256; };
     const size_t wide = round(static_cast<size_t>(tokens) * d * 2), x_scale = round(static_cast<size_t>(tokens) * 4);
-    const size_t pieces = tokens > 0 ? static_cast<size_t>(pairs) * hk::kPieceInts * 4 : 0;
+    const size_t sums = tokens > 0 ? static_cast<size_t>(pairs) * 2 * hk::kTileInts * 4 : 0;
     const size_t w_restored = train_tokens > 0 ? round(static_cast<size_t>(f) * d * 2) : 0;
     const size_t x_restored = round(static_cast<size_t>(train_tokens) * d * 2);
     const size_t ff_pieces = static_cast<size_t>(ff_pairs) * hk::kFfPieceBytes;
     g->status_bytes = (1 + 2 * static_cast<size_t>(pairs) + 2 * static_cast<size_t>(ff_pairs)) * 4;
-    cudaError_t e = cudaMalloc(&g->memory, wide + x_scale + pieces + w_restored + x_restored + ff_pieces + g->status_bytes);
+    cudaError_t e = cudaMalloc(&g->memory, wide + x_scale + sums + w_restored + x_restored + ff_pieces + g->status_bytes);
     if (e == cudaSuccess) {
         uint8_t* m = static_cast<uint8_t*>(g->memory);
         g->wide = reinterpret_cast<uint16_t*>(m);
         g->x_scale = reinterpret_cast<float*>(m += wide);
-        g->pieces = reinterpret_cast<int32_t*>(m += x_scale);
-        g->w_restored = m += pieces;
+        g->sums = reinterpret_cast<int32_t*>(m += x_scale);
+        g->w_restored = m += sums;
         g->x_restored = m += w_restored;
         g->ff_pieces = reinterpret_cast<float*>(m += x_restored);
         g->status = reinterpret_cast<uint32_t*>(m += ff_pieces);
         e = cudaMemset(g->status, 0, g->status_bytes);
+        if (e == cudaSuccess && sums) e = cudaMemset(g->sums, 0, sums);
     }
     if (e == cudaSuccess) e = g->order.create();
     if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
@@ -1187,10 +1213,11 @@ IL_EXPORT hess_status int8_linear_sync(int8_linear_t g, hess_stream_t stream) {
     IL_TRY(cudaMemcpyAsync(&word, g->status, sizeof(word), cudaMemcpyDeviceToHost, s));
     IL_TRY(cudaStreamSynchronize(s));
     if (word == 0) return HESS_OK;
-    // the arrival counts of an interrupted call go with it, when no call on another
+    // the sums and arrival counts of an interrupted call go with it, when no call on another
     // stream is at them, and before the next call may be
     IL_TRY(g->order.begin(s));
     IL_TRY(cudaMemsetAsync(g->status, 0, g->status_bytes, s));
+    if (g->tokens > 0) IL_TRY(cudaMemsetAsync(g->sums, 0, static_cast<size_t>(g->pairs) * 2 * hk::kTileInts * 4, s));
     IL_TRY(cudaStreamSynchronize(s));
     return il_fail(HESS_ERR_TIMEOUT, "a device-side wait ran out (status 0x%x); results are invalid", word);
 }

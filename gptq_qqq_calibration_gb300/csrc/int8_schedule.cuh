@@ -2,6 +2,11 @@
 // Y^T = Wq Xq^T, the units a tile's sum is split in, and the pair that takes each.
 // Host and device functions, so that the kernel, the host library and a CPU test of
 // the schedule (tests/int8_schedule_check.cu) run the same code.
+//
+// Two ways.  Whole tiles in turn, where there are many; the tiles of the last turn may be
+// split along their sums.  Or an even share of all tiles' stages for every pair, where
+// there are few tiles: a pair then has a part of a tile at either end of its share, at
+// most.
 #pragma once
 
 #include <cstdint>
@@ -23,72 +28,117 @@ struct Schedule {
     int32_t tok;      // tokens of a tile, a multiple of 16
     int32_t rows;     // weight rows of a tile per CTA
     int32_t tiles_t, tiles_f;
-    int32_t whole;    // tiles that are not split; they come first
-    int32_t parts;    // units of each tile after them
-    int32_t n_units;
+    int32_t even;     // 1: every pair has an even share of all stages
+    int32_t whole;    // in turn: tiles that are not split; they come first
+    int32_t parts;    // in turn: units of each tile after them
+    int32_t n_units;  // in turn: of all tiles; even shares: stages of all tiles
 };
 
 struct Unit {
     int f0, t0;    // first weight row of the pair's tile, first token
     int kb0, kb1;  // stages of the sum
-    int parts, part, split;  // units of this tile, this one, split tiles before it
+    int parts;     // units of this tile
+    int split;     // number of this tile among those that may be split, where parts > 1
 };
 
-__host__ __device__ inline Unit unit_at(const Schedule& p, int u) {
-    Unit r{};
-    r.parts = 1;
-    if (u >= p.whole) {
-        r.parts = p.parts;
-        r.split = (u - p.whole) / p.parts;
-        r.part = (u - p.whole) - r.split * p.parts;
-        u = p.whole + r.split;
-    }
+__host__ __device__ inline int stages_of(const Schedule& p) { return (p.d + kKB - 1) / kKB; }
+
+// First weight row and first token of a tile: groups of kGroupF row tiles, walked token
+// tile by token tile.
+__host__ __device__ inline void tile_at(const Schedule& p, int tile, Unit& r) {
     const int per = kGroupF * p.tiles_t;
-    const int g = u / per, rest = u - g * per;
+    const int g = tile / per, rest = tile - g * per;
     const int rows = p.tiles_f - g * kGroupF < kGroupF ? p.tiles_f - g * kGroupF : kGroupF;
     const int t = rest / rows;
     r.t0 = t * p.tok;
     r.f0 = (g * kGroupF + (rest - t * rows)) * 2 * p.rows;
-    const int n_kb = (p.d + kKB - 1) / kKB;
-    r.kb0 = n_kb * r.part / r.parts;
-    r.kb1 = n_kb * (r.part + 1) / r.parts;
-    return r;
+}
+
+// The pair whose even share holds stage x of all.
+__host__ __device__ inline int pair_of(const Schedule& p, int64_t x, int n_pairs) {
+    return static_cast<int>((n_pairs * (x + 1) - 1) / p.n_units);
+}
+
+// The i-th unit of a pair; false where there is none.
+__host__ __device__ inline bool unit_of(const Schedule& p, int pair, int n_pairs, int i, Unit& r) {
+    const int n_kb = stages_of(p);
+    if (p.even) {
+        const int64_t from = static_cast<int64_t>(p.n_units) * pair / n_pairs;
+        const int64_t to = static_cast<int64_t>(p.n_units) * (pair + 1) / n_pairs;
+        const int64_t tile = from / n_kb + i, first = tile * n_kb;
+        if (first >= to) return false;
+        r.kb0 = from > first ? static_cast<int>(from - first) : 0;
+        r.kb1 = to < first + n_kb ? static_cast<int>(to - first) : n_kb;
+        r.parts = pair_of(p, first + n_kb - 1, n_pairs) - pair_of(p, first, n_pairs) + 1;
+        r.split = static_cast<int>(tile);
+        tile_at(p, static_cast<int>(tile), r);
+        return true;
+    }
+    int u = pair + i * n_pairs;
+    if (u >= p.n_units) return false;
+    int part = 0;
+    r.parts = 1;
+    r.split = 0;
+    if (u >= p.whole) {
+        r.parts = p.parts;
+        r.split = (u - p.whole) / p.parts;
+        part = (u - p.whole) - r.split * p.parts;
+        u = p.whole + r.split;
+    }
+    tile_at(p, u, r);
+    r.kb0 = n_kb * part / r.parts;
+    r.kb1 = n_kb * (part + 1) / r.parts;
+    return true;
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Pairs that a launch has, out of those that run at once.
+inline int pairs_of(const Schedule& p, int pairs) { return p.n_units < pairs ? p.n_units : pairs; }
+
 // Tiles and splits for n tokens.  In SM cycles, a stage costs what bounds it: the MMAs
-// (4 a token), turning the weights into float16 (kConvert, whatever the number of rows), or the
-// weights' way from memory (5 a row, at 24 bytes a cycle and SM).  A turn of units costs
-// kTurn more, a split kSplit and its pieces' way to memory and back.
+// (4 a token) and their issue (kIssue), the weights' way from memory (16 bytes a row
+// over 3 cycles at 24 bytes a cycle and SM) or the stage's way from L2 at 40 bytes a cycle.
+// A turn of units costs kTurn more, split tiles kSplit and 6 a token for their sums' way to
+// memory and back.
 inline void plan(Schedule& p, int64_t pairs) {
-    constexpr int64_t kConvert = 330, kTurn = 700, kSplit = 2500;
+    constexpr int64_t kIssue = 600, kTurn = 700, kSplit = 3000;
     const int64_t n_kb = ceil_div(p.d, kKB);
     p.tiles_t = static_cast<int32_t>(ceil_div(p.n, kMaxTok));
     p.tok = static_cast<int32_t>(ceil_div(ceil_div(p.n, p.tiles_t), 16) * 16);
     const int64_t most = ceil_div(p.f, 2) < kMaxRows ? ceil_div(p.f, 2) : kMaxRows;
     int64_t best = -1;
+    const auto take = [&](int64_t cost, int64_t rows, int64_t tiles_f, bool even, int64_t whole, int64_t parts,
+                          int64_t units) {
+        if (best >= 0 && cost >= best) return;
+        best = cost;
+        p.rows = static_cast<int32_t>(rows);
+        p.tiles_f = static_cast<int32_t>(tiles_f);
+        p.even = even ? 1 : 0;
+        p.whole = static_cast<int32_t>(whole);
+        p.parts = static_cast<int32_t>(parts);
+        p.n_units = static_cast<int32_t>(units);
+    };
     for (int64_t wide = most; wide > 0; wide -= 4) {
-        const int64_t tiles_f = ceil_div(p.f, 2 * wide), even = ceil_div(p.f, 2 * tiles_f);
-        const int64_t rows = ceil_div(p.f, 2 * even) == tiles_f ? even : wide;  // the same rows in every tile
+        const int64_t tiles_f = ceil_div(p.f, 2 * wide), balanced = ceil_div(p.f, 2 * tiles_f);
+        const int64_t rows = ceil_div(p.f, 2 * balanced) == tiles_f ? balanced : wide;  // the same rows in every tile
         const int64_t tiles = p.tiles_t * tiles_f;
         const int64_t turns = tiles / pairs, rest = tiles % pairs;
         int64_t stage = 4 * p.tok;
-        if (stage < kConvert) stage = kConvert;
+        if (stage < kIssue) stage = kIssue;
         if (stage < 16 * rows / 3) stage = 16 * rows / 3;
+        if (stage < (kKB * rows + kKB * p.tok) / 40) stage = (kKB * rows + kKB * p.tok) / 40;
         for (int64_t s = 1; s <= kMaxParts && s <= n_kb && (s == 1 || rest * s <= pairs); ++s) {
             int64_t cost = turns * (n_kb * stage + kTurn);
             if (rest > 0) cost += ceil_div(n_kb, s) * stage + kTurn;
-            if (s > 1) cost += kSplit + 8 * s * p.tok;
-            if (best < 0 || cost < best) {
-                best = cost;
-                p.rows = static_cast<int32_t>(rows);
-                p.parts = static_cast<int32_t>(s);
-                p.tiles_f = static_cast<int32_t>(tiles_f);
-                p.whole = static_cast<int32_t>(s > 1 ? tiles - rest : tiles);
-                p.n_units = static_cast<int32_t>(s > 1 ? p.whole + rest * s : tiles);
-            }
+            if (s > 1) cost += kSplit + 6 * p.tok;
+            const int64_t whole = s > 1 ? tiles - rest : tiles;
+            take(cost, rows, tiles_f, false, whole, s, s > 1 ? whole + rest * s : tiles);
             if (rest == 0) break;
+        }
+        if (tiles <= pairs) {
+            const int64_t share = ceil_div(tiles * n_kb, pairs);
+            take(share * stage + 2 * kTurn + kSplit + 6 * p.tok, rows, tiles_f, true, 0, 1, tiles * n_kb);
         }
         if (wide <= 8) break;
     }

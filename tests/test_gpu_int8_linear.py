@@ -341,10 +341,11 @@ def test_weights_written_just_before():
 @pytest.mark.parametrize("limit", [0, 500, 2000, 8000])
 def test_waits_that_run_out_end_the_kernel(limit):
     """Split tiles with a limit that some waits keep and others do not: the kernel ends,
-    says so, and the handle works again."""
+    says so, and the handle works again.  (Sums over enough columns that a tile's end is
+    waited for longer than one attempt of a wait lasts.)"""
     from gptq_qqq_calibration_gb300 import HessError, Int8Linear
     from gptq_qqq_calibration_gb300.int8_linear import int8_linear_set_timeout
-    n, d, f = 300, 4112, 520
+    n, d, f = 300, 16400, 4096
     x, (wq, ws), _ = make(n, d, f, torch.bfloat16, 60)
     op = Int8Linear(d, f, tokens=n)
     X, w = x.cuda(), rows8(wq, ws)
