@@ -50,26 +50,31 @@ constexpr uint32_t kRing = 208 * 1024;
 // Slots of A in tensor memory hold a stage (64 columns), or half of one where the
 // sums leave room for no more than three of those.
 constexpr int kMaxSlots = 6;
+constexpr int kNarrowTok = 64;
 constexpr int kCoarseTok = 128;  // the most tokens of a tile with whole stages in slots
 constexpr uint32_t kTmemCols = 512;
 static_assert(2 * kMaxTok + 4 * (kKB / 4) <= kTmemCols, "two sums and four halves of a stage");
 constexpr int kNumBarriers = 4 * kMaxStages + 2 * kMaxSlots + 5;
-constexpr size_t kSmemBytes = 1024 + kRing + 8 * kNumBarriers + 16;
+// What leaves an epilogue half (four warps): sums of eight tokens, or results of sixteen.
+constexpr uint32_t kStagingBytes = 8 * kMaxRows * 4;
+constexpr uint32_t kBarAt = kRing + 2 * 2 * kStagingBytes;  // two buffers for each half
+constexpr size_t kSmemBytes = 1024 + kBarAt + 8 * kNumBarriers + 16;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 constexpr int kThreads = 640;  // warp 0: weights, 1: MMAs, 2: tokens, 4-11: converters, 12-19: epilogue
 constexpr int kFirstEpiWarp = 12, kEpiWarps = 8;
-constexpr int kCols = kMaxTok / 2;  // tokens of an epilogue thread
 constexpr unsigned long long kDrainLimitNs = 1000000000ull;
 constexpr unsigned long long kAbortSettleNs = 2000000ull;
 constexpr int64_t kTileInts = kMaxTok * kMaxRows;  // one CTA's sums of a split tile
 
 struct PairParams : Schedule {
-    CUtensorMap x, w;  // float16 codes [n, d], boxes of tok/2 rows x 64; weights [f, d], boxes of rows x 128
+    // float16 codes [n, d], boxes of tok/2 rows x 64; weights [f, d], boxes of rows x 128;
+    // results [n, f], boxes of 16 tokens x rows
+    CUtensorMap x, w, y;
     int32_t stages;
     int32_t slots;       // of A in tensor memory
     uint32_t acc_cols;   // columns of one sum in tensor memory; the slots follow the second
     uint32_t w_bytes, stage_bytes;  // of a stage; the tokens' two boxes follow the weights
     const float *x_scale, *w_scale;
-    void* out;
     int32_t* sums;      // of the tiles that are split, per CTA; zero between launches
     uint32_t* arrived;  // units of each of them that have come, per CTA; zero between launches
     uint32_t* status;
@@ -158,16 +163,19 @@ __device__ __forceinline__ bool epi_barrier_any(bool x) {
 // Every wait is bounded.  The launch before this one is the kernel that writes the
 // tokens' codes and scales; it waits for all work before it and only then lets this
 // one start, so that only what it writes itself has to be waited for here.
-template <class T, bool kHalves>
+// kTok: the most tokens of a tile.  Narrow tiles get epilogues that hold fewer sums.
+template <class T, int kTok>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int8_pair_kernel(const __grid_constant__ PairParams p) {
+    constexpr bool kHalves = kTok > kCoarseTok;
+    constexpr int kCols = kTok / 2;  // tokens of an epilogue thread
     constexpr uint32_t kSlotCols = kHalves ? kKB / 4 : kKB / 2;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* const gbase = smem_raw + (base - raw);
-    const uint32_t bar0 = base + kRing;
-    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + kRing + 8 * kNumBarriers);
+    const uint32_t bar0 = base + kBarAt;
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + kBarAt + 8 * kNumBarriers);
     auto wfull_bar = [&](int s) { return bar0 + 8u * s; };                      // this CTA's weights have landed
     auto wempty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };      // its converters have read them
     auto xfull_bar = [&](int s) { return bar0 + 8u * (2 * kMaxStages + s); };   // even CTA: the pair's tokens
@@ -179,6 +187,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t drain_bar = bar0 + 8u * (4 * kMaxStages + 2 * kMaxSlots + 4);
     __shared__ volatile int aborted;
     __shared__ volatile int epi_last;
+    __shared__ float4 epi_scales[2][kCols / 4];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -205,6 +214,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_barrier_init();
         prefetch_tensormap(&p.w);
         prefetch_tensormap(&p.x);
+        prefetch_tensormap(&p.y);
     }
     if (warp == 1) {
         tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
@@ -416,8 +426,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         setmaxnreg_inc<136>();
         griddep_wait();
         const int q = warp & 3, row = q * 32 + lane;
-        const int first = ((warp - kFirstEpiWarp) >> 2) * 16;
+        const int group = (warp - kFirstEpiWarp) >> 2, first = group * 16;
+        const bool leader = q == 0 && lane == 0;
+        const uint32_t buffers = base + kRing + group * (2 * kStagingBytes);
+        uint32_t buffer = buffers;
         const uint32_t acce0 = mapa_shared(acce_bar(0), 0);
+        // A half's four warps write one buffer while the other is on its way.
+        const auto begin = [&] {
+            if (leader) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
+        };
+        const auto end = [&](auto issue) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
+            if (leader) {
+                issue();
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            buffer = buffer == buffers ? buffers + kStagingBytes : buffers;
+        };
         bool failed = false;
         int ab = 0;
         uint32_t aphase = 0;
@@ -454,17 +481,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             bool finish = !failed;
             if (un.parts > 1) {
-                // Integers: whoever adds first.  [token][row], so that a warp adds to 128 bytes.
-                int32_t* const all = p.sums + (2 * static_cast<int64_t>(un.split) + rank) * kTileInts + row;
-                if (!failed) {
+                // Integers: whoever adds first.  Eight tokens at a time go through shared
+                // memory and are added to [token][row] in L2 by one bulk reduction.
+                int32_t* const all = p.sums + (2 * static_cast<int64_t>(un.split) + rank) * kTileInts;
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 16) {
-                        const int at = first + 2 * c;
-                        if (at < p.tok && row < p.rows) {
+                for (int c = 0; c < kCols; c += 8) {
+                    const int at = first + 2 * (c & ~15) + (c & 8);
+                    if (at < p.tok && !failed) {
+                        begin();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) atomicAdd(all + (at + i) * kMaxRows, sum[c + i]);
-                        }
+                        for (int i = 0; i < 8; ++i)
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(buffer + (i * kMaxRows + row) * 4), "r"(sum[c + i])
+                                         : "memory");
+                        end([&] {
+                            asm volatile(
+                                "cp.reduce.async.bulk.global.shared::cta.bulk_group.add.s32 [%0], [%1], %2;" ::"l"(
+                                    reinterpret_cast<uint64_t>(all + at * kMaxRows)),
+                                "r"(buffer), "r"(kStagingBytes)
+                                : "memory");
+                        });
                     }
+                }
+                if (leader) {
+                    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                    asm volatile("fence.proxy.async;" ::: "memory");
                     __threadfence();
                 }
                 epi_barrier_any(false);
@@ -479,48 +519,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (finish) {
                     // all parts' sums, and zeros in their place for the next launch
                     __threadfence();
+                    asm volatile("fence.proxy.async;" ::: "memory");
 #pragma unroll
                     for (int c = 0; c < kCols; c += 16) {
                         const int at = first + 2 * c;
-                        if (at < p.tok && row < p.rows) {
+                        if (at < p.tok) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) sum[c + i] = __ldcg(all + (at + i) * kMaxRows);
+                            for (int i = 0; i < 16; ++i) sum[c + i] = __ldcg(all + (at + i) * kMaxRows + row);
                         }
                     }
 #pragma unroll
                     for (int c = 0; c < kCols; c += 16) {
                         const int at = first + 2 * c;
-                        if (at < p.tok && row < p.rows) {
+                        if (at < p.tok) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) __stcg(all + (at + i) * kMaxRows, 0);
+                            for (int i = 0; i < 16; ++i) __stcg(all + (at + i) * kMaxRows + row, 0);
                         }
                     }
                 }
                 epi_barrier_any(false);  // epi_last may be written again
             }
-            const int ch = un.f0 + static_cast<int>(rank) * p.rows + row;
-            if (finish && row < p.rows && ch < p.f) {
-                const float sw = p.w_scale[ch];
-                T* const out = static_cast<T*>(p.out) + static_cast<int64_t>(un.t0) * p.f + ch;
-                const int n = p.n - un.t0;  // tokens of this tile
-                const float* const sx = p.x_scale + un.t0;
+            if (finish) {
+                const int ch = un.f0 + static_cast<int>(rank) * p.rows;
+                const float sw = row < p.rows && ch + row < p.f ? p.w_scale[ch + row] : 0.0f;
+                const int mine = (warp & 3) * 32 + lane;  // of the half's threads
+                if (mine < kCols) {
+                    const int t = un.t0 + first + 2 * (mine & ~15) + (mine & 15);
+                    reinterpret_cast<float*>(epi_scales[group])[mine] = t < p.n ? p.x_scale[t] : 0.0f;
+                }
 #pragma unroll
                 for (int c = 0; c < kCols; c += 16) {
                     const int at = first + 2 * c;
-                    if (at < p.tok && at < n) {
-                        // sixteen scales on their way at once, before the stores
-                        float k[16];
+                    if (at < p.tok) {
+                        begin();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) k[i] = sx[at + i < n ? at + i : n - 1];
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 k = epi_scales[group][(c + i) / 4];
+                            const float s4[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (at + i < n)
-                                out[static_cast<int64_t>(at + i) * p.f] =
-                                    rounded<T>(__fmul_rn(__int2float_rn(sum[c + i]), __fmul_rn(k[i], sw)));
+                            for (int j = 0; j < 4; ++j) {
+                                const T y = rounded<T>(__fmul_rn(__int2float_rn(sum[c + i + j]), __fmul_rn(s4[j], sw)));
+                                uint16_t bits;
+                                memcpy(&bits, &y, 2);
+                                if (row < p.rows)
+                                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(buffer + ((i + j) * p.rows + row) * 2), "h"(bits)
+                                                 : "memory");
+                            }
+                        }
+                        end([&] {
+                            if (ch < p.f && un.t0 + at < p.n)
+                                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                                                 reinterpret_cast<uint64_t>(&p.y)),
+                                             "r"(buffer), "r"(ch), "r"(un.t0 + at)
+                                             : "memory");
+                        });
                     }
                 }
+                asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");  // the scales may be written again
             }
         }
+        if (leader) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (failed && lane == 0) {
             atomicOr(p.status, kStatusTimeoutEpilogue);
             aborted = 1;
@@ -773,8 +831,7 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// Row-major [rows, cols], boxes of box_rows x 128 bytes in the 128-byte swizzle, zeros past the edges.
-hess_status il_encode(CUtensorMap* m, const void* ptr, bool bytes, int64_t rows, int64_t cols, int64_t box_rows) {
+EncodeTiledFn il_encode_fn() {
     static const EncodeTiledFn fn = [] {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -784,20 +841,35 @@ hess_status il_encode(CUtensorMap* m, const void* ptr, bool bytes, int64_t rows,
             return reinterpret_cast<EncodeTiledFn>(p);
         return static_cast<EncodeTiledFn>(nullptr);
     }();
+    return fn;
+}
+
+// Row-major [rows, cols], boxes of box_rows x box_cols, zeros past the edges.
+hess_status il_encode_as(CUtensorMap* m, const void* ptr, CUtensorMapDataType type, int item, int64_t rows, int64_t cols,
+                         int64_t box_rows, int64_t box_cols, CUtensorMapSwizzle swizzle) {
+    const EncodeTiledFn fn = il_encode_fn();
     if (!fn) return il_fail(HESS_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     if (il_injected("encode"))
         return il_fail(HESS_ERR_UNSUPPORTED, "injected tensor-map failure (HESS_FAULT=encode)");
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * (bytes ? 1u : 2u)};
-    const cuuint32_t box[2] = {bytes ? 128u : 64u, static_cast<cuuint32_t>(box_rows)}, es[2] = {1u, 1u};
-    const CUresult r = fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                          const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * item)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)}, es[2] = {1u, 1u};
+    const CUresult r = fn(m, type, 2, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return il_fail(HESS_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled failed (%d) for [%lld, %lld]",
                        static_cast<int>(r), static_cast<long long>(rows), static_cast<long long>(cols));
     return HESS_OK;
+}
+// Operands: boxes of 128 bytes a row in the 128-byte swizzle.
+hess_status il_encode(CUtensorMap* m, const void* ptr, bool bytes, int64_t rows, int64_t cols, int64_t box_rows) {
+    return il_encode_as(m, ptr, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, bytes ? 1 : 2,
+                        rows, cols, box_rows, bytes ? 128 : 64, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// Results: boxes of 16 tokens x the rows of a CTA, as they lie.
+hess_status il_encode_out(CUtensorMap* m, void* ptr, int32_t dtype, int64_t rows, int64_t cols, int64_t box_cols) {
+    return il_encode_as(m, ptr, dtype == HESS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                        rows, cols, 16, box_cols, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 constexpr size_t kFewSmem = 128 * 1024;
@@ -822,6 +894,12 @@ auto few_kernel(int tok, int gran) -> void (*)(FewParams) {
     return nullptr;
 }
 
+template <class T>
+auto pair_kernel(int tok) -> void (*)(PairParams) {
+    return tok <= kNarrowTok ? int8_pair_kernel<T, kNarrowTok> : tok <= kCoarseTok ? int8_pair_kernel<T, kCoarseTok>
+                                                                                   : int8_pair_kernel<T, kMaxTok>;
+}
+
 // Per-device set-up: shared-memory limits, and how many pairs stay resident.
 hess_status il_prepare(int dev, int* pairs, int* sms_out) {
     static std::mutex mu;
@@ -835,9 +913,10 @@ hess_status il_prepare(int dev, int* pairs, int* sms_out) {
                     if (fn)
                         IL_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                     static_cast<int>(kFewSmem)));
-        for (auto fn : {int8_pair_kernel<__nv_bfloat16, true>, int8_pair_kernel<__nv_bfloat16, false>,
-                        int8_pair_kernel<__half, true>, int8_pair_kernel<__half, false>})
-            IL_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)));
+        for (int tok : {kNarrowTok, kCoarseTok, kMaxTok})
+            for (auto fn : {pair_kernel<__nv_bfloat16>(tok), pair_kernel<__half>(tok)})
+                IL_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            static_cast<int>(kSmemBytes)));
         int sms = 0;
         IL_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
         sm_count[dev] = sms;
@@ -846,7 +925,7 @@ hess_status il_prepare(int dev, int* pairs, int* sms_out) {
         cfg.blockDim = dim3(kThreads, 1, 1);
         cfg.dynamicSmemBytes = kSmemBytes;
         int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, int8_pair_kernel<__nv_bfloat16, true>, &cfg) != cudaSuccess ||
+        if (cudaOccupancyMaxActiveClusters(&clusters, pair_kernel<__nv_bfloat16>(kMaxTok), &cfg) != cudaSuccess ||
             clusters <= 0) {
             cudaGetLastError();
             clusters = sms / 2;
@@ -1004,13 +1083,13 @@ hess_status forward(int8_linear_ctx* g, const void* X, const int8_t* codes, cons
     p.slots = slots < kMaxSlots ? slots : kMaxSlots;
     p.x_scale = X ? g->x_scale : scale;
     p.w_scale = W_scale;
-    p.out = Y;
     p.sums = g->sums;
     p.arrived = g->status + 1;
     p.status = g->status;
     p.timeout_ns = g->timeout_ns;
     IL_CHECK(il_encode(&p.x, g->wide, false, n, g->d, p.tok / 2));
     IL_CHECK(il_encode(&p.w, W, true, g->f, g->d, p.rows));
+    IL_CHECK(il_encode_out(&p.y, Y, g->dtype, n, g->f, p.rows));
     IL_TRY(g->order.begin(s));
     if (X)
         IL_TRY(rows8_quantize_launch(X, g->d, n, g->d, g->dtype, 0, nullptr, 0, g->wide, g->d, g->x_scale, s));
@@ -1018,9 +1097,8 @@ hess_status forward(int8_linear_ctx* g, const void* X, const int8_t* codes, cons
         IL_TRY(rows8_restore_launch(codes, g->d, nullptr, n, g->d, 0, g->wide, g->d, HESS_F16, s));
     const int pairs = pairs_of(p, g->pairs);
     const hess_status st = il_launch(
-        g->dtype == HESS_BF16 ? (halves ? int8_pair_kernel<__nv_bfloat16, true> : int8_pair_kernel<__nv_bfloat16, false>)
-                              : (halves ? int8_pair_kernel<__half, true> : int8_pair_kernel<__half, false>),
-        p, 2 * pairs, kThreads, kSmemBytes, s);
+        g->dtype == HESS_BF16 ? pair_kernel<__nv_bfloat16>(p.tok) : pair_kernel<__half>(p.tok), p, 2 * pairs, kThreads,
+        kSmemBytes, s);
     IL_TRY(g->order.end(s));
     return st;
 }

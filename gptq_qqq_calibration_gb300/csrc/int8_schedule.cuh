@@ -17,7 +17,7 @@ namespace hk {
 namespace i8 {
 
 constexpr int kKB = 128;        // contraction steps of one stage
-constexpr int kMaxTok = 192;    // tokens of a tile: the MMA's columns
+constexpr int kMaxTok = 160;    // tokens of a tile: the MMA's columns
 constexpr int kMaxRows = 128;   // weight rows of a tile per CTA: the MMA's rows
 constexpr int kChunk = 8;       // stages whose sums stay below 2^24: 1,024 products of at most 2^14
 constexpr int kGroupF = 8;      // row tiles that run side by side (their token boxes meet in L2)
@@ -26,7 +26,7 @@ constexpr int kMaxParts = 8;
 struct Schedule {
     int32_t n, d, f;
     int32_t tok;      // tokens of a tile, a multiple of 16
-    int32_t rows;     // weight rows of a tile per CTA
+    int32_t rows;     // weight rows of a tile per CTA, a multiple of 8
     int32_t tiles_t, tiles_f;
     int32_t even;     // 1: every pair has an even share of all stages
     int32_t whole;    // in turn: tiles that are not split; they come first
@@ -106,7 +106,8 @@ inline void plan(Schedule& p, int64_t pairs) {
     const int64_t n_kb = ceil_div(p.d, kKB);
     p.tiles_t = static_cast<int32_t>(ceil_div(p.n, kMaxTok));
     p.tok = static_cast<int32_t>(ceil_div(ceil_div(p.n, p.tiles_t), 16) * 16);
-    const int64_t most = ceil_div(p.f, 2) < kMaxRows ? ceil_div(p.f, 2) : kMaxRows;
+    // rows are multiples of 8: 16 bytes of a row of results
+    const int64_t most = p.f < 2 * kMaxRows ? ceil_div(p.f, 16) * 8 : kMaxRows;
     int64_t best = -1;
     const auto take = [&](int64_t cost, int64_t rows, int64_t tiles_f, bool even, int64_t whole, int64_t parts,
                           int64_t units) {
@@ -119,8 +120,8 @@ inline void plan(Schedule& p, int64_t pairs) {
         p.parts = static_cast<int32_t>(parts);
         p.n_units = static_cast<int32_t>(units);
     };
-    for (int64_t wide = most; wide > 0; wide -= 4) {
-        const int64_t tiles_f = ceil_div(p.f, 2 * wide), balanced = ceil_div(p.f, 2 * tiles_f);
+    for (int64_t wide = most; wide > 0; wide -= 8) {
+        const int64_t tiles_f = ceil_div(p.f, 2 * wide), balanced = ceil_div(p.f, 16 * tiles_f) * 8;
         const int64_t rows = ceil_div(p.f, 2 * balanced) == tiles_f ? balanced : wide;  // the same rows in every tile
         const int64_t tiles = p.tiles_t * tiles_f;
         const int64_t turns = tiles / pairs, rest = tiles % pairs;
@@ -140,7 +141,6 @@ inline void plan(Schedule& p, int64_t pairs) {
             const int64_t share = ceil_div(tiles * n_kb, pairs);
             take(share * stage + 2 * kTurn + kSplit + 6 * p.tok, rows, tiles_f, true, 0, 1, tiles * n_kb);
         }
-        if (wide <= 8) break;
     }
 }
 

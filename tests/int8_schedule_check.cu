@@ -1,6 +1,6 @@
 // Checks csrc/int8_schedule.cuh on the CPU.  For many sizes and numbers of pairs:
 //   * tiles are ones the MMA and the copies can take (tokens a multiple of 16, at most
-//     192; at most 128 weight rows per CTA), begin inside the result and cover it once;
+//     192; a multiple of 8, at most 128, of weight rows per CTA), begin inside the result and cover it once;
 //   * every tile's stages are summed once, by as many units as the tile says, none empty;
 //   * split tiles have numbers of their own that fit the workspace;
 //   * even shares differ by one stage at most.
@@ -36,7 +36,7 @@ bool check(int n, int d, int f, int pairs) {
     p.d = d;
     p.f = f;
     plan(p, pairs);
-    CHECK(p.tok % 16 == 0 && p.tok >= 16 && p.tok <= kMaxTok && p.rows >= 1 && p.rows <= kMaxRows);
+    CHECK(p.tok % 16 == 0 && p.tok >= 16 && p.tok <= kMaxTok && p.rows % 8 == 0 && p.rows >= 8 && p.rows <= kMaxRows);
     CHECK(p.parts >= 1 && p.n_units >= 1 && p.whole >= 0);
     split += p.parts > 1;
     split_after_whole += p.parts > 1 && p.whole > 0;
