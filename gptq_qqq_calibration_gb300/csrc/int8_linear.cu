@@ -55,8 +55,8 @@ constexpr int kCoarseTok = 128;  // the most tokens of a tile with whole stages 
 constexpr uint32_t kTmemCols = 512;
 static_assert(2 * kMaxTok + 4 * (kKB / 4) <= kTmemCols, "two sums and four halves of a stage");
 constexpr int kNumBarriers = 4 * kMaxStages + 2 * kMaxSlots + 5;
-// What leaves an epilogue half (four warps): sums of eight tokens, or results of sixteen.
-constexpr uint32_t kStagingBytes = 8 * kMaxRows * 4;
+// Sixteen tokens' results on their way out, of an epilogue half (four warps).
+constexpr uint32_t kStagingBytes = 16 * kMaxRows * 2;
 constexpr uint32_t kBarAt = kRing + 2 * 2 * kStagingBytes;  // two buffers for each half
 constexpr size_t kSmemBytes = 1024 + kBarAt + 8 * kNumBarriers + 16;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -64,7 +64,7 @@ constexpr int kThreads = 640;  // warp 0: weights, 1: MMAs, 2: tokens, 4-11: con
 constexpr int kFirstEpiWarp = 12, kEpiWarps = 8;
 constexpr unsigned long long kDrainLimitNs = 1000000000ull;
 constexpr unsigned long long kAbortSettleNs = 2000000ull;
-constexpr int64_t kTileInts = kMaxTok * kMaxRows;  // one CTA's sums of a split tile
+constexpr int64_t kPieceInts = kMaxTok * kMaxRows;  // one CTA's sums of a unit of a split tile
 
 struct PairParams : Schedule {
     // float16 codes [n, d], boxes of tok/2 rows x 64; weights [f, d], boxes of rows x 128;
@@ -75,8 +75,8 @@ struct PairParams : Schedule {
     uint32_t acc_cols;   // columns of one sum in tensor memory; the slots follow the second
     uint32_t w_bytes, stage_bytes;  // of a stage; the tokens' two boxes follow the weights
     const float *x_scale, *w_scale;
-    int32_t* sums;      // of the tiles that are split, per CTA; zero between launches
-    uint32_t* arrived;  // units of each of them that have come, per CTA; zero between launches
+    int32_t* pieces;    // sums of the units of split tiles
+    uint32_t* arrived;  // units of each split tile that have come, per CTA; zero between launches
     uint32_t* status;
     unsigned long long timeout_ns;
 };
@@ -226,7 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
     if (warp < 4) {
-        setmaxnreg_dec<48>();
+        setmaxnreg_dec<40>();
         if (warp == 0 && lane == 0) {
             bool ok = true;
             int stage = 0;
@@ -369,7 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp < 12) {
         // Converters: the first four warps take the first 64 steps of each stage, the
         // others the rest.  A thread owns one weight row.
-        setmaxnreg_dec<80>();
+        setmaxnreg_dec<72>();
         const int h = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const bool some = (warp & 3) * 32 < p.rows, mine = row < p.rows;
@@ -423,7 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else {
         // Epilogue: a thread owns one weight row (an output channel) and every other
         // sixteen tokens: of the first four warps the even ones, of the others the odd.
-        setmaxnreg_inc<136>();
+        setmaxnreg_inc<144>();
         griddep_wait();
         const int q = warp & 3, row = q * 32 + lane;
         const int group = (warp - kFirstEpiWarp) >> 2, first = group * 16;
@@ -479,32 +479,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     aphase ^= 1u;
                 }
             }
-            bool finish = !failed;
-            if (un.parts > 1) {
-                // Integers: whoever adds first.  Eight tokens at a time go through shared
-                // memory and are added to [token][row] in L2 by one bulk reduction.
-                int32_t* const all = p.sums + (2 * static_cast<int64_t>(un.split) + rank) * kTileInts;
+            const int ch = un.f0 + static_cast<int>(rank) * p.rows;
+            float sw = 0.0f;
+            const auto scales = [&] {
+                if (row < p.rows && ch + row < p.f) sw = p.w_scale[ch + row];
+                if (row < kCols) {
+                    const int t = un.t0 + first + 2 * (row & ~15) + (row & 15);
+                    reinterpret_cast<float*>(epi_scales[group])[row] = t < p.n ? p.x_scale[t] : 0.0f;
+                }
+            };
+            // Sixteen tokens' results, from the sums v on.
+            const auto finish = [&](int c, const int32_t* v) {
+                const int at = first + 2 * c;
+                begin();
 #pragma unroll
-                for (int c = 0; c < kCols; c += 8) {
-                    const int at = first + 2 * (c & ~15) + (c & 8);
-                    if (at < p.tok && !failed) {
-                        begin();
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 k = epi_scales[group][(c + i) / 4];
+                    const float s4[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(buffer + (i * kMaxRows + row) * 4), "r"(sum[c + i])
+                    for (int j = 0; j < 4; ++j) {
+                        const T y = rounded<T>(__fmul_rn(__int2float_rn(v[i + j]), __fmul_rn(s4[j], sw)));
+                        uint16_t bits;
+                        memcpy(&bits, &y, 2);
+                        if (row < p.rows)
+                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(buffer + ((i + j) * p.rows + row) * 2), "h"(bits)
                                          : "memory");
-                        end([&] {
-                            asm volatile(
-                                "cp.reduce.async.bulk.global.shared::cta.bulk_group.add.s32 [%0], [%1], %2;" ::"l"(
-                                    reinterpret_cast<uint64_t>(all + at * kMaxRows)),
-                                "r"(buffer), "r"(kStagingBytes)
-                                : "memory");
-                        });
                     }
                 }
-                if (leader) {
-                    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-                    asm volatile("fence.proxy.async;" ::: "memory");
+                end([&] {
+                    if (ch < p.f && un.t0 + at < p.n)
+                        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                                         reinterpret_cast<uint64_t>(&p.y)),
+                                     "r"(buffer), "r"(ch), "r"(un.t0 + at)
+                                     : "memory");
+                });
+            };
+            bool complete = !failed;
+            if (un.parts > 1) {
+                // pieces: [token][row], so that a warp moves 128 bytes at a time
+                const auto piece = [&](int k) {
+                    return p.pieces + (2 * static_cast<int64_t>(piece_of(p, un, k, n_pairs)) + rank) * kPieceInts + row;
+                };
+                if (!failed) {
+                    int32_t* const to = piece(un.part);
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 16) {
+                        const int at = first + 2 * c;
+                        if (at < p.tok) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) __stcg(to + (at + i) * kMaxRows, sum[c + i]);
+                        }
+                    }
                     __threadfence();
                 }
                 epi_barrier_any(false);
@@ -515,68 +540,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     epi_last = last;
                 }
                 epi_barrier_any(false);
-                finish = epi_last != 0;
-                if (finish) {
-                    // all parts' sums, and zeros in their place for the next launch
+                complete = epi_last != 0;
+                if (complete) {
                     __threadfence();
-                    asm volatile("fence.proxy.async;" ::: "memory");
+                    for (int k = 0; k < un.parts; ++k) {
+                        if (k == un.part) continue;
+                        const int32_t* const from = piece(k);
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 16) {
-                        const int at = first + 2 * c;
-                        if (at < p.tok) {
+                        for (int c = 0; c < kCols; c += 16) {
+                            const int at = first + 2 * c;
+                            if (at < p.tok) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) sum[c + i] = __ldcg(all + (at + i) * kMaxRows + row);
-                        }
-                    }
-#pragma unroll
-                    for (int c = 0; c < kCols; c += 16) {
-                        const int at = first + 2 * c;
-                        if (at < p.tok) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) __stcg(all + (at + i) * kMaxRows + row, 0);
+                                for (int i = 0; i < 16; ++i) sum[c + i] += __ldcg(from + (at + i) * kMaxRows);
+                            }
                         }
                     }
                 }
                 epi_barrier_any(false);  // epi_last may be written again
             }
-            if (finish) {
-                const int ch = un.f0 + static_cast<int>(rank) * p.rows;
-                const float sw = row < p.rows && ch + row < p.f ? p.w_scale[ch + row] : 0.0f;
-                const int mine = (warp & 3) * 32 + lane;  // of the half's threads
-                if (mine < kCols) {
-                    const int t = un.t0 + first + 2 * (mine & ~15) + (mine & 15);
-                    reinterpret_cast<float*>(epi_scales[group])[mine] = t < p.n ? p.x_scale[t] : 0.0f;
-                }
+            if (complete) {
+                scales();
 #pragma unroll
-                for (int c = 0; c < kCols; c += 16) {
-                    const int at = first + 2 * c;
-                    if (at < p.tok) {
-                        begin();
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const float4 k = epi_scales[group][(c + i) / 4];
-                            const float s4[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const T y = rounded<T>(__fmul_rn(__int2float_rn(sum[c + i + j]), __fmul_rn(s4[j], sw)));
-                                uint16_t bits;
-                                memcpy(&bits, &y, 2);
-                                if (row < p.rows)
-                                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(buffer + ((i + j) * p.rows + row) * 2), "h"(bits)
-                                                 : "memory");
-                            }
-                        }
-                        end([&] {
-                            if (ch < p.f && un.t0 + at < p.n)
-                                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                                                 reinterpret_cast<uint64_t>(&p.y)),
-                                             "r"(buffer), "r"(ch), "r"(un.t0 + at)
-                                             : "memory");
-                        });
-                    }
-                }
-                asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");  // the scales may be written again
+                for (int c = 0; c < kCols; c += 16)
+                    if (first + 2 * c < p.tok) finish(c, sum + c);
             }
+            asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");  // the scales may be written again
         }
         if (leader) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (failed && lane == 0) {
@@ -949,7 +937,7 @@ struct int8_linear_ctx {
     void* memory = nullptr;  // holds what follows
     uint16_t* wide = nullptr;       // [tokens, d] float16 codes
     float* x_scale = nullptr;       // [tokens]
-    int32_t* sums = nullptr;        // of split tiles, two CTAs' per pair, zero between calls
+    int32_t* pieces = nullptr;      // two per pair
     void* w_restored = nullptr;     // [f, d]
     void* x_restored = nullptr;     // [train_tokens, d]
     float* ff_pieces = nullptr;
@@ -1083,7 +1071,7 @@ hess_status forward(int8_linear_ctx* g, const void* X, const int8_t* codes, cons
     p.slots = slots < kMaxSlots ? slots : kMaxSlots;
     p.x_scale = X ? g->x_scale : scale;
     p.w_scale = W_scale;
-    p.sums = g->sums;
+    p.pieces = g->pieces;
     p.arrived = g->status + 1;
     p.status = g->status;
     p.timeout_ns = g->timeout_ns;
@@ -1146,23 +1134,22 @@ IL_EXPORT hess_status int8_linear_create(int64_t d, int64_t f, int64_t tokens, i
     g->dtype = dtype;
     const auto round = [](size_t b) { return (b + 255) / 256 * 256; };
     const size_t wide = round(static_cast<size_t>(tokens) * d * 2), x_scale = round(static_cast<size_t>(tokens) * 4);
-    const size_t sums = tokens > 0 ? static_cast<size_t>(pairs) * 2 * hk::kTileInts * 4 : 0;
+    const size_t pieces = tokens > 0 ? static_cast<size_t>(pairs) * 2 * 2 * hk::kPieceInts * 4 : 0;
     const size_t w_restored = train_tokens > 0 ? round(static_cast<size_t>(f) * d * 2) : 0;
     const size_t x_restored = round(static_cast<size_t>(train_tokens) * d * 2);
     const size_t ff_pieces = static_cast<size_t>(ff_pairs) * hk::kFfPieceBytes;
     g->status_bytes = (1 + 2 * static_cast<size_t>(pairs) + 2 * static_cast<size_t>(ff_pairs)) * 4;
-    cudaError_t e = cudaMalloc(&g->memory, wide + x_scale + sums + w_restored + x_restored + ff_pieces + g->status_bytes);
+    cudaError_t e = cudaMalloc(&g->memory, wide + x_scale + pieces + w_restored + x_restored + ff_pieces + g->status_bytes);
     if (e == cudaSuccess) {
         uint8_t* m = static_cast<uint8_t*>(g->memory);
         g->wide = reinterpret_cast<uint16_t*>(m);
         g->x_scale = reinterpret_cast<float*>(m += wide);
-        g->sums = reinterpret_cast<int32_t*>(m += x_scale);
-        g->w_restored = m += sums;
+        g->pieces = reinterpret_cast<int32_t*>(m += x_scale);
+        g->w_restored = m += pieces;
         g->x_restored = m += w_restored;
         g->ff_pieces = reinterpret_cast<float*>(m += x_restored);
         g->status = reinterpret_cast<uint32_t*>(m += ff_pieces);
         e = cudaMemset(g->status, 0, g->status_bytes);
-        if (e == cudaSuccess && sums) e = cudaMemset(g->sums, 0, sums);
     }
     if (e == cudaSuccess) e = g->order.create();
     if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
@@ -1291,11 +1278,10 @@ IL_EXPORT hess_status int8_linear_sync(int8_linear_t g, hess_stream_t stream) {
     IL_TRY(cudaMemcpyAsync(&word, g->status, sizeof(word), cudaMemcpyDeviceToHost, s));
     IL_TRY(cudaStreamSynchronize(s));
     if (word == 0) return HESS_OK;
-    // the sums and arrival counts of an interrupted call go with it, when no call on another
+    // the arrival counts of an interrupted call go with it, when no call on another
     // stream is at them, and before the next call may be
     IL_TRY(g->order.begin(s));
     IL_TRY(cudaMemsetAsync(g->status, 0, g->status_bytes, s));
-    if (g->tokens > 0) IL_TRY(cudaMemsetAsync(g->sums, 0, static_cast<size_t>(g->pairs) * 2 * hk::kTileInts * 4, s));
     IL_TRY(cudaStreamSynchronize(s));
     return il_fail(HESS_ERR_TIMEOUT, "a device-side wait ran out (status 0x%x); results are invalid", word);
 }

@@ -17,7 +17,7 @@ namespace hk {
 namespace i8 {
 
 constexpr int kKB = 128;        // contraction steps of one stage
-constexpr int kMaxTok = 160;    // tokens of a tile: the MMA's columns
+constexpr int kMaxTok = 192;    // tokens of a tile: the MMA's columns
 constexpr int kMaxRows = 128;   // weight rows of a tile per CTA: the MMA's rows
 constexpr int kChunk = 8;       // stages whose sums stay below 2^24: 1,024 products of at most 2^14
 constexpr int kGroupF = 8;      // row tiles that run side by side (their token boxes meet in L2)
@@ -38,7 +38,9 @@ struct Unit {
     int f0, t0;    // first weight row of the pair's tile, first token
     int kb0, kb1;  // stages of the sum
     int parts;     // units of this tile
+    int part;      // this one
     int split;     // number of this tile among those that may be split, where parts > 1
+    int first;     // even shares: the pair that has the tile's first unit
 };
 
 __host__ __device__ inline int stages_of(const Schedule& p) { return (p.d + kKB - 1) / kKB; }
@@ -69,26 +71,35 @@ __host__ __device__ inline bool unit_of(const Schedule& p, int pair, int n_pairs
         if (first >= to) return false;
         r.kb0 = from > first ? static_cast<int>(from - first) : 0;
         r.kb1 = to < first + n_kb ? static_cast<int>(to - first) : n_kb;
-        r.parts = pair_of(p, first + n_kb - 1, n_pairs) - pair_of(p, first, n_pairs) + 1;
+        r.first = pair_of(p, first, n_pairs);
+        r.parts = pair_of(p, first + n_kb - 1, n_pairs) - r.first + 1;
+        r.part = pair - r.first;
         r.split = static_cast<int>(tile);
         tile_at(p, static_cast<int>(tile), r);
         return true;
     }
     int u = pair + i * n_pairs;
     if (u >= p.n_units) return false;
-    int part = 0;
     r.parts = 1;
-    r.split = 0;
+    r.part = r.split = r.first = 0;
     if (u >= p.whole) {
         r.parts = p.parts;
         r.split = (u - p.whole) / p.parts;
-        part = (u - p.whole) - r.split * p.parts;
+        r.part = (u - p.whole) - r.split * p.parts;
         u = p.whole + r.split;
     }
     tile_at(p, u, r);
-    r.kb0 = n_kb * part / r.parts;
-    r.kb1 = n_kb * (part + 1) / r.parts;
+    r.kb0 = n_kb * r.part / r.parts;
+    r.kb1 = n_kb * (r.part + 1) / r.parts;
     return true;
+}
+
+// Where the sums of unit k of a split tile are kept, of 2 * n_pairs places.
+__host__ __device__ inline int piece_of(const Schedule& p, const Unit& un, int k, int n_pairs) {
+    if (!p.even) return un.split * un.parts + k;
+    const int pair = un.first + k;  // it has at most two parts of tiles: its first tile's and its last's
+    const int64_t from = static_cast<int64_t>(p.n_units) * pair / n_pairs;
+    return 2 * pair + (from / stages_of(p) == un.split ? 0 : 1);
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

@@ -2,7 +2,7 @@
 //   * tiles are ones the MMA and the copies can take (tokens a multiple of 16, at most
 //     192; a multiple of 8, at most 128, of weight rows per CTA), begin inside the result and cover it once;
 //   * every tile's stages are summed once, by as many units as the tile says, none empty;
-//   * split tiles have numbers of their own that fit the workspace;
+//   * split tiles have numbers, and their units places, of their own that fit the workspace;
 //   * even shares differ by one stage at most.
 // With "n d f" arguments it prints how those sizes are laid out at 76 pairs instead:
 // tokens and rows of a tile, even shares or not, whole tiles, units of the tiles after them.
@@ -11,6 +11,7 @@
 #include <cstdlib>
 #include <map>
 #include <random>
+#include <set>
 #include <utility>
 #include <vector>
 
@@ -45,9 +46,11 @@ bool check(int n, int d, int f, int pairs) {
     struct Tile {
         int parts = 0, split = 0, came = 0;
         std::vector<char> summed;
+        std::map<int, int> places;
     };
     std::map<std::pair<int, int>, Tile> tiles;
     std::map<int, std::pair<int, int>> numbers;
+    std::set<int> pieces;
     const int n_kb = (d + kKB - 1) / kKB, n_pairs = pairs_of(p, pairs);
     CHECK(n_pairs >= 1);
     int least = 1 << 30, most = 0;
@@ -66,6 +69,17 @@ bool check(int n, int d, int f, int pairs) {
                 if (un.parts > 1) CHECK(un.split >= 0 && un.split < pairs && numbers.insert({un.split, {un.f0, un.t0}}).second);
             }
             CHECK(t.parts == un.parts && (un.parts == 1 || t.split == un.split));
+            CHECK(un.part >= 0 && un.part < un.parts);
+            if (un.parts > 1) {
+                // a place of its own, and the same one whichever unit asks
+                const int piece = piece_of(p, un, un.part, n_pairs);
+                CHECK(piece >= 0 && piece < 2 * pairs && pieces.insert(piece).second);
+                for (int k = 0; k < un.parts; ++k) {
+                    const auto [at, fresh] = t.places.insert({k, piece_of(p, un, k, n_pairs)});
+                    CHECK(at->second == piece_of(p, un, k, n_pairs));
+                }
+                CHECK(t.places[un.part] == piece);
+            }
             ++t.came;
             for (int kb = un.kb0; kb < un.kb1; ++kb) {
                 CHECK(!t.summed[kb]);
