@@ -160,6 +160,70 @@ __device__ __forceinline__ bool epi_barrier_any(bool x) {
     return any != 0;
 }
 
+// Quantization of a token, as rows8_quantize does it (see rows8.cu): codes are rint of
+// the exact quotient x / s.
+template <class T>
+__device__ __forceinline__ float2 unpack2f(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2f<__nv_bfloat16>(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 unpack2f<__half>(uint32_t w) {
+    __half2 h;
+    memcpy(&h, &w, 4);
+    return __half22float2(h);
+}
+
+// The largest magnitude of eight values, as float32 bits.
+template <class T>
+__device__ __forceinline__ uint32_t top_of8(const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("max.u16x2 %0, %1, %2;" : "=r"(top) : "r"(top), "r"(w[i] & 0x7fff7fffu));
+    return __float_as_uint(unpack2f<T>(max(top >> 16, top & 0xffffu)).x);
+}
+
+struct TokenScale {
+    float stored;     // the scale; NaN where a value is not finite
+    float up, s, r;   // values and scale are both taken `up` times (2^64 for a subnormal scale), 1/s
+};
+__device__ __forceinline__ TokenScale token_scale(uint32_t top) {
+    TokenScale k;
+    const bool finite = top < 0x7f800000u;
+    k.s = finite ? __fdiv_rn(__uint_as_float(top), 127.0f) : 0.0f;
+    k.stored = finite ? k.s : __uint_as_float(0x7fffffffu);
+    k.up = k.s < 1.17549435e-38f ? 18446744073709551616.0f : 1.0f;
+    k.s = __fmul_rn(k.s, k.up);
+    k.r = k.s > 0.0f ? __frcp_rn(k.s) : 0.0f;
+    return k;
+}
+__device__ __forceinline__ int token_code(float x, const TokenScale& k) {
+    x = __fmul_rn(x, k.up);
+    const float t = fminf(fmaxf(__fmul_rn(x, k.r), -127.0f), 127.0f);
+    float q = rintf(t);
+    if (fabsf(__fsub_rn(t, q)) > 0.5f - 1.0f / 32768.0f) {
+        const float lo = floorf(t), half = __fadd_rn(lo, 0.5f);
+        const float e = __fmaf_rn(-half, k.s, x);
+        q = e > 0.0f ? __fadd_rn(lo, 1.0f) : e < 0.0f ? lo : rintf(half);
+    }
+    return static_cast<int>(q);
+}
+// Eight codes, as bytes.
+template <class T>
+__device__ __forceinline__ uint2 codes_of8(const uint4& v, const TokenScale& k) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t out[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float2 a = unpack2f<T>(w[2 * i]), b = unpack2f<T>(w[2 * i + 1]);
+        const int q0 = token_code(a.x, k), q1 = token_code(a.y, k), q2 = token_code(b.x, k), q3 = token_code(b.y, k);
+        out[i] = __byte_perm(__byte_perm(q0, q1, 0x0040), __byte_perm(q2, q3, 0x0040), 0x5410);
+    }
+    return k.s > 0.0f ? make_uint2(out[0], out[1]) : make_uint2(0u, 0u);
+}
+
 // Every wait is bounded.  The launch before this one is the kernel that writes the
 // tokens' codes and scales; it waits for all work before it and only then lets this
 // one start, so that only what it writes itself has to be waited for here.
@@ -453,6 +517,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; unit_of(p, pair, n_pairs, i, un); ++i) {
 #pragma unroll
             for (int c = 0; c < kCols; ++c) sum[c] = 0;
+            // the scales, on their way while the sums are made
+            const int ch = un.f0 + static_cast<int>(rank) * p.rows;
+            const float sw = row < p.rows && ch + row < p.f ? p.w_scale[ch + row] : 0.0f;
+            if (row < kCols) {
+                const int t = un.t0 + first + 2 * (row & ~15) + (row & 15);
+                reinterpret_cast<float*>(epi_scales[group])[row] = t < p.n ? p.x_scale[t] : 0.0f;
+            }
             for (int c0 = un.kb0; c0 < un.kb1; c0 += kChunk) {
                 // the warps agree on whether a wait ran out, so that all of them pass the
                 // same barriers
@@ -479,15 +550,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     aphase ^= 1u;
                 }
             }
-            const int ch = un.f0 + static_cast<int>(rank) * p.rows;
-            float sw = 0.0f;
-            const auto scales = [&] {
-                if (row < p.rows && ch + row < p.f) sw = p.w_scale[ch + row];
-                if (row < kCols) {
-                    const int t = un.t0 + first + 2 * (row & ~15) + (row & 15);
-                    reinterpret_cast<float*>(epi_scales[group])[row] = t < p.n ? p.x_scale[t] : 0.0f;
-                }
-            };
             // Sixteen tokens' results, from the sums v on.
             const auto finish = [&](int c, const int32_t* v) {
                 const int at = first + 2 * c;
@@ -543,15 +605,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 complete = epi_last != 0;
                 if (complete) {
                     __threadfence();
-                    for (int k = 0; k < un.parts; ++k) {
-                        if (k == un.part) continue;
-                        const int32_t* const from = piece(k);
+                    // the others' pieces, two at a time
+                    for (int k = 1; k < un.parts; k += 2) {
+                        const int32_t* const a = piece(un.part + k < un.parts ? un.part + k : un.part + k - un.parts);
+                        const bool two = k + 1 < un.parts;
+                        const int32_t* const b =
+                            two ? piece(un.part + k + 1 < un.parts ? un.part + k + 1 : un.part + k + 1 - un.parts) : a;
 #pragma unroll
                         for (int c = 0; c < kCols; c += 16) {
                             const int at = first + 2 * c;
                             if (at < p.tok) {
+                                int32_t v[16], w[16];
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) sum[c + i] += __ldcg(from + (at + i) * kMaxRows);
+                                for (int i = 0; i < 16; ++i) {
+                                    v[i] = __ldcg(a + (at + i) * kMaxRows);
+                                    w[i] = two ? __ldcg(b + (at + i) * kMaxRows) : 0;
+                                }
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) sum[c + i] += v[i] + w[i];
                             }
                         }
                     }
@@ -559,14 +630,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 epi_barrier_any(false);  // epi_last may be written again
             }
             if (complete) {
-                scales();
 #pragma unroll
                 for (int c = 0; c < kCols; c += 16)
                     if (first + 2 * c < p.tok) finish(c, sum + c);
             }
             asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");  // the scales may be written again
         }
-        if (leader) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (leader) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         if (failed && lane == 0) {
             atomicOr(p.status, kStatusTimeoutEpilogue);
             aborted = 1;
@@ -614,31 +684,6 @@ struct FewParams {
     int32_t rows;        // rows of a CTA
 };
 
-// As rows8_quantize: rint of the exact quotient x / s (see rows8.cu).
-__device__ __forceinline__ int few_code(float x, float s, float r) {
-    const float t = fminf(fmaxf(__fmul_rn(x, r), -127.0f), 127.0f);
-    float q = rintf(t);
-    if (fabsf(__fsub_rn(t, q)) > 0.5f - 1.0f / 32768.0f) {
-        const float lo = floorf(t), half = __fadd_rn(lo, 0.5f);
-        const float e = __fmaf_rn(-half, s, x);
-        q = e > 0.0f ? __fadd_rn(lo, 1.0f) : e < 0.0f ? lo : rintf(half);
-    }
-    return static_cast<int>(q);
-}
-
-template <class T>
-__device__ __forceinline__ float2 unpack2f(uint32_t w);
-template <>
-__device__ __forceinline__ float2 unpack2f<__nv_bfloat16>(uint32_t w) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-template <>
-__device__ __forceinline__ float2 unpack2f<__half>(uint32_t w) {
-    __half2 h;
-    memcpy(&h, &w, 4);
-    return __half22float2(h);
-}
-
 // The codes of the tokens into shared memory, [kTok][d], by all warps: kFewWarps / kTok of
 // them take a token.
 template <class T, int kTok>
@@ -650,44 +695,18 @@ __device__ __forceinline__ void few_quantize(const FewParams& p, int8_t* codes, 
     const bool some = token < p.n;
     const uint4* const row = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + static_cast<int64_t>(some ? token : 0) * p.d);
     uint32_t top = 0;
-    if (some) {
-        for (int g = first; g < granules; g += kEach * 32) {
-            const uint4 v = row[g];
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack2f<T>(w[i] & 0x7fff7fffu);
-                top = max(top, max(__float_as_uint(f.x), __float_as_uint(f.y)));
-            }
-        }
-    }
+    if (some)
+        for (int g = first; g < granules; g += kEach * 32) top = max(top, top_of8<T>(row[g]));
     top = __reduce_max_sync(~0u, top);
     if (lane == 0) tops[warp] = top;
     __syncthreads();
     if (!some) return;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) top = max(top, tops[token * kEach + i]);
-    const bool finite = top < 0x7f800000u;
-    float s = finite ? __fdiv_rn(__uint_as_float(top), 127.0f) : 0.0f;
-    if (first == 0) scales[token] = finite ? s : __uint_as_float(0x7fffffffu);
-    // a subnormal scale and its values are both taken 2^64 times (exactly)
-    const float up = s < 1.17549435e-38f ? 18446744073709551616.0f : 1.0f;
-    s = __fmul_rn(s, up);
-    const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
-    for (int g = first; g < granules; g += kEach * 32) {
-        const uint4 v = row[g];  // from L1 this time
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t out[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float2 a = unpack2f<T>(w[2 * i]), b = unpack2f<T>(w[2 * i + 1]);
-            const int q0 = few_code(__fmul_rn(a.x, up), s, r), q1 = few_code(__fmul_rn(a.y, up), s, r);
-            const int q2 = few_code(__fmul_rn(b.x, up), s, r), q3 = few_code(__fmul_rn(b.y, up), s, r);
-            const uint32_t c = __byte_perm(__byte_perm(q0, q1, 0x0040), __byte_perm(q2, q3, 0x0040), 0x5410);
-            out[i] = s > 0.0f ? c : 0u;
-        }
-        *reinterpret_cast<uint2*>(codes + static_cast<int64_t>(token) * p.d + 8 * g) = make_uint2(out[0], out[1]);
-    }
+    const TokenScale k = token_scale(top);
+    if (first == 0) scales[token] = k.stored;
+    for (int g = first; g < granules; g += kEach * 32)  // from L1 this time
+        *reinterpret_cast<uint2*>(codes + static_cast<int64_t>(token) * p.d + 8 * g) = codes_of8<T>(row[g], k);
 }
 
 template <class T, int kTok, int kGran>
