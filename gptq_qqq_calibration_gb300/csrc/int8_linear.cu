@@ -47,13 +47,15 @@ using namespace i8;
 
 constexpr int kMaxStages = 12;
 constexpr uint32_t kRing = 208 * 1024;
-// Slots of A in tensor memory hold a stage (64 columns), or half of one where the
-// sums leave room for no more than three of those.
+// Slots of A in tensor memory hold a stage, 64 columns: two of them, or more where the
+// tile has fewer tokens.  (Half stages in twice as many slots cost a wait more each:
+// 447 us against 415 for 8,192 tokens at 4,096 x 11,008.)
 constexpr int kMaxSlots = 6;
-constexpr int kNarrowTok = 64;
-constexpr int kCoarseTok = 128;  // the most tokens of a tile with whole stages in slots
+constexpr uint32_t kSlotCols = kKB / 2;
 constexpr uint32_t kTmemCols = 512;
-static_assert(2 * kMaxTok + 4 * (kKB / 4) <= kTmemCols, "two sums and four halves of a stage");
+static_assert(2 * kMaxTok + 2 * kSlotCols <= kTmemCols, "two sums and two slots");
+// Tiles of up to so many tokens have epilogues of their own, which hold fewer sums.
+constexpr int kNarrowTok = 64, kMiddleTok = 128;
 constexpr int kNumBarriers = 4 * kMaxStages + 2 * kMaxSlots + 5;
 // Sixteen tokens' results on their way out, of an epilogue half (four warps).
 constexpr uint32_t kStagingBytes = 16 * kMaxRows * 2;
@@ -227,13 +229,12 @@ __device__ __forceinline__ uint2 codes_of8(const uint4& v, const TokenScale& k) 
 // Every wait is bounded.  The launch before this one is the kernel that writes the
 // tokens' codes and scales; it waits for all work before it and only then lets this
 // one start, so that only what it writes itself has to be waited for here.
-// kTok: the most tokens of a tile.  Narrow tiles get epilogues that hold fewer sums.
+// kTok: the most tokens of a tile.
 template <class T, int kTok>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int8_pair_kernel(const __grid_constant__ PairParams p) {
-    constexpr bool kHalves = kTok > kCoarseTok;
     constexpr int kCols = kTok / 2;  // tokens of an epilogue thread
-    constexpr uint32_t kSlotCols = kHalves ? kKB / 4 : kKB / 2;
+    static_assert(kCols % 16 == 0, "sixteen tokens at a time");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -266,7 +267,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(xempty_bar(s), 1);
         }
         for (int s = 0; s < p.slots; ++s) {
-            mbar_init(afull_bar(s), kHalves ? 8 : 16);  // four or eight converter warps of each CTA
+            mbar_init(afull_bar(s), 16);  // eight converter warps of each CTA
             mbar_init(aempty_bar(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -372,36 +373,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             umma_f16_pair_ta(acc, a + 16u, at + 4u, idesc, 1u);
                             umma_f16_pair_ta(acc, a + 24u, at + 6u, idesc, 1u);
                         };
-                        const auto turn = [&] {
-                            if (++slot == static_cast<uint32_t>(p.slots)) {
-                                slot = 0;
-                                sphase ^= 1u;
-                            }
-                        };
-                        const uint32_t slot0 = tmem + 2 * p.acc_cols;
                         ok = __all_sync(~0u, mbar_wait(xfull_bar(stage), phase, limit) &&
                                                  mbar_wait(afull_bar(slot), sphase, limit));
                         if (!ok) break;
                         tc_fence_after();
                         if (elect_one()) {
-                            four(slot0 + slot * kSlotCols, b, kb != c0 ? 1u : 0u);
-                            if constexpr (!kHalves) four(slot0 + slot * kSlotCols + 32u, b + half, 1u);
+                            const uint32_t a = tmem + 2 * p.acc_cols + slot * kSlotCols;
+                            four(a, b, kb != c0 ? 1u : 0u);
+                            four(a + 32u, b + half, 1u);
                             tc_commit_pair_mc(aempty_bar(slot), 0x3);
-                            if constexpr (!kHalves) tc_commit_pair_mc(xempty_bar(stage), 0x3);
+                            tc_commit_pair_mc(xempty_bar(stage), 0x3);
                         }
                         __syncwarp();
-                        turn();
-                        if constexpr (kHalves) {
-                            ok = __all_sync(~0u, mbar_wait(afull_bar(slot), sphase, limit));
-                            if (!ok) break;
-                            tc_fence_after();
-                            if (elect_one()) {
-                                four(slot0 + slot * kSlotCols, b + half, 1u);
-                                tc_commit_pair_mc(aempty_bar(slot), 0x3);
-                                tc_commit_pair_mc(xempty_bar(stage), 0x3);
-                            }
-                            __syncwarp();
-                            turn();
+                        if (++slot == static_cast<uint32_t>(p.slots)) {
+                            slot = 0;
+                            sphase ^= 1u;
                         }
                         b += next;
                         if (++stage == p.stages) {
@@ -439,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool some = (warp & 3) * 32 < p.rows, mine = row < p.rows;
         const uint32_t afull0 = mapa_shared(afull_bar(0), 0);
         bool ok = true;
-        int stage = 0, slot = kHalves ? h : 0;
+        int stage = 0, slot = 0;
         uint32_t phase = 0, sphase = 0;
         Unit un;
         for (int i = 0; ok && unit_of(p, pair, n_pairs, i, un); ++i) {
@@ -465,13 +451,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                if (some) tmem_st32(tmem + lanes + 2 * p.acc_cols + static_cast<uint32_t>(slot) * kSlotCols + (kHalves ? 0u : h * 32u), a);
+                if (some) tmem_st32(tmem + lanes + 2 * p.acc_cols + static_cast<uint32_t>(slot) * kSlotCols + h * 32u, a);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster_relaxed(afull0 + 8u * slot);
-                slot += kHalves ? 2 : 1;
-                if (slot >= p.slots) {
-                    slot = kHalves ? h : 0;
+                if (++slot == p.slots) {
+                    slot = 0;
                     sphase ^= 1u;
                 }
                 if (++stage == p.stages) {
@@ -903,7 +888,7 @@ auto few_kernel(int tok, int gran) -> void (*)(FewParams) {
 
 template <class T>
 auto pair_kernel(int tok) -> void (*)(PairParams) {
-    return tok <= kNarrowTok ? int8_pair_kernel<T, kNarrowTok> : tok <= kCoarseTok ? int8_pair_kernel<T, kCoarseTok>
+    return tok <= kNarrowTok ? int8_pair_kernel<T, kNarrowTok> : tok <= kMiddleTok ? int8_pair_kernel<T, kMiddleTok>
                                                                                    : int8_pair_kernel<T, kMaxTok>;
 }
 
@@ -920,7 +905,7 @@ hess_status il_prepare(int dev, int* pairs, int* sms_out) {
                     if (fn)
                         IL_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                     static_cast<int>(kFewSmem)));
-        for (int tok : {kNarrowTok, kCoarseTok, kMaxTok})
+        for (int tok : {kNarrowTok, kMiddleTok, kMaxTok})
             for (auto fn : {pair_kernel<__nv_bfloat16>(tok), pair_kernel<__half>(tok)})
                 IL_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             static_cast<int>(kSmemBytes)));
@@ -1085,8 +1070,7 @@ hess_status forward(int8_linear_ctx* g, const void* X, const int8_t* codes, cons
     const int fit = static_cast<int>(kRing / p.stage_bytes);
     p.stages = fit < kMaxStages ? fit : kMaxStages;
     p.acc_cols = static_cast<uint32_t>((p.tok + 31) / 32 * 32);
-    const bool halves = p.tok > kCoarseTok;
-    const int slots = static_cast<int>((kTmemCols - 2 * p.acc_cols) / (halves ? kKB / 4 : kKB / 2)) & (halves ? ~1 : ~0);
+    const int slots = static_cast<int>((kTmemCols - 2 * p.acc_cols) / kSlotCols);
     p.slots = slots < kMaxSlots ? slots : kMaxSlots;
     p.x_scale = X ? g->x_scale : scale;
     p.w_scale = W_scale;
