@@ -1271,8 +1271,8 @@ static hess_status ff_backward(gated_ff_t g, const void* X, const FfKept* kept, 
     hk::plan_gradients(q, g->pairs, want_x, want_w);
     FF_CHECK(hk::ff_begin(g, s));
     if (kept)
-        FF_TRY(hk::rows8_restore_launch(kept->codes, g->d, kept->scale, n_tokens, g->d, kept->group, g->restored, g->d,
-                                        g->dtype, s));
+        FF_TRY(hk::rows8_restore_launch({kept->codes, g->d, kept->scale, n_tokens, g->d, kept->group, g->restored, g->d},
+                                        {}, g->dtype, true, s));
     FF_CHECK(hk::ff_launch_pairs<hk::kActGrad>(g, p, s));
     const hess_status st = hk::ff_launch_pairs<hk::kGradients>(g, q, s);
     FF_CHECK(hk::ff_end(g, s));

@@ -1085,7 +1085,7 @@ hess_status forward(int8_linear_ctx* g, const void* X, const int8_t* codes, cons
     if (X)
         IL_TRY(rows8_quantize_launch(X, g->d, n, g->d, g->dtype, 0, nullptr, 0, g->wide, g->d, g->x_scale, s));
     else
-        IL_TRY(rows8_restore_launch(codes, g->d, nullptr, n, g->d, 0, g->wide, g->d, HESS_F16, s));
+        IL_TRY(rows8_restore_launch({codes, g->d, nullptr, n, g->d, 0, g->wide, g->d}, {}, HESS_F16, false, s));
     const int pairs = pairs_of(p, g->pairs);
     const hess_status st = il_launch(
         g->dtype == HESS_BF16 ? pair_kernel<__nv_bfloat16>(p.tok) : pair_kernel<__half>(p.tok), p, 2 * pairs, kThreads,
@@ -1263,10 +1263,10 @@ IL_EXPORT hess_status int8_linear_backward(int8_linear_t g, const void* dY, int6
     a.status = g->status;
     a.timeout_ns = g->timeout_ns;
     IL_TRY(g->order.begin(s));
-    if (want_x)
-        IL_TRY(hk::rows8_restore_launch(W_codes, g->d, W_scale, g->f, g->d, 0, g->w_restored, g->d, g->dtype, s));
-    if (want_w)
-        IL_TRY(hk::rows8_restore_launch(X_codes, g->d, X_scale, n, g->d, group, g->x_restored, g->d, g->dtype, s));
+    hk::RestoreRows w{}, x{};
+    if (want_x) w = {W_codes, g->d, W_scale, g->f, g->d, 0, g->w_restored, g->d};
+    if (want_w) x = {X_codes, g->d, X_scale, n, g->d, group, g->x_restored, g->d};
+    IL_TRY(hk::rows8_restore_launch(w, x, g->dtype, true, s));
     const hess_status st = hk::ff_gradients_single(a, s);
     IL_TRY(g->order.end(s));
     return st;

@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kStreamThreads) rows8_stream_kernel(const __gr
     }
 }
 
-struct RestoreParams {
+struct RestoreJob {
     const int8_t* codes;
     const float* scale;  // NULL: 1
     int64_t ldc, n, ldx;
@@ -573,6 +573,11 @@ struct RestoreParams {
     int64_t groups;  // scales of a row
     int32_t items;   // items of kItemSegments segments in a row
     void* x;
+};
+struct RestoreParams {
+    RestoreJob job[2];
+    int64_t first;   // blocks of the first job
+    int32_t early;   // the next kernel may start before this one's inputs are there
 };
 
 // A byte as a float: 2^23 + (q + 128) has the byte q ^ 0x80 at its low end.
@@ -621,12 +626,16 @@ __device__ __forceinline__ void put(T* out, const float (&x)[V]) {
 }
 
 template <class T, int V>
-__global__ void __launch_bounds__(256) rows8_restore_kernel(const __grid_constant__ RestoreParams p) {
+__global__ void __launch_bounds__(256) rows8_restore_kernel(const __grid_constant__ RestoreParams all) {
     constexpr int kRuns = 8 / V;
+    if (all.early) griddep_launch_dependents();
     griddep_wait();
-    griddep_launch_dependents();
+    if (!all.early) griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const bool second = blockIdx.x >= all.first;
+    const RestoreJob& p = all.job[second ? 1 : 0];
+    const int64_t block = second ? blockIdx.x - all.first : blockIdx.x;
+    const int64_t item = block * 8 + (threadIdx.x >> 5);
     const int64_t r = row_of(item, p.items);
     if (r >= p.n) return;
     const int c00 = static_cast<int>(item - r * p.items) * (kItemSegments * kSegment);
@@ -802,14 +811,21 @@ cudaError_t quantize_of(QuantizeParams& p, cudaStream_t s) {
 template <class T>
 cudaError_t restore_of(RestoreParams& p, cudaStream_t s) {
     // 16 bytes of output a lane
-    const int v = run_of(sizeof(T) == 2 ? 8 : 4, p.d, p.x, p.ldx, sizeof(T), p.codes, p.ldc, 1);
+    int v = sizeof(T) == 2 ? 8 : 4;
+    int64_t blocks = 0;
+    for (RestoreJob& j : p.job) {
+        if (j.n == 0) continue;
+        v = run_of(v, j.d, j.x, j.ldx, sizeof(T), j.codes, j.ldc, 1);
+        blocks += (j.n * j.items + 7) / 8;
+    }
+    p.first = (p.job[0].n * p.job[0].items + 7) / 8;
+    if (blocks == 0) return cudaSuccess;
     if constexpr (sizeof(T) == 4)
-        return rows_launch(v == 4 ? rows8_restore_kernel<T, 4> : rows8_restore_kernel<T, 1>, p, (p.n * p.items + 7) / 8,
-                           256, s);
+        return rows_launch(v == 4 ? rows8_restore_kernel<T, 4> : rows8_restore_kernel<T, 1>, p, blocks, 256, s);
     return rows_launch(v == 8   ? rows8_restore_kernel<T, 8>
                        : v == 4 ? rows8_restore_kernel<T, 4>
                                 : rows8_restore_kernel<T, 1>,
-                       p, (p.n * p.items + 7) / 8, 256, s);
+                       p, blocks, 256, s);
 }
 
 hess_status rows_fail(hess_status s, const char* fmt, ...) {
@@ -893,20 +909,25 @@ cudaError_t rows8_quantize_launch(const void* X, int64_t ldx, int64_t n, int64_t
     return quantize_of<float>(p, s);
 }
 
-cudaError_t rows8_restore_launch(const int8_t* codes, int64_t ldc, const float* scale, int64_t n, int64_t d,
-                                 int32_t group, void* X, int64_t ldx, int32_t dtype, cudaStream_t s) {
-    if (n == 0) return cudaSuccess;
+cudaError_t rows8_restore_launch(const RestoreRows& a, const RestoreRows& b, int32_t dtype, bool early, cudaStream_t s) {
     RestoreParams p{};
-    p.codes = codes;
-    p.scale = scale;
-    p.ldc = ldc;
-    p.n = n;
-    p.d = static_cast<int32_t>(d);
-    p.ldx = ldx;
-    p.shift = group ? log2_of(group) : 31;
-    p.groups = group ? (d + group - 1) / group : 1;
-    p.items = static_cast<int32_t>((d + kItemSegments * kSegment - 1) / (kItemSegments * kSegment));
-    p.x = X;
+    const RestoreRows* const rows[2] = {&a, &b};
+    for (int i = 0; i < 2; ++i) {
+        const RestoreRows& r = *rows[i];
+        RestoreJob& j = p.job[i];
+        j.n = r.n;
+        if (r.n == 0) continue;
+        j.codes = r.codes;
+        j.scale = r.scale;
+        j.ldc = r.ldc;
+        j.d = static_cast<int32_t>(r.d);
+        j.ldx = r.ldx;
+        j.shift = r.group ? log2_of(r.group) : 31;
+        j.groups = r.group ? (r.d + r.group - 1) / r.group : 1;
+        j.items = static_cast<int32_t>((r.d + kItemSegments * kSegment - 1) / (kItemSegments * kSegment));
+        j.x = r.x;
+    }
+    p.early = early ? 1 : 0;
     if (dtype == HESS_BF16) return restore_of<__nv_bfloat16>(p, s);
     if (dtype == HESS_F16) return restore_of<__half>(p, s);
     return restore_of<float>(p, s);
@@ -953,7 +974,7 @@ ROWS_EXPORT hess_status rows8_restore(const int8_t* codes, int64_t ldc, const fl
     if (hk::meet(X_out, x_bytes, codes, (n_rows - 1) * ldc + d))
         return rows_fail(HESS_ERR_INVALID, "X_out overlaps codes");
     if (hk::meet(X_out, x_bytes, scale, scales)) return rows_fail(HESS_ERR_INVALID, "X_out overlaps scale");
-    const cudaError_t e = hk::rows8_restore_launch(codes, ldc, scale, n_rows, d, group, X_out, ldx, dtype,
+    const cudaError_t e = hk::rows8_restore_launch({codes, ldc, scale, n_rows, d, group, X_out, ldx}, {}, dtype, false,
                                                    static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return rows_fail(HESS_ERR_CUDA, "rows8_restore: %s", cudaGetErrorString(e));
     return HESS_OK;
