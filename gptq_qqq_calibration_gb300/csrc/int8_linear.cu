@@ -653,7 +653,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // and token, one warp reduction a row and token (the more granules, the fewer), integer
 // adds in shared memory across warps: exact and independent of the order.
 
-constexpr int64_t kFewTokens = 8;
+constexpr int64_t kFewTokens = 2;
 constexpr int kFewThreads = 512, kFewWarps = kFewThreads / 32;
 constexpr int kFewAhead = 256 * 1024;  // bytes a CTA asks into L2
 
@@ -787,6 +787,149 @@ __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const __grid_c
         if (t < p.n)
             static_cast<T*>(p.out)[static_cast<int64_t>(t) * p.f + row0 + r] =
                 rounded<T>(__fmul_rn(__int2float_rn(sums[r * kTok + t]), __fmul_rn(scales[t], p.w_scale[row0 + r])));
+    }
+}
+
+// ------------------------------------------------------- up to 16 tokens
+//
+// Bound by reading the weights once, too, but with more products than dp4a has time for:
+// warp-level MMAs (m16n8k16, float16, float32 sums) on weights that go from memory
+// straight into registers.  A thread's 16 bytes of a row serve four MMAs: the
+// contraction's order within 64 columns is free, so it is the bytes' order (thread t of
+// a row has columns 16 t .. 16 t + 15; MMA i takes bytes 4 i .. 4 i + 3), and the tokens'
+// values are read in the same order.
+//
+// All CTAs, two per SM, take the same number of weight rows, kTilesM x 16 of them at a
+// time, and a CTA's warps share the columns, 64 at a time in turn: so every weight and every
+// token's value is read by one warp of the CTA, once, and needs no place in shared
+// memory.  A block's weights are fetched two to six blocks ahead, its tokens one.
+
+constexpr int64_t kMidTokens = 16;
+constexpr int kMidThreads = 256, kMidWarps = kMidThreads / 32;
+constexpr int kMidFlush = 1024 / 64;  // blocks whose sums stay below 2^24
+
+struct MidParams {
+    const __half* x;  // [n, d] whole numbers
+    const float *x_scale, *w_scale;
+    const int8_t* w;
+    void* out;
+    int32_t n, d, f, bf16;
+    int32_t rows;  // of a CTA
+};
+
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int kTilesM, int kTilesN>
+__global__ void __launch_bounds__(kMidThreads, 2) int8_mid_kernel(const __grid_constant__ MidParams p) {
+    constexpr int kPitch = kTilesM * 16 + 4;  // of a token's sums: no bank conflicts
+    __shared__ int32_t sums[kMidWarps][kTilesN * 8][kPitch];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int row0 = blockIdx.x * p.rows;
+    const int row1 = row0 + p.rows < p.f ? row0 + p.rows : p.f;
+    const int blocks = (p.d + 63) / 64;
+    bool waited = false;
+    for (int r0 = row0; r0 < row1; r0 += kTilesM * 16) {
+        constexpr int kDepth = kTilesM <= 1 ? 6 : 2;
+        uint4 a[kDepth][kTilesM][2], x[2][kTilesN][2];
+        // the i-th block of this warp: pairs of neighbours, so that a line of memory is read at once
+        const auto block = [&](int i) { return (i >> 1) * (2 * kMidWarps) + 2 * warp + (i & 1); };
+        const auto fetch_w = [&](int kb, uint4 (&to)[kTilesM][2]) {
+            const int k = kb * 64 + t * 16;
+#pragma unroll
+            for (int m = 0; m < kTilesM; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = r0 + m * 16 + h * 8 + g;
+                    to[m][h] = kb < blocks && k < p.d && row < row1
+                                   ? __ldcg(reinterpret_cast<const uint4*>(p.w + static_cast<int64_t>(row) * p.d + k))
+                                   : make_uint4(0, 0, 0, 0);
+                }
+        };
+        const auto fetch_x = [&](int kb, uint4 (&to)[kTilesN][2]) {
+            const int k = kb * 64 + t * 16;
+#pragma unroll
+            for (int c = 0; c < kTilesN; ++c) {
+                const int token = c * 8 + g;
+                to[c][0] = to[c][1] = make_uint4(0, 0, 0, 0);
+                if (token < p.n && kb < blocks && k < p.d) {
+                    const uint4* const src = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(token) * p.d + k);
+                    to[c][0] = __ldcg(src);
+                    to[c][1] = __ldcg(src + 1);
+                }
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kDepth; ++i) fetch_w(block(i), a[i]);  // (complete: see int8_pair_kernel)
+        for (int i = lane; i < kTilesN * 8 * kPitch; i += 32) (&sums[warp][0][0])[i] = 0;
+        __syncwarp();
+        if (!waited) {
+            griddep_wait();
+            griddep_launch_dependents();
+            waited = true;
+        }
+        fetch_x(block(0), x[0]);
+        float acc[kTilesM][kTilesN][4] = {};
+        int held = 0;
+        const auto settle = [&] {
+#pragma unroll
+            for (int m = 0; m < kTilesM; ++m)
+#pragma unroll
+                for (int c = 0; c < kTilesN; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sums[warp][c * 8 + 2 * t + (e & 1)][m * 16 + (e >> 1) * 8 + g] += __float2int_rn(acc[m][c][e]);
+                        acc[m][c][e] = 0.0f;
+                    }
+            held = 0;
+        };
+        const auto work = [&](int at, uint4 (&w)[kTilesM][2], const uint4 (&b)[kTilesN][2], uint4 (&next)[kTilesN][2]) {
+            fetch_x(block(at + 1), next);
+#pragma unroll
+            for (int m = 0; m < kTilesM; ++m) {
+                const uint32_t top[4] = {w[m][0].x, w[m][0].y, w[m][0].z, w[m][0].w};
+                const uint32_t low[4] = {w[m][1].x, w[m][1].y, w[m][1].z, w[m][1].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t a0, a1, a2, a3;
+                    widen4(top[i], a0, a2);
+                    widen4(low[i], a1, a3);
+#pragma unroll
+                    for (int c = 0; c < kTilesN; ++c) {
+                        const uint4 v = b[c][i >> 1];
+                        mma_f16_16816(acc[m][c], a0, a1, a2, a3, i & 1 ? v.z : v.x, i & 1 ? v.w : v.y);
+                    }
+                }
+            }
+            fetch_w(block(at + kDepth), w);
+            if (++held == kMidFlush) settle();
+        };
+        for (int at = 0; block(at) < blocks; at += kDepth) {
+#pragma unroll
+            for (int i = 0; i < kDepth; ++i)
+                if (i == 0 || block(at + i) < blocks) work(at + i, a[i], x[i & 1], x[(i + 1) & 1]);
+        }
+        settle();
+        __syncthreads();
+        const int rows = row1 - r0 < kTilesM * 16 ? row1 - r0 : kTilesM * 16;
+        for (int i = threadIdx.x; i < rows * p.n; i += kMidThreads) {
+            const int c = i / rows, r = i - c * rows;
+            int32_t total = 0;
+#pragma unroll
+            for (int w = 0; w < kMidWarps; ++w) total += sums[w][c][r];
+            const float y = __fmul_rn(__int2float_rn(total), __fmul_rn(p.x_scale[c], p.w_scale[r0 + r]));
+            const int64_t at = static_cast<int64_t>(c) * p.f + r0 + r;
+            if (p.bf16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
+            else static_cast<__half*>(p.out)[at] = __float2half_rn(y);
+        }
+        __syncthreads();  // the sums may be written again
     }
 }
 
@@ -1055,11 +1198,53 @@ hess_status forward_few(const int8_linear_ctx* g, const void* X, const int8_t* c
     return il_launch(kernel, p, grid, kFewThreads, smem, s);
 }
 
+// The tokens' codes as float16 whole numbers, into the workspace.
+hess_status widen_tokens(const int8_linear_ctx* g, const void* X, const int8_t* codes, int64_t n, cudaStream_t s) {
+    if (X)
+        IL_TRY(rows8_quantize_launch(X, g->d, n, g->d, g->dtype, 0, nullptr, 0, g->wide, g->d, g->x_scale, s));
+    else
+        IL_TRY(rows8_restore_launch({codes, g->d, nullptr, n, g->d, 0, g->wide, g->d}, {}, HESS_F16, false, s));
+    return HESS_OK;
+}
+
+// Row tiles that a warp's registers hold.
+constexpr int64_t kMidTiles = 3;
+
+template <int kTilesN>
+auto mid_kernel(int tiles_m) -> void (*)(MidParams) {
+    return tiles_m == 1 ? int8_mid_kernel<1, kTilesN> : tiles_m == 2 ? int8_mid_kernel<2, kTilesN> : int8_mid_kernel<3, kTilesN>;
+}
+
+hess_status forward_mid(int8_linear_ctx* g, const void* X, const int8_t* codes, const float* scale, int64_t n,
+                        const int8_t* W, const float* W_scale, void* Y, cudaStream_t s) {
+    MidParams p{};
+    p.x = reinterpret_cast<const __half*>(g->wide);
+    p.x_scale = X ? g->x_scale : scale;
+    p.w_scale = W_scale;
+    p.w = W;
+    p.out = Y;
+    p.n = static_cast<int32_t>(n);
+    p.d = static_cast<int32_t>(g->d);
+    p.f = static_cast<int32_t>(g->f);
+    p.bf16 = g->dtype == HESS_BF16;
+    const int64_t ctas = g->f < 2 * g->sms ? g->f : 2 * g->sms;
+    p.rows = static_cast<int32_t>(ceil_div(g->f, ctas));
+    const int64_t tiles = ceil_div(p.rows, 16), turns = ceil_div(tiles, kMidTiles);
+    const int tiles_m = static_cast<int>(ceil_div(tiles, turns));
+    const auto kernel = n <= 8 ? mid_kernel<1>(tiles_m) : mid_kernel<2>(tiles_m);
+    IL_TRY(g->order.begin(s));
+    IL_CHECK(widen_tokens(g, X, codes, n, s));
+    const hess_status st = il_launch(kernel, p, ceil_div(g->f, p.rows), kMidThreads, 0, s);
+    IL_TRY(g->order.end(s));
+    return st;
+}
+
 // X in 16 bits, or codes and scale.
 hess_status forward(int8_linear_ctx* g, const void* X, const int8_t* codes, const float* scale, int64_t n,
                     const int8_t* W, const float* W_scale, void* Y, cudaStream_t s) {
     IL_TRY(ensure_context());
     if (is_few(n, g->d)) return forward_few(g, X, codes, scale, n, W, W_scale, Y, s);
+    if (n <= kMidTokens) return forward_mid(g, X, codes, scale, n, W, W_scale, Y, s);
     PairParams p{};
     p.n = static_cast<int32_t>(n);
     p.d = static_cast<int32_t>(g->d);
@@ -1082,10 +1267,7 @@ hess_status forward(int8_linear_ctx* g, const void* X, const int8_t* codes, cons
     IL_CHECK(il_encode(&p.w, W, true, g->f, g->d, p.rows));
     IL_CHECK(il_encode_out(&p.y, Y, g->dtype, n, g->f, p.rows));
     IL_TRY(g->order.begin(s));
-    if (X)
-        IL_TRY(rows8_quantize_launch(X, g->d, n, g->d, g->dtype, 0, nullptr, 0, g->wide, g->d, g->x_scale, s));
-    else
-        IL_TRY(rows8_restore_launch({codes, g->d, nullptr, n, g->d, 0, g->wide, g->d}, {}, HESS_F16, false, s));
+    IL_CHECK(widen_tokens(g, X, codes, n, s));
     const int pairs = pairs_of(p, g->pairs);
     const hess_status st = il_launch(
         g->dtype == HESS_BF16 ? pair_kernel<__nv_bfloat16>(p.tok) : pair_kernel<__half>(p.tok), p, 2 * pairs, kThreads,
