@@ -108,12 +108,12 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int pairs_of(const Schedule& p, int pairs) { return p.n_units < pairs ? p.n_units : pairs; }
 
 // Tiles and splits for n tokens.  In SM cycles, a stage costs what bounds it: the MMAs
-// (4 a token) and their issue (kIssue), the weights' way from memory (16 bytes a row
-// over 3 cycles at 24 bytes a cycle and SM) or the stage's way from L2 at 40 bytes a cycle.
-// A turn of units costs kTurn more, split tiles kSplit and 6 a token for their sums' way to
-// memory and back.
+// (4 a token), their issue and what it waits for (kIssue), or the weights' way from memory
+// (16 bytes a row over 3 cycles at 24 bytes a cycle and SM).  A turn of units costs
+// kTurn more; a tile in pieces kSplit for meeting, and 32 a token for each piece but one that
+// the last pair there reads.
 inline void plan(Schedule& p, int64_t pairs) {
-    constexpr int64_t kIssue = 600, kTurn = 700, kSplit = 3000;
+    constexpr int64_t kIssue = 800, kTurn = 700, kSplit = 9000;
     const int64_t n_kb = ceil_div(p.d, kKB);
     p.tiles_t = static_cast<int32_t>(ceil_div(p.n, kMaxTok));
     p.tok = static_cast<int32_t>(ceil_div(ceil_div(p.n, p.tiles_t), 16) * 16);
@@ -139,18 +139,18 @@ inline void plan(Schedule& p, int64_t pairs) {
         int64_t stage = 4 * p.tok;
         if (stage < kIssue) stage = kIssue;
         if (stage < 16 * rows / 3) stage = 16 * rows / 3;
-        if (stage < (kKB * rows + kKB * p.tok) / 40) stage = (kKB * rows + kKB * p.tok) / 40;
         for (int64_t s = 1; s <= kMaxParts && s <= n_kb && (s == 1 || rest * s <= pairs); ++s) {
             int64_t cost = turns * (n_kb * stage + kTurn);
             if (rest > 0) cost += ceil_div(n_kb, s) * stage + kTurn;
-            if (s > 1) cost += kSplit + 6 * p.tok;
+            if (s > 1) cost += kSplit + 32 * p.tok * (s - 1);
             const int64_t whole = s > 1 ? tiles - rest : tiles;
             take(cost, rows, tiles_f, false, whole, s, s > 1 ? whole + rest * s : tiles);
             if (rest == 0) break;
         }
         if (tiles <= pairs) {
             const int64_t share = ceil_div(tiles * n_kb, pairs);
-            take(share * stage + 2 * kTurn + kSplit + 6 * p.tok, rows, tiles_f, true, 0, 1, tiles * n_kb);
+            const int64_t parts = ceil_div(n_kb, share) + 1;
+            take(share * stage + 2 * kTurn + kSplit + 32 * p.tok * (parts - 1), rows, tiles_f, true, 0, 1, tiles * n_kb);
         }
     }
 }
