@@ -6,8 +6,8 @@
 // so its maximum is a few shuffles; a whole row is held by one CTA, in registers or, where
 // there are many rows, in shared memory, and its maximum meets in shared memory, so
 // that the values are read once either way.  A lane's columns come in runs of V side by
-// side, 32 V columns apart: V is 16 or 8 where rows are multiples of 16 bytes, 4 where they
-// are of half that, else 1, which keeps a warp's accesses contiguous at any alignment.
+// side, 32 V columns apart: V is 16 or 8 where rows are multiples of 16 bytes, 4 or 2 where
+// they are of less, else 1, which keeps a warp's accesses contiguous at any alignment.
 //
 // The whole number nearest to the exact quotient x / s is wanted, and the memory's pace
 // leaves some ten instructions a value.  A multiply-add that adds 1.5 * 2^23 rounds a
@@ -251,6 +251,8 @@ __device__ __forceinline__ void encode(const Raw<T, V>& raw, int r, const Scale&
     }
     if constexpr (V == 1) {
         out[0] = a[0];
+    } else if constexpr (V == 2) {
+        out[0] = __byte_perm(a[0], a[1], 0x0040);
     } else {
 #pragma unroll
         for (int i = 0; i < V / 4; ++i) out[i] = pack_bytes(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
@@ -279,6 +281,9 @@ __device__ __forceinline__ void store(int8_t* codes, __half* wide, int c, const 
     if constexpr (V == 1) {
         if (codes) codes[c] = static_cast<int8_t>(q[0]);
         else wide[c] = __int2half_rn(static_cast<int8_t>(q[0]));
+    } else if constexpr (V == 2) {
+        if (codes) *reinterpret_cast<unsigned short*>(codes + c) = static_cast<unsigned short>(q[0]);
+        else *reinterpret_cast<uint32_t*>(wide + c) = wide4(q[0]).x;
     } else if constexpr (V == 4) {
         if (codes) *reinterpret_cast<uint32_t*>(codes + c) = q[0];
         else *reinterpret_cast<uint2*>(wide + c) = wide4(q[0]);
@@ -608,6 +613,8 @@ __device__ __forceinline__ void put(T* out, const float (&x)[V]) {
     if constexpr (sizeof(T) == 4) {
         if constexpr (V == 1) {
             *reinterpret_cast<float*>(out) = x[0];
+        } else if constexpr (V == 2) {
+            *reinterpret_cast<float2*>(out) = make_float2(x[0], x[1]);
         } else {
 #pragma unroll
             for (int i = 0; i < V; i += 4)
@@ -620,7 +627,8 @@ __device__ __forceinline__ void put(T* out, const float (&x)[V]) {
         uint32_t w[V / 2];
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) w[i] = two_of<T>(x[2 * i], x[2 * i + 1]);
-        if constexpr (V == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+        if constexpr (V == 2) *reinterpret_cast<uint32_t*>(out) = w[0];
+        else if constexpr (V == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
         else *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
@@ -633,7 +641,7 @@ __global__ void __launch_bounds__(256) rows8_restore_kernel(const __grid_constan
     if (!all.early) griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
     const bool second = blockIdx.x >= all.first;
-    const RestoreJob& p = all.job[second ? 1 : 0];
+    const RestoreJob p = second ? all.job[1] : all.job[0];
     const int64_t block = second ? blockIdx.x - all.first : blockIdx.x;
     const int64_t item = block * 8 + (threadIdx.x >> 5);
     const int64_t r = row_of(item, p.items);
@@ -655,6 +663,8 @@ __global__ void __launch_bounds__(256) rows8_restore_kernel(const __grid_constan
                 w[i][k][0] = v.x, w[i][k][1] = v.y;
             } else if constexpr (V == 4) {
                 w[i][k][0] = in ? __ldcs(reinterpret_cast<const uint32_t*>(codes + c)) : 0u;
+            } else if constexpr (V == 2) {
+                w[i][k][0] = in ? __ldcs(reinterpret_cast<const unsigned short*>(codes + c)) : 0u;
             } else {
                 w[i][k][0] = in ? __ldcs(reinterpret_cast<const unsigned char*>(codes + c)) : 0u;
             }
@@ -790,8 +800,8 @@ cudaError_t quantize_as(QuantizeParams& p, cudaStream_t s) {
 
 // The widest run that rows of both matrices allow, and that gives every lane one.
 int run_of(int most, int32_t d, const void* x, int64_t x_row, int x_item, const void* q, int64_t q_row, int q_item) {
-    for (int v : {16, 8, 4})
-        if (v <= most && (v == 4 || 32 * v <= d) && d % v == 0 && aligned(x, x_row * x_item, v * x_item < 16 ? v * x_item : 16) &&
+    for (int v : {16, 8, 4, 2})
+        if (v <= most && (v <= 4 || 32 * v <= d) && d % v == 0 && aligned(x, x_row * x_item, v * x_item < 16 ? v * x_item : 16) &&
             aligned(q, q_row * q_item, v * q_item < 16 ? v * q_item : 16))
             return v;
     return 1;
@@ -805,7 +815,10 @@ cudaError_t quantize_of(QuantizeParams& p, cudaStream_t s) {
     if constexpr (sizeof(T) == 2) {
         if (v == 16) return quantize_as<T, 16>(p, s);
     }
-    return v == 8 ? quantize_as<T, 8>(p, s) : v == 4 ? quantize_as<T, 4>(p, s) : quantize_as<T, 1>(p, s);
+    return v == 8   ? quantize_as<T, 8>(p, s)
+           : v == 4 ? quantize_as<T, 4>(p, s)
+           : v == 2 ? quantize_as<T, 2>(p, s)
+                    : quantize_as<T, 1>(p, s);
 }
 
 template <class T>
@@ -821,9 +834,13 @@ cudaError_t restore_of(RestoreParams& p, cudaStream_t s) {
     p.first = (p.job[0].n * p.job[0].items + 7) / 8;
     if (blocks == 0) return cudaSuccess;
     if constexpr (sizeof(T) == 4)
-        return rows_launch(v == 4 ? rows8_restore_kernel<T, 4> : rows8_restore_kernel<T, 1>, p, blocks, 256, s);
+        return rows_launch(v == 4   ? rows8_restore_kernel<T, 4>
+                           : v == 2 ? rows8_restore_kernel<T, 2>
+                                    : rows8_restore_kernel<T, 1>,
+                           p, blocks, 256, s);
     return rows_launch(v == 8   ? rows8_restore_kernel<T, 8>
                        : v == 4 ? rows8_restore_kernel<T, 4>
+                       : v == 2 ? rows8_restore_kernel<T, 2>
                                 : rows8_restore_kernel<T, 1>,
                        p, blocks, 256, s);
 }

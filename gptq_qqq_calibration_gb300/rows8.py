@@ -59,9 +59,11 @@ def _written(*tensors) -> None:
 def _rows2d(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
     """(rows, d, row stride in elements) of a [..., d] tensor whose rows are
     evenly spaced and contiguous inside."""
+    shape = t.shape
+    if len(shape) == 2 and t.is_cuda and t.is_contiguous() and shape[1]:
+        return shape[0], shape[1], shape[1]
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    shape = t.shape
     if not shape or shape[-1] == 0:
         raise ValueError(f"{name} must have at least one column")
     d = shape[-1]
@@ -89,7 +91,8 @@ def _groups(d: int, group: int) -> int:
 
 
 def _scale(t: torch.Tensor, n: int, d: int, group: int, name: str) -> int:
-    if t.dtype is not torch.float32 or not t.is_cuda or not t.is_contiguous() or t.numel() != n * _groups(d, group):
+    if t.dtype is not torch.float32 or not t.is_cuda or not t.is_contiguous() or \
+            t.numel() != (n * _groups(d, group) if group else n):
         raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of {n} x {_groups(d, group)} scales")
     return t.data_ptr()
 
@@ -153,16 +156,18 @@ def quantize_rows(X: torch.Tensor, group: int = 0, stream=None) -> Rows8:
     """8-bit rows of X [..., d]: one scale per row (group 0), or per ``group``
     (32, 64, 128 or 256) consecutive columns of a row."""
     n, d, ldx = _float_rows(X, "X")
-    shape = X.shape
-    codes = _empty(shape, torch.int8, X, stream)
-    scale = _empty((*shape[:-1], _groups(d, group)) if group else shape[:-1], torch.float32, X, stream)
-    dev = X.get_device()
-    _on(dev, _lib.load().rows8_quantize,
-        (X.data_ptr(), ldx, n, d, _DTYPES[X.dtype], int(group), codes.data_ptr(), d, scale.data_ptr(),
-         _stream(stream, dev)))
-    if stream is not None:
+    shape, device = X.shape, X.device
+    wide = (*shape[:-1], _groups(d, group)) if group else shape[:-1]
+    if stream is None:
+        codes = torch.empty(shape, dtype=torch.int8, device=device)
+        scale = torch.empty(wide, dtype=torch.float32, device=device)
+    else:
+        codes, scale = _empty(shape, torch.int8, X, stream), _empty(wide, torch.float32, X, stream)
         _used_on(stream, X)
-    return Rows8(codes, scale, int(group))
+    dev = device.index
+    _on(dev, _lib.load().rows8_quantize,
+        (X.data_ptr(), ldx, n, d, _DTYPES[X.dtype], group, codes.data_ptr(), d, scale.data_ptr(), _stream(stream, dev)))
+    return Rows8(codes, scale, group)
 
 
 def restore_rows(rows: Rows8, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
@@ -176,10 +181,12 @@ def restore_rows(rows: Rows8, dtype: torch.dtype = torch.bfloat16, out: Optional
     codes, scale, group = rows
     n, d, ldc = _code_rows(codes, "codes")
     dev = _same_device(codes, scale)
-    s = _scale(scale, n, d, group, "scale")
-    out = _empty(codes.shape, dtype, codes, stream)
-    _on(dev, _lib.load().rows8_restore,
-        (codes.data_ptr(), ldc, s, n, d, int(group), out.data_ptr(), d, _DTYPES[dtype], _stream(stream, dev)))
-    if stream is not None:
+    from_scale = _scale(scale, n, d, group, "scale")
+    if stream is None:
+        out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+    else:
+        out = _empty(codes.shape, dtype, codes, stream)
         _used_on(stream, codes, scale)
+    _on(dev, _lib.load().rows8_restore,
+        (codes.data_ptr(), ldc, from_scale, n, d, group, out.data_ptr(), d, _DTYPES[dtype], _stream(stream, dev)))
     return out
