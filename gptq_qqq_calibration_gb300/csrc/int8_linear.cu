@@ -296,8 +296,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             int stage = 0;
             uint32_t phase = 0;
-            Unit un;
-            for (int i = 0; ok && unit_of(p, pair, n_pairs, i, un); ++i) {
+            for (int u = pair; ok && u < p.n_units; u += n_pairs) {
+                const Unit un = unit_at(p, u);
                 const int row = un.f0 + static_cast<int>(rank) * p.rows;
                 for (int kb = un.kb0; kb < un.kb1; ++kb) {
                     if (!mbar_wait(wempty_bar(stage), phase ^ 1u, limit)) {
@@ -323,8 +323,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int stage = 0;
             uint32_t phase = 0;
             const uint32_t box = static_cast<uint32_t>(p.tok) * 64u;  // tok / 2 rows of 128 bytes
-            Unit un;
-            for (int i = 0; ok && unit_of(p, pair, n_pairs, i, un); ++i) {
+            for (int u = pair; ok && u < p.n_units; u += n_pairs) {
+                const Unit un = unit_at(p, u);
                 const int row = un.t0 + static_cast<int>(rank) * (p.tok / 2);
                 for (int kb = un.kb0; kb < un.kb1; ++kb) {
                     if (!mbar_wait(xempty_bar(stage), phase ^ 1u, limit)) {
@@ -359,8 +359,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint64_t first = smem_desc_sw128(base + p.w_bytes, 16u, 1024u);
             const uint64_t next = p.stage_bytes >> 4, half = static_cast<uint64_t>(p.tok) * 4u;
             uint64_t b = first;
-            Unit un;
-            for (int i = 0; ok && unit_of(p, pair, n_pairs, i, un); ++i) {
+            for (int u = pair; ok && u < p.n_units; u += n_pairs) {
+                const Unit un = unit_at(p, u);
                 for (int c0 = un.kb0; ok && c0 < un.kb1; c0 += kChunk) {
                     ok = __all_sync(~0u, mbar_wait(acce_bar(ab), aphase ^ 1u, limit));
                     if (!ok) break;
@@ -427,8 +427,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         int stage = 0, slot = 0;
         uint32_t phase = 0, sphase = 0;
-        Unit un;
-        for (int i = 0; ok && unit_of(p, pair, n_pairs, i, un); ++i) {
+        for (int u = pair; ok && u < p.n_units; u += n_pairs) {
+            const Unit un = unit_at(p, u);
             for (int kb = un.kb0; kb < un.kb1; ++kb) {
                 if (!mbar_wait(wfull_bar(stage), phase, limit)) {
                     ok = false;
@@ -498,8 +498,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int ab = 0;
         uint32_t aphase = 0;
         int32_t sum[kCols];
-        Unit un;
-        for (int i = 0; unit_of(p, pair, n_pairs, i, un); ++i) {
+        for (int u = pair; u < p.n_units; u += n_pairs) {
+            const Unit un = unit_at(p, u);
 #pragma unroll
             for (int c = 0; c < kCols; ++c) sum[c] = 0;
             // the scales, on their way while the sums are made
@@ -565,7 +565,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (un.parts > 1) {
                 // pieces: [token][row], so that a warp moves 128 bytes at a time
                 const auto piece = [&](int k) {
-                    return p.pieces + (2 * static_cast<int64_t>(piece_of(p, un, k, n_pairs)) + rank) * kPieceInts + row;
+                    return p.pieces + (2 * static_cast<int64_t>(un.split * un.parts + k) + rank) * kPieceInts + row;
                 };
                 if (!failed) {
                     int32_t* const to = piece(un.part);
@@ -1084,7 +1084,7 @@ struct int8_linear_ctx {
     void* memory = nullptr;  // holds what follows
     uint16_t* wide = nullptr;       // [tokens, d] float16 codes
     float* x_scale = nullptr;       // [tokens]
-    int32_t* pieces = nullptr;      // two per pair
+    int32_t* pieces = nullptr;      // one per pair
     void* w_restored = nullptr;     // [f, d]
     void* x_restored = nullptr;     // [train_tokens, d]
     float* ff_pieces = nullptr;
@@ -1268,7 +1268,7 @@ hess_status forward(int8_linear_ctx* g, const void* X, const int8_t* codes, cons
     IL_CHECK(il_encode_out(&p.y, Y, g->dtype, n, g->f, p.rows));
     IL_TRY(g->order.begin(s));
     IL_CHECK(widen_tokens(g, X, codes, n, s));
-    const int pairs = pairs_of(p, g->pairs);
+    const int pairs = p.n_units < g->pairs ? p.n_units : g->pairs;
     const hess_status st = il_launch(
         g->dtype == HESS_BF16 ? pair_kernel<__nv_bfloat16>(p.tok) : pair_kernel<__half>(p.tok), p, 2 * pairs, kThreads,
         kSmemBytes, s);
@@ -1319,7 +1319,7 @@ IL_EXPORT hess_status int8_linear_create(int64_t d, int64_t f, int64_t tokens, i
     g->dtype = dtype;
     const auto round = [](size_t b) { return (b + 255) / 256 * 256; };
     const size_t wide = round(static_cast<size_t>(tokens) * d * 2), x_scale = round(static_cast<size_t>(tokens) * 4);
-    const size_t pieces = tokens > 0 ? static_cast<size_t>(pairs) * 2 * 2 * hk::kPieceInts * 4 : 0;
+    const size_t pieces = tokens > 0 ? static_cast<size_t>(pairs) * 2 * hk::kPieceInts * 4 : 0;
     const size_t w_restored = train_tokens > 0 ? round(static_cast<size_t>(f) * d * 2) : 0;
     const size_t x_restored = round(static_cast<size_t>(train_tokens) * d * 2);
     const size_t ff_pieces = static_cast<size_t>(ff_pairs) * hk::kFfPieceBytes;

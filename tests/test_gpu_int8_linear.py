@@ -22,11 +22,12 @@ pytestmark = pytest.mark.gpu
 # tokens, d, f: what the layout has at 76 pairs ("split": tiles in several pieces, "whole": whole
 # tiles before them, "rows": fewer than 128 weight rows per CTA, "tokens": several tiles of tokens)
 LAYOUTS = {
-    (9, 4096, 1400): "split rows",
-    (37, 11008, 4096): "split rows",
-    (37, 4096, 11008): "rows",
-    (300, 4112, 520): "split rows tokens",
-    (1000, 4096, 4096): "split whole tokens",
+    (17, 4096, 1400): "split rows",
+    (37, 11008, 4096): "split",
+    (24, 4096, 11008): "",
+    (20, 65536, 2048): "split",
+    (300, 40000, 2056): "split rows tokens",
+    (1000, 8192, 4096): "split whole tokens",
     (1500, 1040, 2048): "tokens",
 }
 
