@@ -19,8 +19,13 @@
 // memory: two 192-column sums, so that one is drained under the other's products, and
 // two slots of 128 steps of A (more where the tile has fewer tokens).
 //
-// Few tokens (the weights no longer pay for the trip through tensor memory): one pass
-// over the weights with dp4a, the tokens' codes in registers.
+// Many tokens are bound by the tensor pipe: 8,192 at 4,096 x 11,008 take 415 us, 1,780
+// TFLOP/s and 0.94 of the burst rate of a library's 16-bit GEMM.  Up to some 600 the bytes of the
+// weights bound it: 37 tokens there take 19.7 us for 7.0 of bytes, of which the kernel in
+// front, the start and the last tile's way out are some ten; 512 take 40 us.
+//
+// Up to 16 tokens do not pay for the trip through tensor memory: one or two take one pass
+// over the weights with dp4a, three to sixteen one with warp-level MMAs.
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -652,8 +657,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // cover a row, and the CTA's warps cover `rp` rows side by side.  Four dp4a a granule
 // and token, one warp reduction a row and token (the more granules, the fewer), integer
 // adds in shared memory across warps: exact and independent of the order.
+// One token at 4,096 x 11,008: 11.0 us, 4.1 TB/s; at 8,192 x 28,672: 47.7 us, 4.9 TB/s.
 
-constexpr int64_t kFewTokens = 2;
 constexpr int kFewThreads = 512, kFewWarps = kFewThreads / 32;
 constexpr int kFewAhead = 256 * 1024;  // bytes a CTA asks into L2
 
@@ -803,6 +808,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const __grid_c
 // time, and a CTA's warps share the columns, 64 at a time in turn: so every weight and every
 // token's value is read by one warp of the CTA, once, and needs no place in shared
 // memory.  A block's weights are fetched two to six blocks ahead, its tokens one.
+// With the tokens' quantization in front, at 4,096 x 11,008: 8 tokens 14.4 us (20.5 on pairs
+// of SMs), 16 tokens 16.3 (21.7 there; at 17 the pairs take 19.2); at 2,048 x 2,048 16 take 6.1.
 
 constexpr int64_t kMidTokens = 16;
 constexpr int kMidThreads = 256, kMidWarps = kMidThreads / 32;
@@ -1007,26 +1014,12 @@ hess_status il_encode_out(CUtensorMap* m, void* ptr, int32_t dtype, int64_t rows
                         rows, cols, 16, box_cols, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-constexpr size_t kFewSmem = 128 * 1024;
+constexpr size_t kFewSmem = 72 * 1024;  // two tokens of 32,768 codes, and sums
 
-template <class T>
-auto few_kernel(int tok, int gran) -> void (*)(FewParams) {
-    switch (tok * 16 + gran) {
-        case 1 * 16 + 1: return int8_few_kernel<T, 1, 1>;
-        case 1 * 16 + 2: return int8_few_kernel<T, 1, 2>;
-        case 1 * 16 + 4: return int8_few_kernel<T, 1, 4>;
-        case 1 * 16 + 8: return int8_few_kernel<T, 1, 8>;
-        case 2 * 16 + 1: return int8_few_kernel<T, 2, 1>;
-        case 2 * 16 + 2: return int8_few_kernel<T, 2, 2>;
-        case 2 * 16 + 4: return int8_few_kernel<T, 2, 4>;
-        case 2 * 16 + 8: return int8_few_kernel<T, 2, 8>;
-        case 4 * 16 + 1: return int8_few_kernel<T, 4, 1>;
-        case 4 * 16 + 2: return int8_few_kernel<T, 4, 2>;
-        case 4 * 16 + 4: return int8_few_kernel<T, 4, 4>;
-        case 8 * 16 + 1: return int8_few_kernel<T, 8, 1>;
-        case 8 * 16 + 2: return int8_few_kernel<T, 8, 2>;
-    }
-    return nullptr;
+template <class T, int kTok>
+auto few_kernel(int gran) -> void (*)(FewParams) {
+    return gran == 1 ? int8_few_kernel<T, kTok, 1> : gran == 2 ? int8_few_kernel<T, kTok, 2>
+                     : gran == 4 ? int8_few_kernel<T, kTok, 4> : int8_few_kernel<T, kTok, 8>;
 }
 
 template <class T>
@@ -1042,12 +1035,10 @@ hess_status il_prepare(int dev, int* pairs, int* sms_out) {
     std::lock_guard<std::mutex> lk(mu);
     if (dev < 0 || dev >= 128) return il_fail(HESS_ERR_UNSUPPORTED, "device index %d", dev);
     if (!count[dev]) {
-        for (int tok : {1, 2, 4, 8})
-            for (int gran : {1, 2, 4, 8})
-                for (auto fn : {few_kernel<__nv_bfloat16>(tok, gran), few_kernel<__half>(tok, gran)})
-                    if (fn)
-                        IL_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                    static_cast<int>(kFewSmem)));
+        for (int gran : {1, 2, 4, 8})
+            for (auto fn : {few_kernel<__nv_bfloat16, 1>(gran), few_kernel<__nv_bfloat16, 2>(gran),
+                            few_kernel<__half, 1>(gran), few_kernel<__half, 2>(gran)})
+                IL_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kFewSmem)));
         for (int tok : {kNarrowTok, kMiddleTok, kMaxTok})
             for (auto fn : {pair_kernel<__nv_bfloat16>(tok), pair_kernel<__half>(tok)})
                 IL_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1150,17 +1141,15 @@ hess_status il_launch(Kernel kernel, const Params& p, int64_t grid, int threads,
     return HESS_OK;
 }
 
-int few_tokens(int64_t n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : 8; }
-
-// Granules of 16 columns a thread of the few-token kernel takes: the most that the codes'
-// registers allow (4 words a token and granule) without leaving many threads idle; 0
-// where a row does not fit at all.
-int few_granules(int64_t n, int64_t d) {
+// Granules of 16 columns a thread of the few-token kernel takes: as many as there are (the
+// fewer warps share a row, the fewer sums meet), unless that leaves more threads idle; 0
+// where a row is too wide.
+int few_granules(int64_t d) {
     const int64_t granules = d / 16;
     int best = 0;
     double most = 0.0;
-    for (int g = 1; g <= 8 && g * few_tokens(n) <= 16; g *= 2) {
-        const int64_t wr = (granules + 32 * g - 1) / (32 * g);
+    for (int g = 1; g <= 8; g *= 2) {
+        const int64_t wr = ceil_div(granules, 32 * g);
         if (wr > kFewWarps) continue;
         const double used = static_cast<double>(granules) * (kFewWarps / wr) / (32.0 * g * kFewWarps);
         if (used >= 0.85 * most) {
@@ -1170,9 +1159,10 @@ int few_granules(int64_t n, int64_t d) {
     }
     return best;
 }
-bool is_few(int64_t n, int64_t d) {
-    return n <= kFewTokens && few_granules(n, d) > 0 && few_tokens(n) * d <= int64_t(64) * 1024;
-}
+// One or two tokens whose codes fit beside each other: with three, the sums of every
+// token over a warp cost more than tensor cores do (13.6 us either way at 4,096 x 11,008,
+// 18.6 against 15.8 for four at 11,008 x 4,096).
+bool is_few(int64_t n, int64_t d) { return n <= 2 && n * d <= int64_t(64) * 1024; }
 
 hess_status forward_few(const int8_linear_ctx* g, const void* X, const int8_t* codes, const float* scale, int64_t n,
                         const int8_t* W, const float* W_scale, void* Y, cudaStream_t s) {
@@ -1186,15 +1176,17 @@ hess_status forward_few(const int8_linear_ctx* g, const void* X, const int8_t* c
     p.n = static_cast<int32_t>(n);
     p.d = static_cast<int32_t>(g->d);
     p.f = static_cast<int32_t>(g->f);
-    const int gran = few_granules(n, g->d), tok = few_tokens(n);
+    const int gran = few_granules(g->d), tok = static_cast<int>(n);
     p.wr = static_cast<int32_t>(ceil_div(g->d, static_cast<int64_t>(gran) * 512));
     p.rp = kFewWarps / p.wr;
     const int64_t ctas = g->f < g->sms ? g->f : g->sms;
     p.rows = static_cast<int32_t>(ceil_div(g->f, ctas));
     const int64_t grid = ceil_div(g->f, p.rows);
     const size_t smem = static_cast<size_t>(ceil_div(static_cast<int64_t>(p.rows) * tok, 4)) * 16 + (X ? tok * g->d : 0);
-    const auto kernel = g->dtype == HESS_BF16 ? few_kernel<__nv_bfloat16>(tok, gran) : few_kernel<__half>(tok, gran);
-    if (!kernel || smem > kFewSmem) return il_fail(HESS_ERR_INTERNAL, "no kernel for %d tokens and %d granules", tok, gran);
+    const auto kernel = g->dtype == HESS_BF16
+                            ? (tok == 1 ? few_kernel<__nv_bfloat16, 1>(gran) : few_kernel<__nv_bfloat16, 2>(gran))
+                            : (tok == 1 ? few_kernel<__half, 1>(gran) : few_kernel<__half, 2>(gran));
+    if (smem > kFewSmem) return il_fail(HESS_ERR_INTERNAL, "%zu bytes of shared memory", smem);
     return il_launch(kernel, p, grid, kFewThreads, smem, s);
 }
 

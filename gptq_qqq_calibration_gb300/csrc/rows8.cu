@@ -21,6 +21,11 @@
 //   * 32-bit values.  One multiplier below 1/s and one above it: where both products round
 //     alike that is the code, and where they do not (1 value in 10^5) the exact sign of
 //     the remainder at the half between them decides.
+//
+// Bytes bound all of it: 16,384 x 11,008 bf16 take 97 us with a scale per 128 columns, 90
+// with one per row and 80 back (floor 80 at the copy rate of 6,781 GB/s), 32,768 x 4,096 fp32
+// 102 and 100 us (floor 99).  Rows that are no multiples of 16 bytes cost more instructions:
+// 16,383 x 8,191 bf16 97 us per 32 columns, 127 per row and 151 back (floor 59).
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>

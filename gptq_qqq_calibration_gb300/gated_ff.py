@@ -127,7 +127,9 @@ class GatedFF:
     more is refused, a forward is not.  Called as a function, the object is a node
     of an autograd graph.  With ``rows8`` the object can take 8-bit rows in the place of
     X in ``backward`` (2 d bytes of workspace a token of ``train_tokens``), and the node keeps X
-    in that form, with a scale per 128 columns: 1.03 bytes a value instead of 2.
+    in that form, with a scale per 128 columns: 1.03 bytes a value instead of 2.  A captured
+    backward pass belongs into the capture of its forward pass, with no other graph of
+    the same leaf tensors alive.
 
     The object's calls may come on any streams, and may be captured into CUDA
     graphs.  Replays of such graphs are the caller's to order, with each other
@@ -207,6 +209,8 @@ class GatedFF:
         return dx, dwg, dwu
 
     def __call__(self, X: torch.Tensor, W_gate: torch.Tensor, W_up: torch.Tensor) -> torch.Tensor:
+        if self.rows8 and not torch.is_grad_enabled():  # nothing to keep
+            return self.forward(X, W_gate, W_up)
         return _GatedFF.apply(self, X, W_gate, W_up)
 
     def sync(self, stream=None) -> None:

@@ -102,9 +102,11 @@ class Int8Linear:
     on the way, or as 8-bit rows.  ``tokens`` is the most tokens a forward call will
     have, ``train_tokens`` the most of a backward call.
 
-    Called as a function, ``op(X, W)`` with a 16-bit master weight, the object
-    is a node of an autograd graph: it quantizes both, keeps their 8-bit rows
+    Called as a function, ``op(X, W)`` with a 16-bit or fp32 master weight, the
+    object is a node of an autograd graph: it quantizes both, keeps their 8-bit rows
     for the backward pass, and sends gradients straight through the roundings.
+    A captured backward pass belongs into the capture of its forward pass, with no
+    other graph of the same leaf tensors alive.
 
     The object's calls may come on any streams, and may be captured into CUDA
     graphs.  Replays of such graphs are the caller's to order, with each other

@@ -51,12 +51,12 @@ hess_status int8_linear_create(int64_t d, int64_t f, int64_t tokens, int64_t tra
  * managed memory); Y_out must not overlap an input (HESS_ERR_INVALID).
  *   X       : [n_tokens, d] of the handle's type;
  *   W_codes : int8 [f, d];  W_scale : float32 [f];  Y_out : [n_tokens, f].
- * n_tokens 0 is a no-op.  Asynchronous on `stream`.  Calls of more tokens than fit one
- * pass over the weights in registers (8 at d <= 8192, 4 at 16384, 2 at 32768, 1 above) use
- * the handle's workspace: such a call waits for the one before it, whatever its stream
- * (an event); the others may run concurrently.  Calls may be captured into a graph, on any
- * stream; a captured call waits for the earlier ones of its capture, and the caller orders
- * replays with each other and with the handle's other calls. */
+ * n_tokens 0 is a no-op.  Asynchronous on `stream`.  Calls of more than two tokens (or of
+ * two of more than 32,768 columns) use the handle's workspace: such a call waits for the one
+ * before it, whatever its stream (an event); the others may run concurrently.  Calls may
+ * be captured into a graph, on any stream; a captured call waits for the earlier ones of
+ * its capture, and the caller orders replays with each other and with the handle's other
+ * calls. */
 hess_status int8_linear_forward(int8_linear_t g, const void* X, int64_t n_tokens, const int8_t* W_codes,
                                 const float* W_scale, void* Y_out, hess_stream_t stream);
 

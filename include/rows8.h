@@ -15,9 +15,8 @@
  *
  * rint rounds the exact quotient of the two float32 numbers, half to even, so the codes
  * are those of the formula with s rounded once to float32 and x / s taken in 64 bits, bit
- * for bit.  Where s is 0 (all
- * values 0, or a / 127 below float32's smallest number) the codes are 0.  A row or
- * group that holds a NaN or an infinity has s = NaN and codes 0: it comes back as
+ * for bit.  Where s is 0 (all values 0, or a / 127 below float32's smallest number) the
+ * codes are 0.  A row or group that holds a NaN or an infinity has s = NaN and codes 0: it comes back as
  * NaN, and its neighbours are not touched.  |x - x^| is at most s / 2 up to rounding,
  * wherever s is a normal number.
  *
@@ -41,8 +40,9 @@ extern "C" {
  *               between rows are left as they are.
  *   scale_out : float32 [n_rows] (group 0) or [n_rows, ceil(d / group)].
  * All in device memory of the current device, or managed memory.  Outputs must not
- * overlap X or each other, from a matrix's first byte to its last (HESS_ERR_INVALID).  Fastest where rows start on 16 bytes.
- * Asynchronous on `stream`; may be captured into a graph; keeps nothing. */
+ * overlap X or each other, from a matrix's first byte to its last (HESS_ERR_INVALID).
+ * Fastest where rows start on 16 bytes.  Asynchronous on `stream`; may be captured into a
+ * graph; keeps nothing. */
 hess_status rows8_quantize(const void* X, int64_t ldx, int64_t n_rows, int64_t d, int32_t dtype, int32_t group,
                            int8_t* codes_out, int64_t ldc, float* scale_out, hess_stream_t stream);
 
