@@ -67,8 +67,10 @@ constexpr uint32_t kStagingBytes = 16 * kMaxRows * 2;
 constexpr uint32_t kBarAt = kRing + 2 * 2 * kStagingBytes;  // two buffers for each half
 constexpr size_t kSmemBytes = 1024 + kBarAt + 8 * kNumBarriers + 16;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-constexpr int kThreads = 640;  // warp 0: weights, 1: MMAs, 2: tokens, 4-11: converters, 12-19: epilogue
-constexpr int kFirstEpiWarp = 12, kEpiWarps = 8;
+// Warp 0: weights, 1: MMAs, 2: tokens; from 4 on: converters, in groups of four that take the
+// stages in turn; then the epilogue.
+constexpr int kGroups = 2, kFirstEpiWarp = 4 + 4 * kGroups, kEpiWarps = 8;
+constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
 constexpr unsigned long long kDrainLimitNs = 1000000000ull;
 constexpr unsigned long long kAbortSettleNs = 2000000ull;
 constexpr int64_t kPieceInts = kMaxTok * kMaxRows;  // one CTA's sums of a unit of a split tile
@@ -123,8 +125,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t (&a)[16]) {
 __device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t (&a)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
-        "tcgen05.wait::st.sync.aligned;" ::"r"(t),
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
         "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(a[4]), "r"(a[5]), "r"(a[6]), "r"(a[7]), "r"(a[8]), "r"(a[9]),
         "r"(a[10]), "r"(a[11]), "r"(a[12]), "r"(a[13]), "r"(a[14]), "r"(a[15]), "r"(a[16]), "r"(a[17]), "r"(a[18]),
         "r"(a[19]), "r"(a[20]), "r"(a[21]), "r"(a[22]), "r"(a[23]), "r"(a[24]), "r"(a[25]), "r"(a[26]), "r"(a[27]),
@@ -240,6 +241,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int8_pair_kernel(const __grid_constant__ PairParams p) {
     constexpr int kCols = kTok / 2;  // tokens of an epilogue thread
     static_assert(kCols % 16 == 0, "sixteen tokens at a time");
+    // registers of a thread after the split; the launch has 65,536 / threads for each, in eights
+    constexpr int kServeRegs = 40, kConvRegs = 72, kEpiRegs = 144;
+    static_assert(128 * kServeRegs + 128 * kGroups * kConvRegs + 32 * kEpiWarps * kEpiRegs <=
+                      kThreads * (65536 / kThreads / 8 * 8),
+                  "registers");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -267,12 +273,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(wfull_bar(s), 1);
-            mbar_init(wempty_bar(s), 8);
+            mbar_init(wempty_bar(s), 4);
             mbar_init(xfull_bar(s), 1);
             mbar_init(xempty_bar(s), 1);
         }
         for (int s = 0; s < p.slots; ++s) {
-            mbar_init(afull_bar(s), 16);  // eight converter warps of each CTA
+            mbar_init(afull_bar(s), 8);  // four converter warps of each CTA
             mbar_init(aempty_bar(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -296,7 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
     if (warp < 4) {
-        setmaxnreg_dec<40>();
+        setmaxnreg_dec<kServeRegs>();
         if (warp == 0 && lane == 0) {
             bool ok = true;
             int stage = 0;
@@ -421,54 +427,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         }
-    } else if (warp < 12) {
-        // Converters: the first four warps take the first 64 steps of each stage, the
-        // others the rest.  A thread owns one weight row.
-        setmaxnreg_dec<72>();
+    } else if (warp < kFirstEpiWarp) {
+        // Converters: a thread owns one weight row, in every kGroups-th stage.
+        setmaxnreg_dec<kConvRegs>();
         const int h = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const bool some = (warp & 3) * 32 < p.rows, mine = row < p.rows;
         const uint32_t afull0 = mapa_shared(afull_bar(0), 0);
         bool ok = true;
-        int stage = 0, slot = 0;
+        int stage = h, slot = h, skip = h;
         uint32_t phase = 0, sphase = 0;
         for (int u = pair; ok && u < p.n_units; u += n_pairs) {
             const Unit un = unit_at(p, u);
-            for (int kb = un.kb0; kb < un.kb1; ++kb) {
+            int kb = un.kb0 + skip;
+            for (; kb < un.kb1; kb += kGroups) {
                 if (!mbar_wait(wfull_bar(stage), phase, limit)) {
                     ok = false;
                     break;
                 }
-                uint32_t a[32];
                 const uint32_t src = base + stage * p.stage_bytes + row * 128u;
+                const auto load = [&](int j) {
+                    return mine ? lds128(src + ((j ^ (row & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+                };
+                const auto widen16 = [](const uint4& v, uint32_t* a) {
+                    widen4(v.x, a[0], a[1]);
+                    widen4(v.y, a[2], a[3]);
+                    widen4(v.z, a[4], a[5]);
+                    widen4(v.w, a[6], a[7]);
+                };
+                uint32_t a[32];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint4 v = mine ? lds128(src + (((h * 4 + j) ^ (row & 7)) << 4)) : make_uint4(0, 0, 0, 0);
-                    widen4(v.x, a[8 * j], a[8 * j + 1]);
-                    widen4(v.y, a[8 * j + 2], a[8 * j + 3]);
-                    widen4(v.z, a[8 * j + 4], a[8 * j + 5]);
-                    widen4(v.w, a[8 * j + 6], a[8 * j + 7]);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(wempty_bar(stage));
+                for (int j = 0; j < 4; ++j) widen16(load(j), a + 8 * j);
                 if (!mbar_wait(aempty_bar(slot), sphase ^ 1u, limit)) {
                     ok = false;
                     break;
                 }
+                __syncwarp();
                 tc_fence_after();
-                if (some) tmem_st32(tmem + lanes + 2 * p.acc_cols + static_cast<uint32_t>(slot) * kSlotCols + h * 32u, a);
+                const uint32_t to = tmem + lanes + 2 * p.acc_cols + static_cast<uint32_t>(slot) * kSlotCols;
+                if (some) tmem_st32(to, a);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) widen16(load(4 + j), a + 8 * j);
+                if (some) tmem_st32(to + 32u, a);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_relaxed(afull0 + 8u * slot);
-                if (++slot == p.slots) {
-                    slot = 0;
+                if (lane == 0) {
+                    mbar_arrive_cluster_relaxed(afull0 + 8u * slot);
+                    mbar_arrive(wempty_bar(stage));
+                }
+                slot += kGroups;
+                if (slot >= p.slots) {
+                    slot -= p.slots;
                     sphase ^= 1u;
                 }
-                if (++stage == p.stages) {
-                    stage = 0;
+                stage += kGroups;
+                if (stage >= p.stages) {
+                    stage -= p.stages;
                     phase ^= 1u;
                 }
             }
+            skip = kb - un.kb1;
         }
         if (!ok && lane == 0) {
             atomicOr(p.status, kStatusTimeoutLoad);
@@ -477,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else {
         // Epilogue: a thread owns one weight row (an output channel) and every other
         // sixteen tokens: of the first four warps the even ones, of the others the odd.
-        setmaxnreg_inc<144>();
+        setmaxnreg_inc<kEpiRegs>();
         griddep_wait();
         const int q = warp & 3, row = q * 32 + lane;
         const int group = (warp - kFirstEpiWarp) >> 2, first = group * 16;
