@@ -56,12 +56,13 @@ constexpr uint32_t kRing = 208 * 1024;
 // tile has fewer tokens.  (Half stages in twice as many slots cost a wait more each:
 // 447 us against 415 for 8,192 tokens at 4,096 x 11,008.)
 constexpr int kMaxSlots = 6;
+constexpr int kLook = 4;  // stages whose barriers are asked for at once
 constexpr uint32_t kSlotCols = kKB / 2;
 constexpr uint32_t kTmemCols = 512;
 static_assert(2 * kMaxTok + 2 * kSlotCols <= kTmemCols, "two sums and two slots");
 // Tiles of up to so many tokens have epilogues of their own, which hold fewer sums.
 constexpr int kNarrowTok = 64, kMiddleTok = 128;
-constexpr int kNumBarriers = 4 * kMaxStages + 2 * kMaxSlots + 5;
+constexpr int kNumBarriers = 4 * kMaxStages + kMaxSlots + 5;
 // Sixteen tokens' results on their way out, of an epilogue half (four warps).
 constexpr uint32_t kStagingBytes = 16 * kMaxRows * 2;
 constexpr uint32_t kBarAt = kRing + 2 * 2 * kStagingBytes;  // two buffers for each half
@@ -102,13 +103,15 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // D (M = 256 across the pair) (+)= A[tensor memory] * B[shared memory], f16, issued by the even CTA.
-__device__ __forceinline__ void umma_f16_pair_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                                 uint32_t accumulate) {
+// The descriptor's low word holds the address, and no sum of addresses leaves it.
+__device__ __forceinline__ void umma_f16_pair_ta(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t b_high,
+                                                 uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_low), "r"(b_high), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -131,6 +134,41 @@ __device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t (&a)[32]) {
         "r"(a[19]), "r"(a[20]), "r"(a[21]), "r"(a[22]), "r"(a[23]), "r"(a[24]), "r"(a[25]), "r"(a[26]), "r"(a[27]),
         "r"(a[28]), "r"(a[29]), "r"(a[30]), "r"(a[31])
         : "memory");
+}
+
+// Whether the phase with parity `parity` of `bar` has completed by now.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// As mbar_wait, for barriers that have mostly completed when they are asked: without a
+// limit of its own a try_wait answers in 16 cycles, with one in 51.
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_soon(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    if (mbar_try(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        if (mbar_try(bar, parity)) return true;
+        if (globaltimer_ns() - t0 >= limit_ns) return false;
+    }
 }
 
 // Four int8 as two words of two float16: 1024 + (q + 128), less 1152.
@@ -255,12 +293,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto wfull_bar = [&](int s) { return bar0 + 8u * s; };                      // this CTA's weights have landed
     auto wempty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };      // its converters have read them
     auto xfull_bar = [&](int s) { return bar0 + 8u * (2 * kMaxStages + s); };   // even CTA: the pair's tokens
-    auto xempty_bar = [&](int s) { return bar0 + 8u * (3 * kMaxStages + s); };  // MMAs have read them
+    auto done_bar = [&](int s) { return bar0 + 8u * (3 * kMaxStages + s); };    // MMAs have read them, and their slot of A
     auto afull_bar = [&](int s) { return bar0 + 8u * (4 * kMaxStages + s); };   // even CTA: the pair's slot of A
-    auto aempty_bar = [&](int s) { return bar0 + 8u * (4 * kMaxStages + kMaxSlots + s); };
-    auto accf_bar = [&](int b) { return bar0 + 8u * (4 * kMaxStages + 2 * kMaxSlots + b); };
-    auto acce_bar = [&](int b) { return bar0 + 8u * (4 * kMaxStages + 2 * kMaxSlots + 2 + b); };
-    const uint32_t drain_bar = bar0 + 8u * (4 * kMaxStages + 2 * kMaxSlots + 4);
+    auto accf_bar = [&](int b) { return bar0 + 8u * (4 * kMaxStages + kMaxSlots + b); };
+    auto acce_bar = [&](int b) { return bar0 + 8u * (4 * kMaxStages + kMaxSlots + 2 + b); };
+    const uint32_t drain_bar = bar0 + 8u * (4 * kMaxStages + kMaxSlots + 4);
     __shared__ volatile int aborted;
     __shared__ volatile int epi_last;
     __shared__ float4 epi_scales[2][kCols / 4];
@@ -275,12 +312,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(wfull_bar(s), 1);
             mbar_init(wempty_bar(s), 4);
             mbar_init(xfull_bar(s), 1);
-            mbar_init(xempty_bar(s), 1);
+            mbar_init(done_bar(s), 1);
         }
-        for (int s = 0; s < p.slots; ++s) {
-            mbar_init(afull_bar(s), 8);  // four converter warps of each CTA
-            mbar_init(aempty_bar(s), 1);
-        }
+        for (int s = 0; s < p.slots; ++s) mbar_init(afull_bar(s), 8);  // four converter warps of each CTA
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf_bar(b), 1);
             mbar_init(acce_bar(b), 2 * kEpiWarps);
@@ -299,7 +333,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    // through a reduction, so that it lands in a uniform register
+    const uint32_t tmem = __reduce_max_sync(~0u, *reinterpret_cast<volatile uint32_t*>(tmem_slot));
 
     if (warp < 4) {
         setmaxnreg_dec<kServeRegs>();
@@ -311,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const Unit un = unit_at(p, u);
                 const int row = un.f0 + static_cast<int>(rank) * p.rows;
                 for (int kb = un.kb0; kb < un.kb1; ++kb) {
-                    if (!mbar_wait(wempty_bar(stage), phase ^ 1u, limit)) {
+                    if (!mbar_wait_soon(wempty_bar(stage), phase ^ 1u, limit)) {
                         ok = false;
                         break;
                     }
@@ -328,17 +363,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 aborted = 1;
             }
         } else if (warp == 2 && lane == 0) {
-            griddep_wait();
-            griddep_launch_dependents();
             bool ok = true;
             int stage = 0;
             uint32_t phase = 0;
             const uint32_t box = static_cast<uint32_t>(p.tok) * 64u;  // tok / 2 rows of 128 bytes
+            Unit un = unit_at(p, pair);
+            griddep_wait();
+            griddep_launch_dependents();
             for (int u = pair; ok && u < p.n_units; u += n_pairs) {
-                const Unit un = unit_at(p, u);
+                if (u != pair) un = unit_at(p, u);
                 const int row = un.t0 + static_cast<int>(rank) * (p.tok / 2);
                 for (int kb = un.kb0; kb < un.kb1; ++kb) {
-                    if (!mbar_wait(xempty_bar(stage), phase ^ 1u, limit)) {
+                    if (!mbar_wait_soon(done_bar(stage), phase ^ 1u, limit)) {
                         ok = false;
                         break;
                     }
@@ -367,33 +403,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // float32 sums, float16 operands, both contiguous along the contraction
             const uint32_t idesc = (1u << 4) | ((static_cast<uint32_t>(p.tok) >> 3) << 17) | ((256u >> 4) << 24);
             // descriptors count 16 bytes
-            const uint64_t first = smem_desc_sw128(base + p.w_bytes, 16u, 1024u);
-            const uint64_t next = p.stage_bytes >> 4, half = static_cast<uint64_t>(p.tok) * 4u;
-            uint64_t b = first;
+            const uint64_t desc = smem_desc_sw128(base + p.w_bytes, 16u, 1024u);
+            const uint32_t high = static_cast<uint32_t>(desc >> 32), first = static_cast<uint32_t>(desc);
+            const uint32_t next = p.stage_bytes >> 4, half = static_cast<uint32_t>(p.tok) * 4u;
+            uint32_t b = first;
+            // A barrier's answer takes some 120 cycles, so that of a few stages (no more than
+            // there are slots, whose parity would tell of an earlier use) is asked for at once.
+            const int look = p.slots < kLook ? p.slots : kLook, ahead = (lane >> 1) < look ? lane >> 1 : 0;
+            int known = 0;
             for (int u = pair; ok && u < p.n_units; u += n_pairs) {
                 const Unit un = unit_at(p, u);
                 for (int c0 = un.kb0; ok && c0 < un.kb1; c0 += kChunk) {
-                    ok = __all_sync(~0u, mbar_wait(acce_bar(ab), aphase ^ 1u, limit));
+                    ok = __all_sync(~0u, mbar_wait_soon(acce_bar(ab), aphase ^ 1u, limit));
                     if (!ok) break;
                     const uint32_t acc = tmem + static_cast<uint32_t>(ab) * p.acc_cols;
                     const int c1 = c0 + kChunk < un.kb1 ? c0 + kChunk : un.kb1;
                     for (int kb = c0; kb < c1; ++kb) {
-                        const auto four = [&](uint32_t a, uint64_t at, uint32_t add) {
-                            umma_f16_pair_ta(acc, a, at, idesc, add);
-                            umma_f16_pair_ta(acc, a + 8u, at + 2u, idesc, 1u);
-                            umma_f16_pair_ta(acc, a + 16u, at + 4u, idesc, 1u);
-                            umma_f16_pair_ta(acc, a + 24u, at + 6u, idesc, 1u);
+                        const auto four = [&](uint32_t a, uint32_t at, uint32_t add) {
+                            umma_f16_pair_ta(acc, a, at, high, idesc, add);
+                            umma_f16_pair_ta(acc, a + 8u, at + 2u, high, idesc, 1u);
+                            umma_f16_pair_ta(acc, a + 16u, at + 4u, high, idesc, 1u);
+                            umma_f16_pair_ta(acc, a + 24u, at + 6u, high, idesc, 1u);
                         };
-                        ok = __all_sync(~0u, mbar_wait(xfull_bar(stage), phase, limit) &&
-                                                 mbar_wait(afull_bar(slot), sphase, limit));
-                        if (!ok) break;
+                        if (kTok == kMaxTok) {
+                            ok = __all_sync(~0u, mbar_wait_soon(xfull_bar(stage), phase, limit) &&
+                                                     mbar_wait_soon(afull_bar(slot), sphase, limit));
+                            if (!ok) break;
+                        } else if (known == 0) {
+                            // even lanes ask for tokens, odd ones for slots of A, of this stage and those after it
+                            int s = stage + ahead, a = static_cast<int>(slot) + ahead;
+                            uint32_t sp = phase, ap = sphase;
+                            if (s >= p.stages) s -= p.stages, sp ^= 1u;
+                            if (a >= p.slots) a -= p.slots, ap ^= 1u;
+                            const uint32_t bar = lane & 1 ? afull_bar(a) : xfull_bar(s), parity = lane & 1 ? ap : sp;
+                            known = (__ffs(~__ballot_sync(~0u, mbar_test(bar, parity)) | 1 << 2 * look) - 1) >> 1;
+                            if (known == 0) {
+                                ok = __all_sync(~0u, mbar_wait_soon(xfull_bar(stage), phase, limit) &&
+                                                         mbar_wait_soon(afull_bar(slot), sphase, limit));
+                                if (!ok) break;
+                                known = 1;
+                            }
+                        }
+                        --known;
                         tc_fence_after();
                         if (elect_one()) {
                             const uint32_t a = tmem + 2 * p.acc_cols + slot * kSlotCols;
                             four(a, b, kb != c0 ? 1u : 0u);
                             four(a + 32u, b + half, 1u);
-                            tc_commit_pair_mc(aempty_bar(slot), 0x3);
-                            tc_commit_pair_mc(xempty_bar(stage), 0x3);
+                            tc_commit_pair_mc(done_bar(stage), 0x3);
                         }
                         __syncwarp();
                         if (++slot == static_cast<uint32_t>(p.slots)) {
@@ -423,7 +480,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 // every MMA issued has completed before the pair's memories are released
                 tc_commit_pair_mc(drain_bar, 0x1);
-                if (!mbar_wait(drain_bar, 0, kDrainLimitNs)) atomicOr(p.status, kStatusTimeoutDrain);
+                if (!mbar_wait_soon(drain_bar, 0, kDrainLimitNs)) atomicOr(p.status, kStatusTimeoutDrain);
             }
             __syncwarp();
         }
@@ -436,12 +493,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t afull0 = mapa_shared(afull_bar(0), 0);
         bool ok = true;
         int stage = h, slot = h, skip = h;
-        uint32_t phase = 0, sphase = 0;
+        int before = h - p.slots;  // the stage whose slot of A this one takes over
+        uint32_t phase = 0, bphase = 0;
         for (int u = pair; ok && u < p.n_units; u += n_pairs) {
             const Unit un = unit_at(p, u);
             int kb = un.kb0 + skip;
             for (; kb < un.kb1; kb += kGroups) {
-                if (!mbar_wait(wfull_bar(stage), phase, limit)) {
+                if (!mbar_wait_soon(wfull_bar(stage), phase, limit)) {
                     ok = false;
                     break;
                 }
@@ -458,7 +516,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 uint32_t a[32];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) widen16(load(j), a + 8 * j);
-                if (!mbar_wait(aempty_bar(slot), sphase ^ 1u, limit)) {
+                if (before >= 0 && !mbar_wait_soon(done_bar(before), bphase, limit)) {
                     ok = false;
                     break;
                 }
@@ -477,9 +535,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     mbar_arrive(wempty_bar(stage));
                 }
                 slot += kGroups;
-                if (slot >= p.slots) {
-                    slot -= p.slots;
-                    sphase ^= 1u;
+                if (slot >= p.slots) slot -= p.slots;
+                before += kGroups;
+                if (before >= p.stages) {
+                    before -= p.stages;
+                    bphase ^= 1u;
                 }
                 stage += kGroups;
                 if (stage >= p.stages) {
@@ -536,7 +596,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int c0 = un.kb0; c0 < un.kb1; c0 += kChunk) {
                 // the warps agree on whether a wait ran out, so that all of them pass the
                 // same barriers
-                failed = epi_barrier_any(failed || !mbar_wait(accf_bar(ab), aphase, limit));
+                failed = epi_barrier_any(failed || !mbar_wait_soon(accf_bar(ab), aphase, limit));
                 tc_fence_after();
                 if (!failed) {
                     const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(ab) * p.acc_cols;
@@ -1268,6 +1328,7 @@ hess_status forward(int8_linear_ctx* g, const void* X, const int8_t* codes, cons
     p.acc_cols = static_cast<uint32_t>((p.tok + 31) / 32 * 32);
     const int slots = static_cast<int>((kTmemCols - 2 * p.acc_cols) / kSlotCols);
     p.slots = slots < kMaxSlots ? slots : kMaxSlots;
+    if (p.slots >= p.stages) p.slots = p.stages - 1;  // a stage's barrier tells of one use of a slot
     p.x_scale = X ? g->x_scale : scale;
     p.w_scale = W_scale;
     p.pieces = g->pieces;
