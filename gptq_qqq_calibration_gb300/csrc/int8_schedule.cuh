@@ -59,12 +59,13 @@ __host__ __device__ inline Unit unit_at(const Schedule& p, int u) {
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tiles and splits for n tokens.  In SM cycles, a stage costs what bounds it: the MMAs
-// (4 a token), their issue and what it waits for (kIssue), or the weights' way from memory
+// (4 a token), their issue and what it waits for (kIssue; kAlone less where no converter
+// shares the MMAs' scheduler), or the weights' way from memory
 // (16 bytes a row over 3 cycles at 24 bytes a cycle and SM).  A turn of units costs
 // kTurn more; a tile in pieces kSplit for meeting, and 32 a token for each piece but one that
 // the last pair there reads.
 inline void plan(Schedule& p, int64_t pairs) {
-    constexpr int64_t kIssue = 800, kTurn = 700, kSplit = 9000;
+    constexpr int64_t kIssue = 800, kAlone = 100, kTurn = 700, kSplit = 9000;
     const int64_t n_kb = ceil_div(p.d, kKB);
     p.tiles_t = static_cast<int32_t>(ceil_div(p.n, kMaxTok));
     p.tok = static_cast<int32_t>(ceil_div(ceil_div(p.n, p.tiles_t), 16) * 16);
@@ -77,7 +78,7 @@ inline void plan(Schedule& p, int64_t pairs) {
         const int64_t tiles = p.tiles_t * tiles_f;
         const int64_t turns = tiles / pairs, rest = tiles % pairs;
         int64_t stage = 4 * p.tok;
-        if (stage < kIssue) stage = kIssue;
+        if (stage < kIssue) stage = rows > 96 ? kIssue : kIssue - kAlone;
         if (stage < 16 * rows / 3) stage = 16 * rows / 3;
         for (int64_t s = 1; s <= kMaxParts && s <= n_kb && (s == 1 || rest * s <= pairs); ++s) {
             int64_t cost = turns * (n_kb * stage + kTurn);

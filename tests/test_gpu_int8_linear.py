@@ -24,7 +24,7 @@ pytestmark = pytest.mark.gpu
 LAYOUTS = {
     (17, 4096, 1400): "split rows",
     (37, 11008, 4096): "split",
-    (24, 4096, 11008): "",
+    (24, 4096, 11008): "rows",
     (20, 65536, 2048): "split",
     (300, 40000, 2056): "split rows tokens",
     (1000, 8192, 4096): "split whole tokens",
