@@ -19,13 +19,14 @@
 // memory: two 192-column sums, so that one is drained under the other's products, and
 // two slots of 128 steps of A (more where the tile has fewer tokens).
 //
-// Many tokens are bound by the tensor pipe: 8,192 at 4,096 x 11,008 take 415 us, 1,780
-// TFLOP/s and 0.94 of the burst rate of a library's 16-bit GEMM.  Up to some 600 the bytes of the
-// weights bound it: 37 tokens there take 19.7 us for 7.0 of bytes, of which the kernel in
-// front, the start and the last tile's way out are some ten; 512 take 40 us.
+// Many tokens are bound by the tensor pipe: 8,192 at 4,096 x 11,008 take 408 us, 1,810
+// TFLOP/s and 0.96 of the burst rate of a library's 16-bit GEMM.  Up to some 600 the bytes of the
+// weights should bound it, but what shows is latency: 37 tokens there take 16.4 us for 6.8 of
+// bytes: 2.6 us until the kernel in front lets this one start, 3 until the first stage is
+// converted, 8 for 32 stages at some 500 cycles each and 2 for the last tile's way out.
 //
-// Up to 16 tokens do not pay for the trip through tensor memory: one or two take one pass
-// over the weights with dp4a, three to sixteen one with warp-level MMAs.
+// Few tokens do not pay for the trip through tensor memory: one or two take one pass over
+// the weights with dp4a, up to 16 (in small layers 32) one with warp-level MMAs.
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -876,7 +877,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const __grid_c
     }
 }
 
-// ------------------------------------------------------- up to 16 tokens
+// ------------------------------------------------------- up to 32 tokens
 //
 // Bound by reading the weights once, too, but with more products than dp4a has time for:
 // warp-level MMAs (m16n8k16, float16, float32 sums) on weights that go from memory
@@ -889,10 +890,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const __grid_c
 // time, and a CTA's warps share the columns, 64 at a time in turn: so every weight and every
 // token's value is read by one warp of the CTA, once, and needs no place in shared
 // memory.  A block's weights are fetched two to six blocks ahead, its tokens one.
-// With the tokens' quantization in front, at 4,096 x 11,008: 8 tokens 14.4 us (20.5 on pairs
-// of SMs), 16 tokens 16.3 (21.7 there; at 17 the pairs take 19.2); at 2,048 x 2,048 16 take 6.1.
+// With the tokens' quantization in front, at 4,096 x 11,008: 8 tokens 14.4 us (15.7 on pairs
+// of SMs), 16 tokens 16.3 (16.0 there); at 2,048 x 2,048 16 take 6.1 (10.3 there).
 
-constexpr int64_t kMidTokens = 16;
 constexpr int kMidThreads = 256, kMidWarps = kMidThreads / 32;
 constexpr int kMidFlush = 1024 / 64;  // blocks whose sums stay below 2^24
 
@@ -925,7 +925,7 @@ __global__ void __launch_bounds__(kMidThreads, 2) int8_mid_kernel(const __grid_c
     const int blocks = (p.d + 63) / 64;
     bool waited = false;
     for (int r0 = row0; r0 < row1; r0 += kTilesM * 16) {
-        constexpr int kDepth = kTilesM <= 1 ? 6 : 2;
+        constexpr int kDepth = kTilesM > 1 ? 2 : kTilesN <= 2 ? 6 : kTilesN == 3 ? 4 : 2;
         uint4 a[kDepth][kTilesM][2], x[2][kTilesN][2];
         // the i-th block of this warp: pairs of neighbours, so that a line of memory is read at once
         const auto block = [&](int i) { return (i >> 1) * (2 * kMidWarps) + 2 * warp + (i & 1); };
@@ -1280,12 +1280,29 @@ hess_status widen_tokens(const int8_linear_ctx* g, const void* X, const int8_t* 
     return HESS_OK;
 }
 
-// Row tiles that a warp's registers hold.
-constexpr int64_t kMidTiles = 3;
+// Row tiles that a warp's registers hold, for up to 8 `tiles_n` tokens.
+int mid_tiles(int tiles_n) { return tiles_n <= 2 ? 3 : tiles_n == 3 ? 2 : 1; }
 
 template <int kTilesN>
 auto mid_kernel(int tiles_m) -> void (*)(MidParams) {
-    return tiles_m == 1 ? int8_mid_kernel<1, kTilesN> : tiles_m == 2 ? int8_mid_kernel<2, kTilesN> : int8_mid_kernel<3, kTilesN>;
+    if constexpr (kTilesN == 4) return int8_mid_kernel<1, 4>;
+    else if constexpr (kTilesN == 3) return tiles_m == 1 ? int8_mid_kernel<1, 3> : int8_mid_kernel<2, 3>;
+    else
+        return tiles_m == 1   ? int8_mid_kernel<1, kTilesN>
+               : tiles_m == 2 ? int8_mid_kernel<2, kTilesN>
+                              : int8_mid_kernel<3, kTilesN>;
+}
+
+int64_t mid_rows(const int8_linear_ctx* g) { return ceil_div(g->f, 2 * g->sms); }
+
+// From 17 tokens on only small layers, whose rows a CTA takes in one turn: in two turns, or
+// over more columns, every CTA's reading of all tokens costs more than the pairs' start
+// (24 tokens: 2,048 x 2,048 7.0 us against 10.5, 4,096 x 8,192 14.8 against 15.6, but
+// 8,192 x 2,048 17.5 against 14.3; 32 at 4,096 x 4,096 12.4 against 13.5, at 2,560 x 6,912, two
+// turns, 18.4 against 12.4).
+bool is_mid(const int8_linear_ctx* g, int64_t n) {
+    const int tiles_n = static_cast<int>(ceil_div(n, 8));
+    return tiles_n <= 2 || (tiles_n <= 4 && g->d <= 4096 && mid_rows(g) <= 16 * mid_tiles(tiles_n));
 }
 
 hess_status forward_mid(int8_linear_ctx* g, const void* X, const int8_t* codes, const float* scale, int64_t n,
@@ -1300,11 +1317,14 @@ hess_status forward_mid(int8_linear_ctx* g, const void* X, const int8_t* codes, 
     p.d = static_cast<int32_t>(g->d);
     p.f = static_cast<int32_t>(g->f);
     p.bf16 = g->dtype == HESS_BF16;
-    const int64_t ctas = g->f < 2 * g->sms ? g->f : 2 * g->sms;
-    p.rows = static_cast<int32_t>(ceil_div(g->f, ctas));
-    const int64_t tiles = ceil_div(p.rows, 16), turns = ceil_div(tiles, kMidTiles);
+    p.rows = static_cast<int32_t>(mid_rows(g));
+    const int tiles_n = static_cast<int>(ceil_div(n, 8));
+    const int64_t tiles = ceil_div(p.rows, 16), turns = ceil_div(tiles, mid_tiles(tiles_n));
     const int tiles_m = static_cast<int>(ceil_div(tiles, turns));
-    const auto kernel = n <= 8 ? mid_kernel<1>(tiles_m) : mid_kernel<2>(tiles_m);
+    const auto kernel = tiles_n <= 1   ? mid_kernel<1>(tiles_m)
+                        : tiles_n == 2 ? mid_kernel<2>(tiles_m)
+                        : tiles_n == 3 ? mid_kernel<3>(tiles_m)
+                                       : mid_kernel<4>(tiles_m);
     IL_TRY(g->order.begin(s));
     IL_CHECK(widen_tokens(g, X, codes, n, s));
     const hess_status st = il_launch(kernel, p, ceil_div(g->f, p.rows), kMidThreads, 0, s);
@@ -1317,7 +1337,7 @@ hess_status forward(int8_linear_ctx* g, const void* X, const int8_t* codes, cons
                     const int8_t* W, const float* W_scale, void* Y, cudaStream_t s) {
     IL_TRY(ensure_context());
     if (is_few(n, g->d)) return forward_few(g, X, codes, scale, n, W, W_scale, Y, s);
-    if (n <= kMidTokens) return forward_mid(g, X, codes, scale, n, W, W_scale, Y, s);
+    if (is_mid(g, n)) return forward_mid(g, X, codes, scale, n, W, W_scale, Y, s);
     PairParams p{};
     p.n = static_cast<int32_t>(n);
     p.d = static_cast<int32_t>(g->d);

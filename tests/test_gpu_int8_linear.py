@@ -22,7 +22,7 @@ pytestmark = pytest.mark.gpu
 # tokens, d, f: what the layout has at 76 pairs ("split": tiles in several pieces, "whole": whole
 # tiles before them, "rows": fewer than 128 weight rows per CTA, "tokens": several tiles of tokens)
 LAYOUTS = {
-    (17, 4096, 1400): "split rows",
+    (33, 4096, 1400): "split rows",
     (37, 11008, 4096): "split",
     (24, 4096, 11008): "rows",
     (20, 65536, 2048): "split",
@@ -81,7 +81,7 @@ SIZES = [(1, 16, 8), (1, 32, 136), (2, 144, 264), (3, 4096, 520), (4, 1040, 1400
          (9, 16, 8), (9, 144, 24), (16, 528, 1400), (17, 2064, 264), (31, 128, 520), (64, 1040, 4104),
          (128, 4096, 1032), (191, 256, 136), (192, 512, 264), (193, 1024, 520), (385, 2064, 520), (700, 528, 1400),
          (8, 8192, 72), (8, 8208, 72), (4, 16384, 40), (4, 16400, 40), (2, 32768, 24), (2, 32784, 24), (1, 65536, 16),
-         (20, 65536, 16)]
+         (20, 65536, 16), (18, 4096, 9728), (24, 1040, 4872), (32, 4096, 4864), (27, 2048, 4872), (17, 4112, 264)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
@@ -95,7 +95,7 @@ def test_forward_layouts(n, d, f):
     check_forward(n, d, f, torch.bfloat16, n + 1)
 
 
-@pytest.mark.parametrize("n", list(range(1, 13)) + [15, 33, 47, 48, 49, 95, 97])
+@pytest.mark.parametrize("n", list(range(1, 13)) + [15, 17, 23, 24, 25, 31, 32, 33, 47, 48, 49, 95, 97])
 def test_forward_token_counts(n):
     check_forward(n, 1040, 1560, torch.bfloat16, 500 + n)
 
