@@ -339,14 +339,15 @@ def test_weights_written_just_before():
     op.sync()
 
 
+@pytest.mark.parametrize("n", [40, 100, 300])  # a tile width of each kernel
 @pytest.mark.parametrize("limit", [0, 500, 2000, 8000])
-def test_waits_that_run_out_end_the_kernel(limit):
+def test_waits_that_run_out_end_the_kernel(limit, n):
     """Split tiles with a limit that some waits keep and others do not: the kernel ends,
     says so, and the handle works again.  (Sums over enough columns that a tile's end is
     waited for longer than one attempt of a wait lasts.)"""
     from gptq_qqq_calibration_gb300 import HessError, Int8Linear
     from gptq_qqq_calibration_gb300.int8_linear import int8_linear_set_timeout
-    n, d, f = 300, 16400, 4096
+    d, f = 16400, 4096
     x, (wq, ws), _ = make(n, d, f, torch.bfloat16, 60)
     op = Int8Linear(d, f, tokens=n)
     X, w = x.cuda(), rows8(wq, ws)
@@ -364,6 +365,40 @@ def test_waits_that_run_out_end_the_kernel(limit):
             timeouts += 1
         assert torch.equal(op.forward(X, w), want)
     assert timeouts > 0 or limit > 0
+    op.sync()
+
+
+def test_two_threads_share_a_handle():
+    """Host threads with streams of their own: calls of every kernel, forward and backward."""
+    import threading
+    from gptq_qqq_calibration_gb300 import Int8Linear, quantize_rows
+    d, f = 1040, 2056
+    op = Int8Linear(d, f, tokens=300, train_tokens=300)
+    work = []
+    for k, n in enumerate((1, 2, 9, 30, 70, 300)):
+        x, (wq, ws), dy = make(n, d, f, torch.bfloat16, 70 + k)
+        X, w = x.cuda(), rows8(wq, ws)
+        rows = quantize_rows(X)
+        work.append((X, w, rows, dy.cuda()))
+    want = [(op.forward(X, w), *op.backward(dy, rows, w)) for X, w, rows, dy in work]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(order):
+        stream = torch.cuda.Stream()
+        for k in order:
+            X, w, rows, dy = work[k]
+            got = (op.forward(X, w, stream=stream), *op.backward(dy, rows, w, stream=stream))
+            stream.synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, want[k])):
+                wrong.append(k)
+
+    threads = [threading.Thread(target=run, args=(order * 10,)) for order in ([0, 1, 2, 3, 4, 5], [5, 3, 1, 4, 2, 0])]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
     op.sync()
 
 
@@ -387,6 +422,11 @@ def test_autograd_node():
     big[:, :, 1:] = dy.transpose(1, 2)
     op(X2, W.detach()).backward(big[:, :, 1:].transpose(1, 2))
     assert torch.equal(X2.grad, dx)
+    # no tokens at all
+    W2 = W.detach().requires_grad_()
+    none = torch.zeros((0, d), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    op(none, W2).backward(torch.zeros((0, f), dtype=torch.bfloat16, device="cuda"))
+    assert none.grad.shape == (0, d) and (W2.grad == 0).all()
     op.sync()
 
 

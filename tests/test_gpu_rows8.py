@@ -171,10 +171,10 @@ def test_leading_shapes_and_empty():
         assert same(one.codes, formula(x, 0)[0][r:r + 1])
 
 
-def test_past_32_bit_offsets():
-    """More than 2^32 codes: rows at the far end, whole and in groups."""
+@pytest.mark.parametrize("n,d", [(270000, 16384), (33600000, 128), (530003, 8191)])
+def test_past_32_bit_offsets(n, d):
+    """More than 2^32 codes: rows at the far end, whole and in groups; long, joined and odd ones."""
     from gptq_qqq_calibration_gb300 import quantize_rows, restore_rows
-    n, d = 270000, 16384
     g = torch.Generator(device="cuda").manual_seed(1)
     X = torch.empty((n, d), dtype=torch.bfloat16, device="cuda")
     for a in range(0, n, 30000):
