@@ -63,7 +63,7 @@ constexpr uint32_t kTmemCols = 512;
 static_assert(2 * kMaxTok + 2 * kSlotCols <= kTmemCols, "two sums and two slots");
 // Tiles of up to so many tokens have epilogues of their own, which hold fewer sums.
 constexpr int kNarrowTok = 64, kMiddleTok = 128;
-constexpr int kNumBarriers = 4 * kMaxStages + kMaxSlots + 5;
+constexpr int kNumBarriers = 4 * kMaxStages + kMaxSlots + 6;
 // Sixteen tokens' results on their way out, of an epilogue half (four warps).
 constexpr uint32_t kStagingBytes = 16 * kMaxRows * 2;
 constexpr uint32_t kBarAt = kRing + 2 * 2 * kStagingBytes;  // two buffers for each half
@@ -115,6 +115,13 @@ __device__ __forceinline__ void umma_f16_pair_ta(uint32_t d_tmem, uint32_t a_tme
         "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "r"(b_low), "r"(b_high), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// `bytes` of global memory into this CTA's shared memory; counted on its `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t (&a)[16]) {
@@ -299,7 +306,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto afull_bar = [&](int s) { return bar0 + 8u * (4 * kMaxStages + s); };   // even CTA: the pair's slot of A
     auto accf_bar = [&](int b) { return bar0 + 8u * (4 * kMaxStages + kMaxSlots + b); };
     auto acce_bar = [&](int b) { return bar0 + 8u * (4 * kMaxStages + kMaxSlots + 2 + b); };
-    const uint32_t drain_bar = bar0 + 8u * (4 * kMaxStages + kMaxSlots + 4);
+    const uint32_t drain_bar = bar0 + 8u * (4 * kMaxStages + kMaxSlots + 4), piece_bar = drain_bar + 8u;
     __shared__ volatile int aborted;
     __shared__ volatile int epi_last;
     __shared__ float4 epi_scales[2][kCols / 4];
@@ -323,6 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(acce_bar(b), 2 * kEpiWarps);
         }
         mbar_init(drain_bar, 1);
+        mbar_init(piece_bar, 1);
         aborted = 0;
         fence_barrier_init();
         prefetch_tensormap(&p.w);
@@ -664,6 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             for (int i = 0; i < 16; ++i) __stcg(to + (at + i) * kMaxRows, sum[c + i]);
                         }
                     }
+                    asm volatile("fence.proxy.async;" ::: "memory");  // they will be read by a bulk copy
                     __threadfence();
                 }
                 epi_barrier_any(false);
@@ -675,29 +684,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 epi_barrier_any(false);
                 complete = epi_last != 0;
-                if (complete) {
-                    __threadfence();
-                    // the others' pieces, two at a time
-                    for (int k = 1; k < un.parts; k += 2) {
-                        const int32_t* const a = piece(un.part + k < un.parts ? un.part + k : un.part + k - un.parts);
-                        const bool two = k + 1 < un.parts;
-                        const int32_t* const b =
-                            two ? piece(un.part + k + 1 < un.parts ? un.part + k + 1 : un.part + k + 1 - un.parts) : a;
+                // The others' pieces by way of the ring, as many as fit: a pair has at most one
+                // unit of a split tile, its last, and all that the ring was filled for has been read.
+                const uint32_t bytes = static_cast<uint32_t>(p.tok) * (kMaxRows * 4);
+                const int fit = static_cast<int>(kRing / bytes);
+                for (int k = 1, round = 0; complete && k < un.parts; k += fit, ++round) {
+                    const int many = fit < un.parts - k ? fit : un.parts - k;
+                    if (warp == kFirstEpiWarp && lane == 0) {
+                        __threadfence();
+                        asm volatile("fence.proxy.async;" ::: "memory");
+                        mbar_arrive_expect_tx(piece_bar, bytes * static_cast<uint32_t>(many));
+                        for (int j = 0; j < many; ++j) {
+                            const int from = un.part + k + j < un.parts ? un.part + k + j : un.part + k + j - un.parts;
+                            bulk_load(base + j * bytes, piece(from) - row, bytes, piece_bar);
+                        }
+                    }
+                    failed = epi_barrier_any(!mbar_wait_soon(piece_bar, static_cast<uint32_t>(round) & 1u, limit));
+                    complete = !failed;
+                    if (!complete) break;
+                    for (int j = 0; j < many; ++j) {
+                        const int32_t* const from = reinterpret_cast<const int32_t*>(gbase + j * bytes) + row;
 #pragma unroll
                         for (int c = 0; c < kCols; c += 16) {
                             const int at = first + 2 * c;
                             if (at < p.tok) {
-                                int32_t v[16], w[16];
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    v[i] = __ldcg(a + (at + i) * kMaxRows);
-                                    w[i] = two ? __ldcg(b + (at + i) * kMaxRows) : 0;
-                                }
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) sum[c + i] += v[i] + w[i];
+                                for (int i = 0; i < 16; ++i) sum[c + i] += from[(at + i) * kMaxRows];
                             }
                         }
                     }
+                    epi_barrier_any(false);  // the ring may be written again
                 }
                 epi_barrier_any(false);  // epi_last may be written again
             }

@@ -2,7 +2,8 @@
 //   * tiles are ones the MMA and the copies can take (tokens a multiple of 16, at most
 //     192; a multiple of 8, at most 128, of weight rows per CTA), begin inside the result and cover it once;
 //   * every tile's stages are summed once, by its units, in order, none empty;
-//   * pieces and counts of split tiles are each unit's own and fit the workspace.
+//   * pieces and counts of split tiles are each unit's own and fit the workspace, and no pair has a
+//     unit after one of a split tile.
 // With "n d f" arguments it prints how those sizes are laid out at 76 pairs instead:
 // tokens and rows of a tile, whole tiles, units of the tiles after them.
 #include <cmath>
@@ -63,6 +64,7 @@ bool check(int n, int d, int f, int pairs) {
         if (un.parts > 1) {
             const int piece = un.split * un.parts + un.part;
             CHECK(piece < pairs && pieces.insert(piece).second);
+            CHECK(u + pairs >= p.n_units);  // the last unit of its pair
         }
     }
     for (const auto& [key, t] : tiles) CHECK(t.next == n_kb);
