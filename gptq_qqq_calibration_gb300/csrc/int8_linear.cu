@@ -71,7 +71,7 @@ constexpr size_t kSmemBytes = 1024 + kBarAt + 8 * kNumBarriers + 16;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 // Warp 0: weights, 2: tokens, 3: MMAs; from 4 on: converters, in groups of four that take the
 // stages in turn; then the epilogue.  (Tiles of up to 96 rows have no converter on the MMAs'
-// scheduler: 100 tokens at 8,192 x 2,048 20.0 us, 21.1 with warp 1 for the MMAs.)
+// scheduler: 128 tokens at 4,096 x 4,096 17.5 us, 19.1 with warp 1 for the MMAs.)
 constexpr int kGroups = 2, kFirstEpiWarp = 4 + 4 * kGroups, kEpiWarps = 8;
 constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
 constexpr unsigned long long kDrainLimitNs = 1000000000ull;
@@ -204,6 +204,7 @@ __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float x) { retur
 // The epilogue warps' barrier, and whether any thread came with `x`.
 __device__ __forceinline__ bool epi_barrier_any(bool x) {
     uint32_t any;
+    __syncwarp();  // lanes may come from a wait one by one
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
@@ -531,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                __syncwarp();
+                __syncwarp();  // lanes may come from the wait one by one
                 tc_fence_after();
                 const uint32_t to = tmem + lanes + 2 * p.acc_cols + static_cast<uint32_t>(slot) * kSlotCols;
                 tmem_st32(to, a);
