@@ -25,7 +25,7 @@
 // Bytes bound all of it: 16,384 x 11,008 bf16 take 97 us with a scale per 128 columns, 90
 // with one per row and 80 back (floor 80 at the copy rate of 6,781 GB/s), 32,768 x 4,096 fp32
 // 102 and 100 us (floor 99).  Rows that are no multiples of 16 bytes cost more instructions:
-// 16,383 x 8,191 bf16 97 us per 32 columns, 127 per row and 70 back (floor 59).
+// 16,383 x 8,191 bf16 97 us per 32 columns, 74 per row and 70 back (floor 59).
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -600,21 +600,36 @@ __global__ void __launch_bounds__(kGroupWarps * 32, 3) rows8_short_kernel(const 
 // the same granules of eight values, so only the maxima have to meet.  (Rows in
 // registers cost every warp its start and its scale for two segments of a row: 124 us
 // against 90 for 16,384 x 11,008 bf16.)
+// kAny: rows without gaps that start anywhere.  Granules are the matrix's, so that those of
+// values and those of codes fall together; a row's first and last one it shares with its
+// neighbours.  (16,383 x 8,191 bf16: 74 us; in runs that the rows' starts allow 127.)
 constexpr int kStreamThreads = 128;
 
-template <class T>
+template <class T, bool kAny>
 __global__ void __launch_bounds__(kStreamThreads) rows8_stream_kernel(const __grid_constant__ QuantizeParams p) {
     extern __shared__ uint4 buffers[];  // two rows
     __shared__ uint32_t tops[2][kStreamThreads / 32];
-    const int granules = p.d >> 3;
+    const int held = kAny ? (p.d >> 3) + 2 : p.d >> 3;  // granules of a buffer
+    const auto before = [&](int64_t r) { return kAny ? static_cast<int>((r * p.d) & 7) : 0; };
+    const auto granules_of = [&](int64_t r) { return kAny ? (before(r) + p.d + 7) >> 3 : p.d >> 3; };
     griddep_wait();
     griddep_launch_dependents();
     const auto fetch = [&](int64_t r, int b) {
         if (r < p.n) {
-            const uint4* const src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + r * p.ldx);
-            const uint32_t dst = smem_u32(buffers + b * granules);
-            for (int g = threadIdx.x; g < granules; g += kStreamThreads)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * g), "l"(src + g) : "memory");
+            const int granules = granules_of(r);
+            const int64_t start = kAny ? r * p.d - before(r) : r * p.ldx;
+            const uint4* const src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + start);
+            const uint32_t dst = smem_u32(buffers + b * held);
+            for (int g = threadIdx.x; g < granules; g += kStreamThreads) {
+                if constexpr (kAny) {  // nothing behind the matrix is read
+                    const int64_t left = p.n * p.d - start - 8 * static_cast<int64_t>(g);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16 * g), "l"(src + g),
+                                 "r"(left < 8 ? static_cast<uint32_t>(2 * left) : 16u)
+                                 : "memory");
+                } else {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * g), "l"(src + g) : "memory");
+                }
+            }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -624,13 +639,19 @@ __global__ void __launch_bounds__(kStreamThreads) rows8_stream_kernel(const __gr
     for (int64_t r = blockIdx.x; r < p.n; r += gridDim.x, b ^= 1) {
         fetch(r + gridDim.x, b ^ 1);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
-        const uint4* const row = buffers + b * granules;
+        const uint4* const row = buffers + b * held;
+        const int granules = granules_of(r), first = before(r), last = first + p.d;
         Raw<T, 8> raw;
         uint32_t top = 0;
 #pragma unroll 4
         for (int g = threadIdx.x; g < granules; g += kStreamThreads) {
             const uint4 v = row[g];
             raw.w[0] = v.x, raw.w[1] = v.y, raw.w[2] = v.z, raw.w[3] = v.w;
+            if (kAny && (g == 0 || g == granules - 1)) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (8 * g + k < first || 8 * g + k >= last) raw.w[k / 2] &= k & 1 ? 0x0000ffffu : 0xffff0000u;
+            }
             top = max(top, raw.top(0));
         }
         top = __reduce_max_sync(~0u, top);
@@ -640,7 +661,7 @@ __global__ void __launch_bounds__(kStreamThreads) rows8_stream_kernel(const __gr
         for (int i = 0; i < kStreamThreads / 32; ++i) top = max(top, tops[b][i]);
         const Scale s = scale_of<T>(top);
         if (threadIdx.x == 0) p.scale[r] = s.s;
-        int8_t* const codes = p.codes ? p.codes + r * p.ldc : nullptr;
+        int8_t* const codes = kAny ? p.codes + (r * p.d - first) : p.codes ? p.codes + r * p.ldc : nullptr;
         __half* const wide = p.codes ? nullptr : p.wide + r * p.ldw;
 #pragma unroll 2
         for (int g = threadIdx.x; g < granules; g += kStreamThreads) {
@@ -648,7 +669,14 @@ __global__ void __launch_bounds__(kStreamThreads) rows8_stream_kernel(const __gr
             raw.w[0] = v.x, raw.w[1] = v.y, raw.w[2] = v.z, raw.w[3] = v.w;
             uint32_t q[2];
             encode<T, 8>(raw, 0, s, q);
-            store<8>(codes, wide, 8 * g, q);
+            if (kAny && (g == 0 || g == granules - 1)) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (8 * g + k >= first && 8 * g + k < last)
+                        codes[8 * g + k] = static_cast<int8_t>(q[k / 4] >> (8 * (k % 4)));
+            } else {
+                store<8>(codes, wide, 8 * g, q);
+            }
         }
     }
 }
@@ -868,7 +896,8 @@ cudaError_t prepare(int* sms) {
     if (dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lk(mu);
     if (!count[dev]) {
-        for (auto fn : {rows8_stream_kernel<__nv_bfloat16>, rows8_stream_kernel<__half>})
+        for (auto fn : {rows8_stream_kernel<__nv_bfloat16, false>, rows8_stream_kernel<__half, false>,
+                        rows8_stream_kernel<__nv_bfloat16, true>, rows8_stream_kernel<__half, true>})
             if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem)) != cudaSuccess)
                 return e;
         if ((e = cudaDeviceGetAttribute(&count[dev], cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
@@ -887,6 +916,16 @@ cudaError_t launch_walk(Kernel kernel, const QuantizeParams& p, int ctas_per_sm,
     return rows_launch(kernel, p, all < fit ? all : fit, kGroupWarps * 32, s);
 }
 
+template <class Kernel>
+cudaError_t launch_stream(Kernel kernel, const QuantizeParams& p, size_t smem, cudaStream_t s) {
+    int sms = 0, per_sm = 0;
+    cudaError_t e = prepare(&sms);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kStreamThreads, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t fit = static_cast<int64_t>(sms) * (per_sm < 1 ? 1 : per_sm);
+    return rows_launch(kernel, p, p.n < fit ? p.n : fit, kStreamThreads, s, smem);
+}
+
 // A scale for every row of more than 256 values.  Few rows are spread over more warps
 // each, so that a row takes one round trip to memory and little work after it.
 template <class T, int V>
@@ -899,16 +938,8 @@ cudaError_t quantize_rows(QuantizeParams& p, cudaStream_t s) {
         return rows_launch(rows8_short_kernel<T, V>, p, all < fit ? all : fit, kGroupWarps * 32, s);
     }
     if constexpr (V == 8 && sizeof(T) == 2) {
-        const size_t smem = 4 * static_cast<size_t>(p.d);
-        if (p.n > 512 && smem <= kStreamSmem) {
-            int sms = 0, per_sm = 0;
-            cudaError_t e = prepare(&sms);
-            if (e == cudaSuccess)
-                e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, rows8_stream_kernel<T>, kStreamThreads, smem);
-            if (e != cudaSuccess) return e;
-            const int64_t fit = static_cast<int64_t>(sms) * (per_sm < 1 ? 1 : per_sm);
-            return rows_launch(rows8_stream_kernel<T>, p, p.n < fit ? p.n : fit, kStreamThreads, s, smem);
-        }
+        if (p.n > 512 && 4 * static_cast<size_t>(p.d) <= kStreamSmem)
+            return launch_stream(rows8_stream_kernel<T, false>, p, 4 * static_cast<size_t>(p.d), s);
     }
     const int segments = (p.d + kSegment - 1) / kSegment;
     const int h = p.n <= 512 && segments <= kRowWarps ? 1 : segments <= 2 * kRowWarps || sizeof(T) == 4 ? 2 : 4;
@@ -962,6 +993,10 @@ cudaError_t quantize_of(QuantizeParams& p, cudaStream_t s) {
                           : run_of(most, false, p.d, p.x, p.ldx, sizeof(T), p.wide, p.ldw, 2);
     if constexpr (sizeof(T) == 2) {
         if (v == 16) return quantize_as<T, 16>(p, s);
+        const size_t smem = 2 * 16 * static_cast<size_t>((p.d >> 3) + 2);
+        if (v < 8 && p.group == 0 && p.codes && p.ldx == p.d && p.ldc == p.d && p.d > kShort * kSegment && p.n > 512 &&
+            smem <= kStreamSmem && aligned(p.x, 0, 16) && aligned(p.codes, 0, 8))
+            return launch_stream(rows8_stream_kernel<T, true>, p, smem, s);
     }
     return v == 8   ? quantize_as<T, 8>(p, s)
            : v == 4 ? quantize_as<T, 4>(p, s)

@@ -70,7 +70,8 @@ def check(x, group, X=None):
 SIZES = [(1, 1), (1, 8), (3, 7), (2, 31), (5, 33), (4, 256), (3, 257), (7, 520), (1, 1024), (2, 1025), (33, 2564),
          (1, 4096), (600, 264), (513, 1032), (700, 1480), (2, 16384), (2, 16392), (530, 4104), (3, 70000), (1, 69999),
          # rows that join to longer ones, and rows whose ends cut the runs of a restoring lane
-         (67, 128), (1001, 64), (4099, 32), (130, 256), (90, 384), (40, 8191), (11, 17), (600, 35), (300, 259)]
+         (67, 128), (1001, 64), (4099, 32), (130, 256), (90, 384), (40, 8191), (11, 17), (600, 35), (300, 259),
+         (519, 1033), (700, 2049), (1601, 8191), (515, 1990), (2000, 1100)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
