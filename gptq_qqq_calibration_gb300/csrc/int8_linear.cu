@@ -659,18 +659,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             };
             bool complete = !failed;
             if (un.parts > 1) {
-                // pieces: [token][row], so that a warp moves 128 bytes at a time
+                // pieces: [token / 4][row][4], so that a thread moves 16 bytes at a time
                 const auto piece = [&](int k) {
-                    return p.pieces + (2 * static_cast<int64_t>(un.split * un.parts + k) + rank) * kPieceInts + row;
+                    return reinterpret_cast<int4*>(p.pieces + (2 * static_cast<int64_t>(un.split * un.parts + k) + rank) * kPieceInts);
                 };
                 if (!failed) {
-                    int32_t* const to = piece(un.part);
+                    int4* const to = piece(un.part) + row;
 #pragma unroll
                     for (int c = 0; c < kCols; c += 16) {
                         const int at = first + 2 * c;
                         if (at < p.tok) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) __stcg(to + (at + i) * kMaxRows, sum[c + i]);
+                            for (int i = 0; i < 16; i += 4)
+                                __stcg(to + (at + i) / 4 * kMaxRows,
+                                       make_int4(sum[c + i], sum[c + i + 1], sum[c + i + 2], sum[c + i + 3]));
                         }
                     }
                     asm volatile("fence.proxy.async;" ::: "memory");  // they will be read by a bulk copy
@@ -697,20 +699,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         mbar_arrive_expect_tx(piece_bar, bytes * static_cast<uint32_t>(many));
                         for (int j = 0; j < many; ++j) {
                             const int from = un.part + k + j < un.parts ? un.part + k + j : un.part + k + j - un.parts;
-                            bulk_load(base + j * bytes, piece(from) - row, bytes, piece_bar);
+                            bulk_load(base + j * bytes, piece(from), bytes, piece_bar);
                         }
                     }
                     failed = epi_barrier_any(!mbar_wait_soon(piece_bar, static_cast<uint32_t>(round) & 1u, limit));
                     complete = !failed;
                     if (!complete) break;
                     for (int j = 0; j < many; ++j) {
-                        const int32_t* const from = reinterpret_cast<const int32_t*>(gbase + j * bytes) + row;
+                        const int4* const from = reinterpret_cast<const int4*>(gbase + j * bytes) + row;
 #pragma unroll
                         for (int c = 0; c < kCols; c += 16) {
                             const int at = first + 2 * c;
                             if (at < p.tok) {
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) sum[c + i] += from[(at + i) * kMaxRows];
+                                for (int i = 0; i < 16; i += 4) {
+                                    const int4 v = from[(at + i) / 4 * kMaxRows];
+                                    sum[c + i] += v.x, sum[c + i + 1] += v.y, sum[c + i + 2] += v.z, sum[c + i + 3] += v.w;
+                                }
                             }
                         }
                     }

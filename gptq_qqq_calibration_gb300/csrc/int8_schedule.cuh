@@ -60,12 +60,14 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tiles and splits for n tokens.  In SM cycles, a stage costs what bounds it: the MMAs
 // (4 a token), their issue and what it waits for (kIssue; kAlone less where no converter
-// shares the MMAs' scheduler), or the weights' way from memory
-// (16 bytes a row over 3 cycles at 24 bytes a cycle and SM).  A turn of units costs
-// kTurn more; a tile in pieces kSplit for meeting, and 32 a token for each piece but one that
-// the last pair there reads.
+// shares the MMAs' scheduler), or the weights' way from memory (16 bytes a row over 3 cycles
+// at 24 bytes a cycle and SM).  A turn of units costs kTurn more.  Tiles in pieces cost their
+// meeting, and the last pair's reading of each piece but its own: 10,000 cycles and 24 a token,
+// or 5,000 and 12 where whole tiles come before them, whose way out it hides behind.  (Fitted:
+// 1,000 tokens at 8,192 x 4,096 56.7 us, whole tiles alone 65.3; at 4,096 x 4,096 39.0 and 40.7; 200
+// there 17.7 us whole, 18.8 in pieces.)
 inline void plan(Schedule& p, int64_t pairs) {
-    constexpr int64_t kIssue = 800, kAlone = 100, kTurn = 700, kSplit = 9000;
+    constexpr int64_t kIssue = 800, kAlone = 100, kTurn = 700;
     const int64_t n_kb = ceil_div(p.d, kKB);
     p.tiles_t = static_cast<int32_t>(ceil_div(p.n, kMaxTok));
     p.tok = static_cast<int32_t>(ceil_div(ceil_div(p.n, p.tiles_t), 16) * 16);
@@ -83,7 +85,7 @@ inline void plan(Schedule& p, int64_t pairs) {
         for (int64_t s = 1; s <= kMaxParts && s <= n_kb && (s == 1 || rest * s <= pairs); ++s) {
             int64_t cost = turns * (n_kb * stage + kTurn);
             if (rest > 0) cost += ceil_div(n_kb, s) * stage + kTurn;
-            if (s > 1) cost += kSplit + 32 * p.tok * (s - 1);
+            if (s > 1) cost += turns > 0 ? 5000 + 12 * p.tok * (s - 1) : 10000 + 24 * p.tok * (s - 1);
             if (best < 0 || cost < best) {
                 best = cost;
                 p.rows = static_cast<int32_t>(rows);
