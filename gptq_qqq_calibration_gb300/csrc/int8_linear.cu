@@ -511,10 +511,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const Unit un = unit_at(p, u);
             int kb = un.kb0 + skip;
             for (; kb < un.kb1; kb += kGroups) {
-                if (!mbar_wait_soon(wfull_bar(stage), phase, limit)) {
-                    ok = false;
-                    break;
-                }
+                bool come = mbar_wait_soon(wfull_bar(stage), phase, limit);
                 const uint32_t src = base + stage * p.stage_bytes + row * 128u;
                 const auto load = [&](int j) {
                     return mine ? lds128(src + ((j ^ (row & 7)) << 4)) : make_uint4(0, 0, 0, 0);
@@ -528,11 +525,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 uint32_t a[32];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) widen16(load(j), a + 8 * j);
-                if (before >= 0 && !mbar_wait_soon(done_bar(before), bphase, limit)) {
-                    ok = false;
-                    break;
-                }
-                __syncwarp();  // lanes may come from the wait one by one
+                if (before >= 0) come = mbar_wait_soon(done_bar(before), bphase, limit) && come;
+                // The warp goes on together or not at all: each lane's waits have a clock of their own, and
+                // lanes that gave up alone would be waited for below without a limit.  (What was
+                // read above after a wait that ran out goes nowhere.  A vote for each wait spills.)
+                ok = __all_sync(~0u, come);
+                if (!ok) break;
                 tc_fence_after();
                 const uint32_t to = tmem + lanes + 2 * p.acc_cols + static_cast<uint32_t>(slot) * kSlotCols;
                 tmem_st32(to, a);

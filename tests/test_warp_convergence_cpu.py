@@ -1,0 +1,98 @@
+"""Whole warps act together in the kernels' sources: what no run can show safely.
+
+A wait with a limit that each lane of a warp takes for itself may end differently in
+each; unless the warp agrees on the outcome, some lanes leave and the others wait for
+them at the next warp-wide instruction without a limit.  The tests read the kernels'
+sources, so that the fault needs no GPU.
+"""
+
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "gptq_qqq_calibration_gb300", "csrc")
+
+
+def code_of(name):
+    """The file without comments and with its strings kept."""
+    text = open(os.path.join(CSRC, name)).read()
+    return re.sub(r"//[^\n]*", "", text)
+
+
+def body_of(code, kernel):
+    """The body of `kernel`, from its first brace to the one that closes it."""
+    at = code.index("{", code.index(kernel + "("))
+    depth = 0
+    for i in range(at, len(code)):
+        depth += {"{": 1, "}": -1}.get(code[i], 0)
+        if depth == 0:
+            return code[at:i + 1]
+    raise AssertionError("unbalanced braces")
+
+
+def statements(body):
+    """(statement, the headers of the blocks around it) of a body, in order."""
+    found, around, start, parens = [], [], 1, 0
+    for i in range(1, len(body) - 1):
+        c = body[i]
+        parens += {"(": 1, ")": -1}.get(c, 0)
+        # (a lambda's body inside an argument list is part of its statement)
+        if parens == 0 and c in "{};":
+            text = " ".join(body[start:i].split())
+            if c == "{":
+                around.append(text)
+            else:
+                if text:
+                    found.append((text, tuple(around)))
+                if c == "}" and around:
+                    around.pop()
+            start = i + 1
+    return found
+
+
+ONE_LANE = re.compile(r"lane == 0|elect_one\(\)|threadIdx\.x == 0|leader")
+
+
+@pytest.mark.parametrize("text,bad", [
+    ("{ if (warp == 0 && lane == 0) { if (!wait(x)) { ok = 1; } } }", 0),
+    ("{ for (;;) { if (!wait(x)) { ok = 1; break; } } }", 1),
+    ("{ bool come = wait(x); read(); come = wait(y) && come; ok = __all_sync(~0u, come); }", 0),
+    ("{ bool come = wait(x); if (!come) break; ok = __all_sync(~0u, come); }", 1),
+    ("{ ok = __all_sync(~0u, wait(x)); if (elect_one()) { if (!wait(y)) z(); } }", 0)])
+def test_reader(text, bad):
+    assert len(lone_waits(text, "wait")) == bad
+
+
+VOTE = re.compile(r"__all_sync\(|epi_barrier_any\(")
+
+
+def lone_waits(body, wait):
+    """Waits that lanes of a warp take one by one, without agreeing on the outcome: neither
+    in a branch of one lane, nor in a vote, nor kept in a variable that is next seen in one."""
+    lines, headers = [], set()
+    for text, around in statements(body):
+        for k, h in enumerate(around):  # a block's header is a statement of its own
+            if (h, around[:k]) not in headers:
+                headers.add((h, around[:k]))
+                lines.append((h, around[:k]))
+        if text:
+            lines.append((text, around))
+    bad = []
+    for i, (text, around) in enumerate(lines):
+        if wait + "(" not in text or VOTE.search(text) or any(ONE_LANE.search(a) for a in around):
+            continue
+        kept = re.search(r"\b(\w+) = [^=]*" + wait + r"\(", text)
+        if kept:
+            name = kept.group(1)
+            uses = [t for t, _ in lines[i + 1:] if re.search(r"\b%s\b" % name, t) and not re.search(r"\b%s = [^=]*%s\(" % (name, wait), t)]
+            if uses and re.search(r"__all_sync\(~0u, %s\)" % name, uses[0]):
+                continue
+        bad.append(text)
+    return bad
+
+
+def test_integer_layer_waits_are_agreed_on():
+    body = body_of(code_of("int8_linear.cu"), "int8_pair_kernel")
+    assert body.count("mbar_wait_soon(") >= 5
+    assert lone_waits(body, "mbar_wait_soon") == []
