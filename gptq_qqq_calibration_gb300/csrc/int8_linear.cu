@@ -449,6 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             if (a >= p.slots) a -= p.slots, ap ^= 1u;
                             const uint32_t bar = lane & 1 ? afull_bar(a) : xfull_bar(s), parity = lane & 1 ? ap : sp;
                             known = (__ffs(~__ballot_sync(~0u, mbar_test(bar, parity)) | 1 << 2 * look) - 1) >> 1;
+                            __syncwarp();  // what each lane saw complete is complete for the lane that issues (a ballot orders nothing)
                             if (known == 0) {
                                 ok = __all_sync(~0u, mbar_wait_soon(xfull_bar(stage), phase, limit) &&
                                                          mbar_wait_soon(afull_bar(slot), sphase, limit));

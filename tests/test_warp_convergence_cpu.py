@@ -96,3 +96,13 @@ def test_integer_layer_waits_are_agreed_on():
     body = body_of(code_of("int8_linear.cu"), "int8_pair_kernel")
     assert body.count("mbar_wait_soon(") >= 5
     assert lone_waits(body, "mbar_wait_soon") == []
+
+
+def test_barriers_tested_by_other_lanes_are_ordered():
+    """Lanes test barriers for each other: what they saw is passed on by a warp barrier, as votes
+    order no memory."""
+    body = body_of(code_of("int8_linear.cu"), "int8_pair_kernel")
+    order = [text for text, _ in statements(body)]
+    shared = [i for i, text in enumerate(order) if "mbar_test(" in text]
+    assert len(shared) == 1
+    assert "__ballot_sync(" in order[shared[0]] and order[shared[0] + 1] == "__syncwarp()"
