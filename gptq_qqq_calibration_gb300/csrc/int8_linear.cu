@@ -338,6 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&p.x);
         prefetch_tensormap(&p.y);
     }
+    __syncwarp();
     if (warp == 1) {
         tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish_pair();
@@ -575,14 +576,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t buffers = base + kRing + group * (2 * kStagingBytes);
         uint32_t buffer = buffers;
         const uint32_t acce0 = mapa_shared(acce_bar(0), 0);
+        const auto half_barrier = [&] {
+            __syncwarp();  // the barrier takes whole warps, and lanes may come from a branch of their own
+            asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
+        };
         // A half's four warps write one buffer while the other is on its way.
         const auto begin = [&] {
             if (leader) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-            asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
+            half_barrier();
         };
         const auto end = [&](auto issue) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
+            half_barrier();
             if (leader) {
                 issue();
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
@@ -727,7 +732,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < kCols; c += 16)
                     if (first + 2 * c < p.tok) finish(c, sum + c);
             }
-            asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");  // the scales may be written again
+            half_barrier();  // the scales may be written again
         }
         if (leader) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         if (failed && lane == 0) {
@@ -743,6 +748,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < kAbortSettleNs) __nanosleep(1000);
     }
+    __syncwarp();  // each lane has a clock of its own
     tc_fence_before();
     cluster_sync_all();
     if (warp == 1) {

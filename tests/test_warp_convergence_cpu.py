@@ -106,3 +106,35 @@ def test_barriers_tested_by_other_lanes_are_ordered():
     shared = [i for i, text in enumerate(order) if "mbar_test(" in text]
     assert len(shared) == 1
     assert "__ballot_sync(" in order[shared[0]] and order[shared[0] + 1] == "__syncwarp()"
+
+
+WARP_WIDE = re.compile(r"bar\.sync|bar\.red|cluster_sync_all\(\)|tmem_dealloc|tmem_alloc")
+TOGETHER = re.compile(r"__syncwarp\(\)|__syncthreads\(\)|cluster_sync_all\(\)")
+
+
+def loose_barriers(body):
+    """Warp-wide barriers and tensor-memory calls with no point in front where the warp's lanes meet."""
+    order = [text for text, _ in statements(body)]
+    bad = []
+    for i, text in enumerate(order):
+        if not WARP_WIDE.search(text):
+            continue
+        before = [t for t in order[:i] if t and not re.match(r"tc_fence_|tmem_|uint32_t any$", t)]
+        if not before or not TOGETHER.search(before[-1]):
+            bad.append(text)
+    return bad
+
+
+@pytest.mark.parametrize("text,bad", [
+    ("{ __syncwarp(); asm(\"bar.sync 1, 128;\"); }", 0),
+    ("{ if (leader) { issue(); } asm(\"bar.sync 1, 128;\"); }", 1),
+    ("{ __syncthreads(); if (x) { while (late()) nap(); } tc_fence_before(); cluster_sync_all(); }", 1),
+    ("{ __syncwarp(); tc_fence_before(); cluster_sync_all(); if (warp == 1) { tc_fence_after(); tmem_dealloc(t); } }", 0)])
+def test_barrier_reader(text, bad):
+    assert len(loose_barriers(text)) == bad
+
+
+def test_integer_layer_warps_meet_before_barriers():
+    code = code_of("int8_linear.cu")
+    for name in ("epi_barrier_any", "int8_pair_kernel"):
+        assert loose_barriers(body_of(code, name)) == [], name
