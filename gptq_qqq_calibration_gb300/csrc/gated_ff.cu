@@ -157,13 +157,16 @@ __device__ __forceinline__ float gate_sigmoid(float g, int act, float& dz) {
     return __fdividef(1.0f, 1.0f + __expf(-z));
 }
 
-// The epilogue warps' own barrier.
+// The epilogue warps' own barrier.  (Barriers take whole warps: lanes that may come from a
+// branch or from a wait one by one meet first.)
 __device__ __forceinline__ void epi_barrier() {
+    __syncwarp();
     asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
 }
 // The same, and whether any thread came with `x`: every thread gets the same answer.
 __device__ __forceinline__ bool epi_barrier_any(bool x) {
     uint32_t any;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
@@ -184,7 +187,10 @@ struct OutBuffer {
     uint32_t addr;
     int barrier, row;  // this thread's row
     bool leader;
-    __device__ void sync() const { asm volatile("bar.sync %0, 128;" ::"r"(barrier) : "memory"); }
+    __device__ void sync() const {
+        __syncwarp();
+        asm volatile("bar.sync %0, 128;" ::"r"(barrier) : "memory");
+    }
     // the buffer's former content has been read
     __device__ void begin() const {
         if (leader) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -230,6 +236,7 @@ __device__ __forceinline__ void finish_tile(const FfParams& p, const Unit& un, i
                 const T* const dh = static_cast<const T*>(p.dh) + row * p.f + n0 + c;
                 if (in && n0 + c < p.f) dv[0] = *reinterpret_cast<const uint4*>(dh);
                 if (in && n0 + c + 8 < p.f) dv[1] = *reinterpret_cast<const uint4*>(dh + 8);
+                __syncwarp();  // the sums' loads take whole warps
             }
             uint32_t g[16], u[16];
             load(half * 64 + c, g, 128 + half * 64 + c, u);
@@ -329,6 +336,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         aborted = 0;
         fence_barrier_init();
     }
+    __syncwarp();
     if (warp == 1) {
         tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish_pair();
@@ -548,6 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < kAbortSettleNs) __nanosleep(1000);
     }
+    __syncwarp();  // each lane has a clock of its own
     tc_fence_before();
     cluster_sync_all();
     if (warp == 1) {
@@ -637,6 +646,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) gated_ff_few_kernel(const __gr
         fence_barrier_init();
         for (int m = 0; m < 3; ++m) prefetch_tensormap(&p.maps[m]);
     }
+    __syncwarp();
     if (warp == 1) {
         tmem_alloc(smem_u32(tmem_slot), 2 * kFewTokens);
         tmem_relinquish();
@@ -752,6 +762,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) gated_ff_few_kernel(const __gr
             // every epilogue warp takes every turn: they meet at a barrier in each
             for (int c = 0; c < p.n_cols; c += 16) {
                 uint32_t a[16];
+                __syncwarp();  // lanes come from the wait, or from their results, one by one
                 tmem_ld16(acc + c, a);
                 tmem_wait16(a, a);
                 float* const ex = exch + buf * (2 * 16 * 64);
@@ -760,6 +771,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) gated_ff_few_kernel(const __gr
 #pragma unroll
                     for (int i = 0; i < 16; ++i) ex[at + i * 64] = __uint_as_float(a[i]);
                 }
+                __syncwarp();
                 asm volatile("bar.sync 1, 128;" ::: "memory");
                 if (mine && c + c8 < p.n) {
                     uint16_t h[8];
@@ -791,6 +803,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) gated_ff_few_kernel(const __gr
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < kAbortSettleNs) __nanosleep(1000);
     }
+    __syncwarp();  // each lane has a clock of its own
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 2 * kFewTokens);

@@ -138,3 +138,11 @@ def test_integer_layer_warps_meet_before_barriers():
     code = code_of("int8_linear.cu")
     for name in ("epi_barrier_any", "int8_pair_kernel"):
         assert loose_barriers(body_of(code, name)) == [], name
+
+
+def test_feed_forward_warps_meet_before_barriers():
+    code = code_of("gated_ff.cu")
+    for name in ("epi_barrier", "epi_barrier_any", "void sync", "gated_ff_kernel", "gated_ff_few_kernel"):
+        body = body_of(code, name)
+        assert WARP_WIDE.search(body), name
+        assert loose_barriers(body) == [], name
