@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) gated_ff_few_kernel(const __gr
         int ab = 0, buf = 0;
         uint32_t aphase = 0;
         for (int t = blockIdx.x; t < p.n_tiles; t += gridDim.x) {
-            const bool ok = aborted == 0 && mbar_wait(accf_bar(ab), aphase, limit);
+            const bool ok = warp_came(aborted == 0 && mbar_wait(accf_bar(ab), aphase, limit));
             if (!ok && lane == 0) {
                 atomicOr(p.status, kStatusTimeoutEpilogue);
                 aborted = 1;

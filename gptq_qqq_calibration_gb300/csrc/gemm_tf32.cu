@@ -161,8 +161,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tf32_kernel(const __grid_con
     auto convert_stage = [&](int ci, uint32_t converted) -> bool {
         const int s = converted % kLand;
         const int c = converted % kCvt;
-        if (!mbar_wait(land_full(s), (converted / kLand) & 1u, limit) ||
-            !mbar_wait(cvt_empty(c), ((converted / kCvt) & 1u) ^ 1u, limit))
+        if (!warp_came(mbar_wait(land_full(s), (converted / kLand) & 1u, limit) &&
+                       mbar_wait(cvt_empty(c), ((converted / kCvt) & 1u) ^ 1u, limit)))
             return false;
         constexpr int kRoundsPerOp = static_cast<int>(kOpBytes / 16 / kRoundWords);
         constexpr int kLd = kRoundWords / 32;  // 16-byte loads per lane per round
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tf32_kernel(const __grid_con
         int ab = 0;
         uint32_t aphase = 0;
         for (int u = blockIdx.x; u < p.n_units; u += gridDim.x) {
-            if (!mbar_wait(accf_bar(ab), aphase, limit)) {
+            if (!warp_came(mbar_wait(accf_bar(ab), aphase, limit))) {
                 ok = false;
                 break;
             }

@@ -427,7 +427,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int u = pair; ok && u < p.n_units; u += n_pairs) {
                 const Unit un = unit_at(p, u);
                 for (int c0 = un.kb0; ok && c0 < un.kb1; c0 += kChunk) {
-                    ok = __all_sync(~0u, mbar_wait_soon(acce_bar(ab), aphase ^ 1u, limit));
+                    ok = warp_came(mbar_wait_soon(acce_bar(ab), aphase ^ 1u, limit));
                     if (!ok) break;
                     const uint32_t acc = tmem + static_cast<uint32_t>(ab) * p.acc_cols;
                     const int c1 = c0 + kChunk < un.kb1 ? c0 + kChunk : un.kb1;
@@ -439,8 +439,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             umma_f16_pair_ta(acc, a + 24u, at + 6u, high, idesc, 1u);
                         };
                         if (kTok == kMaxTok) {
-                            ok = __all_sync(~0u, mbar_wait_soon(xfull_bar(stage), phase, limit) &&
-                                                     mbar_wait_soon(afull_bar(slot), sphase, limit));
+                            ok = warp_came(mbar_wait_soon(xfull_bar(stage), phase, limit) &&
+                                           mbar_wait_soon(afull_bar(slot), sphase, limit));
                             if (!ok) break;
                         } else if (known == 0) {
                             // even lanes ask for tokens, odd ones for slots of A, of this stage and those after it
@@ -452,8 +452,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             known = (__ffs(~__ballot_sync(~0u, mbar_test(bar, parity)) | 1 << 2 * look) - 1) >> 1;
                             __syncwarp();  // what each lane saw complete is complete for the lane that issues (a ballot orders nothing)
                             if (known == 0) {
-                                ok = __all_sync(~0u, mbar_wait_soon(xfull_bar(stage), phase, limit) &&
-                                                         mbar_wait_soon(afull_bar(slot), sphase, limit));
+                                ok = warp_came(mbar_wait_soon(xfull_bar(stage), phase, limit) &&
+                                               mbar_wait_soon(afull_bar(slot), sphase, limit));
                                 if (!ok) break;
                                 known = 1;
                             }
@@ -531,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // The warp goes on together or not at all: each lane's waits have a clock of their own, and
                 // lanes that gave up alone would be waited for below without a limit.  (What was
                 // read above after a wait that ran out goes nowhere.  A vote for each wait spills.)
-                ok = __all_sync(~0u, come);
+                ok = warp_came(come);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t to = tmem + lanes + 2 * p.acc_cols + static_cast<uint32_t>(slot) * kSlotCols;

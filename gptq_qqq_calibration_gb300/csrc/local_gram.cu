@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) local_gram_kernel(const __grid_const
     int stage = 0, steps = 0;
     uint32_t phase = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(full_bar(stage), phase, p.timeout_ns)) {
+        if (!warp_came(mbar_wait(full_bar(stage), phase, p.timeout_ns))) {
             ok = false;
             break;
         }

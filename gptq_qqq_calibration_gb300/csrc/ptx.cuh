@@ -72,6 +72,11 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
     }
 }
 
+// One outcome for a warp whose lanes have all waited: whether every wait kept its limit.  Each
+// lane's limit is its own, and lanes that gave up alone would be waited for by the others, at
+// the next warp-wide instruction, without one.
+__device__ __forceinline__ bool warp_came(bool came) { return __all_sync(~0u, came) != 0; }
+
 // -------------------------------------------------------------------- TMA
 
 // 2-D tiled load of one box into shared memory; completion is signalled on

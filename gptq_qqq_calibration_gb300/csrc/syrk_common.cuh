@@ -82,7 +82,7 @@ __device__ __forceinline__ void epilogue_t(const SyrkParams& p, uint32_t tmem, i
         }
         int g = 0;  // chunks in mid
         for (int c = 0; c < nch; ++c) {
-            if (!wait_full(accf_bar0 + 8u * ab, aphase)) {
+            if (!warp_came(wait_full(accf_bar0 + 8u * ab, aphase))) {
                 ok = false;
                 break;
             }

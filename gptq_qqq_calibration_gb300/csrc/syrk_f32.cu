@@ -170,8 +170,8 @@ __global__ void __launch_bounds__(kThreads, 1) syrk_f32_kernel(const __grid_cons
     auto convert_stage = [&](int ci, const Cursor& C, uint32_t converted) -> bool {
         const int s = converted % kLand;
         const int c = converted % kCvt;
-        if (!mbar_wait(land_full(s), (converted / kLand) & 1u, limit) ||
-            !mbar_wait(cvt_empty(c), ((converted / kCvt) & 1u) ^ 1u, limit))
+        if (!warp_came(mbar_wait(land_full(s), (converted / kLand) & 1u, limit) &&
+                       mbar_wait(cvt_empty(c), ((converted / kCvt) & 1u) ^ 1u, limit)))
             return false;
         const bool diag = C.un.I == C.un.J;
         constexpr int kRoundsPerOp = static_cast<int>(kOpBytes / 16 / kRoundWords);

@@ -57,14 +57,14 @@ ONE_LANE = re.compile(r"lane == 0|elect_one\(\)|threadIdx\.x == 0|leader")
 @pytest.mark.parametrize("text,bad", [
     ("{ if (warp == 0 && lane == 0) { if (!wait(x)) { ok = 1; } } }", 0),
     ("{ for (;;) { if (!wait(x)) { ok = 1; break; } } }", 1),
-    ("{ bool come = wait(x); read(); come = wait(y) && come; ok = __all_sync(~0u, come); }", 0),
-    ("{ bool come = wait(x); if (!come) break; ok = __all_sync(~0u, come); }", 1),
-    ("{ ok = __all_sync(~0u, wait(x)); if (elect_one()) { if (!wait(y)) z(); } }", 0)])
+    ("{ bool come = wait(x); read(); come = wait(y) && come; ok = warp_came(come); }", 0),
+    ("{ bool come = wait(x); if (!come) break; ok = warp_came(come); }", 1),
+    ("{ ok = warp_came(wait(x)); if (elect_one()) { if (!wait(y)) z(); } }", 0)])
 def test_reader(text, bad):
     assert len(lone_waits(text, "wait")) == bad
 
 
-VOTE = re.compile(r"__all_sync\(|epi_barrier_any\(")
+VOTE = re.compile(r"warp_came\(|epi_barrier_any\(|epilogue_t<")  # (epilogue_t votes itself)
 
 
 def lone_waits(body, wait):
@@ -86,7 +86,7 @@ def lone_waits(body, wait):
         if kept:
             name = kept.group(1)
             uses = [t for t, _ in lines[i + 1:] if re.search(r"\b%s\b" % name, t) and not re.search(r"\b%s = [^=]*%s\(" % (name, wait), t)]
-            if uses and re.search(r"__all_sync\(~0u, %s\)" % name, uses[0]):
+            if uses and re.search(r"warp_came\(%s\)" % name, uses[0]):
                 continue
         bad.append(text)
     return bad
@@ -146,3 +146,17 @@ def test_feed_forward_warps_meet_before_barriers():
         body = body_of(code, name)
         assert WARP_WIDE.search(body), name
         assert loose_barriers(body) == [], name
+
+
+@pytest.mark.parametrize("name,kernels,wait", [
+    ("gated_ff.cu", ["gated_ff_kernel", "gated_ff_few_kernel"], r"mbar_wait"),
+    ("syrk_common.cuh", ["epilogue_t"], "wait_full"), ("syrk_bf16.cu", ["syrk_bf16_kernel"], "mbar_wait"),
+    ("syrk_bf16_2sm.cu", ["syrk_bf16_2sm_kernel"], "mbar_wait"),
+    ("syrk_f32.cu", ["syrk_f32_kernel"], "mbar_wait"), ("gemm_tf32.cu", ["gemm_tf32_kernel"], "mbar_wait"),
+    ("local_gram.cu", ["local_gram_kernel"], "mbar_wait")])
+def test_other_kernels_waits_are_agreed_on(name, kernels, wait):
+    code = code_of(name)
+    for kernel in kernels:
+        body = body_of(code, kernel).replace("mbar_wait_cluster(", "mbar_wait(")
+        assert wait + "(" in body
+        assert lone_waits(body, wait) == [], kernel
