@@ -283,8 +283,10 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t local, uint32_t rank) {
     return r;
 }
 
-// Every thread of every CTA of the cluster; release/acquire at cluster scope.
+// Every thread of every CTA of the cluster; release/acquire at cluster scope.  (The barrier takes
+// whole warps, whose lanes may come from branches of their own.)
 __device__ __forceinline__ void cluster_sync_all() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
 }

@@ -160,3 +160,8 @@ def test_other_kernels_waits_are_agreed_on(name, kernels, wait):
         body = body_of(code, kernel).replace("mbar_wait_cluster(", "mbar_wait(")
         assert wait + "(" in body
         assert lone_waits(body, wait) == [], kernel
+
+
+def test_cluster_barrier_brings_warps_together():
+    order = [text for text, _ in statements(body_of(code_of("ptx.cuh"), "void cluster_sync_all"))]
+    assert order[0] == "__syncwarp()" and "barrier.cluster.arrive" in order[1]
