@@ -1,0 +1,31 @@
+// How a code is decided near a half, and how codes become float16: for the kernels that make
+// or read 8-bit rows (formulas: include/rows8.h).
+#pragma once
+
+#include <cstdint>
+#include <cstring>
+
+#include <cuda_fp16.h>
+
+namespace hk {
+
+// Scales below 2^-100 and their values are taken 2^64 times (exactly), so that no remainder
+// below falls under float32's smallest step: at a scale of 2^-126 it would already be a half
+// of one.
+constexpr float kLiftBelow = 7.888609052210118e-31f;  // 2^-100
+constexpr float kLift = 18446744073709551616.0f;      // 2^64
+
+// rint of the exact quotient x / s, from t within 2^-16 of it and |t| <= 127.  Near a half the
+// sign of x - (half) s, which a fused multiply-add gives exactly, says on which side of it the
+// quotient lies.  s is at least 2^-100.
+__device__ __forceinline__ int nearest_code(float t, float x, float s) {
+    float q = rintf(t);
+    if (fabsf(__fsub_rn(t, q)) > 0.5f - 1.0f / 32768.0f) {
+        const float below = floorf(t), half = __fadd_rn(below, 0.5f);
+        const float e = __fmaf_rn(-half, s, x);
+        q = e > 0.0f ? __fadd_rn(below, 1.0f) : e < 0.0f ? below : rintf(half);
+    }
+    return static_cast<int>(q);
+}
+
+}  // namespace hk

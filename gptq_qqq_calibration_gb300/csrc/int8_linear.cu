@@ -37,6 +37,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "codes8.cuh"
 #include "device_ptr.h"
 #include "int8_linear.cuh"
 #include "int8_linear.h"
@@ -243,28 +244,21 @@ __device__ __forceinline__ uint32_t top_of8(const uint4& v) {
 
 struct TokenScale {
     float stored;     // the scale; NaN where a value is not finite
-    float up, s, r;   // values and scale are both taken `up` times (2^64 for a subnormal scale), 1/s
+    float up, s, r;   // values and scale are both taken `up` times (2^64 for a small scale), 1/s
 };
 __device__ __forceinline__ TokenScale token_scale(uint32_t top) {
     TokenScale k;
     const bool finite = top < 0x7f800000u;
     k.s = finite ? __fdiv_rn(__uint_as_float(top), 127.0f) : 0.0f;
     k.stored = finite ? k.s : __uint_as_float(0x7fffffffu);
-    k.up = k.s < 1.17549435e-38f ? 18446744073709551616.0f : 1.0f;
+    k.up = k.s < kLiftBelow ? kLift : 1.0f;
     k.s = __fmul_rn(k.s, k.up);
     k.r = k.s > 0.0f ? __frcp_rn(k.s) : 0.0f;
     return k;
 }
 __device__ __forceinline__ int token_code(float x, const TokenScale& k) {
     x = __fmul_rn(x, k.up);
-    const float t = fminf(fmaxf(__fmul_rn(x, k.r), -127.0f), 127.0f);
-    float q = rintf(t);
-    if (fabsf(__fsub_rn(t, q)) > 0.5f - 1.0f / 32768.0f) {
-        const float lo = floorf(t), half = __fadd_rn(lo, 0.5f);
-        const float e = __fmaf_rn(-half, k.s, x);
-        q = e > 0.0f ? __fadd_rn(lo, 1.0f) : e < 0.0f ? lo : rintf(half);
-    }
-    return static_cast<int>(q);
+    return nearest_code(fminf(fmaxf(__fmul_rn(x, k.r), -127.0f), 127.0f), x, k.s);
 }
 // Eight codes, as bytes.
 template <class T>

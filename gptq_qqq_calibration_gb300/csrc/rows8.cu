@@ -34,6 +34,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "codes8.cuh"
 #include "device_ptr.h"
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -144,7 +145,6 @@ struct Scale {
     float s, lo, hi;  // 16-bit values: lo alone
     bool plain;       // codes by the multipliers; otherwise by `code_of`
 };
-constexpr float kTwo64 = 18446744073709551616.0f;
 
 template <class T>
 __device__ __forceinline__ Scale scale_of(uint32_t top) {
@@ -181,23 +181,14 @@ __device__ __forceinline__ Scale scale_of(uint32_t top) {
     return k;
 }
 
-// rint(x / s) of the exact quotient.  Near a half the sign of x - (half) s, which a
-// fused multiply-add gives exactly, says on which side of it the quotient lies.  A
-// subnormal scale and its values are both taken 2^64 times (exactly).
+// rint(x / s) of the exact quotient, by a division.
 __device__ __forceinline__ int code_of(float x, float s) {
     if (!(s > 0.0f)) return 0;  // 0 or NaN
-    if (s < 1.17549435e-38f) {
-        s = __fmul_rn(s, kTwo64);
-        x = __fmul_rn(x, kTwo64);
+    if (s < kLiftBelow) {
+        s = __fmul_rn(s, kLift);
+        x = __fmul_rn(x, kLift);
     }
-    const float t = fminf(fmaxf(__fdiv_rn(x, s), -127.0f), 127.0f);
-    float q = rintf(t);
-    if (fabsf(__fsub_rn(t, q)) > 0.5f - 1.0f / 32768.0f) {
-        const float below = floorf(t), half = __fadd_rn(below, 0.5f);
-        const float e = __fmaf_rn(-half, s, x);
-        q = e > 0.0f ? __fadd_rn(below, 1.0f) : e < 0.0f ? below : rintf(half);
-    }
-    return static_cast<int>(q);
+    return nearest_code(fminf(fmaxf(__fdiv_rn(x, s), -127.0f), 127.0f), x, s);
 }
 
 __device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
