@@ -168,6 +168,11 @@ class GatedFF:
         _scale(X.scale, n, self.d, X.group, "X.scale")
         return n
 
+    @staticmethod
+    def _not_rows(X) -> None:
+        if isinstance(X, Rows8):
+            raise ValueError("X must be a tensor here: 8-bit rows are taken by backward")
+
     def _inputs(self, X, W_gate, W_up) -> int:
         n = self._kept(X) if isinstance(X, Rows8) else self._rows(X, "X", self.d)
         if self._rows(W_gate, "W_gate", self.d) != self.f or self._rows(W_up, "W_up", self.d) != self.f:
@@ -177,6 +182,7 @@ class GatedFF:
     def forward(self, X: torch.Tensor, W_gate: torch.Tensor, W_up: torch.Tensor,
                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """h of X [..., d]; ``out`` shares no memory with the inputs."""
+        self._not_rows(X)
         n = self._inputs(X, W_gate, W_up)
         if out is None:
             out = _empty((n, self.f) if X.dim() == 2 else (*X.shape[:-1], self.f), X, stream)
@@ -209,6 +215,7 @@ class GatedFF:
         return dx, dwg, dwu
 
     def __call__(self, X: torch.Tensor, W_gate: torch.Tensor, W_up: torch.Tensor) -> torch.Tensor:
+        self._not_rows(X)
         if self.rows8 and not torch.is_grad_enabled():  # nothing to keep
             return self.forward(X, W_gate, W_up)
         return _GatedFF.apply(self, X, W_gate, W_up)

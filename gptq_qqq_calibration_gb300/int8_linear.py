@@ -14,7 +14,7 @@ import torch
 
 from . import _lib
 from ._lib import HESS_BF16, HESS_F16, HESS_F32, check
-from .rows8 import Rows8, _scale, _stream, _used_on, _written, quantize_rows
+from .rows8 import Rows8, _is_rows, _scale, _stream, _used_on, _written, quantize_rows
 
 __all__ = ["int8_linear_create", "int8_linear_forward", "int8_linear_forward_rows8", "int8_linear_backward",
            "int8_linear_sync", "int8_linear_set_timeout", "int8_linear_destroy", "Int8Linear"]
@@ -131,6 +131,7 @@ class Int8Linear:
         return t.numel() // width
 
     def _weight(self, weight: Rows8) -> None:
+        _is_rows(weight, "weight")
         if weight.group != 0:
             raise ValueError("the weight must have one scale per output channel (group 0)")
         if self._rows(weight.codes, "weight.codes", self.d, torch.int8) != self.f:
@@ -170,6 +171,7 @@ class Int8Linear:
         """(dX, dW) from the 8-bit rows that forward read (or an 8-bit checkpoint of
         them, any group); None for what is not wanted."""
         self._weight(weight)
+        _is_rows(X, "X")
         n = self._rows(dY, "dY", self.f, self.dtype)
         if self._rows(X.codes, "X.codes", self.d, torch.int8) != n:
             raise ValueError(f"X must have {n} rows")

@@ -75,6 +75,8 @@ def _rows2d(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
 
 
 def _float_rows(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
     if t.dtype not in _DTYPES:
         raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
     return _rows2d(t, name)
@@ -84,6 +86,11 @@ def _code_rows(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
     if t.dtype is not torch.int8:
         raise ValueError(f"{name} must be int8, got {t.dtype}")
     return _rows2d(t, name)
+
+
+def _is_rows(rows, name: str) -> None:
+    if not hasattr(rows, "codes"):
+        raise ValueError(f"{name} must be 8-bit rows (Rows8), got {type(rows).__name__}")
 
 
 def _groups(d: int, group: int) -> int:
@@ -135,6 +142,7 @@ def rows8_quantize(X: torch.Tensor, group: int, codes_out: torch.Tensor, scale_o
 
 
 def _restore(rows: Rows8, X, stream) -> None:
+    _is_rows(rows, "rows")
     n, d, ldc = _code_rows(rows.codes, "codes")
     n2, d2, ldx = _float_rows(X, "X_out")
     if (n2, d2) != (n, d):
@@ -178,6 +186,8 @@ def restore_rows(rows: Rows8, dtype: torch.dtype = torch.bfloat16, out: Optional
         return out
     if dtype not in _DTYPES:
         raise ValueError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
+    if isinstance(rows, torch.Tensor):
+        _is_rows(rows, "rows")
     codes, scale, group = rows
     n, d, ldc = _code_rows(codes, "codes")
     dev = _same_device(codes, scale)
