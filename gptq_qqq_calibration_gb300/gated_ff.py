@@ -239,6 +239,8 @@ class _GatedFF(torch.autograd.Function):
     @staticmethod
     def forward(ctx, op, X, W_gate, W_up):
         ctx.op = op
+        if not any(ctx.needs_input_grad):  # nothing to keep
+            return op.forward(X, W_gate, W_up)
         if op.rows8:
             ctx.save_for_backward(*quantize_rows(X, group=128)[:2], W_gate, W_up)
         else:
