@@ -28,4 +28,18 @@ __device__ __forceinline__ int nearest_code(float t, float x, float s) {
     return static_cast<int>(q);
 }
 
+// Four int8 as two words of two float16: 1024 + (q + 128), less 1152.
+__device__ __forceinline__ void widen4(uint32_t q, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = q ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 k = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    __half2 x, y;
+    memcpy(&x, &a, 4);
+    memcpy(&y, &b, 4);
+    x = __hsub2(x, k);
+    y = __hsub2(y, k);
+    memcpy(&lo, &x, 4);
+    memcpy(&hi, &y, 4);
+}
+
 }  // namespace hk

@@ -150,8 +150,9 @@ template <class T>
 __device__ __forceinline__ Scale scale_of(uint32_t top) {
     Scale k;
     const float t = __uint_as_float(top);
-    // From 2^-100 on no step is subnormal, and t c, corrected by its remainder, is
-    // t / 127 correctly rounded (checked for every significand).
+    // From 2^-100 on no step is subnormal, and t c, corrected by its remainder, is t / 127
+    // correctly rounded: a quotient by a divisor known beforehand (Brisebarre, Muller and
+    // Raina, 2004), for every significand (tests/test_gpu_rows8_scales.py).
     if (top - 0x0d800000u < 0x7f800000u - 0x0d800000u) {
         const float c = 1.0f / 127.0f;
         constexpr float kBelow = 1.0f - 1.0f / 2097152.0f, kAbove = 1.0f + 1.0f / 2097152.0f;
@@ -255,50 +256,26 @@ __device__ __forceinline__ void encode(const Raw<T, V>& raw, int r, const Scale&
     }
 }
 
-// Four codes as two words of two float16 whole numbers: 1024 + (q + 128) has the byte
-// q ^ 0x80 at its low end.
-__device__ __forceinline__ uint2 wide4(uint32_t q) {
-    const uint32_t u = q ^ 0x80808080u;
-    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 k = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-    __half2 x, y;
-    memcpy(&x, &a, 4);
-    memcpy(&y, &b, 4);
-    x = __hsub2(x, k);
-    y = __hsub2(y, k);
-    memcpy(&a, &x, 4);
-    memcpy(&b, &y, 4);
-    return make_uint2(a, b);
-}
-
-// The codes of one run at column c, as bytes or as float16 whole numbers.
+// The codes of one run at column c, as bytes or as float16 whole numbers (those in runs of
+// eight or sixteen only).
 template <int V>
 __device__ __forceinline__ void store(int8_t* codes, __half* wide, int c, const uint32_t* q) {
     if constexpr (V == 1) {
-        if (codes) codes[c] = static_cast<int8_t>(q[0]);
-        else wide[c] = __int2half_rn(static_cast<int8_t>(q[0]));
+        codes[c] = static_cast<int8_t>(q[0]);
     } else if constexpr (V == 2) {
-        if (codes) *reinterpret_cast<unsigned short*>(codes + c) = static_cast<unsigned short>(q[0]);
-        else *reinterpret_cast<uint32_t*>(wide + c) = wide4(q[0]).x;
+        *reinterpret_cast<unsigned short*>(codes + c) = static_cast<unsigned short>(q[0]);
     } else if constexpr (V == 4) {
-        if (codes) *reinterpret_cast<uint32_t*>(codes + c) = q[0];
-        else *reinterpret_cast<uint2*>(wide + c) = wide4(q[0]);
-    } else if constexpr (V == 16) {
-        if (codes) {
-            *reinterpret_cast<uint4*>(codes + c) = make_uint4(q[0], q[1], q[2], q[3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint2 a = wide4(q[2 * i]), b = wide4(q[2 * i + 1]);
-                reinterpret_cast<uint4*>(wide + c)[i] = make_uint4(a.x, a.y, b.x, b.y);
-            }
-        }
+        *reinterpret_cast<uint32_t*>(codes + c) = q[0];
+    } else if (codes) {
+        if constexpr (V == 16) *reinterpret_cast<uint4*>(codes + c) = make_uint4(q[0], q[1], q[2], q[3]);
+        else *reinterpret_cast<uint2*>(codes + c) = make_uint2(q[0], q[1]);
     } else {
-        if (codes) {
-            *reinterpret_cast<uint2*>(codes + c) = make_uint2(q[0], q[1]);
-        } else {
-            const uint2 a = wide4(q[0]), b = wide4(q[1]);
-            *reinterpret_cast<uint4*>(wide + c) = make_uint4(a.x, a.y, b.x, b.y);
+#pragma unroll
+        for (int i = 0; i < V / 8; ++i) {
+            uint4 w;
+            widen4(q[2 * i], w.x, w.y);
+            widen4(q[2 * i + 1], w.z, w.w);
+            reinterpret_cast<uint4*>(wide + c)[i] = w;
         }
     }
 }
@@ -313,7 +290,7 @@ struct QuantizeParams {
     const void* x;
     int64_t ldx, n, ldc, ldw;
     int32_t d;
-    int32_t group;    // group kernel: 32 .. 256, or 256 for whole rows of at most 256 columns
+    int32_t group;    // group kernels: 32 .. 256, or 256 for whole rows of at most 256 columns
     int32_t shift;    // its logarithm
     int64_t groups;   // scales of a row
     int32_t items;    // group kernel: segments of a row
@@ -327,44 +304,19 @@ struct QuantizeParams {
 // from memory under the one at work.
 template <class T, int V, int kGroup>
 __device__ __forceinline__ void encode_segment(const QuantizeParams& p, const Raw<T, V>& raw, int64_t r, int c0, int lane) {
-    constexpr int kRuns = lane_values(V) / V;
-    const int group = kGroup ? kGroup : p.group;
-    // within a run a group is group / V lanes; beyond 32 lanes it is several runs
-    uint32_t top[kRuns];
+    static_assert(V >= 8 && kGroup >= 32 && kGroup <= 32 * V, "a lane's run is all it has, and lies in one group");
+    uint32_t top = raw.top(0);
 #pragma unroll
-    for (int k = 0; k < kRuns; ++k) {
-        top[k] = raw.top(k);
-        if constexpr (V == 1) {
-            top[k] = __reduce_max_sync(~0u, top[k]);
-        } else {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                if (o < group / V) top[k] = max(top[k], __shfl_xor_sync(~0u, top[k], o));
-        }
-    }
-    if constexpr (kRuns > 1) {
-#pragma unroll
-        for (int span = 1; span < kRuns; span *= 2)
-            if (group > 32 * V * span) {
-#pragma unroll
-                for (int k = 0; k < kRuns; ++k)
-                    if (!(k & span)) top[k] = top[k ^ span] = max(top[k], top[k ^ span]);
-            }
-    }
+    for (int o = kGroup / V / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
     int8_t* const codes = p.codes ? p.codes + r * p.ldc : nullptr;
     __half* const wide = p.codes ? nullptr : p.wide + r * p.ldw;
-    float* const scale = p.scale + r * p.groups;
-    Scale s;
-#pragma unroll
-    for (int k = 0; k < kRuns; ++k) {
-        const int c = c0 + column<V>(lane, k * V);
-        if (kRuns == 1 || ((32 * V * k) & (group - 1)) == 0) s = scale_of<T>(top[k]);  // a group's first run
-        if (c < p.d) {
-            if ((c & (group - 1)) == 0) scale[c >> p.shift] = s.s;
-            uint32_t q[V > 4 ? V / 4 : 1];
-            encode<T, V>(raw, k, s, q);
-            store<V>(codes, wide, c, q);
-        }
+    const Scale s = scale_of<T>(top);
+    const int c = c0 + lane * V;
+    if (c < p.d) {
+        if ((c & (kGroup - 1)) == 0) p.scale[r * p.groups + (c >> p.shift)] = s.s;
+        uint32_t q[V / 4];
+        encode<T, V>(raw, 0, s, q);
+        store<V>(codes, wide, c, q);
     }
 }
 
@@ -982,6 +934,7 @@ cudaError_t quantize_of(QuantizeParams& p, cudaStream_t s) {
     const int most = sizeof(T) == 2 ? 16 : 8;
     const int v = p.codes ? run_of(most, true, p.d, p.x, p.ldx, sizeof(T), p.codes, p.ldc, 1)
                           : run_of(most, false, p.d, p.x, p.ldx, sizeof(T), p.wide, p.ldw, 2);
+    if (!p.codes && v < 8) return cudaErrorInvalidValue;  // float16 codes leave in runs of at least eight
     if constexpr (sizeof(T) == 2) {
         if (v == 16) return quantize_as<T, 16>(p, s);
         const size_t smem = 2 * 16 * static_cast<size_t>((p.d >> 3) + 2);
