@@ -19,11 +19,13 @@
 // memory: two 192-column sums, so that one is drained under the other's products, and
 // two slots of 128 steps of A (more where the tile has fewer tokens).
 //
-// Many tokens are bound by the tensor pipe: 8,192 at 4,096 x 11,008 take 408 us, 1,810
-// TFLOP/s and 0.96 of the burst rate of a library's 16-bit GEMM.  Up to some 600 the bytes of the
-// weights should bound it, but what shows is latency: 37 tokens there take 16.4 us for 6.8 of
-// bytes: 2.6 us until the kernel in front lets this one start, 3 until the first stage is
-// converted, 8 for 32 stages at some 500 cycles each and 2 for the last tile's way out.
+// Many tokens are bound by the tensor pipe: 8,192 at 4,096 x 11,008 take 413 us in a CUDA graph,
+// 1,790 TFLOP/s and 0.95 of the burst rate of a library's 16-bit GEMM; called one after the other
+// 436 us (0.90), at the power cap.  Up to some 600 the bytes of the weights should bound it, but
+// what shows is latency: 37 tokens there take 15.8 us for 6.8 of bytes: 2.6 us until the kernel
+// in front lets this one start, 3 until the first stage is converted, 8 for 32 stages at some 500
+// cycles each and 2 for the last tile's way out.  (That stage cost does not depend on the rows, so
+// that the plan keeps 96 of them and 58 of 76 pairs are at work.)
 //
 // Few tokens do not pay for the trip through tensor memory: one or two take one pass over
 // the weights with dp4a, up to 16 (in small layers 32) one with warp-level MMAs.
@@ -746,7 +748,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // cover a row, and the CTA's warps cover `rp` rows side by side.  Four dp4a a granule
 // and token, one warp reduction a row and token (the more granules, the fewer), integer
 // adds in shared memory across warps: exact and independent of the order.
-// One token at 4,096 x 11,008: 11.0 us, 4.1 TB/s; at 8,192 x 28,672: 47.7 us, 4.9 TB/s.
+// One token at 4,096 x 11,008: 10.3 us, 4.4 TB/s; at 8,192 x 28,672: 39.0 us, 6.0 TB/s (CUDA
+// graphs of calls on weights from HBM, as the figures below).
 
 constexpr int kFewThreads = 512, kFewWarps = kFewThreads / 32;
 constexpr int kFewAhead = 256 * 1024;  // bytes a CTA asks into L2
@@ -886,7 +889,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const __grid_c
 
 // ------------------------------------------------------- up to 32 tokens
 //
-// Bound by reading the weights once, too, but with more products than dp4a has time for:
+// The weights are read once here, too, but with more products than dp4a has time for:
 // warp-level MMAs (m16n8k16, float16, float32 sums) on weights that go from memory
 // straight into registers.  A thread's 16 bytes of a row serve four MMAs: the
 // contraction's order within 64 columns is free, so it is the bytes' order (thread t of
@@ -896,9 +899,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const __grid_c
 // All CTAs, two per SM, take the same number of weight rows, kTilesM x 16 of them at a
 // time, and a CTA's warps share the columns, 64 at a time in turn: so every weight and every
 // token's value is read by one warp of the CTA, once, and needs no place in shared
-// memory.  A block's weights are fetched two to six blocks ahead, its tokens one.
-// With the tokens' quantization in front, at 4,096 x 11,008: 8 tokens 14.4 us (15.7 on pairs
-// of SMs), 16 tokens 16.3 (16.0 there); at 2,048 x 2,048 16 take 6.1 (10.3 there).
+// memory.  A block's weights are fetched two to six blocks ahead, its tokens one.  What bounds
+// it is both ways into the SMs: every CTA reads all tokens' float16 values from L2, which for
+// 16 tokens are 39 MB beside 45 MB of weights at 4,096 x 11,008, and 103 MB at 11,008 x 4,096.
+// With the tokens' quantization in front, at 4,096 x 11,008: 3 tokens 12.6 us (15.0 on pairs of
+// SMs), 8 13.2 (15.1 there), 16 15.4 (15.1); 16 at 2,048 x 2,048 5.6 (9.9), but at 11,008 x 4,096
+// 19.1 (17.5).
 
 constexpr int kMidThreads = 256, kMidWarps = kMidThreads / 32;
 constexpr int kMidFlush = 1024 / 64;  // blocks whose sums stay below 2^24
@@ -1231,7 +1237,8 @@ hess_status il_launch(Kernel kernel, const Params& p, int64_t grid, int threads,
 
 // Granules of 16 columns a thread of the few-token kernel takes: as many as there are (the
 // fewer warps share a row, the fewer sums meet), unless that leaves more threads idle; 0
-// where a row is too wide.
+// where a row is too wide.  (0.85: one token at 5,120 x 13,824 14.6 us, 16.1 with eight always; at
+// 4,096 x 4,096 5.5 us, 5.9 with the fewest idle threads alone.)
 int few_granules(int64_t d) {
     const int64_t granules = d / 16;
     int best = 0;
@@ -1304,9 +1311,9 @@ int64_t mid_rows(const int8_linear_ctx* g) { return ceil_div(g->f, 2 * g->sms); 
 
 // From 17 tokens on only small layers, whose rows a CTA takes in one turn: in two turns, or
 // over more columns, every CTA's reading of all tokens costs more than the pairs' start
-// (24 tokens: 2,048 x 2,048 7.0 us against 10.5, 4,096 x 8,192 14.8 against 15.6, but
-// 8,192 x 2,048 17.5 against 14.3; 32 at 4,096 x 4,096 12.4 against 13.5, at 2,560 x 6,912, two
-// turns, 18.4 against 12.4).
+// (24 tokens: 2,048 x 2,048 6.4 us against 10.0, 4,096 x 8,192 13.8 against 14.8, but, by an
+// earlier measurement, 8,192 x 2,048 17.5 against 14.3; 32 at 4,096 x 4,096 11.9 against 12.8, at
+// 2,560 x 6,912, two turns, 18.4 against 12.4).
 bool is_mid(const int8_linear_ctx* g, int64_t n) {
     const int tiles_n = static_cast<int>(ceil_div(n, 8));
     return tiles_n <= 2 || (tiles_n <= 4 && g->d <= 4096 && mid_rows(g) <= 16 * mid_tiles(tiles_n));

@@ -64,8 +64,8 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // at 24 bytes a cycle and SM).  A turn of units costs kTurn more.  Tiles in pieces cost their
 // meeting, and the last pair's reading of each piece but its own: 10,000 cycles and 24 a token,
 // or 5,000 and 12 where whole tiles come before them, whose way out it hides behind.  (Fitted:
-// 1,000 tokens at 8,192 x 4,096 56.7 us, whole tiles alone 65.3; at 4,096 x 4,096 39.0 and 40.7; 200
-// there 17.7 us whole, 18.8 in pieces.)
+// 1,000 tokens at 8,192 x 4,096 54.8 us, whole tiles alone 63.1; at 4,096 x 4,096 36.3 and 37.9; 37
+// at 11,008 x 4,096 18.4 and 30.4; 200 at 4,096 x 4,096 17.3 us whole, 18.8 in pieces.)
 inline void plan(Schedule& p, int64_t pairs) {
     constexpr int64_t kIssue = 800, kAlone = 100, kTurn = 700;
     const int64_t n_kb = ceil_div(p.d, kKB);

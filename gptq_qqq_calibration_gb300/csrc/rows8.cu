@@ -22,10 +22,10 @@
 //     alike that is the code, and where they do not (1 value in 10^5) the exact sign of
 //     the remainder at the half between them decides.
 //
-// Bytes bound all of it: 16,384 x 11,008 bf16 take 97 us with a scale per 128 columns, 90
-// with one per row and 80 back (floor 80 at the copy rate of 6,781 GB/s), 32,768 x 4,096 fp32
-// 102 and 100 us (floor 99).  Rows that are no multiples of 16 bytes cost more instructions:
-// 16,383 x 8,191 bf16 97 us per 32 columns, 74 per row and 70 back (floor 59).
+// Bytes bound all of it (times in CUDA graphs): 16,384 x 11,008 bf16 take 92 us with a scale per
+// 128 columns, 89 with one per row and 79 back (floor 80 at the copy rate of 6,781 GB/s),
+// 32,768 x 4,096 fp32 101 and 98 us (floor 99).  Rows that are no multiples of 16 bytes cost more
+// instructions: 16,383 x 8,191 bf16 96 us per 32 columns, 71 per row and 70 back (floor 59).
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -870,7 +870,11 @@ cudaError_t launch_stream(Kernel kernel, const QuantizeParams& p, size_t smem, c
 }
 
 // A scale for every row of more than 256 values.  Few rows are spread over more warps
-// each, so that a row takes one round trip to memory and little work after it.
+// each, so that a row takes one round trip to memory and little work after it; many go one
+// to a warp, or through shared memory.  The border of 512 rows lies between those of narrow
+// rows and of wide 16-bit ones (few / many, us): 1,024 fp32 columns 1.68 / 1.90 at 512 rows, 2.68 / 2.15
+// at 1,024; 4,096 bf16 1.46 / 1.59 at 64, 2.21 / 1.74 at 256, 5.39 / 3.85 at 1,024; 16,384 bf16 4.15 / 4.34
+// at 256, 6.11 / 6.24 at 512, 17.4 / 16.5 at 2,048; 4,100 bf16 1.83 / 2.29 at 256, 6.31 / 4.36 at 1,024.
 template <class T, int V>
 cudaError_t quantize_rows(QuantizeParams& p, cudaStream_t s) {
     if (p.d <= kShort * kSegment && p.n > 512) {
@@ -1042,7 +1046,8 @@ bool meet(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
 
 // Rows that follow each other without a gap, and whose groups end with the row, are as well
 // fewer and longer rows: n, d and group become those, and no lane is left without values at a
-// row's end (131,072 x 128 bf16 with a scale per row: 10.9 us and 8.0 back; one by one 41 and 26).
+// row's end (131,072 x 128 bf16 with a scale per row: 9.6 us and 9.0 back; one by one 41 and 26).
+// Above 2^30 values they are joined by powers of two, which an odd number of rows does not allow.
 static void join_rows(int64_t& n, int64_t& d, int32_t& group, int64_t& ldx, int64_t& ldc) {
     constexpr int64_t kMost = int64_t(1) << 30;  // columns are counted in 32 bits
     const int32_t whole = group ? group : d >= 32 && d <= 256 && (d & (d - 1)) == 0 ? static_cast<int32_t>(d) : 0;

@@ -104,7 +104,8 @@ class Int8Linear:
 
     Called as a function, ``op(X, W)`` with a 16-bit or fp32 master weight, the
     object is a node of an autograd graph: it quantizes both, keeps their 8-bit rows
-    for the backward pass, and sends gradients straight through the roundings.
+    for the backward pass, and sends gradients straight through the roundings.  Gradients
+    are made in fp32 sums and rounded to the object's type, that of an fp32 master weight too.
     A captured backward pass belongs into the capture of its forward pass, with no
     other graph of the same leaf tensors alive.
 

@@ -94,7 +94,10 @@ hess_status gated_ff_reserve_rows8(gated_ff_t g);
  *   X_scale : float32 [n_tokens] (group 0) or [n_tokens, ceil(d / group)].
  * The values that X_codes and X_scale stand for are rounded to the handle's type and take
  * X's place: the result is that of gated_ff_backward on rows8_restore's output, bit for
- * bit.  Needs gated_ff_reserve_rows8 (HESS_ERR_INVALID without it). */
+ * bit.  (The rounding of X^ reaches g and u and enters dW_*: with that of dg and du 3.2e-3
+ * relative to the fp32 formulas in bf16, 1.7e-3 for the results' own rounding alone.  With a
+ * scale per row g and u could be had from the codes themselves; dW_* needs X^ in 16 bits all
+ * the same, and both groups keep one definition.)  Needs gated_ff_reserve_rows8 (HESS_ERR_INVALID without it). */
 hess_status gated_ff_backward_rows8(gated_ff_t g, const int8_t* X_codes, const float* X_scale, int32_t group,
                                     int64_t n_tokens, const void* W_gate, const void* W_up, const void* dH,
                                     void* dX_out, void* dW_gate_out, void* dW_up_out, hess_stream_t stream);

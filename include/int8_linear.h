@@ -19,8 +19,11 @@
  *     dX = dY W^,   dW = dY^T X^,   W^ = sw qw,  X^ = s q
  *
  * W^ and X^ are rounded to the 16-bit type, because the tensor cores take 16-bit
- * operands; sums are fp32 in a fixed order and dX and dW are rounded once: the same
- * call gives the same bits, forward and backward.
+ * operands, and both scales lie along the sums, where they cannot be left for the result.
+ * That moves dX and dW as far as their own rounding does (relative 2-norm 2.35e-3 with both
+ * against 1.66e-3 with one in bf16, 2.9e-4 and 2.1e-4 in f16); a second product with what the
+ * rounding left would take twice the time.  Sums are fp32 in a fixed order and dX and dW are
+ * rounded once: the same call gives the same bits, forward and backward.
  */
 #ifndef GPTQ_QQQ_INT8_LINEAR_H
 #define GPTQ_QQQ_INT8_LINEAR_H

@@ -34,7 +34,8 @@ extern "C" {
 /* Codes and scales of X.
  *   X         : [n_rows, d] of `dtype` (HESS_BF16, HESS_F16 or HESS_F32), row r at
  *               X + r * ldx elements, ldx >= d; aligned to its element.
- *   n_rows    : 0 (a no-op) .. 2^31 - 1;  d : 1 .. 2^24, else HESS_ERR_UNSUPPORTED.
+ *   n_rows    : 0 (a no-op) .. 2^31 - 1;  d : 1 .. 2^24, else HESS_ERR_UNSUPPORTED; so are
+ *               strides (ldx, ldc) above 2^28 and n_rows * ceil(d / 1024) above 2^34 - 8.
  *   group     : 0, 32, 64, 128 or 256, else HESS_ERR_UNSUPPORTED.
  *   codes_out : int8 [n_rows, d], row r at codes_out + r * ldc, ldc >= d; the bytes
  *               between rows are left as they are.
